@@ -339,12 +339,13 @@ def run(st):
         return _plain(st)
     import block_scaled_precision_bf16_amd as mx
     case, op = st["case"], st["case"]["op"]
+    flags = mx.OUT_F32 if case["out"] == "f32" else 0
     if op == "matvec":
-        return mx.nvfp4_matvec(st["x"], st["qw"], st["sw"], st["sg"], out=st["out"])
+        return mx.nvfp4_matvec(st["x"], st["qw"], st["sw"], st["sg"], flags=flags, out=st["out"])
     if op == "matvec_experts":
         return mx.nvfp4_matvec_experts(st["x"], st["experts"], st["qw"], st["sw"], st["sg"],
-                                       out=st["out"])
-    flags = (mx.A_E5M2 if case["a"] == "e5m2" else 0) | (mx.B_E5M2 if case["b"] == "e5m2" else 0) \
+                                       flags=flags, out=st["out"])
+    flags |= (mx.A_E5M2 if case["a"] == "e5m2" else 0) | (mx.B_E5M2 if case["b"] == "e5m2" else 0) \
         | (mx.SCALE_TILED if case["tiled"] else 0)
     args = (st["qa"], st["sa"], st["qb"], st["sb"])
     if op == "matmul":
