@@ -9,7 +9,8 @@ The same names as the C ABI:
     mx_quantize, mx_quantize_workspace_size, mx_scale_size, mx_quantize_grouped,
     mx_quantize_grouped_workspace_size, mx_grouped_scale_size, mx_quantize_gated,
     mx_fused_values, mx_absmax_bf16, nvfp4_quantize_transpose,
-    mx_status_str, mx_abi_version
+    mx_matmul, mx_matmul_grouped, mx_matmul_wgrad_grouped, nvfp4_matvec,
+    nvfp4_matvec_experts, mx_status_str, mx_abi_version
 take torch tensors (bf16 inputs, or int16/uint16 holding bf16 bits, on a ROCm
 device) and return dicts of uint8 / float32 torch tensors on the same device.
 The MXFP8 casts take the format flags ELEM_E5M2 / SCALE_ROUND_UP and the
@@ -31,6 +32,8 @@ SCALE_TILED = 16                     # GEMM-ready scale layout flag, OR-ed into 
 FUSE_NONE, FUSE_GELU, FUSE_DGELU, FUSE_DSILU, FUSE_DBIAS = 0, 1, 2, 3, 0x10
 GATED_SWIGLU, GATED_GEGLU = 1, 2
 OP_GATED, OP_DGATED = 0x100, 0x200
+# flags of the products (with SCALE_TILED): operand formats, output type
+A_E5M2, B_E5M2, OUT_F32, ACCUMULATE = 4, 32, 64, 128
 (MX_OK, MX_ERR_NULL, MX_ERR_ENUM, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_WORKSPACE,
  MX_ERR_ALIAS, MX_ERR_HIP, MX_ERR_UNSUPPORTED) = range(9)
 
@@ -40,6 +43,8 @@ EXPORTS = ("mx_quantize", "mx_quantize_workspace_size", "mx_quantize_noalloc", "
            "mx_quantize_dgated", "mx_fused_values",
            "mx_absmax_bf16", "nvfp4_quantize_transpose", "nvfp4_quantize_transpose_2d",
            "mx_absmax_bf16_grouped", "nvfp4_quantize_transpose_grouped",
+           "mx_matmul", "mx_matmul_grouped", "mx_matmul_wgrad_grouped", "nvfp4_matvec",
+           "nvfp4_matvec_experts",
            "mx_status_str", "mx_abi_version")
 
 
@@ -108,6 +113,18 @@ def lib():
         L.nvfp4_quantize_transpose_grouped.argtypes = [_vp, _i64, _vp, ctypes.c_int, _vp,
                                                        ctypes.c_int, ctypes.c_uint, _vp, _vp,
                                                        _vp, _vp, _vp, _vp]
+        L.mx_matmul.restype = ctypes.c_int
+        L.mx_matmul.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_uint, _vp, _vp]
+        L.mx_matmul_grouped.restype = ctypes.c_int
+        L.mx_matmul_grouped.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _vp, ctypes.c_int,
+                                        ctypes.c_uint, _vp, _vp]
+        L.mx_matmul_wgrad_grouped.restype = ctypes.c_int
+        L.mx_matmul_wgrad_grouped.argtypes = L.mx_matmul_grouped.argtypes
+        L.nvfp4_matvec.restype = ctypes.c_int
+        L.nvfp4_matvec.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, ctypes.c_uint, _vp, _vp]
+        L.nvfp4_matvec_experts.restype = ctypes.c_int
+        L.nvfp4_matvec_experts.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, ctypes.c_int, _i64,
+                                           _i64, ctypes.c_uint, _vp, _vp]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ctypes.c_int]
         L.mx_abi_version.restype = ctypes.c_int
@@ -549,3 +566,179 @@ def mx_quantize_gated_grouped(x, group_rows, act, grad=None, axis=ROWWISE | COLW
                                               axis, act, *ptrs, _stream(dev, stream))
     _check(st, "mx_quantize_gated_grouped")
     return {k: o.get(k) for k in ("q_row", "s_row", "q_col", "s_col")}
+
+
+# ---- products on quantised operands -------------------------------------------
+
+BF16 = torch.bfloat16
+
+
+def _codes(t, name):
+    """An operand's codes or scales: a contiguous uint8 tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype != U8:
+        raise TypeError(f"{name} must be a uint8 tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _want_bytes(t, n, name):
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} bytes, got {t.numel()}")
+
+
+def _product_out(out, shape, flags, dev):
+    """The output tensor: bf16 (int16 / uint16 bits accepted in `out`) or, with
+    OUT_F32, float32; ACCUMULATE needs the caller's."""
+    dtype = F32 if flags & OUT_F32 else BF16
+    if out is None:
+        if flags & ACCUMULATE:
+            raise ValueError("ACCUMULATE adds to `out`: it must be passed")
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a tensor")
+    ok = out.dtype == dtype or (dtype == BF16 and out.dtype in (I16, torch.uint16))
+    n = 1
+    for d in shape:
+        n *= d
+    if not ok or out.numel() != n or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {dtype} tensor of {n} elements on {dev}; got "
+                         f"{out.dtype}, {out.numel()} elements on {out.device}")
+    return out
+
+
+def _scale_bytes(rows, cols, flags):
+    """Bytes of one operand's scales (none for an operand without elements)."""
+    nb = -(-cols // 32)
+    if flags & SCALE_TILED:
+        return -(-rows // 32) * -(-nb // 8) * 256
+    return rows * nb
+
+
+def _launch(where, dev, stream, fn, *args):
+    """Calls fn on the tensors' device (made current for the call) and stream."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(dev, stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev, stream))
+    _check(st, where)
+
+
+def mx_matmul(qa, sa, qb, sb, flags=0, out=None, stream=None):
+    """y[M][N] = A B^T of MXFP8 operands quantised along K: codes qa [M][K],
+    qb [N][K] and their scales sa, sb as the casts return them (compact, or in
+    the tile layout with SCALE_TILED).  bf16, or float32 with OUT_F32; `out`
+    may hold the output (with ACCUMULATE it is added to)."""
+    for t, name in ((qa, "qa"), (sa, "sa"), (qb, "qb"), (sb, "sb")):
+        _codes(t, name)
+    if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] != qb.shape[1]:
+        raise ValueError(f"qa [M][K] and qb [N][K] must be 2-D with one K, got "
+                         f"{tuple(qa.shape)} and {tuple(qb.shape)}")
+    (M, K), N, dev = qa.shape, qb.shape[0], qa.device
+    _want_bytes(sa, _scale_bytes(M, K, flags), "sa")
+    _want_bytes(sb, _scale_bytes(N, K, flags), "sb")
+    y = _product_out(out, (M, N), flags, dev)
+    _on_device(dev, sa, qb, sb)
+    _launch("mx_matmul", dev, stream, lib().mx_matmul, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(),
+            sb.data_ptr(), M, N, K, flags, y.data_ptr())
+    return y
+
+
+def mx_matmul_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, stream=None):
+    """y[M][N]: each group's rows of A (codes qa [M][K], stacked as for
+    mx_quantize_grouped, the groups' scales one after the other) by the group's
+    own B_g [N][K] (codes qb and scales sb of the G matrices one after the
+    other, any shape)."""
+    for t, name in ((qa, "qa"), (sa, "sa"), (qb, "qb"), (sb, "sb")):
+        _codes(t, name)
+    if qa.dim() != 2:
+        raise ValueError(f"qa must be 2-D, got shape {tuple(qa.shape)}")
+    (M, K), G, dev = qa.shape, len(group_rows), qa.device
+    _group_total(group_rows, M)
+    if G == 0 or K == 0 or qb.numel() % (G * K):
+        raise ValueError(f"qb must hold {G} matrices with rows of {K}, got {qb.numel()} bytes")
+    N = qb.numel() // (G * K)
+    _want_bytes(sa, sum(_scale_bytes(int(r), K, flags) for r in group_rows), "sa")
+    _want_bytes(sb, G * _scale_bytes(N, K, flags), "sb")
+    y = _product_out(out, (M, N), flags, dev)
+    _on_device(dev, sa, qb, sb)
+    rows = _rows_arg(group_rows)
+    _launch("mx_matmul_grouped", dev, stream, lib().mx_matmul_grouped, qa.data_ptr(),
+            sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), N, K, ctypes.addressof(rows), G, flags,
+            y.data_ptr())
+    return y
+
+
+def mx_matmul_wgrad_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, stream=None):
+    """dW[G][N][K]: each group's sum over its rows m of dY[m][n] X[m][k], from
+    the transposed outputs (q_col, s_col) of the grouped casts of dY [M][N]
+    (qa, sa) and X [M][K] (qb, sb).  An empty group's gradient is 0 (with
+    ACCUMULATE: unchanged)."""
+    for t, name in ((qa, "qa"), (sa, "sa"), (qb, "qb"), (sb, "sb")):
+        _codes(t, name)
+    G, dev = len(group_rows), qa.device
+    M = sum(int(r) for r in group_rows)
+    _group_total(group_rows, M)
+    if M == 0 or qa.numel() % M or qb.numel() % M:
+        raise ValueError(f"qa and qb must hold whole columns of {M} rows, got {qa.numel()} and "
+                         f"{qb.numel()} bytes")
+    N, K = qa.numel() // M, qb.numel() // M
+    _want_bytes(sa, sum(_scale_bytes(N, int(r), flags) for r in group_rows), "sa")
+    _want_bytes(sb, sum(_scale_bytes(K, int(r), flags) for r in group_rows), "sb")
+    y = _product_out(out, (G, N, K), flags, dev)
+    _on_device(dev, sa, qb, sb)
+    rows = _rows_arg(group_rows)
+    _launch("mx_matmul_wgrad_grouped", dev, stream, lib().mx_matmul_wgrad_grouped, qa.data_ptr(),
+            sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), N, K, ctypes.addressof(rows), G, flags,
+            y.data_ptr())
+    return y
+
+
+def _nv_weights(x, qw, sw, sg, G):
+    """Sizes of x [T][K] and G NVFP4 matrices [N][K] (codes [G * N][ceil(K/2)])."""
+    x = _2d(x, "x")
+    T, K = x.shape
+    pitch, nb = -(-K // 2), -(-K // 16)
+    _codes(qw, "qw")
+    _codes(sw, "sw")
+    if K == 0 or G == 0 or qw.numel() % (G * pitch):
+        raise ValueError(f"qw must hold {G} matrices with rows of {pitch} bytes, got {qw.numel()}")
+    N = qw.numel() // (G * pitch)
+    _want_bytes(sw, G * N * nb, "sw")
+    _f32_vec(sg, G, "sg", x.device)
+    return T, N, K
+
+
+def nvfp4_matvec(x, qw, sw, sg, flags=0, out=None, stream=None):
+    """y[T][N] = x W^T: x bf16 [T][K], W [N][K] as nvfp4_quantize_transpose
+    returns it (q_row, s_row, sg).  bf16, or float32 with OUT_F32."""
+    T, N, K = _nv_weights(x, qw, sw, sg, 1)
+    dev = x.device
+    y = _product_out(out, (T, N), flags, dev)
+    _on_device(dev, qw, sw)
+    _launch("nvfp4_matvec", dev, stream, lib().nvfp4_matvec, x.data_ptr(), T, qw.data_ptr(),
+            sw.data_ptr(), sg.data_ptr(), N, K, flags, y.data_ptr())
+    return y
+
+
+def nvfp4_matvec_experts(x, experts, qw, sw, sg, flags=0, out=None, stream=None):
+    """y[T][top][N]: y[t][j] = x[t] W_e^T with e = experts[t][j] (int32 [T][top])
+    among the G = len(sg) stacked matrices qw [G * N][ceil(K/2)], sw; a row of
+    zeros for an e outside 0 .. G - 1."""
+    if not isinstance(sg, torch.Tensor) or not isinstance(experts, torch.Tensor):
+        raise TypeError("sg and experts must be tensors")
+    G = sg.numel()
+    T, N, K = _nv_weights(x, qw, sw, sg, G)
+    dev = x.device
+    if experts.dtype != torch.int32 or experts.dim() != 2 or experts.shape[0] != T \
+            or not experts.is_contiguous():
+        raise ValueError(f"experts must be a contiguous int32 tensor [{T}][top], got "
+                         f"{experts.dtype} {tuple(experts.shape)}")
+    top = experts.shape[1]
+    y = _product_out(out, (T, top, N), flags, dev)
+    _on_device(dev, experts, qw, sw)
+    _launch("nvfp4_matvec_experts", dev, stream, lib().nvfp4_matvec_experts, x.data_ptr(),
+            experts.data_ptr(), T, top, qw.data_ptr(), sw.data_ptr(), sg.data_ptr(), G, N, K, flags,
+            y.data_ptr())
+    return y

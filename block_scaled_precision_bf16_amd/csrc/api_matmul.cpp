@@ -1,0 +1,231 @@
+// api_matmul.cpp -- the extern "C" entry points of the products on quantised
+// operands (declared and documented in include/mxcast.h): argument validation
+// on the host, then one kernel launch on the caller's stream.  As in api.cpp,
+// validation runs before any HIP call.
+
+#include "mxcast.h"
+
+#include <stdint.h>
+
+#include "launch_mm.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 23;
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxTiles = int64_t(1) << 30;    // workgroups of one launch
+
+constexpr unsigned kMmBits =
+    MX_A_E5M2 | MX_B_E5M2 | MX_SCALE_TILED | MX_OUT_F32 | MX_OUT_ACCUMULATE;
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb)
+{
+    if (!a || !b || na == 0 || nb == 0)
+        return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+
+bool size_ok(int64_t a, int64_t b)
+{
+    return a > 0 && b > 0 && a <= kMaxDim && b <= kMaxDim && a * b <= kMaxElems;
+}
+
+mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes of the scales of a [rows][cols] operand blocked along cols (0 for an
+// operand without elements).
+int64_t scale_bytes(int64_t rows, int64_t cols, bool tiled)
+{
+    const int64_t nb = ceil_div(cols, 32);
+    return tiled ? ceil_div(rows, 32) * ceil_div(nb, 8) * 256 : rows * nb;
+}
+
+// Bytes of each operand of a launch, as the table lays them out.
+struct MmBytes {
+    uint64_t qa, sa, qb, sb, y;
+};
+
+// Validates the group sizes and fills the table but for tile0.  dim and N as
+// in MmArgs.
+bool build_table(const int64_t *rows, int G, int64_t dim, int64_t N, bool sum_rows, bool tiled,
+                 int out_size, mxk::MmTable &t, MmBytes &n)
+{
+    if (!rows || G < 1 || G > mxk::kMmMaxGroups || dim <= 0 || N <= 0)
+        return false;
+    t = mxk::MmTable{};
+    t.count = G;
+    int64_t M = 0, sa = 0, sb = 0;
+    for (int g = 0; g < G; g++) {
+        if (rows[g] < 0 || rows[g] > kMaxDim)
+            return false;
+        M += rows[g];
+    }
+    if (!size_ok(M, dim) || !size_ok(M, N) || !size_ok(dim, N) || G * (dim * N) > kMaxElems)
+        return false;
+    int64_t r = 0;
+    for (int g = 0; g < G; g++) {
+        t.row0[g] = r;
+        t.sa_off[g] = sa;
+        t.sb_off[g] = sb;
+        r += rows[g];
+        if (sum_rows) {
+            sa += scale_bytes(dim, rows[g], tiled);
+            sb += scale_bytes(N, rows[g], tiled);
+        } else {
+            sa += scale_bytes(rows[g], dim, tiled);
+            sb += scale_bytes(N, dim, tiled);
+        }
+    }
+    t.row0[G] = M;
+    n.qa = (uint64_t)(M * dim);
+    n.qb = (uint64_t)(sum_rows ? M * N : G * dim * N);
+    n.sa = (uint64_t)sa;
+    n.sb = (uint64_t)sb;
+    n.y = (uint64_t)(sum_rows ? G * dim * N : M * N) * (uint64_t)out_size;
+    return true;
+}
+
+mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
+                  int64_t dim, int64_t N, const int64_t *rows, int G, bool sum_rows, unsigned flags,
+                  void *y, hipStream_t stream)
+{
+    if ((flags & ~kMmBits) || ((flags & MX_OUT_ACCUMULATE) && !(flags & MX_OUT_F32)))
+        return MX_ERR_ENUM;
+    if (!qa || !sa || !qb || !sb || !y || !rows)
+        return MX_ERR_NULL;
+    const bool tiled = (flags & MX_SCALE_TILED) != 0;
+    mxk::MmTable t;
+    MmBytes n;
+    if (!build_table(rows, G, dim, N, sum_rows, tiled, flags & MX_OUT_F32 ? 4 : 2, t, n))
+        return MX_ERR_SHAPE;
+    if (!aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
+        !aligned(y, 16))
+        return MX_ERR_ALIGN;
+    if (overlap(y, n.y, qa, n.qa) || overlap(y, n.y, sa, n.sa) || overlap(y, n.y, qb, n.qb) ||
+        overlap(y, n.y, sb, n.sb))
+        return MX_ERR_ALIAS;
+
+    mxk::MmArgs a{};
+    a.qa = qa;
+    a.sa = sa;
+    a.qb = qb;
+    a.sb = sb;
+    a.y = y;
+    a.dim = dim;
+    a.N = N;
+    a.sum_rows = sum_rows;
+    a.tiled = tiled;
+    a.a_e5m2 = (flags & MX_A_E5M2) != 0;
+    a.b_e5m2 = (flags & MX_B_E5M2) != 0;
+    a.out_f32 = (flags & MX_OUT_F32) != 0;
+    a.accumulate = (flags & MX_OUT_ACCUMULATE) != 0;
+    a.sa_bytes = (int64_t)n.sa;
+    a.sb_bytes = (int64_t)n.sb;
+    // Rows that all start at a multiple of 16 bytes take the tiled kernel.
+    bool rows16 = dim % 16 == 0;
+    if (sum_rows) {
+        rows16 = true;
+        for (int g = 0; g < G; g++)
+            rows16 = rows16 && rows[g] % 16 == 0;
+    }
+    const bool tile = rows16 && n.sa >= 8 && n.sb >= 8;
+    const int64_t tm = tile ? mxk::kMmTileM : mxk::kMmAnyTile;
+    const int64_t tn = tile ? mxk::kMmTileN : mxk::kMmAnyTile;
+    int64_t tiles = 0;
+    for (int g = 0; g < G; g++) {
+        t.tile0[g] = (int32_t)tiles;
+        tiles += ceil_div(sum_rows ? dim : rows[g], tm) * ceil_div(N, tn);
+        if (tiles > kMaxTiles)
+            return MX_ERR_SHAPE;
+    }
+    t.tile0[G] = (int32_t)tiles;
+    return from_hip(tile ? mxk::launch_mm_tile(a, t, stream) : mxk::launch_mm_any(a, t, stream));
+}
+
+mx_status mv_impl(const void *x, const int32_t *experts, int64_t T, int64_t top, const uint8_t *qw,
+                  const uint8_t *sw, const float *sg, int G, int64_t N, int64_t K, unsigned flags,
+                  void *y, hipStream_t stream)
+{
+    if (!size_ok(T, K) || !size_ok(N, K) || top < 1 || top > 64 || !size_ok(T * top, N) || G < 1 ||
+        G > 1024 || G * (N * K) > kMaxElems)
+        return MX_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 16) || !aligned(y, 16) ||
+        !aligned(sg, 4) || (experts && !aligned(experts, 4)))
+        return MX_ERR_ALIGN;
+    const uint64_t ny = (uint64_t)(T * top * N) * (flags & MX_OUT_F32 ? 4 : 2);
+    if (overlap(y, ny, x, 2 * (uint64_t)(T * K)) ||
+        overlap(y, ny, qw, (uint64_t)(G * N * ((K + 1) / 2))) ||
+        overlap(y, ny, sw, (uint64_t)(G * N * ((K + 15) / 16))) ||
+        overlap(y, ny, sg, 4 * (uint64_t)G) ||
+        overlap(y, ny, experts, 4 * (uint64_t)(T * top)))
+        return MX_ERR_ALIAS;
+
+    mxk::MvArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.experts = experts;
+    a.qw = qw;
+    a.sw = sw;
+    a.sg = sg;
+    a.y = y;
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.top = (int32_t)top;
+    a.G = G;
+    a.out_f32 = (flags & MX_OUT_F32) != 0;
+    return from_hip(mxk::launch_mv(a, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
+                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream)
+{
+    return mm_impl(qa, sa, qb, sb, K, N, &M, 1, false, flags, y, stream);
+}
+
+mx_status mx_matmul_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
+                            const uint8_t *sb, int64_t N, int64_t K, const int64_t *group_rows,
+                            int G, unsigned flags, void *y, hipStream_t stream)
+{
+    return mm_impl(qa, sa, qb, sb, K, N, group_rows, G, false, flags, y, stream);
+}
+
+mx_status mx_matmul_wgrad_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
+                                  const uint8_t *sb, int64_t N, int64_t K,
+                                  const int64_t *group_rows, int G, unsigned flags, void *dw,
+                                  hipStream_t stream)
+{
+    return mm_impl(qa, sa, qb, sb, N, K, group_rows, G, true, flags, dw, stream);
+}
+
+mx_status nvfp4_matvec(const void *x, int64_t T, const uint8_t *qw, const uint8_t *sw,
+                       const float *sg, int64_t N, int64_t K, unsigned flags, void *y,
+                       hipStream_t stream)
+{
+    if (flags & ~MX_OUT_F32)
+        return MX_ERR_ENUM;
+    if (!x || !qw || !sw || !sg || !y)
+        return MX_ERR_NULL;
+    return mv_impl(x, nullptr, T, 1, qw, sw, sg, 1, N, K, flags, y, stream);
+}
+
+mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T, int64_t top,
+                               const uint8_t *qw, const uint8_t *sw, const float *sg, int G,
+                               int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream)
+{
+    if (flags & ~MX_OUT_F32)
+        return MX_ERR_ENUM;
+    if (!x || !experts || !qw || !sw || !sg || !y)
+        return MX_ERR_NULL;
+    return mv_impl(x, experts, T, top, qw, sw, sg, G, N, K, flags, y, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,64 @@
+// launch_mm.h -- internal interface between the host entry points of the
+// products on quantised operands (api_matmul.cpp) and their kernels.  Not
+// installed; the public ABI is mxcast.h.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace mxk {
+
+constexpr int kMmMaxGroups = 64;
+
+// One launch of Y_g = A_g B_g^T over G groups.  Group g multiplies its
+// operands A_g [m_g][k_g] and B_g [N][k_g] (codes row-major, each row's
+// elements along the summed axis) into Y_g [m_g][N].
+//   by expert (sum_rows = 0):  m_g = rows of group g, k_g = dim; the operands
+//       B_g and their scales stand one after the other;
+//   weight gradient (sum_rows = 1):  m_g = dim, k_g = rows of group g; A, B
+//       and their scales hold the groups one after the other, Y is [G][dim][N].
+struct MmTable {
+    int32_t count;
+    int32_t tile0[kMmMaxGroups + 1];    // first workgroup tile of each group
+    int64_t row0[kMmMaxGroups + 1];     // first stacked row of each group
+    int64_t sa_off[kMmMaxGroups];       // byte offsets of the groups' scales
+    int64_t sb_off[kMmMaxGroups];
+};
+
+struct MmArgs {
+    const uint8_t *qa, *sa, *qb, *sb;
+    void *y;
+    int64_t dim, N;
+    int64_t sa_bytes, sb_bytes;         // of all groups' scales
+    int32_t sum_rows;
+    int32_t tiled;                      // scales in MX_SCALE_TILED layout
+    int32_t a_e5m2, b_e5m2;
+    int32_t out_f32, accumulate;        // fp32 output; added to what it holds
+};
+
+// Tile of the any-shape kernel.
+constexpr int kMmAnyTile = 64;
+
+// Tile of the kernel for rows aligned to 16 bytes.
+constexpr int kMmTileM = 256, kMmTileN = 256;
+
+hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
+hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
+hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t stream);
+
+// NVFP4 matrix-vector products.  experts == NULL: y[T][N] = x W^T.  Otherwise
+// slot p = t * top + j of y [T * top][N] takes W_e, e = experts[p], G matrices.
+struct MvArgs {
+    const uint16_t *x;
+    const int32_t *experts;
+    const uint8_t *qw, *sw;
+    const float *sg;
+    void *y;
+    int64_t T, N, K;
+    int32_t top, G;
+    int32_t out_f32;
+};
+
+hipError_t launch_mv(const MvArgs &a, hipStream_t stream);
+
+}  // namespace mxk

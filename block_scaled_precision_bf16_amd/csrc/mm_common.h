@@ -1,0 +1,139 @@
+// mm_common.h -- device code the kernels of the MXFP8 products share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "launch_mm.h"
+
+namespace mxk {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ i32x8_t join(uint4 a, uint4 b)
+{
+    return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// How a product is computed.
+//   kMx: gfx950's block-scaled MFMA on the codes and scale bytes, 32 x 32 x 64.
+//       It sums 8 neighbouring k with the products aligned to the largest one's
+//       exponent and cut below 2^-13 of it (measured; everything beyond those 8
+//       is summed in fp32): an error of the order of 1.5e-5 of the result, 100
+//       times below the rounding of a bf16 output, which is where it is used.
+//   kExact: the codes times their scales as bf16 (exact: at most 4 significant
+//       bits), products exact, sums in fp32, by the bf16 MFMA, 32 x 32 x 16, at
+//       half the rate; for fp32 outputs.
+enum MmMode { kMx, kExact };
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
+
+// Two of the four codes of w (the upper two with HI) times 2^(e - 127), where
+// scale holds e in its exponent field.
+template <int F, bool HI>
+__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t w, float scale)
+{
+    const bf16x2v_t v = F ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, HI)
+                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int F>
+__device__ __forceinline__ bf16x8_t bf16_of_codes8(uint32_t lo, uint32_t hi, float scale)
+{
+    typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
+    const u32x4v_t v = {bf16_of_codes<F, false>(lo, scale), bf16_of_codes<F, true>(lo, scale),
+                        bf16_of_codes<F, false>(hi, scale), bf16_of_codes<F, true>(hi, scale)};
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// fp32 to bf16 bits, to nearest even, NaN kept.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t);
+    uint32_t u;
+    __builtin_memcpy(&u, &v, 4);
+    return u;
+}
+
+// A workgroup's tile: its group's operands and the tile's first row and column.
+struct MmTile {
+    const uint8_t *qa, *sa, *qb, *sb;
+    int64_t M, K, nb;       // the group's output rows, summed length, blocks of 32
+    int64_t sa_left, sb_left;   // bytes from the group's scales to the arrays' ends
+    int64_t y0;             // first element of the group's output
+    int64_t m0, n0;
+};
+
+// Tile number of workgroup `id` of n: each of the 8 XCDs (workgroups go to
+// them in turn) takes a run of consecutive tiles, which share operands in its
+// L2.
+__device__ __forceinline__ int mm_xcd_order(int id, int n)
+{
+    const int x = id & 7, q = n >> 3, rem = n & 7;
+    return x * q + (x < rem ? x : rem) + (id >> 3);
+}
+
+// Tile number `id` of the launch: the group whose range holds it, and in it
+// bands of kBand tile rows, each band's tiles counted down its rows first (so
+// that a run of tiles is about square).  A group without output tiles takes
+// no ids.
+constexpr int kBand = 4;
+__device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int id, int tile_m,
+                                          int tile_n)
+{
+    int g = 0;
+    while (id >= t.tile0[g + 1])
+        g++;
+    const int64_t r0 = t.row0[g], rows = t.row0[g + 1] - r0;
+    MmTile w;
+    w.M = a.sum_rows ? a.dim : rows;
+    w.K = a.sum_rows ? rows : a.dim;
+    w.nb = (w.K + 31) / 32;
+    w.qa = a.qa + r0 * a.dim;
+    w.qb = a.qb + (a.sum_rows ? r0 * a.N : g * a.N * a.dim);
+    w.sa = a.sa + t.sa_off[g];
+    w.sb = a.sb + t.sb_off[g];
+    w.sa_left = a.sa_bytes - t.sa_off[g];
+    w.sb_left = a.sb_bytes - t.sb_off[g];
+    w.y0 = a.sum_rows ? g * a.dim * a.N : r0 * a.N;
+    const int j = id - t.tile0[g], tm = (int)((w.M + tile_m - 1) / tile_m);
+    const int tn = (int)((a.N + tile_n - 1) / tile_n);
+    const int band = j / (kBand * tn), in = j - band * (kBand * tn);
+    const int high = tm - band * kBand < kBand ? tm - band * kBand : kBand;
+    w.m0 = (int64_t)(band * kBand + in % high) * tile_m;
+    w.n0 = (int64_t)(in / high) * tile_n;
+    return w;
+}
+
+// Scale byte of (row, blk) of an operand [rows][nb]; 0 (2^-127) outside it,
+// where every element is 0.
+__device__ __forceinline__ int scale_byte(const uint8_t *s, int64_t rows, int64_t nb, int64_t row,
+                                          int64_t blk, int tiled)
+{
+    if (row >= rows || blk >= nb)
+        return 0;
+    if (!tiled)
+        return s[row * nb + blk];
+    const int64_t tile = (blk >> 3) * ((rows + 31) >> 5) + (row >> 5);
+    return s[tile * 256 + 4 * ((row & 31) + 32 * (blk & 1)) + ((blk & 7) >> 1)];
+}
+
+// The fp32 number whose exponent field is the scale byte.
+__device__ __forceinline__ float scale_float(int byte) { return __uint_as_float((uint32_t)byte << 23); }
+
+__device__ __forceinline__ void store_out(const MmArgs &a, int64_t i, float v)
+{
+    if (a.out_f32) {
+        float *y = static_cast<float *>(a.y);
+        y[i] = a.accumulate ? y[i] + v : v;
+    } else {
+        static_cast<uint16_t *>(a.y)[i] = (uint16_t)bf16_pair(v, 0.f);
+    }
+}
+
+}  // namespace mxk

@@ -23,7 +23,9 @@
  *     rows (PR 3291, the grouped NVFP4 quantize-transpose row);
  *   - format, layout and shape extensions of the MXFP8 casts: E5M2 elements,
  *     the round-up scale rule, GEMM-ready scale tiles, any row count and row
- *     length (partial edge blocks).
+ *     length (partial edge blocks);
+ *   - products of the casts' outputs: MXFP8 matrix products, dense and grouped
+ *     by expert, with their gradients, and NVFP4 matrix-vector products.
  *
  * Numerics (the pages name these formats but do not define their
  * arithmetic; these are the readings the library implements bit-exactly):
@@ -383,7 +385,6 @@ mx_status nvfp4_quantize_transpose_2d(const void *x, int64_t M, int64_t K, const
                                       uint8_t *q_row, uint8_t *s_row, uint8_t *q_col,
                                       uint8_t *s_col, float *global_scale_out, hipStream_t stream);
 
-/* Static string naming a status code. */
 /*
  * Per-group tensor absmax for the grouped NVFP4 cast: amax[g] = max |x| over
  * the rows of group g (0 for an empty group), as fp32.  x, group_rows, G as
@@ -424,6 +425,108 @@ mx_status nvfp4_quantize_transpose_grouped(const void *x, int64_t K, const int64
                                            uint8_t *q_col, uint8_t *s_col,
                                            float *global_scale_out, hipStream_t stream);
 
+/*
+ * Products of MXFP8 operands: what the casts' outputs are for.  An operand
+ * value is its element times 2^(scale byte - 127) of its block; products are
+ * summed in fp32 on the block-scaled matrix cores, in an order that depends
+ * only on the sizes (results are run-to-run identical), and rounded once to
+ * the output type.  A NaN block (scale 0xFF) gives NaN in the output rows and
+ * columns it enters.
+ *
+ * flags, for the three calls:
+ *   MX_A_E5M2, MX_B_E5M2  the operand's elements are E5M2 (MX_ELEM_E5M2 casts)
+ *                      instead of E4M3
+ *   MX_SCALE_TILED     both scale tensors are in the tile layout
+ *   MX_OUT_F32         the output is fp32 instead of bf16
+ *   MX_OUT_ACCUMULATE  with MX_OUT_F32: the product is added to what the
+ *                      output holds (one rounding of that sum to fp32)
+ */
+#define MX_A_E5M2 4u
+#define MX_B_E5M2 32u
+#define MX_OUT_F32 64u
+#define MX_OUT_ACCUMULATE 128u
+
+/*
+ * y[M][N] = A B^T of A [M][K] and B [N][K], both quantised along K.  A layer
+ * with weights W [N][K] computes its forward product with B = q_row / s_row
+ * of W, its input gradient dX [M][K] = dY W with A = q_row / s_row of dY and
+ * B = q_col / s_col of W (that is W^T [K][N], quantised along N), and its
+ * weight gradient dW [N][K] = dY^T X with A = q_col / s_col of dY and
+ * B = q_col / s_col of X.
+ *   qa, sa   elements [M][K] and their scales (mx_scale_size(M, K) bytes)
+ *   qb, sb   elements [N][K] and their scales
+ *   M, N, K  any sizes >= 1, each <= 2^23, every pair's product <= 2^40
+ *   y        bf16 or fp32 [M][N]
+ * Errors: MX_ERR_ENUM for an unknown flag or MX_OUT_ACCUMULATE without
+ * MX_OUT_F32; MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (16 bytes, every
+ * pointer), MX_ERR_ALIAS (y overlaps an operand) as for the casts.
+ */
+mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
+                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream);
+
+/*
+ * The same for G experts in one launch: group g's rows of A, stacked as for
+ * mx_quantize_grouped, by the expert's own B_g [N][K].
+ *   qa, sa      the stacked rows' elements [M][K] and the groups' scales one
+ *               after the other (q_row, s_row of a grouped cast)
+ *   qb, sb      the experts' elements [G][N][K] and scales, one after the other
+ *               (q_row, s_row of the stacked weights' grouped cast; for the
+ *               input gradient its q_col, s_col)
+ *   group_rows  HOST array of G row counts >= 0 with a positive sum M;
+ *               1 <= G <= 64
+ *   y           bf16 or fp32 [M][N]; an empty group has no rows in it
+ */
+mx_status mx_matmul_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
+                            const uint8_t *sb, int64_t N, int64_t K, const int64_t *group_rows,
+                            int G, unsigned flags, void *y, hipStream_t stream);
+
+/*
+ * The experts' weight gradients in one launch: dW_g [N][K] = sum over group
+ * g's rows m of dY[m][n] X[m][k].
+ *   qa, sa      q_col, s_col of the grouped cast of dY [M][N] (group g's
+ *               transposed [N][rows] and its scales, one group after the other)
+ *   qb, sb      q_col, s_col of the grouped cast of X [M][K]
+ *   dw          bf16 or fp32 [G][N][K]; an empty group's gradient is 0 (with
+ *               MX_OUT_ACCUMULATE: unchanged)
+ */
+mx_status mx_matmul_wgrad_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
+                                  const uint8_t *sb, int64_t N, int64_t K,
+                                  const int64_t *group_rows, int G, unsigned flags, void *dw,
+                                  hipStream_t stream);
+
+/*
+ * Matrix-vector products with NVFP4 weights (decoding): y[T][N] = x W^T, with
+ * W [N][K] as nvfp4_quantize_transpose writes it (1D or 2D blocks):
+ *   y[t][n] = S_g * sum_k x[t][k] E2M1(qw[n][k]) E4M3(sw[n][k / 16]),
+ * summed in fp32 and rounded once to the output type; S_g multiplies the sum.
+ *   x        device, bf16 [T][K]; T >= 1 (the weights are read once for up
+ *            to 64 tokens)
+ *   qw, sw   packed E2M1 [N][ceil(K/2)] and E4M3 [N][ceil(K/16)]: q_row, s_row
+ *   sg       device, one fp32: the cast's global scale
+ *   flags    0 or MX_OUT_F32
+ *   y        bf16 or fp32 [T][N]
+ * Any T, N, K >= 1, each <= 2^23, every pair's product <= 2^40.  Every pointer
+ * is 16-byte aligned (sg: 4-byte).
+ */
+mx_status nvfp4_matvec(const void *x, int64_t T, const uint8_t *qw, const uint8_t *sw,
+                       const float *sg, int64_t N, int64_t K, unsigned flags, void *y,
+                       hipStream_t stream);
+
+/*
+ * The same through routed experts: y[t][j] = x[t] W_e^T, e = experts[t][j].
+ *   experts  device, int32 [T][top], 1 <= top <= 64; any values, repeated ones
+ *            too.  An index outside 0 .. G - 1 (a padded slot, an expert that
+ *            another device holds) gives a row of zeros
+ *   qw, sw   the experts' weights one after the other, as
+ *            nvfp4_quantize_transpose_grouped writes G stacked [N][K] matrices;
+ *            sg fp32 [G]; 1 <= G <= 1024, G * N * K <= 2^40
+ *   y        bf16 or fp32 [T][top][N], T * top <= 2^23
+ */
+mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T, int64_t top,
+                               const uint8_t *qw, const uint8_t *sw, const float *sg, int G,
+                               int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream);
+
+/* Static string naming a status code. */
 const char *mx_status_str(int status);
 
 /* MXCAST_ABI_VERSION of the built library. */
