@@ -69,13 +69,17 @@ struct MmTile {
     int64_t m0, n0;
 };
 
-// Tile number of workgroup `id` of n: each of the 8 XCDs (workgroups go to
-// them in turn) takes a run of consecutive tiles, which share operands in its
-// L2.
+// Tile number of workgroup `id` of n.  Workgroups go to the 8 XCDs in turn; runs
+// of kRun consecutive tiles, which share operands in an L2, go to one XCD, the
+// next run to the next (so that groups of unequal work are spread).  What is
+// left behind the last 8 whole runs stays in order.
+constexpr int kRun = 32;
 __device__ __forceinline__ int mm_xcd_order(int id, int n)
 {
-    const int x = id & 7, q = n >> 3, rem = n & 7;
-    return x * q + (x < rem ? x : rem) + (id >> 3);
+    if (id >= n / (8 * kRun) * (8 * kRun))
+        return id;
+    const int x = id & 7, s = id >> 3;
+    return (s / kRun * 8 + x) * kRun + s % kRun;
 }
 
 // Tile number `id` of the launch: the group whose range holds it, and in it

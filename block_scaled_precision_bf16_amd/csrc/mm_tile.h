@@ -82,16 +82,23 @@ struct ScaleRows {
         d = d < last ? d : last;
         return tiled ? (uint32_t)((d >> 5) * 256 + 4 * (d & 31)) : (uint32_t)(d * nb);
     }
-    __device__ __forceinline__ uint64_t load(uint32_t off, int bt) const
+    __device__ __forceinline__ uint32_t limit(int bt) const
+    {
+        const int64_t room = left - bt * 8;
+        return (uint32_t)(room < kMaxRecords ? room : kMaxRecords);
+    }
+    __device__ __forceinline__ void load(uint32_t off, int bt, uint32_t &x, uint32_t &y) const
     {
         const uint8_t *p = base + bt * move;
-        const int64_t room = left - bt * 8;
-        const uint32_t lim = (uint32_t)(room < kMaxRecords ? room : kMaxRecords);
-        const uint32_t o = off < lim ? off : lim;
-        uint32_t x, y;
+        const uint32_t lim = limit(bt), o = off < lim ? off : lim;
         __builtin_memcpy(&x, p + o, 4);
         __builtin_memcpy(&y, p + (o + second), 4);
-        return ((uint64_t)y << 32 | x) >> (8 * (off - o));
+    }
+    // The row's 8 bytes (the lanes' two words) of what load gave.
+    __device__ __forceinline__ uint64_t value(uint32_t off, int bt, uint32_t x, uint32_t y) const
+    {
+        const uint32_t lim = limit(bt), d = off < lim ? 0 : off - lim;
+        return ((uint64_t)y << 32 | x) >> (8 * d);
     }
 };
 
@@ -124,7 +131,7 @@ struct MmKernel {
     uint32_t sel, sel1;            // how the words come out of a row's 8 scale bytes
     f32x16_t acc[MT][NT];
     uint32_t off_a[MT], off_b[NT];
-    uint64_t raw_a[MT], raw_b[NT];
+    uint32_t raw_a[MT][2], raw_b[NT][2];
     // kMx: the words of the lane's blocks (byte j: step j of the next four);
     // kExact: those of even blocks and of odd ones
     static constexpr int W = MODE == kMx ? 1 : 2;
@@ -134,17 +141,15 @@ struct MmKernel {
     // holds.
     __device__ __forceinline__ int brow(int j) const { return wn + 64 * (j >> 1) + 2 * r + (j & 1); }
 
-    __device__ __forceinline__ void issue(int t)
+    // Load i of the wave for tile t (zeros for one behind the last).
+    __device__ __forceinline__ void issue(int t, int i) const
     {
         const uint32_t k0 = 128u * (uint32_t)t;
         const uint32_t dst = lds0 + (uint32_t)(t & 1) * kBuf;
         // 16-byte chunks behind the rows' ends are zeros
         const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
-#pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-            const uint32_t v = 16 * chunk(i) < left ? voff[i] : kDeadRow;
-            load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
-        }
+        const uint32_t v = 16 * chunk(i) < left ? voff[i] : kDeadRow;
+        load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
     }
     // The wave's load i fills 8 rows of LDS, from row8(i) on: a share of A's TM
     // rows, then of B's TN rows behind them.
@@ -184,10 +189,19 @@ struct MmKernel {
     {
 #pragma unroll
         for (int i = 0; i < MT; i++)
-            raw_a[i] = ssa.load(off_a[i], bt);
+            ssa.load(off_a[i], bt, raw_a[i][0], raw_a[i][1]);
 #pragma unroll
         for (int j = 0; j < NT; j++)
-            raw_b[j] = ssb.load(off_b[j], bt);
+            ssb.load(off_b[j], bt, raw_b[j][0], raw_b[j][1]);
+    }
+    __device__ __forceinline__ void settle_scales()
+    {
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+            asm volatile("" : "+v"(raw_a[i][0]), "+v"(raw_a[i][1]));
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            asm volatile("" : "+v"(raw_b[j][0]), "+v"(raw_b[j][1]));
     }
     // The words of blocks 8 bt on; bytes of blocks behind the last one become 0.
     __device__ __forceinline__ void take_scales(int bt)
@@ -196,10 +210,10 @@ struct MmKernel {
         const uint64_t mask = keep >= 8 || a.tiled ? ~0ull : (1ull << (8 * keep)) - 1;
 #pragma unroll
         for (int i = 0; i < MT; i++)
-            words(sa[i], raw_a[i] & mask);
+            words(sa[i], ssa.value(off_a[i], bt, raw_a[i][0], raw_a[i][1]) & mask);
 #pragma unroll
         for (int j = 0; j < NT; j++)
-            words(sb[j], raw_b[j] & mask);
+            words(sb[j], ssb.value(off_b[j], bt, raw_b[j][0], raw_b[j][1]) & mask);
     }
     __device__ __forceinline__ void words(uint32_t (&o)[W], uint64_t v) const
     {
@@ -214,8 +228,8 @@ struct MmKernel {
 
     // The MFMAs of one step on f, with the reads of the next step's fragments
     // between them.
-    template <int J>
-    __device__ __forceinline__ void step(const Frags &f, Frags &next, int tn, int sn)
+    template <int J, bool LOAD>
+    __device__ __forceinline__ void step(const Frags &f, Frags &next, int tn, int sn, int tl)
     {
         if (MODE == kMx) {
             int k = 0;
@@ -224,6 +238,8 @@ struct MmKernel {
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
                     acc[i][j] = mfma_mx<FA, FB, J>(f.a[i], f.b[j], acc[i][j], sa[i][0], sb[j][0]);
+                    if (LOAD && k < kLoads)
+                        issue(tl, k);
                     if (k < MT + NT)
                         read(next, tn, sn, k);
                     k++;
@@ -257,6 +273,8 @@ struct MmKernel {
                             if (jj * MT / NT == i)
                                 b[(part & 1) ^ 1][jj] = conv_b<J>(f, jj, part + 1);
                     }
+                    if (LOAD && part * MT * NT + i * NT + j < kLoads)
+                        issue(tl, part * MT * NT + i * NT + j);
                     if (j == NT - 1) {
 #pragma unroll
                         for (int k = 0; k < MT + NT; k++)
@@ -281,13 +299,15 @@ struct MmKernel {
     }
 
     template <int J>
-    __device__ __forceinline__ void tile(Frags &f0, Frags &f1, int t, int nt)
+    __device__ __forceinline__ void tile(Frags &f0, Frags &f1, int t)
     {
-        step<J>(f0, f1, t, 1);
+        step<J, false>(f0, f1, t, 1, 0);
         wait_all_and_barrier();
-        if (t + 2 < nt)
-            issue(t + 2);
-        step<J + 1>(f1, f0, t + 1, 0);
+        // the scale bytes fetched for the next four steps are here: say so
+        // before more loads are under way, which the compiler would wait for
+        if (J == 2)
+            settle_scales();
+        step<J + 1, true>(f1, f0, t + 1, 0, t + 2);
     }
 
     __device__ __forceinline__ void run()
@@ -320,22 +340,27 @@ struct MmKernel {
             Frags f0, f1;
             fetch_scales(0);
             take_scales(0);
-            issue(0);
+#pragma unroll
+            for (int i = 0; i < kLoads; i++)
+                issue(0, i);
             wait_all_and_barrier();
-            issue(1);
+#pragma unroll
+            for (int i = 0; i < kLoads; i++)
+                issue(1, i);
 #pragma unroll
             for (int i = 0; i < MT + NT; i++)
                 read(f0, 0, 0, i);
             int t = 0;
             do {
                 const int next = t + 2 < nt ? (t >> 1) + 1 : t >> 1;
-                tile<0>(f0, f1, t, nt);
+                tile<0>(f0, f1, t);
                 fetch_scales(next);
-                tile<2>(f0, f1, t + 1, nt);
+                tile<2>(f0, f1, t + 1);
                 take_scales(next);
                 t += 2;
             } while (t < nt);
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the loads of no tile
         store();
     }
 
