@@ -57,6 +57,7 @@ struct MvArgs {
     int64_t T, N, K;
     int32_t top, G;
     int32_t out_f32;
+    int32_t by_slot;                    // set by the launcher
 };
 
 hipError_t launch_mv(const MvArgs &a, hipStream_t stream);

@@ -12,13 +12,13 @@
 // them with up to 16 tokens at once and sum in fp32.  One token costs what 16
 // do.
 //
-// A wave takes R tiles of 16 weight rows.  It walks over k in chunks of 256; the
-// 4 lanes of a row read 64 k each, as two 16-byte loads and one 4-byte load of 4
-// scales, so a row's chunk is a whole 128-byte line.  KS waves of a workgroup
-// take the chunks in turn (more loads in flight, and N rows alone would leave
-// most of the chip idle); WN waves take different rows.  Tokens come through
-// LDS, in the order in which the fragments want them.  The KS partial sums are
-// added through LDS in a fixed order.
+// A wave takes 16 weight rows.  It walks over k in chunks of 256; the 4 lanes of a
+// row read 64 k each, as two 16-byte loads and one 4-byte load of 4 scales, so a
+// row's chunk is a whole 128-byte line.  KS waves of a workgroup take the chunks
+// in turn (more loads in flight, and N rows alone would leave most of the chip
+// idle); WN waves take different rows.  Tokens come through LDS, in the order in
+// which the fragments want them, a stage of chunks at a time.  The KS partial
+// sums are added through LDS in a fixed order.
 #include "launch_mm.h"
 #include "mm_common.h"
 
@@ -30,8 +30,6 @@ typedef float f32x2v_t __attribute__((ext_vector_type(2)));
 
 constexpr int kMvThreads = 512, kMvWaves = 8;
 constexpr int kChunk = 256;            // k of one step of a wave
-constexpr int kMvStage = 65536;        // LDS bytes for tokens: two workgroups per CU
-constexpr int kMvMaxSlots = 64;
 
 // 8 E2M1 codes times their scale, as bf16 (exact).
 __device__ __forceinline__ bf16x8_t weights8(uint32_t w, float s)
@@ -44,6 +42,11 @@ __device__ __forceinline__ bf16x8_t weights8(uint32_t w, float s)
     const u32x4v_t v = {bf16_pair(p0[0] * s, p0[1] * s), bf16_pair(p1[0] * s, p1[1] * s),
                         bf16_pair(p2[0] * s, p2[1] * s), bf16_pair(p3[0] * s, p3[1] * s)};
     return __builtin_bit_cast(bf16x8_t, v);
+}
+
+__device__ __forceinline__ float dot2(bf16x2v_t w, uint32_t x, float c)
+{
+    return __builtin_amdgcn_fdot2_f32_bf16(w, __builtin_bit_cast(bf16x2v_t, x), c, false);
 }
 
 // A lane's share of a chunk of one row: 64 codes and 4 scale bytes.
@@ -64,123 +67,174 @@ __device__ __forceinline__ uint4 shift_down(uint4 v, uint32_t d)
                       __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0, v.w, b));
 }
 
-// TT: tokens at once.  EXPERTS: blockIdx.y is the expert (G: the slots without
-// one, whose rows become zeros); else the tile of TT tokens.
-template <int TT, int R, bool EXPERTS>
-__global__ __launch_bounds__(kMvThreads, 4) void mv_kernel(const MvArgs a)
+__device__ __forceinline__ void store_mv(const MvArgs &a, int64_t i, float v)
 {
-    constexpr int TB = TT / 16;                   // token tiles
-    constexpr int KS = TT == 16 ? 8 : TT == 32 ? 4 : 2, WN = kMvWaves / KS;
-    constexpr int kRows = 16 * R * WN;            // weight rows of a workgroup
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kMvStage];
-    __shared__ int32_t slot[kMvMaxSlots];
+    if (a.out_f32)
+        static_cast<float *>(a.y)[i] = v;
+    else
+        static_cast<uint16_t *>(a.y)[i] = (uint16_t)bf16_pair(v, 0.f);
+}
+
+// Up to TT slots that take expert e (with e = G: that take none), in order from
+// slot `from` on, into slot[]; returns how many.  Called by all waves; slot[] is
+// there after the caller's next barrier.
+template <int TT>
+__device__ __forceinline__ int gather_slots(const MvArgs &a, int e, int64_t from, int32_t *slot,
+                                            int32_t *wave_count)
+{
+    const int64_t slots = a.T * a.top;
+    const int tid = (int)threadIdx.x, L = tid & 63, wave = tid >> 6;
+    const uint64_t below = (1ull << L) - 1;
+    auto takes = [&](int64_t p) {
+        if (p >= slots)
+            return false;
+        const int32_t v = a.experts[p];
+        return e < a.G ? v == e : v < 0 || v >= a.G;
+    };
+    if (slots - from <= 64) {
+        // every wave looks for itself
+        const bool hit = takes(from + L);
+        const uint64_t m = __ballot(hit);
+        const int at = __popcll(m & below), all = __popcll(m);
+        if (wave == 0 && hit && at < TT)
+            slot[at] = (int32_t)from + L;
+        return all < TT ? all : TT;
+    }
+    int count = 0;
+    for (int64_t base = from; base < slots && count < TT; base += kMvThreads) {
+        const bool hit = takes(base + tid);
+        const uint64_t m = __ballot(hit);
+        if (L == 0)
+            wave_count[wave] = __popcll(m);
+        __syncthreads();
+        int at = count + __popcll(m & below);
+#pragma unroll
+        for (int i = 0; i < kMvWaves; i++) {
+            at += i < wave ? wave_count[i] : 0;
+            count += wave_count[i];
+        }
+        if (hit && at < TT)
+            slot[at] = (int32_t)(base + tid);
+        __syncthreads();
+    }
+    return count < TT ? count : TT;
+}
+
+// How a kernel for up to TT tokens is laid out: KS waves share the chunks of a
+// row, each has D of its chunks under way, a stage holds the tokens of D KS
+// chunks.
+template <int TT>
+struct MvPlan {
+    static constexpr int KS = TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 ? 4 : 2;
+    static constexpr int kRows = 16 * WN;                     // weight rows of a workgroup
+    static constexpr int kFit = D * KS;                       // chunks of a stage
+    static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
+    // 1 or 2 tokens: dot products on the vector units, which need no scaled
+    // weights: 1.1 (1.6) vector instructions a weight
+    static constexpr bool kDot = TT <= 2;
+    // LDS: a stage's tokens, later the partial sums of a token tile
+    static constexpr int kLds = kFit * 512 * TT > kMvWaves * 1024 ? kFit * 512 * TT : kMvWaves * 1024;
+    // waves per SIMD: two workgroups per CU, one for 64 tokens (128 KB of LDS)
+    static constexpr int kOccupancy = TT == 64 ? 2 : 4;
+};
+
+// EXPERTS: blockIdx.y is the expert (G: the slots without one, whose rows become
+// zeros) or, with a.by_slot, a slot, whose workgroups serve its expert if no
+// earlier slot has the same; else the tile of TT tokens.
+template <int TT, bool EXPERTS>
+__global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(const MvArgs a)
+{
+    using Plan = MvPlan<TT>;
+    constexpr int TB = (TT + 15) / 16;            // token tiles
+    constexpr int KS = Plan::KS, P = Plan::kPieces, D = Plan::D;
+    constexpr int kMix = TT == 1 ? 3 : 7;         // within a fragment's 4 TT slots
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ int32_t slot[EXPERTS ? TT : 1];
     __shared__ int32_t wave_count[kMvWaves];
 
     const int tid = (int)threadIdx.x, L = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = L & 15, g = L >> 4;
     const int ks = wave % KS, wn = wave / KS;
-    const int64_t n0 = (int64_t)blockIdx.x * kRows;
+    const int64_t n0 = (int64_t)blockIdx.x * Plan::kRows;
     const int64_t nb = (a.K + 15) >> 4, pitch = (a.K + 1) >> 1;
     const int nchunk = (int)((a.K + kChunk - 1) / kChunk);
-    const int e = EXPERTS ? (int)blockIdx.y : 0;
-    const int64_t slots = a.T * a.top;
-    int64_t from = EXPERTS ? 0 : (int64_t)blockIdx.y * TT;    // next slot to look at
-
-    // the workgroup's first row, the lanes' offsets from it (at most 128 rows of
-    // 2^22 bytes), and how far the arrays reach from there
-    const int64_t first = (EXPERTS && e == a.G ? 0 : (int64_t)e * a.N) + n0;
-    const uint8_t *const qbase = a.qw + first * pitch, *const sbase = a.sw + first * nb;
-    const int64_t qleft = ((int64_t)a.G * a.N - first) * pitch - 16;
-    const int64_t sleft = ((int64_t)a.G * a.N - first) * nb - 4;
-    uint32_t qoff[R], soff[R];
-#pragma unroll
-    for (int i = 0; i < R; i++) {
-        int n = 16 * (wn * R + i) + r;
-        n = n0 + n < a.N ? n : (int)(a.N - 1 - n0);
-        qoff[i] = (uint32_t)(n * pitch) + 32 * g;
-        soff[i] = (uint32_t)(n * nb) + 4 * g;
+    int64_t from = 0;                             // the next slot to look at
+    int e = 0;
+    if (EXPERTS) {
+        e = (int)blockIdx.y;
+        if (a.by_slot) {
+            from = e;
+            e = __builtin_amdgcn_readfirstlane(a.experts[from]);
+            if (e < 0 || e >= a.G) {
+                if (tid < Plan::kRows && n0 + tid < a.N)
+                    store_mv(a, from * a.N + n0 + tid, 0.f);
+                return;
+            }
+            bool earlier = false;
+            for (int64_t p = L; p < from; p += 64)
+                earlier |= a.experts[p] == e;
+            if (__ballot(earlier))
+                return;
+        }
+    } else {
+        from = (int64_t)blockIdx.y * TT;
     }
-    auto fetch = [&](Share (&w)[R], int c) {
-        // a chunk inside the rows: as it lies there
-        if ((c + 1) * kChunk <= a.K) {
-#pragma unroll
-            for (int i = 0; i < R; i++) {
-                const uint8_t *q = qbase + c * (kChunk / 2) + qoff[i];
-                __builtin_memcpy(&w[i].q[0], q, 16);
-                __builtin_memcpy(&w[i].q[1], q + 16, 16);
-                __builtin_memcpy(&w[i].s, sbase + c * (kChunk / 16) + soff[i], 4);
-            }
-            return;
-        }
-        // the last, partial one: never read behind the arrays; codes behind a
-        // row's end meet zero tokens, scales there become 0
-#pragma unroll
-        for (int i = 0; i < R; i++) {
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int64_t q = (int64_t)c * (kChunk / 2) + qoff[i] + 16 * h;
-                const int64_t p = q < qleft ? q : qleft;
-                __builtin_memcpy(&w[i].q[h], qbase + p, 16);
-                w[i].q[h] = shift_down(w[i].q[h], (uint32_t)(q - p < 15 ? q - p : 15));
-            }
-            const int64_t s = (int64_t)c * (kChunk / 16) + soff[i];
-            const int64_t p = s < sleft ? s : sleft;
-            __builtin_memcpy(&w[i].s, sbase + p, 4);
-            const int64_t d = s - p, keep = nb - (int64_t)c * (kChunk / 16) - 4 * g;
-            w[i].s = d < 4 ? w[i].s >> (8 * d) : 0;
-            if (keep < 4)
-                w[i].s = keep <= 0 ? 0 : w[i].s & ((1u << (8 * keep)) - 1);
-        }
+
+    // A base a little before the workgroup's first row, the lane's offsets from
+    // it (at most 64 rows of 2^22 bytes), and the last offsets that a load of 16
+    // (4) bytes may have.
+    const int64_t first = (EXPERTS && e == a.G ? 0 : (int64_t)e * a.N) + n0, all = (int64_t)a.G * a.N;
+    const int64_t q0 = first * pitch < 16 ? 0 : first * pitch - 16;
+    const int64_t s0 = first * nb < 4 ? 0 : first * nb - 4;
+    const uint8_t *const qbase = a.qw + q0, *const sbase = a.sw + s0;
+    const int64_t qreach = all * pitch - 16 - q0, sreach = all * nb - 4 - s0;
+    const uint32_t qlast = (uint32_t)(qreach < INT32_MAX ? qreach : INT32_MAX);
+    const uint32_t slast = (uint32_t)(sreach < INT32_MAX ? sreach : INT32_MAX);
+    const int row = 16 * wn + r, last_row = (int)(a.N - 1 - n0 < 1024 ? a.N - 1 - n0 : 1024);
+    const int my_row = row < last_row ? row : last_row;
+    uint32_t qoff = (uint32_t)(first * pitch - q0 + my_row * pitch) + 32 * g;
+    uint32_t soff = (uint32_t)(first * nb - s0 + my_row * nb) + 4 * g;
+
+    // A chunk's bytes, never from behind the arrays' ends: there, those before
+    // the end, which settle() moves where they belong.
+    auto fetch = [&](Share &w, int c) {
+        const uint32_t q = qoff + c * (kChunk / 2), s = soff + c * (kChunk / 16);
+        __builtin_memcpy(&w.q[0], qbase + (q < qlast ? q : qlast), 16);
+        __builtin_memcpy(&w.q[1], qbase + (q + 16 < qlast ? q + 16 : qlast), 16);
+        __builtin_memcpy(&w.s, sbase + (s < slast ? s : slast), 4);
     };
+    // The last, partial chunk: codes behind a row's end are some codes and meet
+    // zero tokens, scales there become 0.
+    auto settle = [&](Share &w, int c) {
+        const int q = (int)(qoff + c * (kChunk / 2) - qlast), s = (int)(soff + c * (kChunk / 16) - slast);
+        if (q > 0)
+            w.q[0] = shift_down(w.q[0], q < 15 ? q : 15);
+        if (q + 16 > 0)
+            w.q[1] = shift_down(w.q[1], q + 16 < 15 ? q + 16 : 15);
+        const int keep = (int)nb - c * (kChunk / 16) - 4 * g;
+        uint32_t v = s > 0 ? (s < 4 ? w.s >> (8 * s) : 0) : w.s;
+        if (keep < 4)
+            v = keep <= 0 ? 0 : v & ((1u << (8 * keep)) - 1);
+        w.s = v;
+    };
+    const int partial = a.K % kChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
 
     for (;;) {
-        Share w[2][R];
-        // this pass's tokens: count of them, their slots in slot[]
-        int count;
+        // (the addresses below are computed in each pass: kept over passes they
+        // cost more registers than there are)
+        asm volatile("" : "+v"(qoff), "+v"(soff));
+        int count;                                // this pass's tokens
         if (EXPERTS) {
-            // the next TT slots of the expert, in order
-            count = 0;
-            int64_t base = from;
-            while (base < slots && count < TT) {
-                const int64_t p = base + tid;
-                int32_t v = -1;
-                if (p < slots)
-                    v = a.experts[p];
-                const bool none = v < 0 || v >= a.G;
-                const bool hit = p < slots && (e < a.G ? v == e : none);
-                const uint64_t m = __ballot(hit);
-                if (L == 0)
-                    wave_count[wave] = __popcll(m);
-                __syncthreads();
-                int at = count, all = count;
-#pragma unroll
-                for (int i = 0; i < kMvWaves; i++) {
-                    at += i < wave ? wave_count[i] : 0;
-                    all += wave_count[i];
-                }
-                at += __popcll(m & ((1ull << L) - 1));
-                if (hit && at < TT)
-                    slot[at] = (int32_t)p;
-                count = all;
-                base += kMvThreads;
-                __syncthreads();
-            }
-            if (count > TT)
-                count = TT;
+            count = gather_slots<TT>(a, e, from, slot, wave_count);
             if (count == 0)
                 return;
-            from = slot[count - 1] + 1;
             if (e == a.G) {
-                for (int64_t i = tid; i < (int64_t)count * kRows; i += kMvThreads) {
-                    const int64_t n = n0 + i % kRows, o = (int64_t)slot[i / kRows] * a.N + n;
-                    if (n >= a.N)
-                        continue;
-                    if (a.out_f32)
-                        static_cast<float *>(a.y)[o] = 0.f;
-                    else
-                        static_cast<uint16_t *>(a.y)[o] = 0;
-                }
+                __syncthreads();
+                for (int i = tid; i < count * Plan::kRows; i += kMvThreads)
+                    if (n0 + i % Plan::kRows < a.N)
+                        store_mv(a, (int64_t)slot[i / Plan::kRows] * a.N + n0 + i % Plan::kRows, 0.f);
+                from = slot[count - 1] + 1;
                 __syncthreads();
                 continue;
             }
@@ -188,135 +242,204 @@ __global__ __launch_bounds__(kMvThreads, 4) void mv_kernel(const MvArgs a)
             if (from >= a.T)
                 return;
             count = (int)(a.T - from < TT ? a.T - from : TT);
-            __syncthreads();
         }
-        if (ks < nchunk)
-            fetch(w[0], ks);
+        Share w[D];
+#pragma unroll
+        for (int j = 0; j < D; j++)
+            if (ks + j * KS < nchunk)
+                fetch(w[j], ks + j * KS);
+        if (EXPERTS)
+            __syncthreads();                      // slot[]
 
-        f32x4_t acc[TB][R];
+        // The tokens of a stage, in fragment order: 8 k of one token per 16
+        // bytes; k = 64 g + 32 h + 8 d of a chunk belongs to fragment f = 4 h + d
+        // at lane group g, and lies in slot (g TT + token) ^ f of the fragment's
+        // 4 TT (one token: ^ f % 4) (the writes of 8 neighbouring pieces go to 8 fragments, the reads
+        // stay in one: both touch all banks).  A thread moves P pieces, at the same places in every
+        // stage, through registers: all loads before the first store, and
+        // those of the next stage while this one is used.
+        // Thread tid: piece tid % 32 of a chunk; the 16 rows tid / 32 are
+        // tokens (TT < 16: TT tokens of 16 / TT chunks), TB times over.
+        constexpr int kSide = TT < 16 ? 16 / TT : 1;
+        const int q = tid & 31, c_side = (tid >> 5) / (TT < 16 ? TT : 16);
+        const int xk = c_side * kChunk + 8 * q;
+        int64_t xo[TB];                           // element offset in x
+#pragma unroll
+        for (int b = 0; b < TB; b++) {
+            int t = (tid >> 5) % TT + 16 * b;
+            t = t < count ? t : count - 1;        // a place of no token: any
+            xo[b] = (EXPERTS ? slot[t] / a.top : from + t) * a.K + xk;
+        }
+        uint4 *const xl = reinterpret_cast<uint4 *>(lds) + (8 * c_side + (q & 7)) * 4 * TT +
+                          (((q >> 3) * TT + (tid >> 5) % TT) ^ (q & kMix));
+        uint4 xv[P];
+        // never from behind x's end: there, the 16 bytes before it
+        const int64_t x_end = a.T * a.K - 8;
+        auto load_tokens = [&](int st) {
+#pragma unroll
+            for (int j = 0; j < P; j++) {
+                const int64_t o = xo[j % TB] + (st * Plan::kFit + j / TB * kSide) * kChunk;
+                __builtin_memcpy(&xv[j], a.x + (o < x_end ? o : x_end), 16);
+            }
+        };
+        auto store_tokens = [&](int st) {
+            if ((st + 1) * Plan::kFit * kChunk > a.K) {
+                // what lies behind a row's end becomes 0
+#pragma unroll
+                for (int j = 0; j < P; j++) {
+                    const int k0 = (st * Plan::kFit + j / TB * kSide) * kChunk;
+                    const int64_t d = 2 * (xo[j % TB] + k0 - x_end);
+                    const int keep = (int)a.K - k0 - xk;
+                    uint4 v = xv[j];
+                    if (d > 0)
+                        v = shift_down(v, d < 15 ? (uint32_t)d : 15);
+                    const uint32_t half = keep & 1 ? 0xFFFFu : 0;
+                    v.x &= keep >= 2 ? ~0u : keep > 0 ? half : 0;
+                    v.y &= keep >= 4 ? ~0u : keep > 2 ? half : 0;
+                    v.z &= keep >= 6 ? ~0u : keep > 4 ? half : 0;
+                    v.w &= keep >= 8 ? ~0u : keep > 6 ? half : 0;
+                    xv[j] = v;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < P; j++)
+                xl[j / TB * kSide * 32 * TT + 16 * (j % TB)] = xv[j];
+        };
+        load_tokens(0);
+
+        f32x4_t acc[TB];                          // kDot: acc[0][t] of token t
 #pragma unroll
         for (int t = 0; t < TB; t++)
+            acc[t] = f32x4_t{};
+        // chunk number `chunk`, chunk c of the stage, from u
+        auto work = [&](Share &u, int c, int chunk) {
+            if (chunk >= partial)
+                settle(u, chunk);
+            const uint4 *xs = reinterpret_cast<const uint4 *>(lds) + 32 * TT * c;
 #pragma unroll
-            for (int i = 0; i < R; i++)
-                acc[t][i] = f32x4_t{};
-
-        // chunks whose tokens fit the stage at once: a multiple of KS
-        const int fit = kMvStage / (512 * count) / KS * KS;
-        for (int c0 = 0; c0 < nchunk; c0 += fit) {
-            const int nc = nchunk - c0 < fit ? nchunk - c0 : fit;
-            __syncthreads();
-            // 8 k of one token per 16 bytes; k = 64 g + 32 h + 8 d of a chunk
-            // lies in fragment 4 h + d at lane group g
-            for (int i = tid; i < nc * 32 * count; i += kMvThreads) {
-                const int q = i & 31, t = (i >> 5) % count, c = (i >> 5) / count;
-                const int64_t row = EXPERTS ? slot[t] / a.top : from + t;
-                const int64_t k = (int64_t)(c0 + c) * kChunk + 8 * q;
-                const uint16_t *x = a.x + row * a.K + k;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (k + 8 <= a.K) {
-                    __builtin_memcpy(&v, x, 16);
-                } else if (k < a.K) {
-                    uint32_t u[4] = {0, 0, 0, 0};
+            for (int b = 0; b < 4; b++) {         // block b of the lane's 4: fragments 2b, 2b + 1
+                const float s = b == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 0)
+                                : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 1)
+                                : b == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 2)
+                                         : __builtin_amdgcn_cvt_f32_fp8((int)u.s, 3);
+                float sum[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 7; j++)
-                        if (k + j < a.K)
-                            u[j >> 1] |= (uint32_t)x[j] << (16 * (j & 1));
-                    v = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-                const int frag = 8 * c + (q & 7), lg = q >> 3;
-                reinterpret_cast<uint4 *>(lds)[(frag * 4 + lg) * count + t] = v;
-            }
-            __syncthreads();
-            const uint4 *xs = reinterpret_cast<const uint4 *>(lds);
-            auto work = [&](const Share (&u)[R], int c) {
+                for (int f = 2 * b; f < 2 * b + 2; f++) {
+                    const uint4 q = u.q[f >> 2];
+                    const uint32_t d = (f & 3) == 0 ? q.x : (f & 3) == 1 ? q.y : (f & 3) == 2 ? q.z : q.w;
+                    if constexpr (Plan::kDot) {
+                        const bf16x2v_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
+                        const bf16x2v_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
+                        const bf16x2v_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2);
+                        const bf16x2v_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3);
 #pragma unroll
-                for (int f = 0; f < 8; f++) {
-                    bf16x8_t xf[TB];
-#pragma unroll
-                    for (int t = 0; t < TB; t++) {
-                        // a lane behind the last token repeats it: its column
-                        // is not stored
-                        const int tt = 16 * t + r < count ? 16 * t + r : count - 1;
-                        xf[t] = __builtin_bit_cast(bf16x8_t, xs[((8 * c + f) * 4 + g) * count + tt]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < R; i++) {
-                        const uint4 q = u[i].q[f >> 2];
-                        const uint32_t d = (f & 3) == 0 ? q.x : (f & 3) == 1 ? q.y : (f & 3) == 2 ? q.z : q.w;
-                        const float s = (f >> 1) == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)u[i].s, 0)
-                                        : (f >> 1) == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)u[i].s, 1)
-                                        : (f >> 1) == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u[i].s, 2)
-                                                        : __builtin_amdgcn_cvt_f32_fp8((int)u[i].s, 3);
+                        for (int t = 0; t < TT; t++) {
+                            const uint4 x = xs[4 * f * TT + ((g * TT + t) ^ (f & kMix))];
+                            sum[t] = dot2(w0, x.x, sum[t]);
+                            sum[t] = dot2(w1, x.y, sum[t]);
+                            sum[t] = dot2(w2, x.z, sum[t]);
+                            sum[t] = dot2(w3, x.w, sum[t]);
+                        }
+                    } else {
                         const bf16x8_t wf = weights8(d, s);
 #pragma unroll
-                        for (int t = 0; t < TB; t++)
-                            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[t], acc[t][i], 0, 0, 0);
+                        for (int t = 0; t < TB; t++) {
+                            // columns behind the last token are of any value and
+                            // not stored
+                            const bf16x8_t xf = __builtin_bit_cast(
+                                bf16x8_t, xs[4 * f * TT + ((g * TT + (r < TT ? r : 0)) ^ (f & kMix)) + 16 * t]);
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[t], 0, 0, 0);
+                        }
                     }
-                    __builtin_amdgcn_sched_barrier(0);   // keeps the conversions of few fragments alive
                 }
-            };
-            for (int c = ks; c < nc; c += 2 * KS) {
-                if (c0 + c + KS < nchunk)
-                    fetch(w[1], c0 + c + KS);
-                work(w[0], c);
-                if (c + KS < nc) {
-                    if (c0 + c + 2 * KS < nchunk)
-                        fetch(w[0], c0 + c + 2 * KS);
-                    work(w[1], c + KS);
-                } else {
+                if constexpr (Plan::kDot) {
 #pragma unroll
-                    for (int i = 0; i < R; i++)
-                        w[0][i] = w[1][i];
+                    for (int t = 0; t < TT; t++)
+                        acc[0][t] = __builtin_fmaf(sum[t], s, acc[0][t]);
                 }
+            }
+        };
+        const int stages = (nchunk + Plan::kFit - 1) / Plan::kFit;
+        for (int st = 0; st < stages; st++) {
+            __syncthreads();
+            store_tokens(st);
+            __syncthreads();
+            if (st + 1 < stages)
+                load_tokens(st + 1);
+#pragma unroll
+            for (int j = 0; j < D; j++) {
+                const int c = st * Plan::kFit + ks + j * KS;
+                if (c < nchunk)
+                    work(w[j], ks + j * KS, c);
+                if (c + Plan::kFit < nchunk)
+                    fetch(w[j], c + Plan::kFit);
             }
         }
 
+        const float sg = a.sg[e];
+        if constexpr (Plan::kDot) {
+            // lane (r, g): row r's sums over its k; over g, then over KS
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+                acc[0][t] += __shfl_xor(acc[0][t], 16);
+                acc[0][t] += __shfl_xor(acc[0][t], 32);
+            }
+            __syncthreads();
+            float *part = reinterpret_cast<float *>(lds);
+            if (g < TT)
+                part[(wave * TT + g) * 16 + r] = g ? acc[0][1] : acc[0][0];
+            __syncthreads();
+            const int v = tid / (16 * TT), t = tid / 16 % TT, n = 16 * v + tid % 16;
+            if (v < Plan::WN && t < count && n0 + n < a.N) {
+                float sum = part[(v * KS * TT + t) * 16 + tid % 16];
+#pragma unroll
+                for (int k = 1; k < KS; k++)
+                    sum += part[((v * KS + k) * TT + t) * 16 + tid % 16];
+                store_mv(a, (EXPERTS ? slot[t] : from + t) * a.N + n0 + n, sum * sg);
+            }
+        }
         // the KS partial sums, token tile by token tile; lane (r, g), register
         // j of a tile: weight row 4 g + j, token r
-        float sg = a.sg[e];
 #pragma unroll
-        for (int t = 0; t < TB; t++) {
+        for (int t = 0; t < (Plan::kDot ? 0 : TB); t++) {
             __syncthreads();
             f32x4_t *part = reinterpret_cast<f32x4_t *>(lds);
-#pragma unroll
-            for (int i = 0; i < R; i++)
-                part[(wave * R + i) * 64 + L] = acc[t][i];
+            part[tid] = acc[t];
             __syncthreads();
-            for (int u = tid; u < WN * R * 64; u += kMvThreads) {
-                const int i = (u >> 6) % R, v = (u >> 6) / R, l = u & 63;
-                f32x4_t sum = part[(v * KS * R + i) * 64 + l];
+            if (tid < Plan::WN * 64) {
+                const int v = tid >> 6;
+                f32x4_t sum = part[v * KS * 64 + L];
+#pragma unroll
                 for (int k = 1; k < KS; k++)
-                    sum += part[((v * KS + k) * R + i) * 64 + l];
-                const int tok = 16 * t + (l & 15);
-                const int64_t n = n0 + 16 * (v * R + i) + 4 * (l >> 4);
-                if (tok >= count || n >= a.N)
-                    continue;
-                const int64_t o = (EXPERTS ? slot[tok] : from + tok) * a.N + n;
-                sum *= sg;
-                if ((a.N & 3) == 0) {
-                    if (a.out_f32)
-                        *reinterpret_cast<f32x4_t *>(static_cast<float *>(a.y) + o) = sum;
-                    else
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + o) =
-                            make_uint2(bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3]));
-                } else {
-                    for (int j = 0; j < 4 && n + j < a.N; j++) {
+                    sum += part[(v * KS + k) * 64 + L];
+                const int tok = 16 * t + r;
+                const int64_t n = n0 + 16 * v + 4 * g;
+                if (tok < count && n < a.N) {
+                    const int64_t o = (EXPERTS ? slot[tok] : from + tok) * a.N + n;
+                    sum *= sg;
+                    if ((a.N & 3) == 0) {
                         if (a.out_f32)
-                            static_cast<float *>(a.y)[o + j] = sum[j];
+                            *reinterpret_cast<f32x4_t *>(static_cast<float *>(a.y) + o) = sum;
                         else
-                            static_cast<uint16_t *>(a.y)[o + j] = (uint16_t)bf16_pair(sum[j], 0.f);
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + o) =
+                                make_uint2(bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3]));
+                    } else {
+                        for (int j = 0; j < 4 && n + j < a.N; j++)
+                            store_mv(a, o + j, sum[j]);
                     }
                 }
             }
         }
-        if (!EXPERTS)
+        if (EXPERTS)
+            from = slot[count - 1] + 1;
+        else
             from += (int64_t)gridDim.y * TT;
         __syncthreads();
     }
 }
 
-// Weights of fewer than 16 bytes of codes or 4 of scales, which the loads above
-// do not fit: a wave per output row, bytes one by one.
+// Weights of fewer than 16 bytes of codes or 4 of scales, or fewer than 8 token
+// elements, which the loads above do not fit: a wave per output row, bytes one by one.
 __global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
 {
     const int lane = (int)threadIdx.x;
@@ -335,25 +458,36 @@ __global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
                 }
                 sum *= a.sg[e];
             }
-            if (a.out_f32)
-                static_cast<float *>(a.y)[p * a.N + n] = sum;
-            else
-                static_cast<uint16_t *>(a.y)[p * a.N + n] = (uint16_t)bf16_pair(sum, 0.f);
+            store_mv(a, p * a.N + n, sum);
         }
 }
 
-template <int TT, int R>
-hipError_t launch(const MvArgs &a, hipStream_t stream)
+template <int TT>
+hipError_t launch(MvArgs a, hipStream_t stream)
 {
-    constexpr int KS = TT == 16 ? 8 : TT == 32 ? 4 : 2, rows = 16 * R * (kMvWaves / KS);
-    const unsigned nx = (unsigned)((a.N + rows - 1) / rows);
-    if (a.experts)
-        hipLaunchKernelGGL((mv_kernel<TT, R, true>), dim3(nx, (unsigned)a.G + 1), dim3(kMvThreads), 0,
-                           stream, a);
-    else
-        hipLaunchKernelGGL((mv_kernel<TT, R, false>),
-                           dim3(nx, (unsigned)(a.T < 4096 * TT ? (a.T + TT - 1) / TT : 4096)),
-                           dim3(kMvThreads), 0, stream, a);
+    using Plan = MvPlan<TT>;
+    const unsigned nx = (unsigned)((a.N + Plan::kRows - 1) / Plan::kRows);
+    const int64_t slots = a.T * a.top;
+    const int lds = Plan::kLds;
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(
+            a.experts ? reinterpret_cast<const void *>(mv_kernel<TT, true>)
+                      : reinterpret_cast<const void *>(mv_kernel<TT, false>),
+            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (a.experts) {
+        // few slots: by slot, so that no workgroup is started for an expert
+        // that nobody picked
+        a.by_slot = slots <= a.G;
+        hipLaunchKernelGGL((mv_kernel<TT, true>), dim3(nx, (unsigned)(a.by_slot ? slots : a.G + 1)),
+                           dim3(kMvThreads), lds, stream, a);
+    } else {
+        const int64_t tiles = (a.T + TT - 1) / TT;
+        hipLaunchKernelGGL((mv_kernel<TT, false>), dim3(nx, (unsigned)(tiles < 4096 ? tiles : 4096)),
+                           dim3(kMvThreads), lds, stream, a);
+    }
     return hipGetLastError();
 }
 
@@ -361,7 +495,7 @@ hipError_t launch(const MvArgs &a, hipStream_t stream)
 
 hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
 {
-    if (a.G * a.N * ((a.K + 1) / 2) < 16 || a.G * a.N * ((a.K + 15) / 16) < 4) {
+    if (a.G * a.N * ((a.K + 1) / 2) < 16 || a.G * a.N * ((a.K + 15) / 16) < 4 || a.T * a.K < 8) {
         const int64_t n = (a.T * a.top + 63) / 64;
         hipLaunchKernelGGL(mv_tiny_kernel, dim3((unsigned)(n < 4096 ? n : 4096)), dim3(64), 0, stream, a);
         return hipGetLastError();
@@ -370,18 +504,12 @@ hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
     const int64_t slots = a.T * a.top;
     const int64_t tokens = a.experts ? (2 * slots + a.G - 1) / a.G : a.T;
     const int64_t most = slots < tokens ? slots : tokens;
-    if (most > 32)
-        return launch<64, 1>(a, stream);
-    if (most > 16)
-        return launch<32, 2>(a, stream);
-    // more rows per wave where that leaves two workgroups per CU: the tokens
-    // are then staged for more rows at once
-    const int64_t tiles = (a.N + 15) / 16 * (a.experts ? (slots < a.G ? slots : a.G) : 1);
-    if (tiles >= 2048)
-        return launch<16, 4>(a, stream);
-    if (tiles >= 1024)
-        return launch<16, 2>(a, stream);
-    return launch<16, 1>(a, stream);
+    return most <= 1    ? launch<1>(a, stream)
+           : most <= 2  ? launch<2>(a, stream)
+           : most <= 8  ? launch<8>(a, stream)
+           : most <= 16 ? launch<16>(a, stream)
+           : most <= 32 ? launch<32>(a, stream)
+                        : launch<64>(a, stream);
 }
 
 }  // namespace mxk
