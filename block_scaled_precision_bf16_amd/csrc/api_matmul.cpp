@@ -124,18 +124,22 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
     a.b_e5m2 = (flags & MX_B_E5M2) != 0;
     a.out_f32 = (flags & MX_OUT_F32) != 0;
     a.accumulate = (flags & MX_OUT_ACCUMULATE) != 0;
+    a.qa_bytes = (int64_t)n.qa;
+    a.qb_bytes = (int64_t)n.qb;
     a.sa_bytes = (int64_t)n.sa;
     a.sb_bytes = (int64_t)n.sb;
-    // Rows that all start at a multiple of 16 bytes take the tiled kernel.
+    // Rows that all start at a multiple of 16 bytes take the kernel that loads
+    // them straight into LDS, others the one that goes through registers; the
+    // any-shape kernel is for operands too small for 16-byte reads.
     bool rows16 = dim % 16 == 0;
     if (sum_rows) {
         rows16 = true;
         for (int g = 0; g < G; g++)
             rows16 = rows16 && rows[g] % 16 == 0;
     }
-    const bool tile = rows16 && n.sa >= 8 && n.sb >= 8;
-    const int64_t tm = tile ? mxk::kMmTileM : mxk::kMmAnyTile;
-    const int64_t tn = tile ? mxk::kMmTileN : mxk::kMmAnyTile;
+    const bool any = n.qa < 16 || n.qb < 16 || n.sa < 16 || n.sb < 16;
+    const int64_t tm = any ? mxk::kMmAnyTile : rows16 ? mxk::kMmTileM : mxk::kMmByteM;
+    const int64_t tn = any ? mxk::kMmAnyTile : rows16 ? mxk::kMmTileN : mxk::kMmByteN;
     int64_t tiles = 0;
     for (int g = 0; g < G; g++) {
         t.tile0[g] = (int32_t)tiles;
@@ -144,7 +148,10 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
             return MX_ERR_SHAPE;
     }
     t.tile0[G] = (int32_t)tiles;
-    return from_hip(tile ? mxk::launch_mm_tile(a, t, stream) : mxk::launch_mm_any(a, t, stream));
+    const auto launch = any      ? mxk::launch_mm_any
+                        : rows16 ? (a.out_f32 ? mxk::launch_mm_tile_f32 : mxk::launch_mm_tile)
+                                 : (a.out_f32 ? mxk::launch_mm_byte_f32 : mxk::launch_mm_byte);
+    return from_hip(launch(a, t, stream));
 }
 
 mx_status mv_impl(const void *x, const int32_t *experts, int64_t T, int64_t top, const uint8_t *qw,

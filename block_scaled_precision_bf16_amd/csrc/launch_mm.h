@@ -29,7 +29,8 @@ struct MmArgs {
     const uint8_t *qa, *sa, *qb, *sb;
     void *y;
     int64_t dim, N;
-    int64_t sa_bytes, sb_bytes;         // of all groups' scales
+    int64_t qa_bytes, qb_bytes;         // of all groups' codes and scales
+    int64_t sa_bytes, sb_bytes;
     int32_t sum_rows;
     int32_t tiled;                      // scales in MX_SCALE_TILED layout
     int32_t a_e5m2, b_e5m2;
@@ -39,11 +40,15 @@ struct MmArgs {
 // Tile of the any-shape kernel.
 constexpr int kMmAnyTile = 64;
 
-// Tile of the kernel for rows aligned to 16 bytes.
+// Tiles of the tiled kernel: rows that all start at a multiple of 16 bytes, and
+// rows at any byte.
 constexpr int kMmTileM = 256, kMmTileN = 256;
+constexpr int kMmByteM = 256, kMmByteN = 128;
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
+hipError_t launch_mm_byte(const MmArgs &a, const MmTable &t, hipStream_t stream);
+hipError_t launch_mm_byte_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t stream);
 
 // NVFP4 matrix-vector products.  experts == NULL: y[T][N] = x W^T.  Otherwise

@@ -1,0 +1,12 @@
+// mm_byte.hip -- the tiled MXFP8 product kernel, rows at any byte, bf16 outputs.
+#include "mm_tile.h"
+
+namespace mxk {
+
+hipError_t launch_mm_byte(const MmArgs &a, const MmTable &t, hipStream_t stream)
+{
+    return a.tiled ? launch_mm_tile_mode<kMx, kMmByteM, kMmByteN, true, false>(a, t, stream)
+                   : launch_mm_tile_mode<kMx, kMmByteM, kMmByteN, false, false>(a, t, stream);
+}
+
+}  // namespace mxk

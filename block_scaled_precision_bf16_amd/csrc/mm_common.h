@@ -64,7 +64,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 struct MmTile {
     const uint8_t *qa, *sa, *qb, *sb;
     int64_t M, K, nb;       // the group's output rows, summed length, blocks of 32
-    int64_t sa_left, sb_left;   // bytes from the group's scales to the arrays' ends
+    int64_t qa_left, qb_left;   // bytes from the group's operands to the arrays' ends
+    int64_t sa_left, sb_left;
     int64_t y0;             // first element of the group's output
     int64_t m0, n0;
 };
@@ -102,6 +103,8 @@ __device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int
     w.qb = a.qb + (a.sum_rows ? r0 * a.N : g * a.N * a.dim);
     w.sa = a.sa + t.sa_off[g];
     w.sb = a.sb + t.sb_off[g];
+    w.qa_left = a.qa_bytes - (w.qa - a.qa);
+    w.qb_left = a.qb_bytes - (w.qb - a.qb);
     w.sa_left = a.sa_bytes - t.sa_off[g];
     w.sb_left = a.sb_bytes - t.sb_off[g];
     w.y0 = a.sum_rows ? g * a.dim * a.N : r0 * a.N;

@@ -49,56 +49,75 @@ __device__ __forceinline__ void load_to_lds(mm_rsrc_t rsrc, uint32_t voff, uint3
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff));
 }
 
-__device__ __forceinline__ mm_rsrc_t rows_rsrc(const uint8_t *p)
+// Rows of `pitch` bytes at p, of which `rows` exist: a load's voff is a place in
+// them, its soff a step along k that stays inside the row, so whether or not the
+// bound is compared with soff too, rows behind the last one load zeros.
+__device__ __forceinline__ mm_rsrc_t rows_rsrc(const uint8_t *p, int64_t rows, int64_t pitch)
 {
-    // no bound but kDeadRow: every other offset lies in the operand
     const uint64_t u = reinterpret_cast<uint64_t>(p);
-    return mm_rsrc_t{(uint32_t)u, (uint32_t)(u >> 32) & 0xFFFFu, 0xFFFFFF00u, 0x00020000u};
+    return mm_rsrc_t{(uint32_t)u, (uint32_t)(u >> 32) & 0xFFFFu,
+                     (uint32_t)(rows < 256 ? rows : 256) * (uint32_t)pitch, 0x00020000u};
 }
-constexpr uint32_t kDeadRow = 0xFFFFFFF0u;   // out of every range: loads zeros
+constexpr uint32_t kDeadRow = 0xFFFFFFF0u;   // behind every bound: loads zeros
 
-// Where the scales of one operand's rows lie for a workgroup tile, 8 blocks
-// (256 k) at a time: two 4-byte loads per row, `second` bytes apart, at a lane's
-// offset from a base that moves by `move` bytes per 8 blocks.  Compact, they are
-// the row's 8 bytes, taken from up to 7 bytes before where the array would end
-// inside them; tiled, the words of the row's two lanes (blocks 2j, 2j + 1).
-struct ScaleRows {
+__device__ __forceinline__ uint32_t clip31(int64_t v)
+{
+    return (uint32_t)(v < kMaxRecords ? v : kMaxRecords);
+}
+
+// v moved down by d bytes (d < 16).
+__device__ __forceinline__ uint4 bytes_down(uint4 v, uint32_t d)
+{
+    if (d & 8)
+        v = make_uint4(v.z, v.w, 0, 0);
+    if (d & 4)
+        v = make_uint4(v.y, v.z, v.w, 0);
+    const uint32_t b = d & 3;
+    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, b), __builtin_amdgcn_alignbyte(v.z, v.y, b),
+                      __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0, v.w, b));
+}
+
+// The first n of v's 16 bytes, zeros behind them.
+__device__ __forceinline__ uint4 bytes_keep(uint4 v, int n)
+{
+    auto word = [n](uint32_t w, int at) {
+        return n >= at + 4 ? w : n <= at ? 0u : w & ((1u << (8 * (n - at))) - 1);
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
+}
+
+// Byte rows that are read B bytes (16 or 8) at a time at any place, the last ones
+// of an array too: a base inside the array, up to B bytes before the tile's
+// first row, and the last offset from it that B bytes may be read at.  A read
+// that would pass it is taken there and moved down.
+template <int B>
+struct ByteRows {
     const uint8_t *base;
-    int64_t left;              // compact: bytes from base to 8 before the array's end
-    uint32_t second;
-    int64_t move;
+    int64_t last;
+    uint32_t lead;             // offset of the tile's first row
 
-    __device__ __forceinline__ ScaleRows(const uint8_t *s, int64_t bytes, int64_t rows, int64_t nb,
-                                         int64_t r0, int tiled)
-        : base(s + (tiled ? (r0 >> 5) * 256 : r0 * nb)),
-          left(tiled ? kMaxRecords : bytes - 8 - r0 * nb), second(tiled ? 128 : 4),
-          move(tiled ? ((rows + 31) >> 5) * 256 : 8)
+    // rows of `pitch` bytes from `first` on, of an array that `left` bytes from
+    // there on belong to
+    __device__ __forceinline__ ByteRows(const uint8_t *array, const uint8_t *first, int64_t left)
+        : base(first - array < B ? array : first - B), last(left + (first - base) - B),
+          lead((uint32_t)(first - base))
     {
     }
-    // Offset of row r0 + d from the base.
-    __device__ __forceinline__ static uint32_t row(int64_t rows, int64_t nb, int64_t r0, int d, int tiled)
+    template <typename V>
+    __device__ __forceinline__ V load(uint32_t off, int64_t at) const
     {
-        const int last = (int)(rows - 1 - r0 < 1024 ? rows - 1 - r0 : 1024);
-        d = d < last ? d : last;
-        return tiled ? (uint32_t)((d >> 5) * 256 + 4 * (d & 31)) : (uint32_t)(d * nb);
+        static_assert(sizeof(V) == B, "one read");
+        const uint8_t *p = base + at;
+        const uint32_t lim = clip31(last - at);
+        V v;
+        __builtin_memcpy(&v, p + (off < lim ? off : lim), B);
+        return v;
     }
-    __device__ __forceinline__ uint32_t limit(int bt) const
+    // What load(off, at) read, with n of its bytes inside the row.
+    __device__ __forceinline__ uint4 fix(uint4 v, uint32_t off, int64_t at, int n) const
     {
-        const int64_t room = left - bt * 8;
-        return (uint32_t)(room < kMaxRecords ? room : kMaxRecords);
-    }
-    __device__ __forceinline__ void load(uint32_t off, int bt, uint32_t &x, uint32_t &y) const
-    {
-        const uint8_t *p = base + bt * move;
-        const uint32_t lim = limit(bt), o = off < lim ? off : lim;
-        __builtin_memcpy(&x, p + o, 4);
-        __builtin_memcpy(&y, p + (o + second), 4);
-    }
-    // The row's 8 bytes (the lanes' two words) of what load gave.
-    __device__ __forceinline__ uint64_t value(uint32_t off, int bt, uint32_t x, uint32_t y) const
-    {
-        const uint32_t lim = limit(bt), d = off < lim ? 0 : off - lim;
-        return ((uint64_t)y << 32 | x) >> (8 * d);
+        const uint32_t lim = clip31(last - at), d = off < lim ? 0 : off - lim;
+        return bytes_keep(bytes_down(v, d < 15 ? d : 15), n);
     }
 };
 
@@ -108,7 +127,7 @@ __device__ __forceinline__ f32x16_t mfma_mx(i32x8_t a, i32x8_t b, f32x16_t c, ui
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, FB, J, (int)sa, J, (int)sb);
 }
 
-template <MmMode MODE, int FA, int FB, int TM, int TN>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
 struct MmKernel {
     static constexpr int MT = TM / 64, NT = TN / 64;      // 32-row tiles of a wave
     static constexpr int kBuf = (TM + TN) * 128;          // bytes of an LDS buffer
@@ -121,35 +140,69 @@ struct MmKernel {
 
     const MmArgs &a;
     const MmTile &w;
-    const ScaleRows ssa, ssb;
+    const ByteRows<16> qra, qrb;   // !ALIGNED: the codes
+    const ByteRows<8> sra, srb;    // !TILED: the scales
     uint8_t *lds;
     uint32_t lds0;                 // its LDS address
     int L, wave, h, r;
     int wm, wn;                    // the wave's rows and columns in the tile
-    uint32_t voff[kLoads];
+    uint32_t voff[3];              // A; B's loads of even and odd numbers
     mm_rsrc_t ra, rb;
-    uint32_t sel, sel1;            // how the words come out of a row's 8 scale bytes
-    f32x16_t acc[MT][NT];
-    uint32_t off_a[MT], off_b[NT];
-    uint32_t raw_a[MT][2], raw_b[NT][2];
+    uint32_t last_a, last_b;       // the last rows of the operands in the tile
+    uint4 pend[ALIGNED ? 1 : kLoads];   // !ALIGNED: the codes under way
+    uint32_t sel;                  // compact: how a word comes out of 8 scale bytes
+    // Scales.  Tiled: a lane loads its words of 4 steps (2 tiles) as they lie.
+    // Compact: a thread loads the 8 bytes of one row of A and of one of B and puts
+    // them into LDS (two buffers), from where the lanes take their words.
+    uint32_t off_a[TILED ? MT : 1], off_b[TILED ? NT : 1];
+    static constexpr int W = MODE == kMx ? 1 : 2;
+    uint32_t raw_a[TILED ? MT : 1][TILED ? W : 2], raw_b[TILED ? NT : 1][TILED ? W : 2];
     // kMx: the words of the lane's blocks (byte j: step j of the next four);
     // kExact: those of even blocks and of odd ones
-    static constexpr int W = MODE == kMx ? 1 : 2;
     uint32_t sa[MT][W], sb[NT][W];
+    f32x16_t acc[MT][NT];
 
     // Row of B in the workgroup tile that lane r of the wave's column tile j
     // holds.
     __device__ __forceinline__ int brow(int j) const { return wn + 64 * (j >> 1) + 2 * r + (j & 1); }
 
-    // Load i of the wave for tile t (zeros for one behind the last).
-    __device__ __forceinline__ void issue(int t, int i) const
+    // Load i of the wave for tile t (zeros for one behind the last).  ALIGNED: into
+    // LDS; else into registers, from where commit() writes them.
+    __device__ __forceinline__ void issue(int t, int i)
     {
         const uint32_t k0 = 128u * (uint32_t)t;
-        const uint32_t dst = lds0 + (uint32_t)(t & 1) * kBuf;
-        // 16-byte chunks behind the rows' ends are zeros
-        const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
-        const uint32_t v = 16 * chunk(i) < left ? voff[i] : kDeadRow;
-        load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
+        if constexpr (ALIGNED) {
+            // 16-byte chunks behind the rows' ends are zeros
+            const uint32_t dst = lds0 + (uint32_t)(t & 1) * kBuf;
+            const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
+            const uint32_t v = 16 * chunk(i) < left ? offset(i) : kDeadRow;
+            load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
+        } else {
+            pend[i] = (is_a(i) ? qra : qrb).template load<uint4>(offset(i), k0 < w.K ? k0 : 0);
+        }
+    }
+    __device__ __forceinline__ void commit(int t, int i)
+    {
+        const uint32_t k0 = 128u * (uint32_t)t;
+        uint4 v = pend[i];
+        if (k0 + 128 > w.K)
+            v = (is_a(i) ? qra : qrb).fix(v, offset(i), k0 < w.K ? k0 : 0, (int)w.K - (int)k0 - 16 * (int)chunk(i));
+        reinterpret_cast<uint4 *>(lds + (t & 1) * kBuf + row8(i) * 128)[L] = v;
+    }
+    // The loads (writes) that go with MFMA k of n.
+    __device__ __forceinline__ void issue_share(int t, int k, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; i++)
+            if (i * n / kLoads == k)
+                issue(t, i);
+    }
+    __device__ __forceinline__ void commit_share(int t, int k, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; i++)
+            if (i * n / kLoads == k)
+                commit(t, i);
     }
     // The wave's load i fills 8 rows of LDS, from row8(i) on: a share of A's TM
     // rows, then of B's TN rows behind them.
@@ -158,6 +211,18 @@ struct MmKernel {
     __device__ __forceinline__ int row8(int i) const
     {
         return 8 * (is_a(i) ? wave * kLoadsA + i : TM / 8 + wave * (TN / 32) + i - kLoadsA);
+    }
+    // Where in the tile's rows lane L's load i starts (!ALIGNED: from the base of
+    // ByteRows; rows behind the last one: the last one, whose reads are bounded).
+    __device__ __forceinline__ uint32_t offset(int i) const
+    {
+        const int nth = is_a(i) ? i : i - kLoadsA;
+        const uint32_t o = voff[is_a(i) ? 0 : 1 + (nth & 1)] + 8 * nth * (uint32_t)w.K;
+        if (ALIGNED)
+            return o;
+        const uint32_t last = is_a(i) ? last_a : last_b;
+        const int row = row8(i) + (L >> 3) - (is_a(i) ? 0 : TM);
+        return (row < (int)last ? o : o - (row - last) * (uint32_t)w.K);
     }
     // The chunk of its row that lane L loads (the slot's exchange, above).
     __device__ __forceinline__ uint32_t chunk(int i) const
@@ -185,45 +250,103 @@ struct MmKernel {
             f.a[i - NT] = frag_a(t, s, i - NT);
     }
 
+    // Offset of the scales of the tile's row d of an operand (rows behind the last
+    // one: the last one's).
+    __device__ __forceinline__ uint32_t scale_offset(uint32_t last, int d) const
+    {
+        d = d < (int)last ? d : (int)last;
+        if (TILED)
+            return (uint32_t)((d >> 5) * 256 + 4 * (d & 31)) + (MODE == kMx ? 128 * h : 0);
+        return (uint32_t)(d * (int)w.nb);
+    }
+    // Loads the scales of blocks 8 bt on (for bt behind the last: some).
     __device__ __forceinline__ void fetch_scales(int bt)
     {
+        if constexpr (TILED) {
+            const uint8_t *pa = w.sa + (bt * ((w.M + 31) >> 5) + (w.m0 >> 5)) * 256;
+            const uint8_t *pb = w.sb + (bt * ((a.N + 31) >> 5) + (w.n0 >> 5)) * 256;
 #pragma unroll
-        for (int i = 0; i < MT; i++)
-            ssa.load(off_a[i], bt, raw_a[i][0], raw_a[i][1]);
+            for (int k = 0; k < W; k++) {
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-            ssb.load(off_b[j], bt, raw_b[j][0], raw_b[j][1]);
+                for (int i = 0; i < MT; i++)
+                    raw_a[i][k] = *reinterpret_cast<const uint32_t *>(pa + off_a[i] + 128 * k);
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+                    raw_b[j][k] = *reinterpret_cast<const uint32_t *>(pb + off_b[j] + 128 * k);
+            }
+        } else {
+            const int64_t at = 8 * bt < w.nb ? 8 * bt : 0;
+            const uint2 x = sra.load<uint2>(off_a[0], at), y = srb.load<uint2>(off_b[0], at);
+            raw_a[0][0] = x.x, raw_a[0][1] = x.y;
+            raw_b[0][0] = y.x, raw_b[0][1] = y.y;
+        }
     }
+    // Says that the fetched scales are here (they are: after a wait for every
+    // load), before more loads are under way that the compiler would wait for.
     __device__ __forceinline__ void settle_scales()
     {
 #pragma unroll
-        for (int i = 0; i < MT; i++)
-            asm volatile("" : "+v"(raw_a[i][0]), "+v"(raw_a[i][1]));
+        for (int k = 0; k < (TILED ? W : 2); k++) {
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-            asm volatile("" : "+v"(raw_b[j][0]), "+v"(raw_b[j][1]));
-    }
-    // The words of blocks 8 bt on; bytes of blocks behind the last one become 0.
-    __device__ __forceinline__ void take_scales(int bt)
-    {
-        const int64_t keep = w.nb - 8 * bt;
-        const uint64_t mask = keep >= 8 || a.tiled ? ~0ull : (1ull << (8 * keep)) - 1;
+            for (int i = 0; i < (TILED ? MT : 1); i++)
+                asm volatile("" : "+v"(raw_a[i][k]));
 #pragma unroll
-        for (int i = 0; i < MT; i++)
-            words(sa[i], ssa.value(off_a[i], bt, raw_a[i][0], raw_a[i][1]) & mask);
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-            words(sb[j], ssb.value(off_b[j], bt, raw_b[j][0], raw_b[j][1]) & mask);
-    }
-    __device__ __forceinline__ void words(uint32_t (&o)[W], uint64_t v) const
-    {
-        const uint32_t hi = (uint32_t)(v >> 32), lo = (uint32_t)v;
-        if (MODE == kMx) {
-            o[0] = __builtin_amdgcn_perm(hi, lo, sel);
-        } else {
-            o[0] = __builtin_amdgcn_perm(hi, lo, sel);
-            o[W - 1] = __builtin_amdgcn_perm(hi, lo, sel1);
+            for (int j = 0; j < (TILED ? NT : 1); j++)
+                asm volatile("" : "+v"(raw_b[j][k]));
         }
+    }
+    // Tiled: puts the fetched words in use.
+    __device__ __forceinline__ void take_scales()
+    {
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+                sa[i][k] = raw_a[TILED ? i : 0][k];
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                sb[j][k] = raw_b[TILED ? j : 0][k];
+        }
+    }
+    // Compact: the scales fetched for blocks 8 bt on into LDS buffer bt % 2; those
+    // behind the last block become 0.
+    __device__ __forceinline__ void write_scales(int bt)
+    {
+        uint2 x = make_uint2(raw_a[0][0], raw_a[0][1]), y = make_uint2(raw_b[0][0], raw_b[0][1]);
+        const int64_t keep = w.nb - 8 * bt;
+        if (keep < 8) {
+            x = keep8(x, sra, off_a[0], 8 * bt, (int)keep);
+            y = keep8(y, srb, off_b[0], 8 * bt, (int)keep);
+        }
+        uint2 *p = reinterpret_cast<uint2 *>(lds + 2 * kBuf) + (bt & 1) * (TM + TN) + 64 * wave + L;
+        p[0] = x;
+        if (TN == TM || wave < TN / 64)
+            p[TM] = y;
+    }
+    __device__ __forceinline__ static uint2 keep8(uint2 v, const ByteRows<8> &rows, uint32_t off, int64_t at,
+                                                  int n)
+    {
+        if (n <= 0)
+            return make_uint2(0, 0);
+        const uint4 u = rows.fix(make_uint4(v.x, v.y, 0, 0), off, at, n);
+        return make_uint2(u.x, u.y);
+    }
+    // Compact: the words of the four steps of blocks 8 bt on in use.
+    __device__ __forceinline__ void read_scales(int bt)
+    {
+        const uint2 *p = reinterpret_cast<const uint2 *>(lds + 2 * kBuf) + (bt & 1) * (TM + TN);
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+            words(sa[i], p[wm + 32 * i + r]);
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            words(sb[j], p[TM + brow(j)]);
+    }
+    __device__ __forceinline__ void words(uint32_t (&o)[W], uint2 v) const
+    {
+        o[0] = __builtin_amdgcn_perm(v.y, v.x, sel);
+        if (MODE == kExact)
+            o[W - 1] = __builtin_amdgcn_perm(v.y, v.x, 0x07050301u);
     }
 
     // The MFMAs of one step on f, with the reads of the next step's fragments
@@ -238,8 +361,10 @@ struct MmKernel {
 #pragma unroll
                 for (int j = 0; j < NT; j++) {
                     acc[i][j] = mfma_mx<FA, FB, J>(f.a[i], f.b[j], acc[i][j], sa[i][0], sb[j][0]);
-                    if (LOAD && k < kLoads)
-                        issue(tl, k);
+                    if (LOAD)
+                        issue_share(tl, k, MT * NT);
+                    else if (!ALIGNED)
+                        commit_share(tl, k, MT * NT);
                     if (k < MT + NT)
                         read(next, tn, sn, k);
                     k++;
@@ -273,8 +398,11 @@ struct MmKernel {
                             if (jj * MT / NT == i)
                                 b[(part & 1) ^ 1][jj] = conv_b<J>(f, jj, part + 1);
                     }
-                    if (LOAD && part * MT * NT + i * NT + j < kLoads)
-                        issue(tl, part * MT * NT + i * NT + j);
+                    // (the loads in the first half, the writes in the second)
+                    if (LOAD && part < 2)
+                        issue_share(tl, part * MT * NT + i * NT + j, 2 * MT * NT);
+                    else if (!LOAD && !ALIGNED && part >= 2)
+                        commit_share(tl, (part - 2) * MT * NT + i * NT + j, 2 * MT * NT);
                     if (j == NT - 1) {
 #pragma unroll
                         for (int k = 0; k < MT + NT; k++)
@@ -298,14 +426,14 @@ struct MmKernel {
         return bf16_of_codes8<FB>((uint32_t)f.b[j][2 * part], (uint32_t)f.b[j][2 * part + 1], s);
     }
 
-    template <int J>
+    // Tile t, steps J and J + 1 of the scale words.  SETTLE: the scales fetched
+    // before have to be here at its barrier.
+    template <int J, bool SETTLE>
     __device__ __forceinline__ void tile(Frags &f0, Frags &f1, int t)
     {
-        step<J, false>(f0, f1, t, 1, 0);
+        step<J, false>(f0, f1, t, 1, t + 1);
         wait_all_and_barrier();
-        // the scale bytes fetched for the next four steps are here: say so
-        // before more loads are under way, which the compiler would wait for
-        if (J == 2)
+        if (SETTLE)
             settle_scales();
         step<J + 1, true>(f1, f0, t + 1, 0, t + 2);
     }
@@ -314,49 +442,78 @@ struct MmKernel {
     {
         // an even number of tiles: one behind the last k holds zeros
         const int nt = 2 * (int)((w.K + 255) / 256);
-        const uint32_t even = a.tiled ? 0x03020100u : 0x06040200u;
-        const uint32_t odd = a.tiled ? 0x07060504u : 0x07050301u;
-        sel = MODE == kMx && h ? odd : even;
-        sel1 = odd;
-        ra = rows_rsrc(w.qa + w.m0 * w.K);
-        rb = rows_rsrc(w.qb + w.n0 * w.K);
+        sel = MODE == kMx && h ? 0x07050301u : 0x06040200u;
+        ra = rows_rsrc(w.qa + w.m0 * w.K, w.M - w.m0, w.K);
+        rb = rows_rsrc(w.qb + w.n0 * w.K, a.N - w.n0, w.K);
+        last_a = (uint32_t)(w.M - w.m0 < TM ? w.M - w.m0 : TM) - 1;
+        last_b = (uint32_t)(a.N - w.n0 < TN ? a.N - w.n0 : TN) - 1;
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-            const int64_t last = is_a(i) ? w.M - 1 - w.m0 : a.N - 1 - w.n0;
-            const int64_t rr = row8(i) + (L >> 3) - (is_a(i) ? 0 : TM);
-            voff[i] = (uint32_t)((rr < last ? rr : last) * w.K) + 16 * chunk(i);
+        for (int i = 0; i < 3; i++) {
+            const int l = i == 0 ? 0 : kLoadsA + i - 1;    // the load it is for
+            const int row = row8(l) + (L >> 3) - (i ? TM : 0) - (i == 2 ? 8 : 0);
+            voff[i] = (uint32_t)(row * (int)w.K) + 16 * chunk(l);
+            if (!ALIGNED)
+                voff[i] += i ? qrb.lead : qra.lead;
         }
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            off_a[i] = ScaleRows::row(w.M, w.nb, w.m0, wm + 32 * i + r, a.tiled);
+        for (int i = 0; i < MT; i++)
 #pragma unroll
             for (int j = 0; j < NT; j++)
                 acc[i][j] = f32x16_t{};
-        }
+        if constexpr (TILED) {
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-            off_b[j] = ScaleRows::row(a.N, w.nb, w.n0, brow(j), a.tiled);
+            for (int i = 0; i < MT; i++)
+                off_a[i] = scale_offset(last_a, wm + 32 * i + r);
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                off_b[j] = scale_offset(last_b, brow(j));
+        } else {
+            static_assert(TM == 256 && TN <= 256, "a thread per row");
+            off_a[0] = scale_offset(last_a, 64 * wave + L) + sra.lead;
+            off_b[0] = scale_offset(last_b, 64 * wave + L) + srb.lead;
+        }
         if (nt > 0) {
             Frags f0, f1;
             fetch_scales(0);
-            take_scales(0);
 #pragma unroll
             for (int i = 0; i < kLoads; i++)
                 issue(0, i);
+            if constexpr (TILED) {
+                take_scales();
+            } else {
+                write_scales(0);
+                fetch_scales(1);
+            }
+            if constexpr (!ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < kLoads; i++)
+                    commit(0, i);
+            }
             wait_all_and_barrier();
 #pragma unroll
             for (int i = 0; i < kLoads; i++)
                 issue(1, i);
+            if constexpr (!TILED)
+                read_scales(0);
 #pragma unroll
             for (int i = 0; i < MT + NT; i++)
                 read(f0, 0, 0, i);
             int t = 0;
             do {
-                const int next = t + 2 < nt ? (t >> 1) + 1 : t >> 1;
-                tile<0>(f0, f1, t);
-                fetch_scales(next);
-                tile<2>(f0, f1, t + 1);
-                take_scales(next);
+                // scale words of two tiles at a time.  Tiled: fetched in the
+                // first, here at the second one's barrier, in use after it.
+                // Compact: fetched two tiles earlier, put into LDS before the
+                // first tile's barrier and taken from there after the second.
+                const int next = (t >> 1) + 1;
+                if constexpr (!TILED)
+                    write_scales(next);
+                tile<0, false>(f0, f1, t);
+                fetch_scales(TILED ? (t + 2 < nt ? next : next - 1) : next + 1);
+                tile<2, true>(f0, f1, t + 1);
+                if constexpr (TILED)
+                    take_scales();
+                else
+                    read_scales(next);
                 t += 2;
             } while (t < nt);
         }
@@ -432,14 +589,18 @@ struct MmKernel {
     }
 };
 
-template <MmMode MODE, int FA, int FB, int TM, int TN>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
 __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const MmTable t)
 {
     extern __shared__ uint8_t mm_lds[];
     typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
     const MmTile w = mm_tile(a, t, mm_xcd_order((int)blockIdx.x, (int)gridDim.x), TM, TN);
-    MmKernel<MODE, FA, FB, TM, TN> k{a, w, ScaleRows(w.sa, w.sa_left, w.M, w.nb, w.m0, a.tiled),
-                               ScaleRows(w.sb, w.sb_left, a.N, w.nb, w.n0, a.tiled)};
+    MmKernel<MODE, FA, FB, TM, TN, TILED, ALIGNED> k{
+        a, w,
+        ByteRows<16>(a.qa, w.qa + w.m0 * w.K, w.qa_left - w.m0 * w.K),
+        ByteRows<16>(a.qb, w.qb + w.n0 * w.K, w.qb_left - w.n0 * w.K),
+        ByteRows<8>(a.sa, w.sa + w.m0 * w.nb, w.sa_left - w.m0 * w.nb),
+        ByteRows<8>(a.sb, w.sb + w.n0 * w.nb, w.sb_left - w.n0 * w.nb)};
     k.lds = mm_lds;
     k.lds0 = (uint32_t)(uintptr_t)(lds_byte_t *)mm_lds;
     k.L = (int)threadIdx.x & 63;
@@ -451,30 +612,30 @@ __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const M
     k.run();
 }
 
-template <MmMode MODE, int FA, int FB, int TM, int TN>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
 hipError_t launch_mm_tile_one(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    constexpr int lds = 2 * (TM + TN) * 128;
+    constexpr int lds = 2 * (TM + TN) * (128 + (TILED ? 0 : 8));
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN>),
+        hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN>), dim3((unsigned)t.tile0[t.count]),
+    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>), dim3((unsigned)t.tile0[t.count]),
                        dim3(256), lds, stream, a, t);
     return hipGetLastError();
 }
 
-template <MmMode MODE, int TM, int TN>
+template <MmMode MODE, int TM, int TN, bool TILED, bool ALIGNED>
 hipError_t launch_mm_tile_mode(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
     if (!a.a_e5m2 && !a.b_e5m2)
-        return launch_mm_tile_one<MODE, 0, 0, TM, TN>(a, t, stream);
+        return launch_mm_tile_one<MODE, 0, 0, TM, TN, TILED, ALIGNED>(a, t, stream);
     if (a.a_e5m2 && !a.b_e5m2)
-        return launch_mm_tile_one<MODE, 1, 0, TM, TN>(a, t, stream);
+        return launch_mm_tile_one<MODE, 1, 0, TM, TN, TILED, ALIGNED>(a, t, stream);
     if (!a.a_e5m2)
-        return launch_mm_tile_one<MODE, 0, 1, TM, TN>(a, t, stream);
-    return launch_mm_tile_one<MODE, 1, 1, TM, TN>(a, t, stream);
+        return launch_mm_tile_one<MODE, 0, 1, TM, TN, TILED, ALIGNED>(a, t, stream);
+    return launch_mm_tile_one<MODE, 1, 1, TM, TN, TILED, ALIGNED>(a, t, stream);
 }
 
 }  // namespace mxk
