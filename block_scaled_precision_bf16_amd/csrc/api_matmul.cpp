@@ -67,11 +67,25 @@ bool build_table(const int64_t *rows, int G, int64_t dim, int64_t N, bool sum_ro
     }
     if (!size_ok(M, dim) || !size_ok(M, N) || !size_ok(dim, N) || G * (dim * N) > kMaxElems)
         return false;
+    // Weight gradients: the longest sums first, so that short ones fill the end.
+    int order[mxk::kMmMaxGroups];
+    for (int g = 0; g < G; g++) {
+        int at = g;
+        for (; sum_rows && at > 0 && rows[order[at - 1]] < rows[g]; at--)
+            order[at] = order[at - 1];
+        order[at] = g;
+    }
+    int place[mxk::kMmMaxGroups];
+    for (int i = 0; i < G; i++)
+        place[order[i]] = i;
     int64_t r = 0;
     for (int g = 0; g < G; g++) {
-        t.row0[g] = r;
-        t.sa_off[g] = sa;
-        t.sb_off[g] = sb;
+        const int i = place[g];
+        t.rows[i] = (int32_t)rows[g];
+        t.index[i] = g;
+        t.row0[i] = r;
+        t.sa_off[i] = sa;
+        t.sb_off[i] = sb;
         r += rows[g];
         if (sum_rows) {
             sa += scale_bytes(dim, rows[g], tiled);
@@ -81,7 +95,6 @@ bool build_table(const int64_t *rows, int G, int64_t dim, int64_t N, bool sum_ro
             sb += scale_bytes(N, dim, tiled);
         }
     }
-    t.row0[G] = M;
     n.qa = (uint64_t)(M * dim);
     n.qb = (uint64_t)(sum_rows ? M * N : G * dim * N);
     n.sa = (uint64_t)sa;
@@ -143,11 +156,17 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
     int64_t tiles = 0;
     for (int g = 0; g < G; g++) {
         t.tile0[g] = (int32_t)tiles;
-        tiles += ceil_div(sum_rows ? dim : rows[g], tm) * ceil_div(N, tn);
+        tiles += ceil_div(sum_rows ? dim : t.rows[g], tm) * ceil_div(N, tn);
         if (tiles > kMaxTiles)
             return MX_ERR_SHAPE;
     }
     t.tile0[G] = (int32_t)tiles;
+    // Tiles that do not fill the CUs once more go in parts of 128 x 128, if those
+    // take at most three rounds (one takes about 0.3 of a whole tile's time).
+    t.whole = (int32_t)tiles;
+    const int64_t parts = tm * tn / (mxk::kMmPart * mxk::kMmPart);
+    if (!any && tiles % mxk::kMmCUs * parts <= mxk::kMmCUs * 3)
+        t.whole -= t.whole % mxk::kMmCUs;
     const auto launch = any      ? mxk::launch_mm_any
                         : rows16 ? (a.out_f32 ? mxk::launch_mm_tile_f32 : mxk::launch_mm_tile)
                                  : (a.out_f32 ? mxk::launch_mm_byte_f32 : mxk::launch_mm_byte);

@@ -18,10 +18,13 @@ constexpr int kMmMaxGroups = 64;
 //   weight gradient (sum_rows = 1):  m_g = dim, k_g = rows of group g; A, B
 //       and their scales hold the groups one after the other, Y is [G][dim][N].
 struct MmTable {
-    int32_t count;
-    int32_t tile0[kMmMaxGroups + 1];    // first workgroup tile of each group
-    int64_t row0[kMmMaxGroups + 1];     // first stacked row of each group
-    int64_t sa_off[kMmMaxGroups];       // byte offsets of the groups' scales
+    int32_t count;                      // the groups, in the order of their tiles
+    int32_t whole;                      // tiles not taken in parts
+    int32_t tile0[kMmMaxGroups + 1];    // first workgroup tile of each
+    int32_t rows[kMmMaxGroups];
+    int32_t index[kMmMaxGroups];        // its place in the caller's order
+    int64_t row0[kMmMaxGroups];         // its first stacked row
+    int64_t sa_off[kMmMaxGroups];       // byte offsets of its scales
     int64_t sb_off[kMmMaxGroups];
 };
 
@@ -44,6 +47,9 @@ constexpr int kMmAnyTile = 64;
 // rows at any byte.
 constexpr int kMmTileM = 256, kMmTileN = 256;
 constexpr int kMmByteM = 256, kMmByteN = 128;
+constexpr int kMmPart = 128;            // side of the parts
+
+constexpr int kMmCUs = 256;
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);

@@ -94,20 +94,20 @@ __device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int
     int g = 0;
     while (id >= t.tile0[g + 1])
         g++;
-    const int64_t r0 = t.row0[g], rows = t.row0[g + 1] - r0;
+    const int64_t r0 = t.row0[g], rows = t.rows[g];
     MmTile w;
     w.M = a.sum_rows ? a.dim : rows;
     w.K = a.sum_rows ? rows : a.dim;
     w.nb = (w.K + 31) / 32;
     w.qa = a.qa + r0 * a.dim;
-    w.qb = a.qb + (a.sum_rows ? r0 * a.N : g * a.N * a.dim);
+    w.qb = a.qb + (a.sum_rows ? r0 * a.N : t.index[g] * a.N * a.dim);
     w.sa = a.sa + t.sa_off[g];
     w.sb = a.sb + t.sb_off[g];
     w.qa_left = a.qa_bytes - (w.qa - a.qa);
     w.qb_left = a.qb_bytes - (w.qb - a.qb);
     w.sa_left = a.sa_bytes - t.sa_off[g];
     w.sb_left = a.sb_bytes - t.sb_off[g];
-    w.y0 = a.sum_rows ? g * a.dim * a.N : r0 * a.N;
+    w.y0 = a.sum_rows ? t.index[g] * a.dim * a.N : r0 * a.N;
     const int j = id - t.tile0[g], tm = (int)((w.M + tile_m - 1) / tile_m);
     const int tn = (int)((a.N + tile_n - 1) / tile_n);
     const int band = j / (kBand * tn), in = j - band * (kBand * tn);

@@ -319,8 +319,9 @@ struct MmKernel {
             y = keep8(y, srb, off_b[0], 8 * bt, (int)keep);
         }
         uint2 *p = reinterpret_cast<uint2 *>(lds + 2 * kBuf) + (bt & 1) * (TM + TN) + 64 * wave + L;
-        p[0] = x;
-        if (TN == TM || wave < TN / 64)
+        if (TM == 256 || wave < TM / 64)
+            p[0] = x;
+        if (TN == 256 || wave < TN / 64)
             p[TM] = y;
     }
     __device__ __forceinline__ static uint2 keep8(uint2 v, const ByteRows<8> &rows, uint32_t off, int64_t at,
@@ -468,7 +469,7 @@ struct MmKernel {
             for (int j = 0; j < NT; j++)
                 off_b[j] = scale_offset(last_b, brow(j));
         } else {
-            static_assert(TM == 256 && TN <= 256, "a thread per row");
+            static_assert(TM <= 256 && TN <= 256, "a thread per row");
             off_a[0] = scale_offset(last_a, 64 * wave + L) + sra.lead;
             off_b[0] = scale_offset(last_b, 64 * wave + L) + srb.lead;
         }
@@ -590,19 +591,17 @@ struct MmKernel {
 };
 
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
-__global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const MmTable t)
+__device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, uint8_t *lds)
 {
-    extern __shared__ uint8_t mm_lds[];
     typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
-    const MmTile w = mm_tile(a, t, mm_xcd_order((int)blockIdx.x, (int)gridDim.x), TM, TN);
     MmKernel<MODE, FA, FB, TM, TN, TILED, ALIGNED> k{
         a, w,
         ByteRows<16>(a.qa, w.qa + w.m0 * w.K, w.qa_left - w.m0 * w.K),
         ByteRows<16>(a.qb, w.qb + w.n0 * w.K, w.qb_left - w.n0 * w.K),
         ByteRows<8>(a.sa, w.sa + w.m0 * w.nb, w.sa_left - w.m0 * w.nb),
         ByteRows<8>(a.sb, w.sb + w.n0 * w.nb, w.sb_left - w.n0 * w.nb)};
-    k.lds = mm_lds;
-    k.lds0 = (uint32_t)(uintptr_t)(lds_byte_t *)mm_lds;
+    k.lds = lds;
+    k.lds0 = (uint32_t)(uintptr_t)(lds_byte_t *)lds;
     k.L = (int)threadIdx.x & 63;
     k.wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     k.h = k.L >> 5;
@@ -612,17 +611,37 @@ __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const M
     k.run();
 }
 
+// The first t.whole workgroups take a whole tile each.  The tiles behind them,
+// too few to fill the CUs once more, go in parts of 128 x 128.
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
+__global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const MmTable t)
+{
+    extern __shared__ uint8_t mm_lds[];
+    const int id = (int)blockIdx.x;
+    if (id < t.whole) {
+        const MmTile w = mm_tile(a, t, mm_xcd_order(id, t.whole), TM, TN);
+        mm_tile_run<MODE, FA, FB, TM, TN, TILED, ALIGNED>(a, w, mm_lds);
+    } else {
+        constexpr int S = kMmPart, PM = TM / S, parts = PM * (TN / S);
+        const int q = id - t.whole;
+        MmTile w = mm_tile(a, t, t.whole + q / parts, TM, TN);
+        w.m0 += q % PM * S;
+        w.n0 += q % parts / PM * S;
+        if (w.m0 < w.M && w.n0 < a.N)
+            mm_tile_run<MODE, FA, FB, S, S, TILED, ALIGNED>(a, w, mm_lds);
+    }
+}
+
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
 hipError_t launch_mm_tile_one(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    constexpr int lds = 2 * (TM + TN) * (128 + (TILED ? 0 : 8));
+    constexpr int lds = 2 * (TM + TN) * (128 + (TILED ? 0 : 8)), parts = TM * TN / (kMmPart * kMmPart);
     const hipError_t e =
         hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>), dim3((unsigned)t.tile0[t.count]),
-                       dim3(256), lds, stream, a, t);
+    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>), dim3((unsigned)(t.whole + parts * (t.tile0[t.count] - t.whole))), dim3(256), lds, stream, a, t);
     return hipGetLastError();
 }
 
