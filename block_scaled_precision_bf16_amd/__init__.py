@@ -9,8 +9,9 @@ The same names as the C ABI:
     mx_quantize, mx_quantize_workspace_size, mx_scale_size, mx_quantize_grouped,
     mx_quantize_grouped_workspace_size, mx_grouped_scale_size, mx_quantize_gated,
     mx_fused_values, mx_absmax_bf16, nvfp4_quantize_transpose,
-    mx_matmul, mx_matmul_grouped, mx_matmul_wgrad_grouped, nvfp4_matvec,
-    nvfp4_matvec_experts, mx_status_str, mx_abi_version
+    mx_matmul, mx_matmul_grouped, mx_matmul_wgrad_grouped, their
+    *_workspace_size, nvfp4_matvec, nvfp4_matvec_experts, mx_status_str,
+    mx_abi_version
 take torch tensors (bf16 inputs, or int16/uint16 holding bf16 bits, on a ROCm
 device) and return dicts of uint8 / float32 torch tensors on the same device.
 The MXFP8 casts take the format flags ELEM_E5M2 / SCALE_ROUND_UP and the
@@ -43,8 +44,9 @@ EXPORTS = ("mx_quantize", "mx_quantize_workspace_size", "mx_quantize_noalloc", "
            "mx_quantize_dgated", "mx_fused_values",
            "mx_absmax_bf16", "nvfp4_quantize_transpose", "nvfp4_quantize_transpose_2d",
            "mx_absmax_bf16_grouped", "nvfp4_quantize_transpose_grouped",
-           "mx_matmul", "mx_matmul_grouped", "mx_matmul_wgrad_grouped", "nvfp4_matvec",
-           "nvfp4_matvec_experts",
+           "mx_matmul", "mx_matmul_grouped", "mx_matmul_wgrad_grouped",
+           "mx_matmul_workspace_size", "mx_matmul_grouped_workspace_size",
+           "mx_matmul_wgrad_grouped_workspace_size", "nvfp4_matvec", "nvfp4_matvec_experts",
            "mx_status_str", "mx_abi_version")
 
 
@@ -114,12 +116,18 @@ def lib():
                                                        ctypes.c_int, ctypes.c_uint, _vp, _vp,
                                                        _vp, _vp, _vp, _vp]
         L.mx_matmul.restype = ctypes.c_int
-        L.mx_matmul.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_uint, _vp, _vp]
+        L.mx_matmul.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_uint, _vp, _vp,
+                                ctypes.c_size_t, _vp]
         L.mx_matmul_grouped.restype = ctypes.c_int
         L.mx_matmul_grouped.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _vp, ctypes.c_int,
-                                        ctypes.c_uint, _vp, _vp]
+                                        ctypes.c_uint, _vp, _vp, ctypes.c_size_t, _vp]
         L.mx_matmul_wgrad_grouped.restype = ctypes.c_int
         L.mx_matmul_wgrad_grouped.argtypes = L.mx_matmul_grouped.argtypes
+        L.mx_matmul_workspace_size.restype = ctypes.c_size_t
+        L.mx_matmul_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_uint]
+        for f in (L.mx_matmul_grouped_workspace_size, L.mx_matmul_wgrad_grouped_workspace_size):
+            f.restype = ctypes.c_size_t
+            f.argtypes = [_i64, _i64, _vp, ctypes.c_int, ctypes.c_uint]
         L.nvfp4_matvec.restype = ctypes.c_int
         L.nvfp4_matvec.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, ctypes.c_uint, _vp, _vp]
         L.nvfp4_matvec_experts.restype = ctypes.c_int
@@ -587,14 +595,14 @@ def _want_bytes(t, n, name):
         raise ValueError(f"{name} must have {n} bytes, got {t.numel()}")
 
 
-def _product_out(out, shape, flags, dev):
+def _product_out(out, shape, flags, dev, stream):
     """The output tensor: bf16 (int16 / uint16 bits accepted in `out`) or, with
     OUT_F32, float32; ACCUMULATE needs the caller's."""
     dtype = F32 if flags & OUT_F32 else BF16
     if out is None:
         if flags & ACCUMULATE:
             raise ValueError("ACCUMULATE adds to `out`: it must be passed")
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev, stream)
     if not isinstance(out, torch.Tensor):
         raise TypeError("out must be a tensor")
     ok = out.dtype == dtype or (dtype == BF16 and out.dtype in (I16, torch.uint16))
@@ -605,6 +613,15 @@ def _product_out(out, shape, flags, dev):
         raise ValueError(f"out must be a contiguous {dtype} tensor of {n} elements on {dev}; got "
                          f"{out.dtype}, {out.numel()} elements on {out.device}")
     return out
+
+
+def _empty(shape, dtype, dev, stream):
+    """Device memory for work on `stream`: taken from that stream's pool, so that
+    no other stream's pending work still uses it."""
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _scale_bytes(rows, cols, flags):
@@ -622,14 +639,43 @@ def _launch(where, dev, stream, fn, *args):
     else:
         with torch.cuda.device(dev):
             st = fn(*args, _stream(dev, stream))
-    _check(st, where)
+    if st:
+        _check(st, where)
 
 
-def mx_matmul(qa, sa, qb, sb, flags=0, out=None, stream=None):
+def _product_ws(workspace, need, dev, stream):
+    """The products' workspace: (tensor to keep, pointer, bytes)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _empty((need,), U8, dev, stream)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() \
+            or workspace.device != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def mx_matmul_workspace_size(M: int, N: int, K: int, flags: int = 0) -> int:
+    return lib().mx_matmul_workspace_size(M, N, K, flags)
+
+
+def mx_matmul_grouped_workspace_size(N: int, K: int, group_rows, flags: int = 0) -> int:
+    rows = _rows_arg(group_rows)
+    return lib().mx_matmul_grouped_workspace_size(N, K, ctypes.addressof(rows), len(group_rows), flags)
+
+
+def mx_matmul_wgrad_grouped_workspace_size(N: int, K: int, group_rows, flags: int = 0) -> int:
+    rows = _rows_arg(group_rows)
+    return lib().mx_matmul_wgrad_grouped_workspace_size(N, K, ctypes.addressof(rows),
+                                                        len(group_rows), flags)
+
+
+def mx_matmul(qa, sa, qb, sb, flags=0, out=None, workspace=None, stream=None):
     """y[M][N] = A B^T of MXFP8 operands quantised along K: codes qa [M][K],
     qb [N][K] and their scales sa, sb as the casts return them (compact, or in
     the tile layout with SCALE_TILED).  bf16, or float32 with OUT_F32; `out`
-    may hold the output (with ACCUMULATE it is added to)."""
+    may hold the output (with ACCUMULATE it is added to) and `workspace` the
+    device scratch (mx_matmul_workspace_size bytes)."""
     for t, name in ((qa, "qa"), (sa, "sa"), (qb, "qb"), (sb, "sb")):
         _codes(t, name)
     if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] != qb.shape[1]:
@@ -638,14 +684,16 @@ def mx_matmul(qa, sa, qb, sb, flags=0, out=None, stream=None):
     (M, K), N, dev = qa.shape, qb.shape[0], qa.device
     _want_bytes(sa, _scale_bytes(M, K, flags), "sa")
     _want_bytes(sb, _scale_bytes(N, K, flags), "sb")
-    y = _product_out(out, (M, N), flags, dev)
+    y = _product_out(out, (M, N), flags, dev, stream)
     _on_device(dev, sa, qb, sb)
-    _launch("mx_matmul", dev, stream, lib().mx_matmul, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(),
-            sb.data_ptr(), M, N, K, flags, y.data_ptr())
+    L = lib()
+    ws, wp, wn = _product_ws(workspace, L.mx_matmul_workspace_size(M, N, K, flags), dev, stream)
+    _launch("mx_matmul", dev, stream, L.mx_matmul, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(),
+            sb.data_ptr(), M, N, K, flags, y.data_ptr(), wp, wn)
     return y
 
 
-def mx_matmul_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, stream=None):
+def mx_matmul_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, workspace=None, stream=None):
     """y[M][N]: each group's rows of A (codes qa [M][K], stacked as for
     mx_quantize_grouped, the groups' scales one after the other) by the group's
     own B_g [N][K] (codes qb and scales sb of the G matrices one after the
@@ -661,16 +709,19 @@ def mx_matmul_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, stream=None
     N = qb.numel() // (G * K)
     _want_bytes(sa, sum(_scale_bytes(int(r), K, flags) for r in group_rows), "sa")
     _want_bytes(sb, G * _scale_bytes(N, K, flags), "sb")
-    y = _product_out(out, (M, N), flags, dev)
+    y = _product_out(out, (M, N), flags, dev, stream)
     _on_device(dev, sa, qb, sb)
-    rows = _rows_arg(group_rows)
-    _launch("mx_matmul_grouped", dev, stream, lib().mx_matmul_grouped, qa.data_ptr(),
-            sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), N, K, ctypes.addressof(rows), G, flags,
-            y.data_ptr())
+    L, rows = lib(), _rows_arg(group_rows)
+    rp = ctypes.addressof(rows)
+    ws, wp, wn = _product_ws(workspace, L.mx_matmul_grouped_workspace_size(N, K, rp, G, flags), dev,
+                             stream)
+    _launch("mx_matmul_grouped", dev, stream, L.mx_matmul_grouped, qa.data_ptr(), sa.data_ptr(),
+            qb.data_ptr(), sb.data_ptr(), N, K, rp, G, flags, y.data_ptr(), wp, wn)
     return y
 
 
-def mx_matmul_wgrad_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, stream=None):
+def mx_matmul_wgrad_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, workspace=None,
+                            stream=None):
     """dW[G][N][K]: each group's sum over its rows m of dY[m][n] X[m][k], from
     the transposed outputs (q_col, s_col) of the grouped casts of dY [M][N]
     (qa, sa) and X [M][K] (qb, sb).  An empty group's gradient is 0 (with
@@ -686,12 +737,14 @@ def mx_matmul_wgrad_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, strea
     N, K = qa.numel() // M, qb.numel() // M
     _want_bytes(sa, sum(_scale_bytes(N, int(r), flags) for r in group_rows), "sa")
     _want_bytes(sb, sum(_scale_bytes(K, int(r), flags) for r in group_rows), "sb")
-    y = _product_out(out, (G, N, K), flags, dev)
+    y = _product_out(out, (G, N, K), flags, dev, stream)
     _on_device(dev, sa, qb, sb)
-    rows = _rows_arg(group_rows)
-    _launch("mx_matmul_wgrad_grouped", dev, stream, lib().mx_matmul_wgrad_grouped, qa.data_ptr(),
-            sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), N, K, ctypes.addressof(rows), G, flags,
-            y.data_ptr())
+    L, rows = lib(), _rows_arg(group_rows)
+    rp = ctypes.addressof(rows)
+    ws, wp, wn = _product_ws(workspace, L.mx_matmul_wgrad_grouped_workspace_size(N, K, rp, G, flags),
+                             dev, stream)
+    _launch("mx_matmul_wgrad_grouped", dev, stream, L.mx_matmul_wgrad_grouped, qa.data_ptr(),
+            sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), N, K, rp, G, flags, y.data_ptr(), wp, wn)
     return y
 
 
@@ -715,7 +768,7 @@ def nvfp4_matvec(x, qw, sw, sg, flags=0, out=None, stream=None):
     returns it (q_row, s_row, sg).  bf16, or float32 with OUT_F32."""
     T, N, K = _nv_weights(x, qw, sw, sg, 1)
     dev = x.device
-    y = _product_out(out, (T, N), flags, dev)
+    y = _product_out(out, (T, N), flags, dev, stream)
     _on_device(dev, qw, sw)
     _launch("nvfp4_matvec", dev, stream, lib().nvfp4_matvec, x.data_ptr(), T, qw.data_ptr(),
             sw.data_ptr(), sg.data_ptr(), N, K, flags, y.data_ptr())
@@ -736,7 +789,7 @@ def nvfp4_matvec_experts(x, experts, qw, sw, sg, flags=0, out=None, stream=None)
         raise ValueError(f"experts must be a contiguous int32 tensor [{T}][top], got "
                          f"{experts.dtype} {tuple(experts.shape)}")
     top = experts.shape[1]
-    y = _product_out(out, (T, top, N), flags, dev)
+    y = _product_out(out, (T, top, N), flags, dev, stream)
     _on_device(dev, experts, qw, sw)
     _launch("nvfp4_matvec_experts", dev, stream, lib().nvfp4_matvec_experts, x.data_ptr(),
             experts.data_ptr(), T, top, qw.data_ptr(), sw.data_ptr(), sg.data_ptr(), G, N, K, flags,

@@ -103,32 +103,79 @@ bool build_table(const int64_t *rows, int G, int64_t dim, int64_t N, bool sum_ro
     return true;
 }
 
-mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
-                  int64_t dim, int64_t N, const int64_t *rows, int G, bool sum_rows, unsigned flags,
-                  void *y, hipStream_t stream)
+// How a product is computed.
+enum MmKind { kAny, kSmall, kTiles };
+
+struct MmPlan {
+    MmKind kind;
+    int tile_m, tile_n;
+    bool pack;                 // rows are copied to 128-byte boundaries first
+    int64_t pack_a, pack_b;    // bytes of the copies
+};
+
+// The kernel for a launch and, in t, its tiles.  False if there are too many.
+bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
 {
-    if ((flags & ~kMmBits) || ((flags & MX_OUT_ACCUMULATE) && !(flags & MX_OUT_F32)))
-        return MX_ERR_ENUM;
-    if (!qa || !sa || !qb || !sb || !y || !rows)
-        return MX_ERR_NULL;
+    const int G = t.count;
+    int64_t most_m = 0, most_k = 0, big = 0, small_bytes = 0, pitches = 0;
+    bool rows16 = true;
+    for (int g = 0; g < G; g++) {
+        const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
+        rows16 = rows16 && k % 16 == 0;
+        most_m = m > most_m ? m : most_m;
+        most_k = k > most_k ? k : most_k;
+        big += ceil_div(m, mxk::kMmTileM) * ceil_div(a.N, mxk::kMmTileN);
+        t.packed0[g] = pitches;
+        pitches += mxk::mm_pitch(k);
+    }
+    const int small_m = most_m <= 32 ? 32 : 64;
+    for (int g = 0; g < G; g++) {
+        const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
+        small_bytes += ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN) * (small_m + mxk::kMmSmallN) * k;
+    }
+    p = MmPlan{};
+    // The small kernel reads each output tile's operands for itself, at about
+    // 8 TB/s from the caches; the tiled one takes about 1 us for 128 k of a
+    // round of tiles (half of that in parts).  Both start in about the same time.
+    const int64_t parts = (int64_t)(mxk::kMmTileM / mxk::kMmPart) * (mxk::kMmTileN / mxk::kMmPart);
+    const double rounds = (double)(big / mxk::kMmCUs) +
+                          0.5 * (double)ceil_div(big % mxk::kMmCUs * parts, mxk::kMmCUs);
+    const double tile_us = rounds * (double)ceil_div(most_k, 128) + (rows16 ? 0.0 : 5.0);
+    if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8)
+        p = MmPlan{kAny, mxk::kMmAnyTile, mxk::kMmAnyTile, false, 0, 0};
+    else if ((double)small_bytes / 8e6 < tile_us)
+        p = MmPlan{kSmall, small_m, mxk::kMmSmallN, false, 0, 0};
+    else
+        p = MmPlan{kTiles, mxk::kMmTileM, mxk::kMmTileN, !rows16, 0, 0};
+    if (p.pack) {
+        const int64_t rows_a = a.sum_rows ? 0 : (int64_t)n.qa / a.dim, pitch = mxk::mm_pitch(a.dim);
+        p.pack_a = a.sum_rows ? pitches * a.dim : rows_a * pitch;
+        p.pack_b = a.sum_rows ? pitches * a.N : (int64_t)n.qb / a.dim * pitch;
+    }
+    int64_t tiles = 0;
+    for (int g = 0; g < G; g++) {
+        t.tile0[g] = (int32_t)tiles;
+        tiles += ceil_div(a.sum_rows ? a.dim : t.rows[g], p.tile_m) * ceil_div(a.N, p.tile_n);
+        if (tiles > kMaxTiles)
+            return false;
+    }
+    t.tile0[G] = (int32_t)tiles;
+    // Tiles that do not fill the CUs once more go in parts of 128 x 128, if those
+    // take at most three rounds.
+    t.whole = (int32_t)tiles;
+    if (p.kind == kTiles && tiles % mxk::kMmCUs * parts <= mxk::kMmCUs * 3)
+        t.whole -= t.whole % mxk::kMmCUs;
+    return true;
+}
+
+// Arguments, table and plan of a product, from valid flags; an error otherwise.
+mx_status mm_setup(int64_t dim, int64_t N, const int64_t *rows, int G, bool sum_rows, unsigned flags,
+                   mxk::MmArgs &a, mxk::MmTable &t, MmBytes &n, MmPlan &p)
+{
     const bool tiled = (flags & MX_SCALE_TILED) != 0;
-    mxk::MmTable t;
-    MmBytes n;
     if (!build_table(rows, G, dim, N, sum_rows, tiled, flags & MX_OUT_F32 ? 4 : 2, t, n))
         return MX_ERR_SHAPE;
-    if (!aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
-        !aligned(y, 16))
-        return MX_ERR_ALIGN;
-    if (overlap(y, n.y, qa, n.qa) || overlap(y, n.y, sa, n.sa) || overlap(y, n.y, qb, n.qb) ||
-        overlap(y, n.y, sb, n.sb))
-        return MX_ERR_ALIAS;
-
-    mxk::MmArgs a{};
-    a.qa = qa;
-    a.sa = sa;
-    a.qb = qb;
-    a.sb = sb;
-    a.y = y;
+    a = mxk::MmArgs{};
     a.dim = dim;
     a.N = N;
     a.sum_rows = sum_rows;
@@ -141,36 +188,73 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
     a.qb_bytes = (int64_t)n.qb;
     a.sa_bytes = (int64_t)n.sa;
     a.sb_bytes = (int64_t)n.sb;
-    // Rows that all start at a multiple of 16 bytes take the kernel that loads
-    // them straight into LDS, others the one that goes through registers; the
-    // any-shape kernel is for operands too small for 16-byte reads.
-    bool rows16 = dim % 16 == 0;
-    if (sum_rows) {
-        rows16 = true;
-        for (int g = 0; g < G; g++)
-            rows16 = rows16 && rows[g] % 16 == 0;
+    return plan_mm(a, t, n, p) ? MX_OK : MX_ERR_SHAPE;
+}
+
+bool mm_flags_ok(unsigned flags)
+{
+    return !(flags & ~kMmBits) && (!(flags & MX_OUT_ACCUMULATE) || (flags & MX_OUT_F32));
+}
+
+size_t mm_workspace(int64_t dim, int64_t N, const int64_t *rows, int G, bool sum_rows, unsigned flags)
+{
+    mxk::MmArgs a;
+    mxk::MmTable t;
+    MmBytes n;
+    MmPlan p;
+    if (!mm_flags_ok(flags) || mm_setup(dim, N, rows, G, sum_rows, flags, a, t, n, p) != MX_OK)
+        return 0;
+    return (size_t)(p.pack_a + p.pack_b);
+}
+
+mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
+                  int64_t dim, int64_t N, const int64_t *rows, int G, bool sum_rows, unsigned flags,
+                  void *y, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!mm_flags_ok(flags))
+        return MX_ERR_ENUM;
+    if (!qa || !sa || !qb || !sb || !y || !rows)
+        return MX_ERR_NULL;
+    mxk::MmArgs a;
+    mxk::MmTable t;
+    MmBytes n;
+    MmPlan p;
+    const mx_status st = mm_setup(dim, N, rows, G, sum_rows, flags, a, t, n, p);
+    if (st != MX_OK)
+        return st;
+    if (!aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
+        !aligned(y, 16) || (p.pack && !aligned(workspace, 16)))
+        return MX_ERR_ALIGN;
+    const uint64_t nw = p.pack ? (uint64_t)(p.pack_a + p.pack_b) : 0;
+    if (nw && (!workspace || workspace_bytes < nw))
+        return MX_ERR_WORKSPACE;
+    const void *in[4] = {qa, sa, qb, sb};
+    const uint64_t in_bytes[4] = {n.qa, n.sa, n.qb, n.sb};
+    for (int i = 0; i < 4; i++)
+        if (overlap(y, n.y, in[i], in_bytes[i]) || overlap(workspace, nw, in[i], in_bytes[i]))
+            return MX_ERR_ALIAS;
+    if (overlap(y, n.y, workspace, nw))
+        return MX_ERR_ALIAS;
+
+    a.qa = qa;
+    a.sa = sa;
+    a.qb = qb;
+    a.sb = sb;
+    a.y = y;
+    if (p.kind == kAny)
+        return from_hip(mxk::launch_mm_any(a, t, stream));
+    if (p.kind == kSmall)
+        return from_hip(mxk::launch_mm_small(a, t, p.tile_m, stream));
+    if (p.pack) {
+        uint8_t *const wa = static_cast<uint8_t *>(workspace), *const wb = wa + p.pack_a;
+        const hipError_t e = mxk::launch_mm_pack(a, t, wa, wb, stream);
+        if (e != hipSuccess)
+            return MX_ERR_HIP;
+        a.packed = 1;
+        a.qa = wa;
+        a.qb = wb;
     }
-    const bool any = n.qa < 16 || n.qb < 16 || n.sa < 16 || n.sb < 16;
-    const int64_t tm = any ? mxk::kMmAnyTile : rows16 ? mxk::kMmTileM : mxk::kMmByteM;
-    const int64_t tn = any ? mxk::kMmAnyTile : rows16 ? mxk::kMmTileN : mxk::kMmByteN;
-    int64_t tiles = 0;
-    for (int g = 0; g < G; g++) {
-        t.tile0[g] = (int32_t)tiles;
-        tiles += ceil_div(sum_rows ? dim : t.rows[g], tm) * ceil_div(N, tn);
-        if (tiles > kMaxTiles)
-            return MX_ERR_SHAPE;
-    }
-    t.tile0[G] = (int32_t)tiles;
-    // Tiles that do not fill the CUs once more go in parts of 128 x 128, if those
-    // take at most three rounds (one takes about 0.3 of a whole tile's time).
-    t.whole = (int32_t)tiles;
-    const int64_t parts = tm * tn / (mxk::kMmPart * mxk::kMmPart);
-    if (!any && tiles % mxk::kMmCUs * parts <= mxk::kMmCUs * 3)
-        t.whole -= t.whole % mxk::kMmCUs;
-    const auto launch = any      ? mxk::launch_mm_any
-                        : rows16 ? (a.out_f32 ? mxk::launch_mm_tile_f32 : mxk::launch_mm_tile)
-                                 : (a.out_f32 ? mxk::launch_mm_byte_f32 : mxk::launch_mm_byte);
-    return from_hip(launch(a, t, stream));
+    return from_hip((a.out_f32 ? mxk::launch_mm_tile_f32 : mxk::launch_mm_tile)(a, t, stream));
 }
 
 mx_status mv_impl(const void *x, const int32_t *experts, int64_t T, int64_t top, const uint8_t *qw,
@@ -211,25 +295,46 @@ mx_status mv_impl(const void *x, const int32_t *experts, int64_t T, int64_t top,
 
 extern "C" {
 
-mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
-                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream)
+size_t mx_matmul_workspace_size(int64_t M, int64_t N, int64_t K, unsigned flags)
 {
-    return mm_impl(qa, sa, qb, sb, K, N, &M, 1, false, flags, y, stream);
+    return mm_workspace(K, N, &M, 1, false, flags);
+}
+
+size_t mx_matmul_grouped_workspace_size(int64_t N, int64_t K, const int64_t *group_rows, int G,
+                                        unsigned flags)
+{
+    return mm_workspace(K, N, group_rows, G, false, flags);
+}
+
+size_t mx_matmul_wgrad_grouped_workspace_size(int64_t N, int64_t K, const int64_t *group_rows, int G,
+                                              unsigned flags)
+{
+    return mm_workspace(N, K, group_rows, G, true, flags);
+}
+
+mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
+                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream)
+{
+    return mm_impl(qa, sa, qb, sb, K, N, &M, 1, false, flags, y, workspace, workspace_bytes, stream);
 }
 
 mx_status mx_matmul_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
                             const uint8_t *sb, int64_t N, int64_t K, const int64_t *group_rows,
-                            int G, unsigned flags, void *y, hipStream_t stream)
+                            int G, unsigned flags, void *y, void *workspace, size_t workspace_bytes,
+                            hipStream_t stream)
 {
-    return mm_impl(qa, sa, qb, sb, K, N, group_rows, G, false, flags, y, stream);
+    return mm_impl(qa, sa, qb, sb, K, N, group_rows, G, false, flags, y, workspace, workspace_bytes,
+                   stream);
 }
 
 mx_status mx_matmul_wgrad_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
                                   const uint8_t *sb, int64_t N, int64_t K,
                                   const int64_t *group_rows, int G, unsigned flags, void *dw,
-                                  hipStream_t stream)
+                                  void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
-    return mm_impl(qa, sa, qb, sb, N, K, group_rows, G, true, flags, dw, stream);
+    return mm_impl(qa, sa, qb, sb, N, K, group_rows, G, true, flags, dw, workspace, workspace_bytes,
+                   stream);
 }
 
 mx_status nvfp4_matvec(const void *x, int64_t T, const uint8_t *qw, const uint8_t *sw,

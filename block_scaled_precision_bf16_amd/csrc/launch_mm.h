@@ -24,6 +24,8 @@ struct MmTable {
     int32_t rows[kMmMaxGroups];
     int32_t index[kMmMaxGroups];        // its place in the caller's order
     int64_t row0[kMmMaxGroups];         // its first stacked row
+    int64_t packed0[kMmMaxGroups];      // packed weight gradient operands: the
+                                        // pitches of the groups before it
     int64_t sa_off[kMmMaxGroups];       // byte offsets of its scales
     int64_t sb_off[kMmMaxGroups];
 };
@@ -35,27 +37,32 @@ struct MmArgs {
     int64_t qa_bytes, qb_bytes;         // of all groups' codes and scales
     int64_t sa_bytes, sb_bytes;
     int32_t sum_rows;
+    int32_t packed;                     // operands as launch_mm_pack lays them out
     int32_t tiled;                      // scales in MX_SCALE_TILED layout
     int32_t a_e5m2, b_e5m2;
     int32_t out_f32, accumulate;        // fp32 output; added to what it holds
 };
 
-// Tile of the any-shape kernel.
-constexpr int kMmAnyTile = 64;
+// Bytes between the rows of packed operands of K codes: whole 128-byte lines,
+// filled up with zeros.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+constexpr int64_t mm_pitch(int64_t K) { return (K + 127) / 128 * 128; }
 
-// Tiles of the tiled kernel: rows that all start at a multiple of 16 bytes, and
-// rows at any byte.
-constexpr int kMmTileM = 256, kMmTileN = 256;
-constexpr int kMmByteM = 256, kMmByteN = 128;
-constexpr int kMmPart = 128;            // side of the parts
-
+// The tiled kernel: its tiles, and the parts in which the last ones go.
+constexpr int kMmTileM = 256, kMmTileN = 256, kMmPart = 128;
 constexpr int kMmCUs = 256;
+// The any-shape kernel's tile, and the columns of the small kernel's (32 or 64
+// rows).
+constexpr int kMmAnyTile = 64, kMmSmallN = 32;
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
-hipError_t launch_mm_byte(const MmArgs &a, const MmTable &t, hipStream_t stream);
-hipError_t launch_mm_byte_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
+hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, hipStream_t stream);
 hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t stream);
+// Copies the operands' rows to qa and qb, mm_pitch apart.
+hipError_t launch_mm_pack(const MmArgs &a, const MmTable &t, uint8_t *qa, uint8_t *qb, hipStream_t stream);
 
 // NVFP4 matrix-vector products.  experts == NULL: y[T][N] = x W^T.  Otherwise
 // slot p = t * top + j of y [T * top][N] takes W_e, e = experts[p], G matrices.

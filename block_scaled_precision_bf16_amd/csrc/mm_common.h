@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "bufio.h"
 #include "launch_mm.h"
 
 namespace mxk {
@@ -99,8 +100,16 @@ __device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int
     w.M = a.sum_rows ? a.dim : rows;
     w.K = a.sum_rows ? rows : a.dim;
     w.nb = (w.K + 31) / 32;
-    w.qa = a.qa + r0 * a.dim;
-    w.qb = a.qb + (a.sum_rows ? r0 * a.N : t.index[g] * a.N * a.dim);
+    if (a.packed) {
+        // the rows' zeros behind the last code count as codes
+        w.K = mm_pitch(w.K);
+        const int64_t p0 = t.packed0[g];
+        w.qa = a.qa + (a.sum_rows ? p0 * a.dim : r0 * w.K);
+        w.qb = a.qb + (a.sum_rows ? p0 * a.N : t.index[g] * a.N * w.K);
+    } else {
+        w.qa = a.qa + r0 * a.dim;
+        w.qb = a.qb + (a.sum_rows ? r0 * a.N : t.index[g] * a.N * a.dim);
+    }
     w.sa = a.sa + t.sa_off[g];
     w.sb = a.sb + t.sb_off[g];
     w.qa_left = a.qa_bytes - (w.qa - a.qa);
@@ -141,6 +150,81 @@ __device__ __forceinline__ void store_out(const MmArgs &a, int64_t i, float v)
     } else {
         static_cast<uint16_t *>(a.y)[i] = (uint16_t)bf16_pair(v, 0.f);
     }
+}
+
+__device__ __forceinline__ uint32_t clip31(int64_t v)
+{
+    return (uint32_t)(v < kMaxRecords ? v : kMaxRecords);
+}
+
+// v moved down by d bytes (d < 16).
+__device__ __forceinline__ uint4 bytes_down(uint4 v, uint32_t d)
+{
+    if (d & 8)
+        v = make_uint4(v.z, v.w, 0, 0);
+    if (d & 4)
+        v = make_uint4(v.y, v.z, v.w, 0);
+    const uint32_t b = d & 3;
+    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, b), __builtin_amdgcn_alignbyte(v.z, v.y, b),
+                      __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0, v.w, b));
+}
+
+// The first n of v's 16 bytes, zeros behind them.
+__device__ __forceinline__ uint4 bytes_keep(uint4 v, int n)
+{
+    auto word = [n](uint32_t w, int at) {
+        return n >= at + 4 ? w : n <= at ? 0u : w & ((1u << (8 * (n - at))) - 1);
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
+}
+
+// Byte rows that are read B bytes (16 or 8) at a time at any place, the last ones
+// of an array too: a base inside the array, up to B bytes before the tile's
+// first row, and the last offset from it that B bytes may be read at.  A read
+// that would pass it is taken there and moved down.
+template <int B>
+struct ByteRows {
+    const uint8_t *base;
+    int64_t last;
+    uint32_t lead;             // offset of the tile's first row
+
+    // rows of `pitch` bytes from `first` on, of an array that `left` bytes from
+    // there on belong to
+    __device__ __forceinline__ ByteRows(const uint8_t *array, const uint8_t *first, int64_t left)
+        : base(first - array < B ? array : first - B), last(left + (first - base) - B),
+          lead((uint32_t)(first - base))
+    {
+    }
+    // B bytes at off + at (at: the part that all lanes share), or the array's last B.
+    template <typename V>
+    __device__ __forceinline__ V load(uint32_t off, int64_t at) const
+    {
+        static_assert(sizeof(V) == B, "one read");
+        const int64_t to = at < last ? at : last;
+        const uint8_t *p = base + to;
+        const uint32_t lim = clip31(last - to);
+        V v;
+        __builtin_memcpy(&v, p + (off < lim ? off : lim), B);
+        return v;
+    }
+    // By how many bytes what load(off, at) read has to move down (more than any
+    // row needs: for reads behind the array).
+    __device__ __forceinline__ uint32_t behind(uint32_t off, int64_t at) const
+    {
+        const int64_t d = off + at - last;
+        return d <= 0 ? 0 : d < 15 ? (uint32_t)d : 15;
+    }
+    // What load(off, at) read, with n of its bytes inside the row.
+    __device__ __forceinline__ uint4 fix(uint4 v, uint32_t off, int64_t at, int n) const
+    {
+        return bytes_keep(bytes_down(v, behind(off, at)), n);
+    }
+};
+
+template <int FA, int FB, int J>
+__device__ __forceinline__ f32x16_t mfma_mx(i32x8_t a, i32x8_t b, f32x16_t c, uint32_t sa, uint32_t sb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, FB, J, (int)sa, J, (int)sb);
 }
 
 }  // namespace mxk

@@ -22,7 +22,6 @@
 // outputs leave as whole 128-byte lines from registers.
 #pragma once
 
-#include "bufio.h"
 #include "mm_common.h"
 
 namespace mxk {
@@ -60,74 +59,7 @@ __device__ __forceinline__ mm_rsrc_t rows_rsrc(const uint8_t *p, int64_t rows, i
 }
 constexpr uint32_t kDeadRow = 0xFFFFFFF0u;   // behind every bound: loads zeros
 
-__device__ __forceinline__ uint32_t clip31(int64_t v)
-{
-    return (uint32_t)(v < kMaxRecords ? v : kMaxRecords);
-}
-
-// v moved down by d bytes (d < 16).
-__device__ __forceinline__ uint4 bytes_down(uint4 v, uint32_t d)
-{
-    if (d & 8)
-        v = make_uint4(v.z, v.w, 0, 0);
-    if (d & 4)
-        v = make_uint4(v.y, v.z, v.w, 0);
-    const uint32_t b = d & 3;
-    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, b), __builtin_amdgcn_alignbyte(v.z, v.y, b),
-                      __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0, v.w, b));
-}
-
-// The first n of v's 16 bytes, zeros behind them.
-__device__ __forceinline__ uint4 bytes_keep(uint4 v, int n)
-{
-    auto word = [n](uint32_t w, int at) {
-        return n >= at + 4 ? w : n <= at ? 0u : w & ((1u << (8 * (n - at))) - 1);
-    };
-    return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
-}
-
-// Byte rows that are read B bytes (16 or 8) at a time at any place, the last ones
-// of an array too: a base inside the array, up to B bytes before the tile's
-// first row, and the last offset from it that B bytes may be read at.  A read
-// that would pass it is taken there and moved down.
-template <int B>
-struct ByteRows {
-    const uint8_t *base;
-    int64_t last;
-    uint32_t lead;             // offset of the tile's first row
-
-    // rows of `pitch` bytes from `first` on, of an array that `left` bytes from
-    // there on belong to
-    __device__ __forceinline__ ByteRows(const uint8_t *array, const uint8_t *first, int64_t left)
-        : base(first - array < B ? array : first - B), last(left + (first - base) - B),
-          lead((uint32_t)(first - base))
-    {
-    }
-    template <typename V>
-    __device__ __forceinline__ V load(uint32_t off, int64_t at) const
-    {
-        static_assert(sizeof(V) == B, "one read");
-        const uint8_t *p = base + at;
-        const uint32_t lim = clip31(last - at);
-        V v;
-        __builtin_memcpy(&v, p + (off < lim ? off : lim), B);
-        return v;
-    }
-    // What load(off, at) read, with n of its bytes inside the row.
-    __device__ __forceinline__ uint4 fix(uint4 v, uint32_t off, int64_t at, int n) const
-    {
-        const uint32_t lim = clip31(last - at), d = off < lim ? 0 : off - lim;
-        return bytes_keep(bytes_down(v, d < 15 ? d : 15), n);
-    }
-};
-
-template <int FA, int FB, int J>
-__device__ __forceinline__ f32x16_t mfma_mx(i32x8_t a, i32x8_t b, f32x16_t c, uint32_t sa, uint32_t sb)
-{
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, FB, J, (int)sa, J, (int)sb);
-}
-
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 struct MmKernel {
     static constexpr int MT = TM / 64, NT = TN / 64;      // 32-row tiles of a wave
     static constexpr int kBuf = (TM + TN) * 128;          // bytes of an LDS buffer
@@ -140,7 +72,6 @@ struct MmKernel {
 
     const MmArgs &a;
     const MmTile &w;
-    const ByteRows<16> qra, qrb;   // !ALIGNED: the codes
     const ByteRows<8> sra, srb;    // !TILED: the scales
     uint8_t *lds;
     uint32_t lds0;                 // its LDS address
@@ -148,8 +79,7 @@ struct MmKernel {
     int wm, wn;                    // the wave's rows and columns in the tile
     uint32_t voff[3];              // A; B's loads of even and odd numbers
     mm_rsrc_t ra, rb;
-    uint32_t last_a, last_b;       // the last rows of the operands in the tile
-    uint4 pend[ALIGNED ? 1 : kLoads];   // !ALIGNED: the codes under way
+    uint32_t last_a, last_b;       // the operands' last rows in the tile
     uint32_t sel;                  // compact: how a word comes out of 8 scale bytes
     // Scales.  Tiled: a lane loads its words of 4 steps (2 tiles) as they lie.
     // Compact: a thread loads the 8 bytes of one row of A and of one of B and puts
@@ -166,43 +96,22 @@ struct MmKernel {
     // holds.
     __device__ __forceinline__ int brow(int j) const { return wn + 64 * (j >> 1) + 2 * r + (j & 1); }
 
-    // Load i of the wave for tile t (zeros for one behind the last).  ALIGNED: into
-    // LDS; else into registers, from where commit() writes them.
-    __device__ __forceinline__ void issue(int t, int i)
+    // Load i of the wave for tile t (zeros for one behind the last).
+    __device__ __forceinline__ void issue(int t, int i) const
     {
-        const uint32_t k0 = 128u * (uint32_t)t;
-        if constexpr (ALIGNED) {
-            // 16-byte chunks behind the rows' ends are zeros
-            const uint32_t dst = lds0 + (uint32_t)(t & 1) * kBuf;
-            const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
-            const uint32_t v = 16 * chunk(i) < left ? offset(i) : kDeadRow;
-            load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
-        } else {
-            pend[i] = (is_a(i) ? qra : qrb).template load<uint4>(offset(i), k0 < w.K ? k0 : 0);
-        }
+        const uint32_t k0 = 128u * (uint32_t)t, dst = lds0 + (uint32_t)(t & 1) * kBuf;
+        // 16-byte chunks behind the rows' ends are zeros
+        const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
+        const uint32_t v = 16 * chunk(i) < left ? offset(i) : kDeadRow;
+        load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
     }
-    __device__ __forceinline__ void commit(int t, int i)
-    {
-        const uint32_t k0 = 128u * (uint32_t)t;
-        uint4 v = pend[i];
-        if (k0 + 128 > w.K)
-            v = (is_a(i) ? qra : qrb).fix(v, offset(i), k0 < w.K ? k0 : 0, (int)w.K - (int)k0 - 16 * (int)chunk(i));
-        reinterpret_cast<uint4 *>(lds + (t & 1) * kBuf + row8(i) * 128)[L] = v;
-    }
-    // The loads (writes) that go with MFMA k of n.
-    __device__ __forceinline__ void issue_share(int t, int k, int n)
+    // The loads that go with MFMA k of n.
+    __device__ __forceinline__ void issue_share(int t, int k, int n) const
     {
 #pragma unroll
         for (int i = 0; i < kLoads; i++)
             if (i * n / kLoads == k)
                 issue(t, i);
-    }
-    __device__ __forceinline__ void commit_share(int t, int k, int n)
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; i++)
-            if (i * n / kLoads == k)
-                commit(t, i);
     }
     // The wave's load i fills 8 rows of LDS, from row8(i) on: a share of A's TM
     // rows, then of B's TN rows behind them.
@@ -212,17 +121,11 @@ struct MmKernel {
     {
         return 8 * (is_a(i) ? wave * kLoadsA + i : TM / 8 + wave * (TN / 32) + i - kLoadsA);
     }
-    // Where in the tile's rows lane L's load i starts (!ALIGNED: from the base of
-    // ByteRows; rows behind the last one: the last one, whose reads are bounded).
+    // Where in the tile's rows lane L's load i starts.
     __device__ __forceinline__ uint32_t offset(int i) const
     {
         const int nth = is_a(i) ? i : i - kLoadsA;
-        const uint32_t o = voff[is_a(i) ? 0 : 1 + (nth & 1)] + 8 * nth * (uint32_t)w.K;
-        if (ALIGNED)
-            return o;
-        const uint32_t last = is_a(i) ? last_a : last_b;
-        const int row = row8(i) + (L >> 3) - (is_a(i) ? 0 : TM);
-        return (row < (int)last ? o : o - (row - last) * (uint32_t)w.K);
+        return voff[is_a(i) ? 0 : 1 + (nth & 1)] + 8 * nth * (uint32_t)w.K;
     }
     // The chunk of its row that lane L loads (the slot's exchange, above).
     __device__ __forceinline__ uint32_t chunk(int i) const
@@ -364,8 +267,6 @@ struct MmKernel {
                     acc[i][j] = mfma_mx<FA, FB, J>(f.a[i], f.b[j], acc[i][j], sa[i][0], sb[j][0]);
                     if (LOAD)
                         issue_share(tl, k, MT * NT);
-                    else if (!ALIGNED)
-                        commit_share(tl, k, MT * NT);
                     if (k < MT + NT)
                         read(next, tn, sn, k);
                     k++;
@@ -399,11 +300,8 @@ struct MmKernel {
                             if (jj * MT / NT == i)
                                 b[(part & 1) ^ 1][jj] = conv_b<J>(f, jj, part + 1);
                     }
-                    // (the loads in the first half, the writes in the second)
                     if (LOAD && part < 2)
                         issue_share(tl, part * MT * NT + i * NT + j, 2 * MT * NT);
-                    else if (!LOAD && !ALIGNED && part >= 2)
-                        commit_share(tl, (part - 2) * MT * NT + i * NT + j, 2 * MT * NT);
                     if (j == NT - 1) {
 #pragma unroll
                         for (int k = 0; k < MT + NT; k++)
@@ -432,7 +330,7 @@ struct MmKernel {
     template <int J, bool SETTLE>
     __device__ __forceinline__ void tile(Frags &f0, Frags &f1, int t)
     {
-        step<J, false>(f0, f1, t, 1, t + 1);
+        step<J, false>(f0, f1, t, 1, 0);
         wait_all_and_barrier();
         if (SETTLE)
             settle_scales();
@@ -453,8 +351,6 @@ struct MmKernel {
             const int l = i == 0 ? 0 : kLoadsA + i - 1;    // the load it is for
             const int row = row8(l) + (L >> 3) - (i ? TM : 0) - (i == 2 ? 8 : 0);
             voff[i] = (uint32_t)(row * (int)w.K) + 16 * chunk(l);
-            if (!ALIGNED)
-                voff[i] += i ? qrb.lead : qra.lead;
         }
 #pragma unroll
         for (int i = 0; i < MT; i++)
@@ -484,11 +380,6 @@ struct MmKernel {
             } else {
                 write_scales(0);
                 fetch_scales(1);
-            }
-            if constexpr (!ALIGNED) {
-#pragma unroll
-                for (int i = 0; i < kLoads; i++)
-                    commit(0, i);
             }
             wait_all_and_barrier();
 #pragma unroll
@@ -590,14 +481,12 @@ struct MmKernel {
     }
 };
 
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 __device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, uint8_t *lds)
 {
     typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
-    MmKernel<MODE, FA, FB, TM, TN, TILED, ALIGNED> k{
+    MmKernel<MODE, FA, FB, TM, TN, TILED> k{
         a, w,
-        ByteRows<16>(a.qa, w.qa + w.m0 * w.K, w.qa_left - w.m0 * w.K),
-        ByteRows<16>(a.qb, w.qb + w.n0 * w.K, w.qb_left - w.n0 * w.K),
         ByteRows<8>(a.sa, w.sa + w.m0 * w.nb, w.sa_left - w.m0 * w.nb),
         ByteRows<8>(a.sb, w.sb + w.n0 * w.nb, w.sb_left - w.n0 * w.nb)};
     k.lds = lds;
@@ -613,14 +502,14 @@ __device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, ui
 
 // The first t.whole workgroups take a whole tile each.  The tiles behind them,
 // too few to fill the CUs once more, go in parts of 128 x 128.
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const MmTable t)
 {
     extern __shared__ uint8_t mm_lds[];
     const int id = (int)blockIdx.x;
     if (id < t.whole) {
         const MmTile w = mm_tile(a, t, mm_xcd_order(id, t.whole), TM, TN);
-        mm_tile_run<MODE, FA, FB, TM, TN, TILED, ALIGNED>(a, w, mm_lds);
+        mm_tile_run<MODE, FA, FB, TM, TN, TILED>(a, w, mm_lds);
     } else {
         constexpr int S = kMmPart, PM = TM / S, parts = PM * (TN / S);
         const int q = id - t.whole;
@@ -628,33 +517,33 @@ __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const M
         w.m0 += q % PM * S;
         w.n0 += q % parts / PM * S;
         if (w.m0 < w.M && w.n0 < a.N)
-            mm_tile_run<MODE, FA, FB, S, S, TILED, ALIGNED>(a, w, mm_lds);
+            mm_tile_run<MODE, FA, FB, S, S, TILED>(a, w, mm_lds);
     }
 }
 
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool ALIGNED>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 hipError_t launch_mm_tile_one(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
     constexpr int lds = 2 * (TM + TN) * (128 + (TILED ? 0 : 8)), parts = TM * TN / (kMmPart * kMmPart);
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>),
+        hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN, TILED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED, ALIGNED>), dim3((unsigned)(t.whole + parts * (t.tile0[t.count] - t.whole))), dim3(256), lds, stream, a, t);
+    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED>), dim3((unsigned)(t.whole + parts * (t.tile0[t.count] - t.whole))), dim3(256), lds, stream, a, t);
     return hipGetLastError();
 }
 
-template <MmMode MODE, int TM, int TN, bool TILED, bool ALIGNED>
+template <MmMode MODE, int TM, int TN, bool TILED>
 hipError_t launch_mm_tile_mode(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
     if (!a.a_e5m2 && !a.b_e5m2)
-        return launch_mm_tile_one<MODE, 0, 0, TM, TN, TILED, ALIGNED>(a, t, stream);
+        return launch_mm_tile_one<MODE, 0, 0, TM, TN, TILED>(a, t, stream);
     if (a.a_e5m2 && !a.b_e5m2)
-        return launch_mm_tile_one<MODE, 1, 0, TM, TN, TILED, ALIGNED>(a, t, stream);
+        return launch_mm_tile_one<MODE, 1, 0, TM, TN, TILED>(a, t, stream);
     if (!a.a_e5m2)
-        return launch_mm_tile_one<MODE, 0, 1, TM, TN, TILED, ALIGNED>(a, t, stream);
-    return launch_mm_tile_one<MODE, 1, 1, TM, TN, TILED, ALIGNED>(a, t, stream);
+        return launch_mm_tile_one<MODE, 0, 1, TM, TN, TILED>(a, t, stream);
+    return launch_mm_tile_one<MODE, 1, 1, TM, TN, TILED>(a, t, stream);
 }
 
 }  // namespace mxk

@@ -5,8 +5,8 @@ namespace mxk {
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    return a.tiled ? launch_mm_tile_mode<kMx, kMmTileM, kMmTileN, true, true>(a, t, stream)
-                   : launch_mm_tile_mode<kMx, kMmTileM, kMmTileN, false, true>(a, t, stream);
+    return a.tiled ? launch_mm_tile_mode<kMx, kMmTileM, kMmTileN, true>(a, t, stream)
+                   : launch_mm_tile_mode<kMx, kMmTileM, kMmTileN, false>(a, t, stream);
 }
 
 }  // namespace mxk

@@ -5,8 +5,8 @@ namespace mxk {
 
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    return a.tiled ? launch_mm_tile_mode<kExact, kMmTileM, kMmTileN, true, true>(a, t, stream)
-                   : launch_mm_tile_mode<kExact, kMmTileM, kMmTileN, false, true>(a, t, stream);
+    return a.tiled ? launch_mm_tile_mode<kExact, kMmTileM, kMmTileN, true>(a, t, stream)
+                   : launch_mm_tile_mode<kExact, kMmTileM, kMmTileN, false>(a, t, stream);
 }
 
 }  // namespace mxk

@@ -457,12 +457,16 @@ mx_status nvfp4_quantize_transpose_grouped(const void *x, int64_t K, const int64
  *   qb, sb   elements [N][K] and their scales
  *   M, N, K  any sizes >= 1, each <= 2^23, every pair's product <= 2^40
  *   y        bf16 or fp32 [M][N]
+ *   workspace, workspace_bytes  device scratch of at least
+ *            mx_matmul_workspace_size() bytes (NULL and 0 where that is 0)
  * Errors: MX_ERR_ENUM for an unknown flag or MX_OUT_ACCUMULATE without
  * MX_OUT_F32; MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN (16 bytes, every
- * pointer), MX_ERR_ALIAS (y overlaps an operand) as for the casts.
+ * pointer), MX_ERR_WORKSPACE, MX_ERR_ALIAS (y overlaps an operand or the
+ * workspace) as for the casts.
  */
 mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const uint8_t *sb,
-                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream);
+                    int64_t M, int64_t N, int64_t K, unsigned flags, void *y, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream);
 
 /*
  * The same for G experts in one launch: group g's rows of A, stacked as for
@@ -478,7 +482,8 @@ mx_status mx_matmul(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, con
  */
 mx_status mx_matmul_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
                             const uint8_t *sb, int64_t N, int64_t K, const int64_t *group_rows,
-                            int G, unsigned flags, void *y, hipStream_t stream);
+                            int G, unsigned flags, void *y, void *workspace, size_t workspace_bytes,
+                            hipStream_t stream);
 
 /*
  * The experts' weight gradients in one launch: dW_g [N][K] = sum over group
@@ -492,7 +497,18 @@ mx_status mx_matmul_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t 
 mx_status mx_matmul_wgrad_grouped(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb,
                                   const uint8_t *sb, int64_t N, int64_t K,
                                   const int64_t *group_rows, int G, unsigned flags, void *dw,
-                                  hipStream_t stream);
+                                  void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace the three products need (0 for most sizes, and for invalid
+ * arguments): copies of operands whose rows do not all start at multiples of 16
+ * bytes (K, or for weight gradients a group's rows, no multiple of 16), unless
+ * the product is small.  Contents on entry are ignored and on exit undefined;
+ * calls that may overlap in time need workspaces of their own. */
+size_t mx_matmul_workspace_size(int64_t M, int64_t N, int64_t K, unsigned flags);
+size_t mx_matmul_grouped_workspace_size(int64_t N, int64_t K, const int64_t *group_rows, int G,
+                                        unsigned flags);
+size_t mx_matmul_wgrad_grouped_workspace_size(int64_t N, int64_t K, const int64_t *group_rows, int G,
+                                              unsigned flags);
 
 /*
  * Matrix-vector products with NVFP4 weights (decoding): y[T][N] = x W^T, with
