@@ -80,6 +80,7 @@ struct MmKernel {
     uint32_t voff[3];              // A; B's loads of even and odd numbers
     mm_rsrc_t ra, rb;
     uint32_t last_a, last_b;       // the operands' last rows in the tile
+    int nt, phase;                 // tiles of k, the first one
     uint32_t sel;                  // compact: how a word comes out of 8 scale bytes
     // Scales.  Tiled: a lane loads its words of 4 steps (2 tiles) as they lie.
     // Compact: a thread loads the 8 bytes of one row of A and of one of B and puts
@@ -96,10 +97,16 @@ struct MmKernel {
     // holds.
     __device__ __forceinline__ int brow(int j) const { return wn + 64 * (j >> 1) + 2 * r + (j & 1); }
 
-    // Load i of the wave for tile t (zeros for one behind the last).
+    // The tile of k that comes in place t: workgroups start at different ones
+    // (see run()).
+    __device__ __forceinline__ int turned(int t) const
+    {
+        return t >= nt ? t : t + phase < nt ? t + phase : t + phase - nt;
+    }
+    // Load i of the wave for the tile in place t (zeros behind the last).
     __device__ __forceinline__ void issue(int t, int i) const
     {
-        const uint32_t k0 = 128u * (uint32_t)t, dst = lds0 + (uint32_t)(t & 1) * kBuf;
+        const uint32_t k0 = 128u * (uint32_t)turned(t), dst = lds0 + (uint32_t)(t & 1) * kBuf;
         // 16-byte chunks behind the rows' ends are zeros
         const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
         const uint32_t v = 16 * chunk(i) < left ? offset(i) : kDeadRow;
@@ -162,9 +169,11 @@ struct MmKernel {
             return (uint32_t)((d >> 5) * 256 + 4 * (d & 31)) + (MODE == kMx ? 128 * h : 0);
         return (uint32_t)(d * (int)w.nb);
     }
-    // Loads the scales of blocks 8 bt on (for bt behind the last: some).
-    __device__ __forceinline__ void fetch_scales(int bt)
+    // Loads the scales of 8 blocks, those of the two tiles in places 2 place and on
+    // (for a place behind the last: some).
+    __device__ __forceinline__ void fetch_scales(int place)
     {
+        const int bt = turned(2 * place) >> 1;
         if constexpr (TILED) {
             const uint8_t *pa = w.sa + (bt * ((w.M + 31) >> 5) + (w.m0 >> 5)) * 256;
             const uint8_t *pb = w.sb + (bt * ((a.N + 31) >> 5) + (w.n0 >> 5)) * 256;
@@ -211,17 +220,18 @@ struct MmKernel {
                 sb[j][k] = raw_b[TILED ? j : 0][k];
         }
     }
-    // Compact: the scales fetched for blocks 8 bt on into LDS buffer bt % 2; those
+    // Compact: the scales fetched for `place` into LDS buffer place % 2; those
     // behind the last block become 0.
-    __device__ __forceinline__ void write_scales(int bt)
+    __device__ __forceinline__ void write_scales(int place)
     {
+        const int bt = turned(2 * place) >> 1;
         uint2 x = make_uint2(raw_a[0][0], raw_a[0][1]), y = make_uint2(raw_b[0][0], raw_b[0][1]);
         const int64_t keep = w.nb - 8 * bt;
         if (keep < 8) {
             x = keep8(x, sra, off_a[0], 8 * bt, (int)keep);
             y = keep8(y, srb, off_b[0], 8 * bt, (int)keep);
         }
-        uint2 *p = reinterpret_cast<uint2 *>(lds + 2 * kBuf) + (bt & 1) * (TM + TN) + 64 * wave + L;
+        uint2 *p = reinterpret_cast<uint2 *>(lds + 2 * kBuf) + (place & 1) * (TM + TN) + 64 * wave + L;
         if (TM == 256 || wave < TM / 64)
             p[0] = x;
         if (TN == 256 || wave < TN / 64)
@@ -235,10 +245,10 @@ struct MmKernel {
         const uint4 u = rows.fix(make_uint4(v.x, v.y, 0, 0), off, at, n);
         return make_uint2(u.x, u.y);
     }
-    // Compact: the words of the four steps of blocks 8 bt on in use.
-    __device__ __forceinline__ void read_scales(int bt)
+    // Compact: the words of the four steps of `place` in use.
+    __device__ __forceinline__ void read_scales(int place)
     {
-        const uint2 *p = reinterpret_cast<const uint2 *>(lds + 2 * kBuf) + (bt & 1) * (TM + TN);
+        const uint2 *p = reinterpret_cast<const uint2 *>(lds + 2 * kBuf) + (place & 1) * (TM + TN);
 #pragma unroll
         for (int i = 0; i < MT; i++)
             words(sa[i], p[wm + 32 * i + r]);
@@ -340,7 +350,12 @@ struct MmKernel {
     __device__ __forceinline__ void run()
     {
         // an even number of tiles: one behind the last k holds zeros
-        const int nt = 2 * (int)((w.K + 255) / 256);
+        nt = 2 * (int)((w.K + 255) / 256);
+        // Rows a multiple of 256 bytes apart lie in few of the L2's channels at
+        // any one k, and the workgroups of an XCD walk along k at about the same
+        // pace: columns of tiles start in four different places, 256 k apart.
+        phase = 2 * (int)((w.n0 / TN) & 3);
+        phase = phase < nt ? phase : 0;
         sel = MODE == kMx && h ? 0x07050301u : 0x06040200u;
         ra = rows_rsrc(w.qa + w.m0 * w.K, w.M - w.m0, w.K);
         rb = rows_rsrc(w.qb + w.n0 * w.K, a.N - w.n0, w.K);
