@@ -282,9 +282,9 @@ mx_status mv_impl(const void *x, const int32_t *experts, int64_t T, int64_t top,
     a.sw = sw;
     a.sg = sg;
     a.y = y;
-    a.T = T;
-    a.N = N;
-    a.K = K;
+    a.T = (int32_t)T;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
     a.top = (int32_t)top;
     a.G = G;
     a.out_f32 = (flags & MX_OUT_F32) != 0;

@@ -72,7 +72,7 @@ struct MvArgs {
     const uint8_t *qw, *sw;
     const float *sg;
     void *y;
-    int64_t T, N, K;
+    int32_t T, N, K;                    // each at most 2^23, T * top too
     int32_t top, G;
     int32_t out_f32;
     int32_t by_slot;                    // set by the launcher

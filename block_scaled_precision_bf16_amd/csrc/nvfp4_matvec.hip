@@ -79,13 +79,13 @@ __device__ __forceinline__ void store_mv(const MvArgs &a, int64_t i, float v)
 // slot `from` on, into slot[]; returns how many.  Called by all waves; slot[] is
 // there after the caller's next barrier.
 template <int TT>
-__device__ __forceinline__ int gather_slots(const MvArgs &a, int e, int64_t from, int32_t *slot,
+__device__ __forceinline__ int gather_slots(const MvArgs &a, int e, int from, int32_t *slot,
                                             int32_t *wave_count)
 {
-    const int64_t slots = a.T * a.top;
+    const int slots = a.T * a.top;
     const int tid = (int)threadIdx.x, L = tid & 63, wave = tid >> 6;
     const uint64_t below = (1ull << L) - 1;
-    auto takes = [&](int64_t p) {
+    auto takes = [&](int p) {
         if (p >= slots)
             return false;
         const int32_t v = a.experts[p];
@@ -97,11 +97,11 @@ __device__ __forceinline__ int gather_slots(const MvArgs &a, int e, int64_t from
         const uint64_t m = __ballot(hit);
         const int at = __popcll(m & below), all = __popcll(m);
         if (wave == 0 && hit && at < TT)
-            slot[at] = (int32_t)from + L;
+            slot[at] = from + L;
         return all < TT ? all : TT;
     }
     int count = 0;
-    for (int64_t base = from; base < slots && count < TT; base += kMvThreads) {
+    for (int base = from; base < slots && count < TT; base += kMvThreads) {
         const bool hit = takes(base + tid);
         const uint64_t m = __ballot(hit);
         if (L == 0)
@@ -114,37 +114,95 @@ __device__ __forceinline__ int gather_slots(const MvArgs &a, int e, int64_t from
             count += wave_count[i];
         }
         if (hit && at < TT)
-            slot[at] = (int32_t)(base + tid);
+            slot[at] = base + tid;
         __syncthreads();
     }
     return count < TT ? count : TT;
 }
 
+// Zeros in the workgroup's share of the rows of slots p + 0 .. or slot[0] ...
+__device__ __forceinline__ void zero_rows(const MvArgs &a, const int32_t *slot, int p, int count)
+{
+    for (int t = 0; t < count; t++)
+        for (int n = (int)(blockIdx.x * kMvThreads + threadIdx.x); n < a.N; n += (int)gridDim.x * kMvThreads)
+            store_mv(a, (int64_t)(slot ? slot[t] : p + t) * a.N + n, 0.f);
+}
+
+// Waves per SIMD: two workgroups per CU, one for 64 tokens (136 KB of LDS).
+constexpr int mv_occupancy(int tokens) { return tokens == 64 ? 2 : 4; }
+
 // How a kernel for up to TT tokens is laid out: KS waves share the chunks of a
 // row, each has D of its chunks under way, a stage holds the tokens of D KS
 // chunks.
-template <int TT>
+template <int TT, bool EXPERTS>
 struct MvPlan {
-    static constexpr int KS = TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 ? 4 : 2;
-    static constexpr int kRows = 16 * WN;                     // weight rows of a workgroup
+    static constexpr int KS = TT <= 2 && EXPERTS ? 8 : TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 && !EXPERTS ? 4 : 2;
+    static constexpr int kRows = 16 * WN;                     // weight rows of a block
     static constexpr int kFit = D * KS;                       // chunks of a stage
     static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
     // 1 or 2 tokens: dot products on the vector units, which need no scaled
     // weights: 1.1 (1.6) vector instructions a weight
     static constexpr bool kDot = TT <= 2;
-    // LDS: a stage's tokens, later the partial sums of a token tile
-    static constexpr int kLds = kFit * 512 * TT > kMvWaves * 1024 ? kFit * 512 * TT : kMvWaves * 1024;
-    // waves per SIMD: two workgroups per CU, one for 64 tokens (128 KB of LDS)
-    static constexpr int kOccupancy = TT == 64 ? 2 : 4;
+    // LDS: a stage's tokens, then the waves' sums of a token tile
+    static constexpr int kTokens = kFit * 512 * TT, kLds = kTokens + kMvWaves * 1024;
 };
 
-// EXPERTS: blockIdx.y is the expert (G: the slots without one, whose rows become
-// zeros) or, with a.by_slot, a slot, whose workgroups serve its expert if no
-// earlier slot has the same; else the tile of TT tokens.
+// Where a workgroup finds the weights of a block of rows.
+struct Aim {
+    const uint8_t *q, *s;       // bases a little before the block's first row
+    uint32_t qlast, slast;      // the last offsets that a load of 16 (4) bytes may have
+    uint32_t qoff, soff;        // the lane's (at most 64 rows of 2^22 bytes)
+
+    __device__ __forceinline__ Aim(const MvArgs &a, int e, int n0, int row, int g)
+    {
+        const int nb = (a.K + 15) >> 4, pitch = (a.K + 1) >> 1;
+        const int64_t first = (int64_t)e * a.N + n0, all = (int64_t)a.G * a.N;
+        const int64_t q0 = first * pitch < 16 ? 0 : first * pitch - 16;
+        const int64_t s0 = first * nb < 4 ? 0 : first * nb - 4;
+        q = a.qw + q0;
+        s = a.sw + s0;
+        const int64_t qreach = all * pitch - 16 - q0, sreach = all * nb - 4 - s0;
+        qlast = (uint32_t)(qreach < INT32_MAX ? qreach : INT32_MAX);
+        slast = (uint32_t)(sreach < INT32_MAX ? sreach : INT32_MAX);
+        row = row < a.N - 1 - n0 ? row : a.N - 1 - n0;
+        qoff = (uint32_t)(first * pitch - q0) + (uint32_t)(row * pitch) + 32 * g;
+        soff = (uint32_t)(first * nb - s0) + (uint32_t)(row * nb) + 4 * g;
+    }
+    // A chunk's bytes, never from behind the arrays' ends: there, those before
+    // the end, which settle() moves where they belong.
+    __device__ __forceinline__ void fetch(Share &w, int c) const
+    {
+        const uint32_t o = qoff + c * (kChunk / 2), p = soff + c * (kChunk / 16);
+        __builtin_memcpy(&w.q[0], q + (o < qlast ? o : qlast), 16);
+        __builtin_memcpy(&w.q[1], q + (o + 16 < qlast ? o + 16 : qlast), 16);
+        __builtin_memcpy(&w.s, s + (p < slast ? p : slast), 4);
+    }
+    // The last, partial chunk: codes behind a row's end are some codes and meet
+    // zero tokens, scales there (from block nb on) become 0.
+    __device__ __forceinline__ void settle(Share &w, int c, int nb, int g) const
+    {
+        const int o = (int)(qoff + c * (kChunk / 2) - qlast), p = (int)(soff + c * (kChunk / 16) - slast);
+        if (o > 0)
+            w.q[0] = shift_down(w.q[0], o < 15 ? o : 15);
+        if (o + 16 > 0)
+            w.q[1] = shift_down(w.q[1], o + 16 < 15 ? o + 16 : 15);
+        const int keep = nb - c * (kChunk / 16) - 4 * g;
+        uint32_t v = p > 0 ? (p < 4 ? w.s >> (8 * p) : 0) : w.s;
+        if (keep < 4)
+            v = keep <= 0 ? 0 : v & ((1u << (8 * keep)) - 1);
+        w.s = v;
+    }
+};
+
+// A workgroup takes row block blockIdx.x, with EXPERTS also + gridDim.x, ...
+// (which costs registers, and gains where a workgroup's own work is short).
+// EXPERTS: blockIdx.y is the expert (G: the slots without one, whose rows become zeros)
+// or, with a.by_slot, a slot, whose workgroups serve its expert if no earlier
+// slot has the same; else the tile of TT tokens.
 template <int TT, bool EXPERTS>
-__global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(const MvArgs a)
+__global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const MvArgs a)
 {
-    using Plan = MvPlan<TT>;
+    using Plan = MvPlan<TT, EXPERTS>;
     constexpr int TB = (TT + 15) / 16;            // token tiles
     constexpr int KS = Plan::KS, P = Plan::kPieces, D = Plan::D;
     constexpr int kMix = TT == 1 ? 3 : 7;         // within a fragment's 4 TT slots
@@ -152,14 +210,11 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
     __shared__ int32_t slot[EXPERTS ? TT : 1];
     __shared__ int32_t wave_count[kMvWaves];
 
-    const int tid = (int)threadIdx.x, L = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = L & 15, g = L >> 4;
-    const int ks = wave % KS, wn = wave / KS;
-    const int64_t n0 = (int64_t)blockIdx.x * Plan::kRows;
-    const int64_t nb = (a.K + 15) >> 4, pitch = (a.K + 1) >> 1;
-    const int nchunk = (int)((a.K + kChunk - 1) / kChunk);
-    int64_t from = 0;                             // the next slot to look at
+    const int blocks = (a.N + Plan::kRows - 1) / Plan::kRows, step = (int)gridDim.x;
+    const int nb = (a.K + 15) >> 4, nchunk = (a.K + kChunk - 1) / kChunk;
+    const int partial = a.K % kChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
+    const int stages = (nchunk + Plan::kFit - 1) / Plan::kFit;
+    int from = 0;                                 // the next slot to look at
     int e = 0;
     if (EXPERTS) {
         e = (int)blockIdx.y;
@@ -167,63 +222,27 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
             from = e;
             e = __builtin_amdgcn_readfirstlane(a.experts[from]);
             if (e < 0 || e >= a.G) {
-                if (tid < Plan::kRows && n0 + tid < a.N)
-                    store_mv(a, from * a.N + n0 + tid, 0.f);
+                zero_rows(a, nullptr, from, 1);
                 return;
             }
             bool earlier = false;
-            for (int64_t p = L; p < from; p += 64)
+            for (int p = threadIdx.x & 63; p < from; p += 64)
                 earlier |= a.experts[p] == e;
             if (__ballot(earlier))
                 return;
         }
     } else {
-        from = (int64_t)blockIdx.y * TT;
+        from = (int)blockIdx.y * TT;
     }
 
-    // A base a little before the workgroup's first row, the lane's offsets from
-    // it (at most 64 rows of 2^22 bytes), and the last offsets that a load of 16
-    // (4) bytes may have.
-    const int64_t first = (EXPERTS && e == a.G ? 0 : (int64_t)e * a.N) + n0, all = (int64_t)a.G * a.N;
-    const int64_t q0 = first * pitch < 16 ? 0 : first * pitch - 16;
-    const int64_t s0 = first * nb < 4 ? 0 : first * nb - 4;
-    const uint8_t *const qbase = a.qw + q0, *const sbase = a.sw + s0;
-    const int64_t qreach = all * pitch - 16 - q0, sreach = all * nb - 4 - s0;
-    const uint32_t qlast = (uint32_t)(qreach < INT32_MAX ? qreach : INT32_MAX);
-    const uint32_t slast = (uint32_t)(sreach < INT32_MAX ? sreach : INT32_MAX);
-    const int row = 16 * wn + r, last_row = (int)(a.N - 1 - n0 < 1024 ? a.N - 1 - n0 : 1024);
-    const int my_row = row < last_row ? row : last_row;
-    uint32_t qoff = (uint32_t)(first * pitch - q0 + my_row * pitch) + 32 * g;
-    uint32_t soff = (uint32_t)(first * nb - s0 + my_row * nb) + 4 * g;
-
-    // A chunk's bytes, never from behind the arrays' ends: there, those before
-    // the end, which settle() moves where they belong.
-    auto fetch = [&](Share &w, int c) {
-        const uint32_t q = qoff + c * (kChunk / 2), s = soff + c * (kChunk / 16);
-        __builtin_memcpy(&w.q[0], qbase + (q < qlast ? q : qlast), 16);
-        __builtin_memcpy(&w.q[1], qbase + (q + 16 < qlast ? q + 16 : qlast), 16);
-        __builtin_memcpy(&w.s, sbase + (s < slast ? s : slast), 4);
-    };
-    // The last, partial chunk: codes behind a row's end are some codes and meet
-    // zero tokens, scales there become 0.
-    auto settle = [&](Share &w, int c) {
-        const int q = (int)(qoff + c * (kChunk / 2) - qlast), s = (int)(soff + c * (kChunk / 16) - slast);
-        if (q > 0)
-            w.q[0] = shift_down(w.q[0], q < 15 ? q : 15);
-        if (q + 16 > 0)
-            w.q[1] = shift_down(w.q[1], q + 16 < 15 ? q + 16 : 15);
-        const int keep = (int)nb - c * (kChunk / 16) - 4 * g;
-        uint32_t v = s > 0 ? (s < 4 ? w.s >> (8 * s) : 0) : w.s;
-        if (keep < 4)
-            v = keep <= 0 ? 0 : v & ((1u << (8 * keep)) - 1);
-        w.s = v;
-    };
-    const int partial = a.K % kChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
-
     for (;;) {
-        // (the addresses below are computed in each pass: kept over passes they
+        // (the lane's places are worked out in each pass: kept over passes they
         // cost more registers than there are)
-        asm volatile("" : "+v"(qoff), "+v"(soff));
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int L = tid & 63, r = L & 15, g = L >> 4;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int ks = wave % KS, wn = wave / KS;
         int count;                                // this pass's tokens
         if (EXPERTS) {
             count = gather_slots<TT>(a, e, from, slot, wave_count);
@@ -231,9 +250,7 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
                 return;
             if (e == a.G) {
                 __syncthreads();
-                for (int i = tid; i < count * Plan::kRows; i += kMvThreads)
-                    if (n0 + i % Plan::kRows < a.N)
-                        store_mv(a, (int64_t)slot[i / Plan::kRows] * a.N + n0 + i % Plan::kRows, 0.f);
+                zero_rows(a, slot, 0, count);
                 from = slot[count - 1] + 1;
                 __syncthreads();
                 continue;
@@ -241,23 +258,25 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
         } else {
             if (from >= a.T)
                 return;
-            count = (int)(a.T - from < TT ? a.T - from : TT);
+            count = a.T - from < TT ? a.T - from : TT;
         }
         Share w[D];
+        Aim next(a, e, (int)blockIdx.x * Plan::kRows, 16 * wn + r, g);
 #pragma unroll
         for (int j = 0; j < D; j++)
             if (ks + j * KS < nchunk)
-                fetch(w[j], ks + j * KS);
+                next.fetch(w[j], ks + j * KS);
         if (EXPERTS)
             __syncthreads();                      // slot[]
 
         // The tokens of a stage, in fragment order: 8 k of one token per 16
         // bytes; k = 64 g + 32 h + 8 d of a chunk belongs to fragment f = 4 h + d
         // at lane group g, and lies in slot (g TT + token) ^ f of the fragment's
-        // 4 TT (one token: ^ f % 4) (the writes of 8 neighbouring pieces go to 8 fragments, the reads
-        // stay in one: both touch all banks).  A thread moves P pieces, at the same places in every
-        // stage, through registers: all loads before the first store, and
-        // those of the next stage while this one is used.
+        // 4 TT (one token: ^ f % 4; the writes of 8 neighbouring pieces go to 8
+        // fragments, the reads stay in one: both touch all banks).  A thread
+        // moves P pieces, at the same places in every stage, through registers:
+        // all loads before the first store, and those of the next stage while
+        // this one is used.
         // Thread tid: piece tid % 32 of a chunk; the 16 rows tid / 32 are
         // tokens (TT < 16: TT tokens of 16 / TT chunks), TB times over.
         constexpr int kSide = TT < 16 ? 16 / TT : 1;
@@ -268,13 +287,13 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
         for (int b = 0; b < TB; b++) {
             int t = (tid >> 5) % TT + 16 * b;
             t = t < count ? t : count - 1;        // a place of no token: any
-            xo[b] = (EXPERTS ? slot[t] / a.top : from + t) * a.K + xk;
+            xo[b] = (int64_t)(EXPERTS ? slot[t] / a.top : from + t) * a.K + xk;
         }
         uint4 *const xl = reinterpret_cast<uint4 *>(lds) + (8 * c_side + (q & 7)) * 4 * TT +
                           (((q >> 3) * TT + (tid >> 5) % TT) ^ (q & kMix));
         uint4 xv[P];
         // never from behind x's end: there, the 16 bytes before it
-        const int64_t x_end = a.T * a.K - 8;
+        const int64_t x_end = (int64_t)a.T * a.K - 8;
         auto load_tokens = [&](int st) {
 #pragma unroll
             for (int j = 0; j < P; j++) {
@@ -289,7 +308,7 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
                 for (int j = 0; j < P; j++) {
                     const int k0 = (st * Plan::kFit + j / TB * kSide) * kChunk;
                     const int64_t d = 2 * (xo[j % TB] + k0 - x_end);
-                    const int keep = (int)a.K - k0 - xk;
+                    const int keep = a.K - k0 - xk;
                     uint4 v = xv[j];
                     if (d > 0)
                         v = shift_down(v, d < 15 ? (uint32_t)d : 15);
@@ -306,126 +325,146 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
                 xl[j / TB * kSide * 32 * TT + 16 * (j % TB)] = xv[j];
         };
         load_tokens(0);
+        const float sg = a.sg[e];
 
-        f32x4_t acc[TB];                          // kDot: acc[0][t] of token t
+        for (int block = (int)blockIdx.x; block < blocks; block += EXPERTS ? step : blocks) {
+            Aim aim = next;
+            // (what depends on these is computed where it is used: kept over the
+            // loop it costs more registers than there are)
+            if (EXPERTS)
+                asm volatile("" : "+v"(aim.qoff), "+v"(aim.soff));
+            const int n0 = block * Plan::kRows;
+            const bool more = EXPERTS && block + step < blocks;
+            if (more)
+                next = Aim(a, e, n0 + step * Plan::kRows, 16 * wn + r, g);
+            f32x4_t acc[TB];                      // kDot: acc[0][t] of token t
 #pragma unroll
-        for (int t = 0; t < TB; t++)
-            acc[t] = f32x4_t{};
-        // chunk number `chunk`, chunk c of the stage, from u
-        auto work = [&](Share &u, int c, int chunk) {
-            if (chunk >= partial)
-                settle(u, chunk);
-            const uint4 *xs = reinterpret_cast<const uint4 *>(lds) + 32 * TT * c;
+            for (int t = 0; t < TB; t++)
+                acc[t] = f32x4_t{};
+            // chunk number `chunk`, chunk c of the stage
+            auto work = [&](Share &u, int c, int chunk) {
+                if (chunk >= partial)
+                    aim.settle(u, chunk, nb, g);
+                const uint4 *xs = reinterpret_cast<const uint4 *>(lds) + 32 * TT * c;
 #pragma unroll
-            for (int b = 0; b < 4; b++) {         // block b of the lane's 4: fragments 2b, 2b + 1
-                const float s = b == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 0)
-                                : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 1)
-                                : b == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 2)
-                                         : __builtin_amdgcn_cvt_f32_fp8((int)u.s, 3);
-                float sum[2] = {0.f, 0.f};
+                for (int b = 0; b < 4; b++) {     // block b of the lane's 4: fragments 2b, 2b + 1
+                    const float s = b == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 0)
+                                    : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 1)
+                                    : b == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 2)
+                                             : __builtin_amdgcn_cvt_f32_fp8((int)u.s, 3);
+                    float sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int f = 2 * b; f < 2 * b + 2; f++) {
-                    const uint4 q = u.q[f >> 2];
-                    const uint32_t d = (f & 3) == 0 ? q.x : (f & 3) == 1 ? q.y : (f & 3) == 2 ? q.z : q.w;
-                    if constexpr (Plan::kDot) {
-                        const bf16x2v_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
-                        const bf16x2v_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
-                        const bf16x2v_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2);
-                        const bf16x2v_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3);
+                    for (int f = 2 * b; f < 2 * b + 2; f++) {
+                        const uint4 v = u.q[f >> 2];
+                        const uint32_t d = (f & 3) == 0 ? v.x : (f & 3) == 1 ? v.y : (f & 3) == 2 ? v.z : v.w;
+                        if constexpr (Plan::kDot) {
+                            const bf16x2v_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
+                            const bf16x2v_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
+                            const bf16x2v_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2);
+                            const bf16x2v_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3);
 #pragma unroll
-                        for (int t = 0; t < TT; t++) {
-                            const uint4 x = xs[4 * f * TT + ((g * TT + t) ^ (f & kMix))];
-                            sum[t] = dot2(w0, x.x, sum[t]);
-                            sum[t] = dot2(w1, x.y, sum[t]);
-                            sum[t] = dot2(w2, x.z, sum[t]);
-                            sum[t] = dot2(w3, x.w, sum[t]);
-                        }
-                    } else {
-                        const bf16x8_t wf = weights8(d, s);
+                            for (int t = 0; t < TT; t++) {
+                                const uint4 x = xs[4 * f * TT + ((g * TT + t) ^ (f & kMix))];
+                                sum[t] = dot2(w0, x.x, sum[t]);
+                                sum[t] = dot2(w1, x.y, sum[t]);
+                                sum[t] = dot2(w2, x.z, sum[t]);
+                                sum[t] = dot2(w3, x.w, sum[t]);
+                            }
+                        } else {
+                            const bf16x8_t wf = weights8(d, s);
 #pragma unroll
-                        for (int t = 0; t < TB; t++) {
-                            // columns behind the last token are of any value and
-                            // not stored
-                            const bf16x8_t xf = __builtin_bit_cast(
-                                bf16x8_t, xs[4 * f * TT + ((g * TT + (r < TT ? r : 0)) ^ (f & kMix)) + 16 * t]);
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[t], 0, 0, 0);
+                            for (int t = 0; t < TB; t++) {
+                                // columns behind the last token are of any value
+                                // and not stored
+                                const bf16x8_t xf = __builtin_bit_cast(
+                                    bf16x8_t, xs[4 * f * TT + ((g * TT + (r < TT ? r : 0)) ^ (f & kMix)) + 16 * t]);
+                                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[t], 0, 0, 0);
+                            }
                         }
                     }
-                }
-                if constexpr (Plan::kDot) {
+                    if constexpr (Plan::kDot) {
 #pragma unroll
-                    for (int t = 0; t < TT; t++)
-                        acc[0][t] = __builtin_fmaf(sum[t], s, acc[0][t]);
+                        for (int t = 0; t < TT; t++)
+                            acc[0][t] = __builtin_fmaf(sum[t], s, acc[0][t]);
+                        if (TT == 2)
+                            __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            };
+            for (int st = 0; st < stages; st++) {
+                // tokens that fit one stage stay for all blocks
+                if (stages > 1 || block == (int)blockIdx.x) {
+                    __syncthreads();
+                    store_tokens(st);
+                    __syncthreads();
+                    if (stages > 1 && (st + 1 < stages || more))
+                        load_tokens(st + 1 < stages ? st + 1 : 0);
+                }
+#pragma unroll
+                for (int j = 0; j < D; j++) {
+                    const int c = st * Plan::kFit + ks + j * KS;
+                    if (c < nchunk)
+                        work(w[j], ks + j * KS, c);
+                    if (Plan::kDot)
+                        __builtin_amdgcn_sched_barrier(0);   // one chunk's fragments at a time
+                    // the next stage's chunk, or the next block's
+                    if (c + Plan::kFit < nchunk)
+                        aim.fetch(w[j], c + Plan::kFit);
+                    else if (more && ks + j * KS < nchunk)
+                        next.fetch(w[j], ks + j * KS);
                 }
             }
-        };
-        const int stages = (nchunk + Plan::kFit - 1) / Plan::kFit;
-        for (int st = 0; st < stages; st++) {
-            __syncthreads();
-            store_tokens(st);
-            __syncthreads();
-            if (st + 1 < stages)
-                load_tokens(st + 1);
-#pragma unroll
-            for (int j = 0; j < D; j++) {
-                const int c = st * Plan::kFit + ks + j * KS;
-                if (c < nchunk)
-                    work(w[j], ks + j * KS, c);
-                if (c + Plan::kFit < nchunk)
-                    fetch(w[j], c + Plan::kFit);
-            }
-        }
 
-        const float sg = a.sg[e];
-        if constexpr (Plan::kDot) {
-            // lane (r, g): row r's sums over its k; over g, then over KS
+            if constexpr (Plan::kDot) {
+                // lane (r, g): row r's sums over its k; over g, then over KS
 #pragma unroll
-            for (int t = 0; t < TT; t++) {
-                acc[0][t] += __shfl_xor(acc[0][t], 16);
-                acc[0][t] += __shfl_xor(acc[0][t], 32);
+                for (int t = 0; t < TT; t++) {
+                    acc[0][t] += __shfl_xor(acc[0][t], 16);
+                    acc[0][t] += __shfl_xor(acc[0][t], 32);
+                }
+                float *part = reinterpret_cast<float *>(lds + Plan::kTokens);
+                __syncthreads();
+                if (g < TT)
+                    part[(wave * TT + g) * 16 + r] = g ? acc[0][1] : acc[0][0];
+                __syncthreads();
+                const int v = tid / (16 * TT), t = tid / 16 % TT, n = 16 * v + tid % 16;
+                if (v < Plan::WN && t < count && n0 + n < a.N) {
+                    float sum = part[(v * KS * TT + t) * 16 + tid % 16];
+#pragma unroll
+                    for (int k = 1; k < KS; k++)
+                        sum += part[((v * KS + k) * TT + t) * 16 + tid % 16];
+                    store_mv(a, (int64_t)(EXPERTS ? slot[t] : from + t) * a.N + n0 + n, sum * sg);
+                }
             }
-            __syncthreads();
-            float *part = reinterpret_cast<float *>(lds);
-            if (g < TT)
-                part[(wave * TT + g) * 16 + r] = g ? acc[0][1] : acc[0][0];
-            __syncthreads();
-            const int v = tid / (16 * TT), t = tid / 16 % TT, n = 16 * v + tid % 16;
-            if (v < Plan::WN && t < count && n0 + n < a.N) {
-                float sum = part[(v * KS * TT + t) * 16 + tid % 16];
+            // the KS partial sums, token tile by token tile; lane (r, g), register
+            // j of a tile: weight row 4 g + j, token r
 #pragma unroll
-                for (int k = 1; k < KS; k++)
-                    sum += part[((v * KS + k) * TT + t) * 16 + tid % 16];
-                store_mv(a, (EXPERTS ? slot[t] : from + t) * a.N + n0 + n, sum * sg);
-            }
-        }
-        // the KS partial sums, token tile by token tile; lane (r, g), register
-        // j of a tile: weight row 4 g + j, token r
+            for (int t = 0; t < (Plan::kDot ? 0 : TB); t++) {
+                f32x4_t *part = reinterpret_cast<f32x4_t *>(lds + Plan::kTokens);
+                __syncthreads();
+                part[tid] = acc[t];
+                __syncthreads();
+                if (tid < Plan::WN * 64) {
+                    const int v = tid >> 6;
+                    f32x4_t sum = part[v * KS * 64 + L];
 #pragma unroll
-        for (int t = 0; t < (Plan::kDot ? 0 : TB); t++) {
-            __syncthreads();
-            f32x4_t *part = reinterpret_cast<f32x4_t *>(lds);
-            part[tid] = acc[t];
-            __syncthreads();
-            if (tid < Plan::WN * 64) {
-                const int v = tid >> 6;
-                f32x4_t sum = part[v * KS * 64 + L];
-#pragma unroll
-                for (int k = 1; k < KS; k++)
-                    sum += part[(v * KS + k) * 64 + L];
-                const int tok = 16 * t + r;
-                const int64_t n = n0 + 16 * v + 4 * g;
-                if (tok < count && n < a.N) {
-                    const int64_t o = (EXPERTS ? slot[tok] : from + tok) * a.N + n;
-                    sum *= sg;
-                    if ((a.N & 3) == 0) {
-                        if (a.out_f32)
-                            *reinterpret_cast<f32x4_t *>(static_cast<float *>(a.y) + o) = sum;
-                        else
-                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + o) =
-                                make_uint2(bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3]));
-                    } else {
-                        for (int j = 0; j < 4 && n + j < a.N; j++)
-                            store_mv(a, o + j, sum[j]);
+                    for (int k = 1; k < KS; k++)
+                        sum += part[(v * KS + k) * 64 + L];
+                    const int tok = 16 * t + r;
+                    const int n = n0 + 16 * v + 4 * g;
+                    if (tok < count && n < a.N) {
+                        const int64_t o = (int64_t)(EXPERTS ? slot[tok] : from + tok) * a.N + n;
+                        sum *= sg;
+                        if ((a.N & 3) == 0) {
+                            if (a.out_f32)
+                                *reinterpret_cast<f32x4_t *>(static_cast<float *>(a.y) + o) = sum;
+                            else
+                                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + o) =
+                                    make_uint2(bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3]));
+                        } else {
+                            for (int j = 0; j < 4 && n + j < a.N; j++)
+                                store_mv(a, o + j, sum[j]);
+                        }
                     }
                 }
             }
@@ -433,7 +472,7 @@ __global__ __launch_bounds__(kMvThreads, MvPlan<TT>::kOccupancy) void mv_kernel(
         if (EXPERTS)
             from = slot[count - 1] + 1;
         else
-            from += (int64_t)gridDim.y * TT;
+            from += (int)gridDim.y * TT;
         __syncthreads();
     }
 }
@@ -449,7 +488,7 @@ __global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
             const int e = a.experts ? a.experts[p] : 0;
             float sum = 0.f;
             if (e >= 0 && e < a.G) {
-                const int64_t row = e * a.N + n;
+                const int64_t row = (int64_t)e * a.N + n;
                 for (int64_t k = 0; k < a.K; k++) {
                     const uint32_t code = a.qw[row * pitch + (k >> 1)] >> (4 * (k & 1));
                     const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.sw[row * nb + (k >> 4)], 0);
@@ -462,46 +501,54 @@ __global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
         }
 }
 
-template <int TT>
-hipError_t launch(MvArgs a, hipStream_t stream)
+template <int TT, bool EXPERTS>
+hipError_t launch_one(MvArgs a, hipStream_t stream)
 {
-    using Plan = MvPlan<TT>;
-    const unsigned nx = (unsigned)((a.N + Plan::kRows - 1) / Plan::kRows);
-    const int64_t slots = a.T * a.top;
-    const int lds = Plan::kLds;
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(
-            a.experts ? reinterpret_cast<const void *>(mv_kernel<TT, true>)
-                      : reinterpret_cast<const void *>(mv_kernel<TT, false>),
-            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    using Plan = MvPlan<TT, EXPERTS>;
+    const int64_t slots = (int64_t)a.T * a.top, blocks = (a.N + Plan::kRows - 1) / Plan::kRows;
+    if (Plan::kLds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(mv_kernel<TT, EXPERTS>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, Plan::kLds);
         if (e != hipSuccess)
             return e;
     }
-    if (a.experts) {
-        // few slots: by slot, so that no workgroup is started for an expert
-        // that nobody picked
-        a.by_slot = slots <= a.G;
-        hipLaunchKernelGGL((mv_kernel<TT, true>), dim3(nx, (unsigned)(a.by_slot ? slots : a.G + 1)),
-                           dim3(kMvThreads), lds, stream, a);
-    } else {
-        const int64_t tiles = (a.T + TT - 1) / TT;
-        hipLaunchKernelGGL((mv_kernel<TT, false>), dim3(nx, (unsigned)(tiles < 4096 ? tiles : 4096)),
-                           dim3(kMvThreads), lds, stream, a);
+    // Few slots: by slot, so that no workgroup is started for an expert that
+    // nobody picked.
+    a.by_slot = EXPERTS && slots <= a.G;
+    const int64_t tiles = (a.T + TT - 1) / TT;
+    const int64_t ny = !EXPERTS ? (tiles < 4096 ? tiles : 4096) : a.by_slot ? slots : a.G + 1;
+    // Experts' tokens whose k fits one stage are staged once for all of a
+    // workgroup's blocks: then as many workgroups as fit the CUs (two each), so
+    // that weights are always under way.  Otherwise a workgroup per block.
+    int64_t nx = blocks;
+    if (EXPERTS && a.K <= Plan::kFit * kChunk) {
+        const int64_t fill = 2 * 256 / ny > 1 ? 2 * 256 / ny : 1;
+        const int64_t each = (blocks + fill - 1) / fill;
+        nx = (blocks + each - 1) / each;
     }
+    hipLaunchKernelGGL((mv_kernel<TT, EXPERTS>), dim3((unsigned)nx, (unsigned)ny), dim3(kMvThreads),
+                       Plan::kLds, stream, a);
     return hipGetLastError();
+}
+
+template <int TT>
+hipError_t launch(const MvArgs &a, hipStream_t stream)
+{
+    return a.experts ? launch_one<TT, true>(a, stream) : launch_one<TT, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
 {
-    if (a.G * a.N * ((a.K + 1) / 2) < 16 || a.G * a.N * ((a.K + 15) / 16) < 4 || a.T * a.K < 8) {
-        const int64_t n = (a.T * a.top + 63) / 64;
+    const int64_t rows = (int64_t)a.G * a.N;
+    if (rows * ((a.K + 1) / 2) < 16 || rows * ((a.K + 15) / 16) < 4 || (int64_t)a.T * a.K < 8) {
+        const int64_t n = ((int64_t)a.T * a.top + 63) / 64;
         hipLaunchKernelGGL(mv_tiny_kernel, dim3((unsigned)(n < 4096 ? n : 4096)), dim3(64), 0, stream, a);
         return hipGetLastError();
     }
     // tokens that a weight matrix meets: all, or an expert's fair share twice over
-    const int64_t slots = a.T * a.top;
+    const int64_t slots = (int64_t)a.T * a.top;
     const int64_t tokens = a.experts ? (2 * slots + a.G - 1) / a.G : a.T;
     const int64_t most = slots < tokens ? slots : tokens;
     return most <= 1    ? launch<1>(a, stream)
