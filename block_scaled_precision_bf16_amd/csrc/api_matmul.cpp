@@ -13,7 +13,9 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 23;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-constexpr int64_t kMaxTiles = int64_t(1) << 30;    // workgroups of one launch
+// Workgroups of one launch (256 threads each, 2^32 threads in all, and a last
+// round in parts).
+constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 4096;
 
 constexpr unsigned kMmBits =
     MX_A_E5M2 | MX_B_E5M2 | MX_SCALE_TILED | MX_OUT_F32 | MX_OUT_ACCUMULATE;
@@ -117,7 +119,7 @@ struct MmPlan {
 bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
 {
     const int G = t.count;
-    int64_t most_m = 0, most_k = 0, big = 0, small_bytes = 0, pitches = 0;
+    int64_t most_m = 0, most_k = 0, big = 0, small = 0, small_bytes = 0, pitches = 0;
     bool rows16 = true;
     for (int g = 0; g < G; g++) {
         const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
@@ -131,7 +133,9 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
     const int small_m = most_m <= 32 ? 32 : 64;
     for (int g = 0; g < G; g++) {
         const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
-        small_bytes += ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN) * (small_m + mxk::kMmSmallN) * k;
+        const int64_t n = ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN);
+        small += n;
+        small_bytes += n * (small_m + mxk::kMmSmallN) * k;
     }
     p = MmPlan{};
     // The small kernel reads each output tile's operands for itself, at about
@@ -143,7 +147,7 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
     const double tile_us = rounds * (double)ceil_div(most_k, 128) + (rows16 ? 0.0 : 5.0);
     if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8)
         p = MmPlan{kAny, mxk::kMmAnyTile, mxk::kMmAnyTile, false, 0, 0};
-    else if ((double)small_bytes / 8e6 < tile_us)
+    else if ((double)small_bytes / 8e6 < tile_us && small <= kMaxTiles)
         p = MmPlan{kSmall, small_m, mxk::kMmSmallN, false, 0, 0};
     else
         p = MmPlan{kTiles, mxk::kMmTileM, mxk::kMmTileN, !rows16, 0, 0};
