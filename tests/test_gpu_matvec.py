@@ -16,7 +16,7 @@ import torch
 
 import block_scaled_precision_bf16_amd as mx
 import workloads as W
-from product_util import E4M3, Guarded, assert_close, assert_equal, nv_values, product, to_dev
+from product_util import E2M1, E4M3, Guarded, assert_close, assert_equal, nv_values, product, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +245,43 @@ def test_captured_on_another_stream_and_repeats():
     other = mx.nvfp4_matvec_experts(x, e, q, s, sg, stream=st)
     st.synchronize()
     assert torch.equal(other, step()[0])
+
+
+@pytest.mark.parametrize("T,N,K,G", [
+    (1, 65600, 131088, 0), (20, 65600, 131088, 0),       # codes past 2^32 bytes
+    (32800, 32800, 32, 0), (70001, 64, 32784, 0),        # the output, the tokens
+    (3, 16400, 8208, 66), (100, 16400, 8208, 66)])       # the last experts' codes
+def test_past_32_bits(T, N, K, G):
+    """Exact operands made on the GPU: tokens n in {-4 .. 4}, scales 1/2, 1 and 2,
+    so products are multiples of 1/4 and no sum here passes 2^24 of them."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rows = max(G, 1) * N
+
+    def bytes_(r, c, lo=0, hi=256):
+        return torch.randint(lo, hi, (r, c), dtype=torch.uint8, device="cuda", generator=gen)
+
+    qw, sw, x = bytes_(rows, K // 2), 0x30 + 8 * bytes_(rows, K // 16, 0, 3), torch.empty(
+        T, K, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, 8192):
+        x[i:i + 8192] = bytes_(min(8192, T - i), K, 0, 9) - 4.0
+    e2m1 = torch.from_numpy(E2M1).cuda()
+
+    def weights(r):
+        q = qw[r].int()
+        v = e2m1[torch.stack([q & 15, q >> 4], dim=-1).view(len(r), K)]
+        return v * torch.exp2((sw[r].double() - 0x38) / 8).repeat_interleave(16, 1)
+
+    cpu = torch.Generator().manual_seed(6)
+    n = torch.cat([torch.tensor([0, N - 1]), torch.randint(0, N, (20,), generator=cpu)]).cuda()
+    t = torch.cat([torch.tensor([0, T - 1]), torch.randint(0, T, (6,), generator=cpu)]).cuda()
+    sg = torch.ones(max(G, 1), device="cuda")
+    if not G:
+        y = mx.nvfp4_matvec(x, qw, sw, sg, flags=mx.OUT_F32)
+        assert torch.equal(y[t][:, n].double(), x[t].double() @ weights(n).t())
+        return
+    e = torch.randint(G - 3, G, (T, 2), dtype=torch.int32, device="cuda", generator=gen)
+    y = mx.nvfp4_matvec_experts(x, e, qw, sw, sg, flags=mx.OUT_F32)
+    for i in t.tolist():
+        for j in range(2):
+            w = weights(int(e[i, j]) * N + n)
+            assert torch.equal(y[i, j, n].double(), w @ x[i].double())
