@@ -115,6 +115,15 @@ struct MmPlan {
     int64_t pack_a, pack_b;    // bytes of the copies
 };
 
+// In how many parts each of the last of n tiles, too few to fill the CUs, goes:
+// 128 x 128 or 256 x 128, if those fill them once at most (2048 x 4096 outputs with
+// 4096 k: 53 us in two rounds of 128 x 128, 51 us whole, 40 us in halves).
+int last_parts(int64_t n)
+{
+    const int64_t last = n % mxk::kMmCUs;
+    return last == 0 ? 1 : 4 * last <= mxk::kMmCUs ? 4 : 2 * last <= mxk::kMmCUs ? 2 : 1;
+}
+
 // The kernel for a launch and, in t, its tiles.  False if there are too many.
 bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
 {
@@ -138,19 +147,35 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
         small_bytes += n * (small_m + mxk::kMmSmallN) * k;
     }
     p = MmPlan{};
-    // The small kernel reads each output tile's operands for itself, at about
-    // 8 TB/s from the caches; the tiled one takes about 1 us for 128 k of a
-    // round of tiles (half of that in parts).  Both start in about the same time.
-    const int64_t parts = (int64_t)(mxk::kMmTileM / mxk::kMmPart) * (mxk::kMmTileN / mxk::kMmPart);
-    const double rounds = (double)(big / mxk::kMmCUs) +
-                          0.5 * (double)ceil_div(big % mxk::kMmCUs * parts, mxk::kMmCUs);
-    const double tile_us = rounds * (double)ceil_div(most_k, 128) + (rows16 ? 0.0 : 5.0);
-    if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8)
-        p = MmPlan{kAny, mxk::kMmAnyTile, mxk::kMmAnyTile, false, 0, 0};
-    else if ((double)small_bytes / 8e6 < tile_us && small <= kMaxTiles)
-        p = MmPlan{kSmall, small_m, mxk::kMmSmallN, false, 0, 0};
-    else
-        p = MmPlan{kTiles, mxk::kMmTileM, mxk::kMmTileN, !rows16, 0, 0};
+    // Microseconds, as measured (graph replays).  The small kernel: its waves' share
+    // of k, one after the other, and the operands, which each output tile reads for
+    // itself at 8.3 TB/s.  The tiled one: rounds of tiles and the last, partial one;
+    // twice the time for fp32 outputs; the copy of unaligned rows.
+    const double lat = (double)ceil_div(most_k, 128) * (small_m == 32 ? 0.25 : 0.4);
+    const double read = (double)small_bytes / 8.3e6;
+    const double small_us = 3 + (lat + read / 2 > read ? lat + read / 2 : read);
+    const int parts = last_parts(big);
+    const double steps = (double)ceil_div(most_k, 128), slow = a.out_f32 ? 2 : 1;
+    double tile_us = 4 + (double)(big / mxk::kMmCUs) * (6 + 1.5 * slow * steps);
+    if (big % mxk::kMmCUs != 0)
+        tile_us += parts == 4   ? (a.out_f32 ? 0.85 : 0.55) * steps
+                   : parts == 2 ? 2 + 0.95 * slow * steps
+                                : 6 + 1.5 * slow * steps;
+    if (!rows16)
+        tile_us += 3 + (double)(n.qa + n.qb) / 2e6;
+    if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8) {
+        p.kind = kAny;
+        p.tile_m = p.tile_n = mxk::kMmAnyTile;
+    } else if (small_us < tile_us && small <= kMaxTiles) {
+        p.kind = kSmall;
+        p.tile_m = small_m;
+        p.tile_n = mxk::kMmSmallN;
+    } else {
+        p.kind = kTiles;
+        p.tile_m = mxk::kMmTileM;
+        p.tile_n = mxk::kMmTileN;
+        p.pack = !rows16;
+    }
     if (p.pack) {
         const int64_t rows_a = a.sum_rows ? 0 : (int64_t)n.qa / a.dim, pitch = mxk::mm_pitch(a.dim);
         p.pack_a = a.sum_rows ? pitches * a.dim : rows_a * pitch;
@@ -164,11 +189,8 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
             return false;
     }
     t.tile0[G] = (int32_t)tiles;
-    // Tiles that do not fill the CUs once more go in parts of 128 x 128, if those
-    // take at most three rounds.
-    t.whole = (int32_t)tiles;
-    if (p.kind == kTiles && tiles % mxk::kMmCUs * parts <= mxk::kMmCUs * 3)
-        t.whole -= t.whole % mxk::kMmCUs;
+    t.parts = p.kind == kTiles ? parts : 1;
+    t.whole = (int32_t)(t.parts == 1 ? tiles : tiles - tiles % mxk::kMmCUs);
     return true;
 }
 
@@ -226,10 +248,10 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
     const mx_status st = mm_setup(dim, N, rows, G, sum_rows, flags, a, t, n, p);
     if (st != MX_OK)
         return st;
+    const uint64_t nw = (uint64_t)(p.pack_a + p.pack_b);
     if (!aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
-        !aligned(y, 16) || (p.pack && !aligned(workspace, 16)))
+        !aligned(y, 16) || (nw && !aligned(workspace, 16)))
         return MX_ERR_ALIGN;
-    const uint64_t nw = p.pack ? (uint64_t)(p.pack_a + p.pack_b) : 0;
     if (nw && (!workspace || workspace_bytes < nw))
         return MX_ERR_WORKSPACE;
     const void *in[4] = {qa, sa, qb, sb};

@@ -20,6 +20,7 @@ constexpr int kMmMaxGroups = 64;
 struct MmTable {
     int32_t count;                      // the groups, in the order of their tiles
     int32_t whole;                      // tiles not taken in parts
+    int32_t parts;                      // of each of the others
     int32_t tile0[kMmMaxGroups + 1];    // first workgroup tile of each
     int32_t rows[kMmMaxGroups];
     int32_t index[kMmMaxGroups];        // its place in the caller's order
@@ -50,7 +51,8 @@ __host__ __device__
 #endif
 constexpr int64_t mm_pitch(int64_t K) { return (K + 127) / 128 * 128; }
 
-// The tiled kernel: its tiles, and the parts in which the last ones go.
+// The tiled kernel: its tiles, and the sides of the parts (128 x 128 or 256 x 128) in
+// which the last ones go.
 constexpr int kMmTileM = 256, kMmTileN = 256, kMmPart = 128;
 constexpr int kMmCUs = 256;
 // The any-shape kernel's tile, and the columns of the small kernel's (32 or 64

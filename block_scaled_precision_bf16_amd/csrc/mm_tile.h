@@ -4,12 +4,12 @@
 // gfx950's block-scaled MFMA (32 x 32 x 64) takes the codes and scale bytes as
 // the casts wrote them.  A workgroup of 4 waves (2 x 2) owns TM x TN outputs.
 // The codes come into LDS 128 k at a time by loads that write LDS directly (no
-// registers), two buffers in turn; fragments are double buffered in registers,
+// registers), into NB buffers in turn; fragments are double buffered in registers,
 // so that a step's MFMAs run while the next step's fragments are read:
 //
 //   step 0 of tile t:  MFMAs on F0, reads of F1 (step 1 of tile t)
 //   wait for the loads of tile t + 1 and the reads of F1; barrier: every wave is
-//   done with tile t's buffer, and tile t + 1 is there; load tile t + 2
+//   done with tile t's buffer, and tile t + 1 is there; load tile t + NB
 //   step 1 of tile t:  MFMAs on F1, reads of F0 (step 0 of tile t + 1)
 //
 // LDS holds rows of 128 bytes; 16-byte chunk c of a row sits in slot c ^ s(row),
@@ -20,17 +20,28 @@
 // B's rows are dealt to the lanes in pairs: of two neighbouring 32-column
 // tiles, lane r holds columns 2r (first tile) and 2r + 1 (second), so that the
 // outputs leave as whole 128-byte lines from registers.
+//
+// Measured: 8192^3 to bf16 in 420 us, 2.6 PFLOP/s (a library's fp8 product without
+// block scales reaches 2.96 on this card); the matrix cores are busy 74% of the
+// time at the clock the power limit leaves them (1.7 - 2.0 GHz), and LDS moves
+// 1536 of a tile's 2048 cycles.  To fp32 (twice the MFMA time) 800 us.  A round
+// of 256 tiles takes 6 us + 1.5 us for 128 k, a last round of 128 x 128 parts,
+// which LDS bounds (768 cycles of reads and writes to 512 of MFMA), 0.55 us for
+// 128 k, one of 256 x 128 parts 1.0 us: 64 tiles of 8192 k take 40 us in parts and
+// 92 us whole.  Two buffers instead of four there: 50 us.
 #pragma once
 
 #include "mm_common.h"
 
 namespace mxk {
 
-// Waits until at most the given counts are outstanding, with no motion of
-// memory operations across.
-__device__ __forceinline__ void wait_all_and_barrier()
+// Waits until at most N loads (and no LDS reads) are outstanding and for the other
+// waves, with no motion of memory operations across.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    static_assert(N < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
 }
 
 typedef unsigned int mm_rsrc_t __attribute__((ext_vector_type(4)));
@@ -48,14 +59,27 @@ __device__ __forceinline__ void load_to_lds(mm_rsrc_t rsrc, uint32_t voff, uint3
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff));
 }
 
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load_words_to_lds(mm_rsrc_t rsrc, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc));
+}
+
+// `bytes` bytes at p.
+__device__ __forceinline__ mm_rsrc_t bytes_rsrc(const uint8_t *p, uint32_t bytes)
+{
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return mm_rsrc_t{(uint32_t)u, (uint32_t)(u >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+
 // Rows of `pitch` bytes at p, of which `rows` exist: a load's voff is a place in
 // them, its soff a step along k that stays inside the row, so whether or not the
 // bound is compared with soff too, rows behind the last one load zeros.
 __device__ __forceinline__ mm_rsrc_t rows_rsrc(const uint8_t *p, int64_t rows, int64_t pitch)
 {
-    const uint64_t u = reinterpret_cast<uint64_t>(p);
-    return mm_rsrc_t{(uint32_t)u, (uint32_t)(u >> 32) & 0xFFFFu,
-                     (uint32_t)(rows < 256 ? rows : 256) * (uint32_t)pitch, 0x00020000u};
+    return bytes_rsrc(p, (uint32_t)(rows < 256 ? rows : 256) * (uint32_t)pitch);
 }
 constexpr uint32_t kDeadRow = 0xFFFFFFF0u;   // behind every bound: loads zeros
 
@@ -64,6 +88,23 @@ struct MmKernel {
     static constexpr int MT = TM / 64, NT = TN / 64;      // 32-row tiles of a wave
     static constexpr int kBuf = (TM + TN) * 128;          // bytes of an LDS buffer
     static constexpr int kLoads = (TM + TN) / 32;         // loads of a wave per tile
+    // LDS buffers: smaller tiles take less time, and have more of them under way.
+    // (Compact scales come through registers, which the compiler waits for with
+    // all loads: two buffers.)
+    static constexpr int NB = !TILED ? 2 : TM == 128 ? 4 : TN == 128 ? 3 : 2;
+    // Scales of 8 blocks and all rows; of the tiled ones, (NB + 1) / 2 buffers and
+    // a wave's share of the loads, which go with those of the first of two tiles.
+    static constexpr int kScales = (TM + TN) * 8;
+    static constexpr int kScaleLoads = TILED ? (TM + TN) / 128 : 0;
+    static constexpr int kLds = NB * kBuf + (TILED ? (NB + 1) / 2 : 2) * kScales;
+    // Loads of the tiles from..to (relative to an even one).
+    static constexpr int loads(int from, int to)
+    {
+        int n = 0;
+        for (int u = from; u <= to; u++)
+            n += kLoads + (u % 2 == 0 ? kScaleLoads : 0);
+        return n;
+    }
     static_assert(NT % 2 == 0, "column tiles come in pairs");
 
     struct Frags {
@@ -82,12 +123,11 @@ struct MmKernel {
     uint32_t last_a, last_b;       // the operands' last rows in the tile
     int nt, phase;                 // tiles of k, the first one
     uint32_t sel;                  // compact: how a word comes out of 8 scale bytes
-    // Scales.  Tiled: a lane loads its words of 4 steps (2 tiles) as they lie.
-    // Compact: a thread loads the 8 bytes of one row of A and of one of B and puts
-    // them into LDS (two buffers), from where the lanes take their words.
-    uint32_t off_a[TILED ? MT : 1], off_b[TILED ? NT : 1];
+    // Scales, for 4 steps (2 tiles) at a time, in LDS.  Tiled: direct loads of the
+    // words as they lie.  Compact: a thread loads the 8 bytes of one row of A and of
+    // one of B and puts them there, from where the lanes make their words.
+    uint32_t off_a, off_b, raw_a[2], raw_b[2];     // compact
     static constexpr int W = MODE == kMx ? 1 : 2;
-    uint32_t raw_a[TILED ? MT : 1][TILED ? W : 2], raw_b[TILED ? NT : 1][TILED ? W : 2];
     // kMx: the words of the lane's blocks (byte j: step j of the next four);
     // kExact: those of even blocks and of odd ones
     uint32_t sa[MT][W], sb[NT][W];
@@ -103,14 +143,42 @@ struct MmKernel {
     {
         return t >= nt ? t : t + phase < nt ? t + phase : t + phase - nt;
     }
+    // Where in LDS the tile in place t goes.
+    __device__ __forceinline__ uint32_t buf(int t) const { return (uint32_t)t % NB * kBuf; }
+    // Tiled: where the scales of the tiles in places t (even) and t + 1 go.
+    __device__ __forceinline__ uint32_t scale_buf(int t) const
+    {
+        return NB * kBuf + (uint32_t)(t >> 1) % ((NB + 1) / 2) * kScales;
+    }
     // Load i of the wave for the tile in place t (zeros behind the last).
     __device__ __forceinline__ void issue(int t, int i) const
     {
-        const uint32_t k0 = 128u * (uint32_t)turned(t), dst = lds0 + (uint32_t)(t & 1) * kBuf;
+        const uint32_t k0 = 128u * (uint32_t)turned(t), dst = lds0 + buf(t);
         // 16-byte chunks behind the rows' ends are zeros
         const uint32_t left = k0 < w.K ? (uint32_t)(w.K - k0) : 0;
         const uint32_t v = 16 * chunk(i) < left ? offset(i) : kDeadRow;
         load_to_lds(is_a(i) ? ra : rb, v, k0, dst + (uint32_t)row8(i) * 128);
+    }
+    // The wave's loads of the scales for the tiles in places t and t + 1: of each
+    // operand's 32-row tiles, one load each.
+    __device__ __forceinline__ void issue_scales(int t) const
+    {
+        const int bt = turned(t) >> 1;
+        const bool live = t < nt;
+        const int64_t ta = (w.M + 31) >> 5, tb = (a.N + 31) >> 5;
+        const mm_rsrc_t qa = bytes_rsrc(w.sa + (live ? bt * ta + (w.m0 >> 5) : 0) * 256, live ? last_a / 32 * 256 + 256 : 0);
+        const mm_rsrc_t qb = bytes_rsrc(w.sb + (live ? bt * tb + (w.n0 >> 5) : 0) * 256, live ? last_b / 32 * 256 + 256 : 0);
+        const uint32_t dst = lds0 + scale_buf(t);
+#pragma unroll
+        for (int i = 0; i < TM / 128; i++) {
+            const uint32_t x = 256 * (uint32_t)(wave * (TM / 128) + i);
+            load_words_to_lds(qa, x + 4 * (uint32_t)L, dst + x);
+        }
+#pragma unroll
+        for (int i = 0; i < TN / 128; i++) {
+            const uint32_t x = 256 * (uint32_t)(wave * (TN / 128) + i);
+            load_words_to_lds(qb, x + 4 * (uint32_t)L, dst + TM * 8 + x);
+        }
     }
     // The loads that go with MFMA k of n.
     __device__ __forceinline__ void issue_share(int t, int k, int n) const
@@ -143,12 +211,12 @@ struct MmKernel {
 
     __device__ __forceinline__ i32x8_t frag_a(int t, int s, int i) const
     {
-        const uint4 *p = reinterpret_cast<const uint4 *>(lds + (t & 1) * kBuf) + (wm + 32 * i + r) * 8;
+        const uint4 *p = reinterpret_cast<const uint4 *>(lds + buf(t)) + (wm + 32 * i + r) * 8;
         return join(p[(4 * s + h) ^ (r & 7)], p[(4 * s + 2 + h) ^ (r & 7)]);
     }
     __device__ __forceinline__ i32x8_t frag_b(int t, int s, int j) const
     {
-        const uint4 *p = reinterpret_cast<const uint4 *>(lds + (t & 1) * kBuf) + (TM + brow(j)) * 8;
+        const uint4 *p = reinterpret_cast<const uint4 *>(lds + buf(t)) + (TM + brow(j)) * 8;
         return join(p[(4 * s + h) ^ (r & 7)], p[(4 * s + 2 + h) ^ (r & 7)]);
     }
     // One of a step's MT + NT fragments.
@@ -160,64 +228,61 @@ struct MmKernel {
             f.a[i - NT] = frag_a(t, s, i - NT);
     }
 
-    // Offset of the scales of the tile's row d of an operand (rows behind the last
-    // one: the last one's).
+    // Tiled: the words of the tiles in places t (even) and t + 1.
+    struct Words {
+        uint32_t a[MT][W], b[NT][W];
+    };
+    __device__ __forceinline__ void read_words(Words &o, int t) const
+    {
+        const uint8_t *p = lds + scale_buf(t);
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+            const int at = 128 * (MODE == kMx ? h : k);
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                o.b[j][k] = *reinterpret_cast<const uint32_t *>(p + TM * 8 + (brow(j) >> 5) * 256 + 4 * (brow(j) & 31) + at);
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+                o.a[i][k] = *reinterpret_cast<const uint32_t *>(p + ((wm >> 5) + i) * 256 + 4 * r + at);
+        }
+    }
+    __device__ __forceinline__ void take_words(const Words &o)
+    {
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+                sa[i][k] = o.a[i][k];
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                sb[j][k] = o.b[j][k];
+        }
+    }
+
+    // Compact: offset of the scales of the tile's row d of an operand (rows behind
+    // the last one: the last one's).
     __device__ __forceinline__ uint32_t scale_offset(uint32_t last, int d) const
     {
-        d = d < (int)last ? d : (int)last;
-        if (TILED)
-            return (uint32_t)((d >> 5) * 256 + 4 * (d & 31)) + (MODE == kMx ? 128 * h : 0);
-        return (uint32_t)(d * (int)w.nb);
+        return (uint32_t)((d < (int)last ? d : (int)last) * (int)w.nb);
     }
-    // Loads the scales of 8 blocks, those of the two tiles in places 2 place and on
-    // (for a place behind the last: some).
+    // Compact: loads the scales of 8 blocks, those of the two tiles in places
+    // 2 place and on (for a place behind the last: some).
     __device__ __forceinline__ void fetch_scales(int place)
     {
         const int bt = turned(2 * place) >> 1;
-        if constexpr (TILED) {
-            const uint8_t *pa = w.sa + (bt * ((w.M + 31) >> 5) + (w.m0 >> 5)) * 256;
-            const uint8_t *pb = w.sb + (bt * ((a.N + 31) >> 5) + (w.n0 >> 5)) * 256;
-#pragma unroll
-            for (int k = 0; k < W; k++) {
-#pragma unroll
-                for (int i = 0; i < MT; i++)
-                    raw_a[i][k] = *reinterpret_cast<const uint32_t *>(pa + off_a[i] + 128 * k);
-#pragma unroll
-                for (int j = 0; j < NT; j++)
-                    raw_b[j][k] = *reinterpret_cast<const uint32_t *>(pb + off_b[j] + 128 * k);
-            }
-        } else {
-            const int64_t at = 8 * bt < w.nb ? 8 * bt : 0;
-            const uint2 x = sra.load<uint2>(off_a[0], at), y = srb.load<uint2>(off_b[0], at);
-            raw_a[0][0] = x.x, raw_a[0][1] = x.y;
-            raw_b[0][0] = y.x, raw_b[0][1] = y.y;
-        }
+        const int64_t at = 8 * bt < w.nb ? 8 * bt : 0;
+        const uint2 x = sra.load<uint2>(off_a, at), y = srb.load<uint2>(off_b, at);
+        raw_a[0] = x.x, raw_a[1] = x.y;
+        raw_b[0] = y.x, raw_b[1] = y.y;
     }
     // Says that the fetched scales are here (they are: after a wait for every
     // load), before more loads are under way that the compiler would wait for.
     __device__ __forceinline__ void settle_scales()
     {
 #pragma unroll
-        for (int k = 0; k < (TILED ? W : 2); k++) {
-#pragma unroll
-            for (int i = 0; i < (TILED ? MT : 1); i++)
-                asm volatile("" : "+v"(raw_a[i][k]));
-#pragma unroll
-            for (int j = 0; j < (TILED ? NT : 1); j++)
-                asm volatile("" : "+v"(raw_b[j][k]));
-        }
-    }
-    // Tiled: puts the fetched words in use.
-    __device__ __forceinline__ void take_scales()
-    {
-#pragma unroll
-        for (int k = 0; k < W; k++) {
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-                sa[i][k] = raw_a[TILED ? i : 0][k];
-#pragma unroll
-            for (int j = 0; j < NT; j++)
-                sb[j][k] = raw_b[TILED ? j : 0][k];
+        for (int k = 0; k < 2; k++) {
+            asm volatile("" : "+v"(raw_a[k]));
+            asm volatile("" : "+v"(raw_b[k]));
         }
     }
     // Compact: the scales fetched for `place` into LDS buffer place % 2; those
@@ -225,13 +290,13 @@ struct MmKernel {
     __device__ __forceinline__ void write_scales(int place)
     {
         const int bt = turned(2 * place) >> 1;
-        uint2 x = make_uint2(raw_a[0][0], raw_a[0][1]), y = make_uint2(raw_b[0][0], raw_b[0][1]);
+        uint2 x = make_uint2(raw_a[0], raw_a[1]), y = make_uint2(raw_b[0], raw_b[1]);
         const int64_t keep = w.nb - 8 * bt;
         if (keep < 8) {
-            x = keep8(x, sra, off_a[0], 8 * bt, (int)keep);
-            y = keep8(y, srb, off_b[0], 8 * bt, (int)keep);
+            x = keep8(x, sra, off_a, 8 * bt, (int)keep);
+            y = keep8(y, srb, off_b, 8 * bt, (int)keep);
         }
-        uint2 *p = reinterpret_cast<uint2 *>(lds + 2 * kBuf) + (place & 1) * (TM + TN) + 64 * wave + L;
+        uint2 *p = reinterpret_cast<uint2 *>(lds + NB * kBuf) + (place & 1) * (TM + TN) + 64 * wave + L;
         if (TM == 256 || wave < TM / 64)
             p[0] = x;
         if (TN == 256 || wave < TN / 64)
@@ -248,7 +313,7 @@ struct MmKernel {
     // Compact: the words of the four steps of `place` in use.
     __device__ __forceinline__ void read_scales(int place)
     {
-        const uint2 *p = reinterpret_cast<const uint2 *>(lds + 2 * kBuf) + (place & 1) * (TM + TN);
+        const uint2 *p = reinterpret_cast<const uint2 *>(lds + NB * kBuf) + (place & 1) * (TM + TN);
 #pragma unroll
         for (int i = 0; i < MT; i++)
             words(sa[i], p[wm + 32 * i + r]);
@@ -335,16 +400,23 @@ struct MmKernel {
         return bf16_of_codes8<FB>((uint32_t)f.b[j][2 * part], (uint32_t)f.b[j][2 * part + 1], s);
     }
 
-    // Tile t, steps J and J + 1 of the scale words.  SETTLE: the scales fetched
-    // before have to be here at its barrier.
-    template <int J, bool SETTLE>
-    __device__ __forceinline__ void tile(Frags &f0, Frags &f1, int t)
+    // The tile in place t, steps J and J + 1 of the scale words (J: 0 in even
+    // places, 2 in odd ones).
+    template <int J>
+    __device__ __forceinline__ void tile(Frags &f0, Frags &f1, Words &next, int t)
     {
+        constexpr int odd = J / 2;
         step<J, false>(f0, f1, t, 1, 0);
-        wait_all_and_barrier();
-        if (SETTLE)
-            settle_scales();
-        step<J + 1, true>(f1, f0, t + 1, 0, t + 2);
+        wait_and_barrier<loads(odd + 2, odd + NB - 1)>();
+        if constexpr (TILED) {
+            if (odd)
+                read_words(next, t + 1);
+            if ((odd + NB) % 2 == 0)
+                issue_scales(t + NB);
+        } else if (odd) {
+            settle_scales();       // fetched before: no more loads than here
+        }
+        step<J + 1, true>(f1, f0, t + 1, 0, t + NB);
     }
 
     __device__ __forceinline__ void run()
@@ -372,55 +444,60 @@ struct MmKernel {
 #pragma unroll
             for (int j = 0; j < NT; j++)
                 acc[i][j] = f32x16_t{};
-        if constexpr (TILED) {
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-                off_a[i] = scale_offset(last_a, wm + 32 * i + r);
-#pragma unroll
-            for (int j = 0; j < NT; j++)
-                off_b[j] = scale_offset(last_b, brow(j));
-        } else {
-            static_assert(TM <= 256 && TN <= 256, "a thread per row");
-            off_a[0] = scale_offset(last_a, 64 * wave + L) + sra.lead;
-            off_b[0] = scale_offset(last_b, 64 * wave + L) + srb.lead;
+        static_assert(TM <= 256 && TN <= 256, "compact scales: a thread per row");
+        if constexpr (!TILED) {
+            off_a = scale_offset(last_a, 64 * wave + L) + sra.lead;
+            off_b = scale_offset(last_b, 64 * wave + L) + srb.lead;
         }
         if (nt > 0) {
             Frags f0, f1;
-            fetch_scales(0);
-#pragma unroll
-            for (int i = 0; i < kLoads; i++)
-                issue(0, i);
-            if constexpr (TILED) {
-                take_scales();
-            } else {
-                write_scales(0);
+            Words next;
+            uint32_t behind[4];
+            if constexpr (!TILED) {
                 fetch_scales(1);
+                behind[0] = raw_a[0], behind[1] = raw_a[1], behind[2] = raw_b[0], behind[3] = raw_b[1];
+                fetch_scales(0);
             }
-            wait_all_and_barrier();
 #pragma unroll
-            for (int i = 0; i < kLoads; i++)
-                issue(1, i);
-            if constexpr (!TILED)
+            for (int t = 0; t < NB; t++) {
+                if (TILED && t % 2 == 0)
+                    issue_scales(t);
+#pragma unroll
+                for (int i = 0; i < kLoads; i++)
+                    issue(t, i);
+                if (!TILED && t == 0) {
+                    write_scales(0);
+                    raw_a[0] = behind[0], raw_a[1] = behind[1], raw_b[0] = behind[2], raw_b[1] = behind[3];
+                    settle_scales();
+                }
+            }
+            wait_and_barrier<loads(1, NB - 1)>();
+            if constexpr (TILED) {
+                read_words(next, 0);
+                take_words(next);
+            } else {
                 read_scales(0);
+            }
 #pragma unroll
             for (int i = 0; i < MT + NT; i++)
                 read(f0, 0, 0, i);
             int t = 0;
             do {
-                // scale words of two tiles at a time.  Tiled: fetched in the
-                // first, here at the second one's barrier, in use after it.
-                // Compact: fetched two tiles earlier, put into LDS before the
-                // first tile's barrier and taken from there after the second.
-                const int next = (t >> 1) + 1;
+                // scale words of two tiles at a time.  Tiled: read from LDS behind
+                // the second one's barrier.  Compact: fetched two tiles earlier, put
+                // into LDS before the first tile's barrier and taken from there
+                // after the second.
+                const int place = (t >> 1) + 1;
                 if constexpr (!TILED)
-                    write_scales(next);
-                tile<0, false>(f0, f1, t);
-                fetch_scales(TILED ? (t + 2 < nt ? next : next - 1) : next + 1);
-                tile<2, true>(f0, f1, t + 1);
+                    write_scales(place);
+                tile<0>(f0, f1, next, t);
+                if constexpr (!TILED)
+                    fetch_scales(place + 1);
+                tile<2>(f0, f1, next, t + 1);
                 if constexpr (TILED)
-                    take_scales();
+                    take_words(next);
                 else
-                    read_scales(next);
+                    read_scales(place);
                 t += 2;
             } while (t < nt);
         }
@@ -516,36 +593,45 @@ __device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, ui
 }
 
 // The first t.whole workgroups take a whole tile each.  The tiles behind them,
-// too few to fill the CUs once more, go in parts of 128 x 128.
+// too few to fill the CUs once more, go in t.parts parts.
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const MmTable t)
 {
     extern __shared__ uint8_t mm_lds[];
-    const int id = (int)blockIdx.x;
-    if (id < t.whole) {
+    constexpr int S = kMmPart;
+    static_assert(TM == 2 * S && TN == 2 * S, "parts: halves of the sides");
+    const int id = (int)blockIdx.x, q = id - t.whole;
+    if (q < 0) {
         const MmTile w = mm_tile(a, t, mm_xcd_order(id, t.whole), TM, TN);
         mm_tile_run<MODE, FA, FB, TM, TN, TILED>(a, w, mm_lds);
-    } else {
-        constexpr int S = kMmPart, PM = TM / S, parts = PM * (TN / S);
-        const int q = id - t.whole;
-        MmTile w = mm_tile(a, t, t.whole + q / parts, TM, TN);
-        w.m0 += q % PM * S;
-        w.n0 += q % parts / PM * S;
-        if (w.m0 < w.M && w.n0 < a.N)
-            mm_tile_run<MODE, FA, FB, S, S, TILED>(a, w, mm_lds);
+        return;
     }
+    MmTile w = mm_tile(a, t, t.whole + q / t.parts, TM, TN);
+    w.n0 += q & 1 ? S : 0;
+    w.m0 += q & 2 && t.parts == 4 ? S : 0;
+    if (w.m0 >= w.M || w.n0 >= a.N)
+        return;
+    if (t.parts == 2)
+        mm_tile_run<MODE, FA, FB, TM, S, TILED>(a, w, mm_lds);
+    else
+        mm_tile_run<MODE, FA, FB, S, S, TILED>(a, w, mm_lds);
 }
 
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 hipError_t launch_mm_tile_one(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    constexpr int lds = 2 * (TM + TN) * (128 + (TILED ? 0 : 8)), parts = TM * TN / (kMmPart * kMmPart);
+    constexpr int S = kMmPart;
+    constexpr int l0 = MmKernel<MODE, FA, FB, TM, TN, TILED>::kLds, l1 = MmKernel<MODE, FA, FB, TM, S, TILED>::kLds,
+                  l2 = MmKernel<MODE, FA, FB, S, S, TILED>::kLds;
+    constexpr int lds = l0 > l1 ? (l0 > l2 ? l0 : l2) : l1 > l2 ? l1 : l2;
+    static_assert(lds <= 160 * 1024, "a CU's LDS");
     const hipError_t e =
         hipFuncSetAttribute(reinterpret_cast<const void *>(mm_tile_kernel<MODE, FA, FB, TM, TN, TILED>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED>), dim3((unsigned)(t.whole + parts * (t.tile0[t.count] - t.whole))), dim3(256), lds, stream, a, t);
+    const unsigned n = (unsigned)(t.whole + t.parts * (t.tile0[t.count] - t.whole));
+    hipLaunchKernelGGL((mm_tile_kernel<MODE, FA, FB, TM, TN, TILED>), dim3(n), dim3(256), lds, stream, a, t);
     return hipGetLastError();
 }
 

@@ -153,11 +153,12 @@ int main()
         CHECK(g_a.qa_bytes == qa && g_a.qb_bytes == qb && g_a.sa_bytes == sa && g_a.sb_bytes == sb);
         // reads of 16 and 8 bytes fit the operands
         CHECK(g_kind == kAnyL || (qa >= 16 && qb >= 16 && sa >= 8 && sb >= 8));
-        const int64_t total = g_t.tile0[G], pieces = tm * tn / (kMmPart * kMmPart);
+        const int64_t total = g_t.tile0[G], pieces = g_t.parts;
+        CHECK(pieces == 1 || (tiles && (pieces == 2 || pieces == 4)));
         CHECK(total > 0 && g_t.whole >= 0 && g_t.whole <= total);
-        CHECK(g_t.whole == total || (tiles && g_t.whole % kMmCUs == 0 && (total - g_t.whole) * pieces <= 3 * kMmCUs));
+        CHECK(g_t.whole == total || (pieces > 1 && g_t.whole % kMmCUs == 0 && (total - g_t.whole) * pieces <= kMmCUs));
         parts += g_t.whole < total;
-        CHECK((tiles ? g_t.whole + pieces * (total - g_t.whole) : total) * 256 < ((int64_t)1 << 32));
+        CHECK((g_t.whole + pieces * (total - g_t.whole)) * 256 < ((int64_t)1 << 32));
         // the tiled kernel's rows start at multiples of 16 bytes
         bool aligned = true;
         for (int g = 0; g < G; g++)
