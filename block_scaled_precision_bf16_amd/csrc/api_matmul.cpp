@@ -111,6 +111,7 @@ enum MmKind { kAny, kSmall, kTiles };
 struct MmPlan {
     MmKind kind;
     int tile_m, tile_n;
+    int waves;                 // of a small product's workgroup
     bool pack;                 // rows are copied to 128-byte boundaries first
     int64_t pack_a, pack_b;    // bytes of the copies
 };
@@ -128,39 +129,56 @@ int last_parts(int64_t n)
 bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
 {
     const int G = t.count;
-    int64_t most_m = 0, most_k = 0, big = 0, small = 0, small_bytes = 0, pitches = 0;
+    int64_t most_m = 0, most_k = 0, big = 0, small32 = 0, small64 = 0, pitches = 0;
+    double tile_steps = 0;
     bool rows16 = true;
     for (int g = 0; g < G; g++) {
         const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
         rows16 = rows16 && k % 16 == 0;
         most_m = m > most_m ? m : most_m;
         most_k = k > most_k ? k : most_k;
-        big += ceil_div(m, mxk::kMmTileM) * ceil_div(a.N, mxk::kMmTileN);
+        const int64_t tiles = ceil_div(m, mxk::kMmTileM) * ceil_div(a.N, mxk::kMmTileN);
+        big += tiles;
+        tile_steps += (double)(tiles * ceil_div(k, 128));
+        small32 += ceil_div(m, 32) * ceil_div(a.N, mxk::kMmSmallN);
+        small64 += ceil_div(m, 64) * ceil_div(a.N, mxk::kMmSmallN);
         t.packed0[g] = pitches;
         pitches += mxk::mm_pitch(k);
     }
-    const int small_m = most_m <= 32 ? 32 : 64;
+    // Small products: 32 rows at a time where that still does not fill the CUs more
+    // than once (64 x 2048 outputs with 2048 k: 5.7 us, 64 rows at a time 7.5 us), or
+    // there are no more; otherwise 64 share the loads of B (512 x 2048: 13.4 and 12
+    // us).
+    const int small_m = small32 <= mxk::kMmCUs || most_m <= 32 ? 32 : 64;
+    const int64_t small = small_m == 32 ? small32 : small64;
+    double small_bytes = 0;
     for (int g = 0; g < G; g++) {
         const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
-        const int64_t n = ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN);
-        small += n;
-        small_bytes += n * (small_m + mxk::kMmSmallN) * k;
+        small_bytes += (double)(ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN) * (small_m + mxk::kMmSmallN) * k);
     }
     p = MmPlan{};
+    p.waves = small <= mxk::kMmCUs ? 8 : 4;
     // Microseconds, as measured (graph replays).  The small kernel: its waves' share
-    // of k, one after the other, and the operands, which each output tile reads for
-    // itself at 8.3 TB/s.  The tiled one: rounds of tiles and the last, partial one;
-    // twice the time for fp32 outputs; the copy of unaligned rows.
-    const double lat = (double)ceil_div(most_k, 128) * (small_m == 32 ? 0.25 : 0.4);
-    const double read = (double)small_bytes / 8.3e6;
-    const double small_us = 3 + (lat + read / 2 > read ? lat + read / 2 : read);
+    // of k, one after the other, and what each workgroup reads for itself, at 14 TB/s
+    // from the caches, partly at the same time; 5.4 ns for each workgroup that does not
+    // start at once.  The tiled one: rounds of tiles, of which the outputs are 8 us (in
+    // fp32 14), and the last, partial one, whose steps in parts take longer than their
+    // share; in fp32 twice the time of a step; the copy of unaligned rows.
+    const double f = a.out_f32 ? 2 : 1;
+    const double lat = (double)ceil_div(most_k, 128) * (a.out_f32 ? 1.2 : 1.0) *
+                       (small_m == 32 ? p.waves == 8 ? 0.10 : 0.14 : p.waves == 8 ? 0.19 : 0.22);
+    const double read = small_bytes / 14e6;
+    const double small_us = 3 + (lat > read ? lat + read / 4 : read + lat / 4) +
+                            (small > mxk::kMmCUs ? 5.4e-3 * (double)(small - mxk::kMmCUs) : 0);
     const int parts = last_parts(big);
-    const double steps = (double)ceil_div(most_k, 128), slow = a.out_f32 ? 2 : 1;
-    double tile_us = 4 + (double)(big / mxk::kMmCUs) * (6 + 1.5 * slow * steps);
-    if (big % mxk::kMmCUs != 0)
-        tile_us += parts == 4   ? (a.out_f32 ? 0.85 : 0.55) * steps
-                   : parts == 2 ? 2 + 0.95 * slow * steps
-                                : 6 + 1.5 * slow * steps;
+    const int64_t last = big % mxk::kMmCUs;
+    const double steps = tile_steps / (double)big;      // a tile's, on average
+    const double round = a.out_f32 ? 14 + 3 * steps : 8 + 1.5 * steps;
+    double tile_us = 4 + (double)(big / mxk::kMmCUs) * round;
+    if (last != 0)
+        tile_us += parts == 4   ? 1 + (a.out_f32 ? 0.8 : 0.5) * steps + f * (double)last / 32
+                   : parts == 2 ? 4 * f + 0.95 * f * steps
+                                : round;
     if (!rows16)
         tile_us += 3 + (double)(n.qa + n.qb) / 2e6;
     if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8) {
@@ -270,7 +288,7 @@ mx_status mm_impl(const uint8_t *qa, const uint8_t *sa, const uint8_t *qb, const
     if (p.kind == kAny)
         return from_hip(mxk::launch_mm_any(a, t, stream));
     if (p.kind == kSmall)
-        return from_hip(mxk::launch_mm_small(a, t, p.tile_m, stream));
+        return from_hip(mxk::launch_mm_small(a, t, p.tile_m, p.waves, stream));
     if (p.pack) {
         uint8_t *const wa = static_cast<uint8_t *>(workspace), *const wb = wa + p.pack_a;
         const hipError_t e = mxk::launch_mm_pack(a, t, wa, wb, stream);

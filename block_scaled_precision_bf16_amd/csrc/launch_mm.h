@@ -61,7 +61,7 @@ constexpr int kMmAnyTile = 64, kMmSmallN = 32;
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
-hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, hipStream_t stream);
+hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, int waves, hipStream_t stream);
 hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t stream);
 // Copies the operands' rows to qa and qb, mm_pitch apart.
 hipError_t launch_mm_pack(const MmArgs &a, const MmTable &t, uint8_t *qa, uint8_t *qb, hipStream_t stream);

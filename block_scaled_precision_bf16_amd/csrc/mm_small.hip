@@ -1,22 +1,33 @@
 // mm_small.hip -- small products of MXFP8 operands: few rows, or few outputs.
 //
 // Here the operands are read about once and there is too little work for the
-// tiled kernel, whose workgroups walk along k alone and pay a memory latency per
-// 128 k.  A workgroup of 4 waves owns 32 MT x 32 outputs, and its waves take
-// pieces of 128 k in turn, straight from memory into the fragments (rows at any
-// byte), two pieces under way per wave.  The 4 partial sums are added through LDS
-// in a fixed order.
+// tiled kernel, whose workgroups walk along k alone.  A workgroup of KW waves owns
+// 32 MT x 32 outputs, and its waves take pieces of 128 k in turn, two under way
+// per wave, without barriers.  A wave loads a piece's rows as whole 128-byte lines
+// (rows at any byte) and turns them into fragment order through LDS of its own: 16
+// bytes of 32 rows per load, straight into the fragments, cost the memory pipeline
+// four times the lines (16 x 512 outputs with 8192 k: 17.5 us, with LDS 12.1 us).  The
+// KW partial sums are added through LDS in a fixed order.
+//
+// 8 waves where those workgroups do not fill the CUs more than once (the same product
+// 10.2 us, 64 x 8192 outputs 22.7 us for 23.3), else 4 (16 experts' 64 rows by 4096 x
+// 2048 each: 24.7 us, with 8 waves 36 us); these 25 us are for 105 MB of weights,
+// 4.3 TB/s.
 #include "mm_common.h"
 
 namespace mxk {
 namespace {
 
-constexpr int kWavesK = 4;
+// A wave's share of a piece, 32 rows of 128 k, as it is loaded: lane L holds 16-byte
+// chunk L % 8 of rows L / 8, 8 + L / 8, ...; and the four scale bytes of row L % 32.
+struct Load {
+    uint4 q[4];
+    uint32_t s, odd;           // tiled: the words of even and of odd blocks
+};
 
-// A row's share of a piece: the lane's four 16-byte chunks and the scale bytes of
-// the piece's four blocks.
+// In fragment order: chunks 2 s + h and 2 s + 2 + h of row r in f[s].
 struct Piece {
-    i32x8_t f[2];              // chunks 2 s and 2 s + 1: step s
+    i32x8_t f[2];
     uint32_t s;
 };
 
@@ -30,7 +41,7 @@ struct Rows {
     ByteRows<16> q;
     ByteRows<4> sc;            // compact scales
     const uint8_t *stile;      // tiled ones
-    uint32_t qoff, soff;
+    uint32_t qoff[4], soff;
     int64_t K, nb;
     int32_t tiled;
     int64_t rt;                // tiled: bytes from one block tile to the next
@@ -41,48 +52,70 @@ struct Rows {
         : q(qarray, qg + r0 * K_, qleft - r0 * K_), sc(sarray, sg + r0 * nb_, sleft - r0 * nb_),
           stile(sg + (r0 >> 5) * 256), K(K_), nb(nb_), tiled(tiled_), rt(((rows + 31) >> 5) * 256)
     {
-        const int h = lane >> 5;
-        int r = lane & 31;
-        r = r0 + r < rows ? r : (int)(rows - 1 - r0);
-        qoff = q.lead + (uint32_t)(r * (int)K) + 16 * h;
+        const int last = (int)(rows - 1 - r0 < 31 ? rows - 1 - r0 : 31);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = 8 * i + (lane >> 3);
+            qoff[i] = q.lead + (uint32_t)((r < last ? r : last) * (int)K) + 16 * (lane & 7);
+        }
+        const int r = (lane & 31) < last ? lane & 31 : last;
         soff = tiled ? 4 * r : sc.lead + (uint32_t)(r * (int)nb);
     }
     // Piece u (128 k from 128 u on; u inside the rows).
-    __device__ __forceinline__ void load(Piece &p, int u) const
+    __device__ __forceinline__ void load(Load &p, int u) const
     {
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-            p.f[i] = join(q.load<uint4>(qoff + 64 * i, 128 * (int64_t)u),
-                          q.load<uint4>(qoff + 64 * i + 32, 128 * (int64_t)u));
+        for (int i = 0; i < 4; i++)
+            p.q[i] = q.load<uint4>(qoff[i], 128 * (int64_t)u);
         if (tiled) {
             const uint8_t *s = stile + (u >> 1) * rt + soff;
-            uint32_t even, odd;
-            __builtin_memcpy(&even, s, 4);
-            __builtin_memcpy(&odd, s + 128, 4);
-            // bytes 2 (u % 2), + 1 of each: blocks 4u, 4u + 2 and 4u + 1, 4u + 3
-            p.s = __builtin_amdgcn_perm(odd, even, u & 1 ? 0x07030602u : 0x05010400u);
+            __builtin_memcpy(&p.s, s, 4);
+            __builtin_memcpy(&p.odd, s + 128, 4);
         } else {
             p.s = sc.load<uint32_t>(soff, 4 * (int64_t)u);
         }
     }
-    // The last piece: what lies behind the row's end becomes 0.
-    __device__ __forceinline__ void fix(Piece &p, int u, int h) const
+    // The scale bytes of piece u, once they are here.
+    __device__ __forceinline__ uint32_t scales(const Load &p, int u) const
+    {
+        // bytes 2 (u % 2), + 1 of each: blocks 4u, 4u + 2 and 4u + 1, 4u + 3
+        return tiled ? __builtin_amdgcn_perm(p.odd, p.s, u & 1 ? 0x07030602u : 0x05010400u) : p.s;
+    }
+    // The last piece: what lies behind the row's end becomes 0 (tiled scales there
+    // are 0).
+    __device__ __forceinline__ void fix(Load &p, int u, int lane) const
     {
         const int left = (int)(K - 128 * (int64_t)u);
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-            p.f[i] = join(q.fix(half_of(p.f[i], 0), qoff + 64 * i, 128 * (int64_t)u, left - 64 * i - 16 * h),
-                          q.fix(half_of(p.f[i], 1), qoff + 64 * i + 32, 128 * (int64_t)u,
-                                left - 64 * i - 32 - 16 * h));
-        const int keep = (int)(nb - 4 * (int64_t)u);
+        for (int i = 0; i < 4; i++)
+            p.q[i] = q.fix(p.q[i], qoff[i], 128 * (int64_t)u, left - 16 * (lane & 7));
         if (!tiled) {
+            const int keep = (int)(nb - 4 * (int64_t)u);
             const uint32_t d = sc.behind(soff, 4 * (int64_t)u);
             p.s = d < 4 ? p.s >> (8 * d) : 0;
+            if (keep < 4)
+                p.s &= (1u << (8 * keep)) - 1;
         }
-        if (keep < 4)
-            p.s &= (1u << (8 * keep)) - 1;
     }
 };
+
+// Through the wave's own 4 KB of LDS (whose accesses come in order): chunk c of row
+// R lies in slot c ^ R % 8 of the row, so that 8 lanes that are served together
+// use all banks, writing and reading.
+__device__ __forceinline__ void turn(const Rows &rows, const Load &p, int u, Piece &o, uint4 *lds, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        lds[64 * i + (lane & 56) + ((lane & 7) ^ (lane >> 3))] = p.q[i];
+    asm volatile("" ::: "memory");
+    const uint4 *row = lds + 8 * (lane & 31);
+    const int h = lane >> 5, x = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        o.f[i] = join(row[(4 * i + h) ^ x], row[(4 * i + 2 + h) ^ x]);
+    asm volatile("" ::: "memory");
+    o.s = rows.scales(p, u);
+}
 
 // acc += A B^T over a piece: two steps of 64 k.  Chunk 2 s + b of a lane (r, h)
 // holds k 16 h .. + 15 of block 2 s + b.
@@ -108,10 +141,11 @@ __device__ __forceinline__ void multiply(const Piece &x, const Piece &y, f32x16_
     }
 }
 
-template <MmMode MODE, int FA, int FB, int MT>
-__global__ __launch_bounds__(64 * kWavesK, MT == 1 ? 3 : 2) void mm_small_kernel(const MmArgs a, const MmTable t)
+template <MmMode MODE, int FA, int FB, int MT, int KW>
+__global__ __launch_bounds__(64 * KW, MT == 1 && KW == 4 ? 3 : 2) void mm_small_kernel(const MmArgs a, const MmTable t)
 {
-    __shared__ float part[kWavesK / 2 * MT * 1024];
+    __shared__ uint4 lds[KW * (MT + 1) * 256];
+    float *const part = reinterpret_cast<float *>(lds);    // the partial sums, at the end
     const int tid = (int)threadIdx.x, L = tid & 63, h = L >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const MmTile w = mm_tile(a, t, (int)blockIdx.x, 32 * MT, 32);
@@ -125,63 +159,70 @@ __global__ __launch_bounds__(64 * kWavesK, MT == 1 ? 3 : 2) void mm_small_kernel
         const Rows ra0(a.qa, w.qa, w.qa_left, a.sa, w.sa, w.sa_left, w.M, w.m0, w.K, w.nb, a.tiled, L);
         const int64_t m1 = w.m0 + 32 < w.M ? w.m0 + 32 : w.m0;
         const Rows ra1(a.qa, w.qa, w.qa_left, a.sa, w.sa, w.sa_left, w.M, m1, w.K, w.nb, a.tiled, L);
-        Piece pa[2][MT], pb[2];
+        Load pa[2][MT], pb[2];
+        uint4 *const mine = lds + wave * (MT + 1) * 256;
         auto load = [&](int i, int u) {
             rb.load(pb[i], u);
             ra0.load(pa[i][0], u);
             if constexpr (MT == 2)
                 ra1.load(pa[i][MT - 1], u);
         };
-        auto work = [&](int i) {
+        auto work = [&](int i, int u) {
+            Piece x[MT], y;
+            turn(rb, pb[i], u, y, mine, L);
 #pragma unroll
             for (int m = 0; m < MT; m++)
-                multiply<MODE, FA, FB>(pa[i][m], pb[i], acc[m], h);
+                turn(m ? ra1 : ra0, pa[i][m], u, x[m], mine + 256 * (m + 1), L);
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+                multiply<MODE, FA, FB>(x[m], y, acc[m], h);
         };
         // the partial piece, by the wave whose turn it is, first
-        const bool partial = whole < pieces && wave == whole % kWavesK;
+        const bool partial = whole < pieces && wave == whole % KW;
         if (partial)
             load(1, whole);
         if (wave < whole)
             load(0, wave);
         if (partial) {
-            rb.fix(pb[1], whole, h);
-            ra0.fix(pa[1][0], whole, h);
+            rb.fix(pb[1], whole, L);
+            ra0.fix(pa[1][0], whole, L);
             if constexpr (MT == 2)
-                ra1.fix(pa[1][MT - 1], whole, h);
-            work(1);
+                ra1.fix(pa[1][MT - 1], whole, L);
+            work(1, whole);
         }
-        for (int u = wave; u < whole; u += 2 * kWavesK) {
-            if (u + kWavesK < whole)
-                load(1, u + kWavesK);
-            work(0);
-            if (u + 2 * kWavesK < whole)
-                load(0, u + 2 * kWavesK);
-            if (u + kWavesK < whole)
-                work(1);
+        for (int u = wave; u < whole; u += 2 * KW) {
+            if (u + KW < whole)
+                load(1, u + KW);
+            work(0, u);
+            if (u + 2 * KW < whole)
+                load(0, u + 2 * KW);
+            if (u + KW < whole)
+                work(1, u + KW);
         }
     }
+    __syncthreads();
     // the upper half of the waves hands its sums to the lower
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
         for (int e = 0; e < 16; e++)
-            if (wave >= kWavesK / 2)
-                part[((wave - kWavesK / 2) * MT + i) * 1024 + 64 * e + L] = acc[i][e];
+            if (wave >= KW / 2)
+                part[((wave - KW / 2) * MT + i) * 1024 + 64 * e + L] = acc[i][e];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
         for (int e = 0; e < 16; e++)
-            if (wave < kWavesK / 2)
+            if (wave < KW / 2)
                 part[(wave * MT + i) * 1024 + 64 * e + L] += acc[i][e];
     __syncthreads();
     // register e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4, column r
-    for (int o = tid; o < MT * 1024; o += 64 * kWavesK) {
+    for (int o = tid; o < MT * 1024; o += 64 * KW) {
         const int i = o >> 10, m = o >> 5 & 31, n = o & 31;
         const int e = (m >> 3) * 4 + (m & 3), lane = n + 32 * (m >> 2 & 1);
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWavesK / 2; k++)
+        for (int k = 0; k < KW / 2; k++)
             v += part[(k * MT + i) * 1024 + 64 * e + lane];
         const int64_t row = w.m0 + 32 * i + m, col = w.n0 + n;
         if (row < w.M && col < a.N)
@@ -189,28 +230,32 @@ __global__ __launch_bounds__(64 * kWavesK, MT == 1 ? 3 : 2) void mm_small_kernel
     }
 }
 
-template <MmMode MODE, int MT>
+template <MmMode MODE, int MT, int KW>
 hipError_t launch(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
-    const dim3 grid((unsigned)t.tile0[t.count]), block(64 * kWavesK);
+    const dim3 grid((unsigned)t.tile0[t.count]), block(64 * KW);
     if (!a.a_e5m2 && !a.b_e5m2)
-        hipLaunchKernelGGL((mm_small_kernel<MODE, 0, 0, MT>), grid, block, 0, stream, a, t);
+        hipLaunchKernelGGL((mm_small_kernel<MODE, 0, 0, MT, KW>), grid, block, 0, stream, a, t);
     else if (a.a_e5m2 && !a.b_e5m2)
-        hipLaunchKernelGGL((mm_small_kernel<MODE, 1, 0, MT>), grid, block, 0, stream, a, t);
+        hipLaunchKernelGGL((mm_small_kernel<MODE, 1, 0, MT, KW>), grid, block, 0, stream, a, t);
     else if (!a.a_e5m2)
-        hipLaunchKernelGGL((mm_small_kernel<MODE, 0, 1, MT>), grid, block, 0, stream, a, t);
+        hipLaunchKernelGGL((mm_small_kernel<MODE, 0, 1, MT, KW>), grid, block, 0, stream, a, t);
     else
-        hipLaunchKernelGGL((mm_small_kernel<MODE, 1, 1, MT>), grid, block, 0, stream, a, t);
+        hipLaunchKernelGGL((mm_small_kernel<MODE, 1, 1, MT, KW>), grid, block, 0, stream, a, t);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, hipStream_t stream)
+hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, int waves, hipStream_t stream)
 {
-    if (rows == 32)
-        return a.out_f32 ? launch<kExact, 1>(a, t, stream) : launch<kMx, 1>(a, t, stream);
-    return a.out_f32 ? launch<kExact, 2>(a, t, stream) : launch<kMx, 2>(a, t, stream);
+    if (a.out_f32)
+        return rows == 32 ? waves == 8 ? launch<kExact, 1, 8>(a, t, stream) : launch<kExact, 1, 4>(a, t, stream)
+               : waves == 8 ? launch<kExact, 2, 8>(a, t, stream)
+                            : launch<kExact, 2, 4>(a, t, stream);
+    return rows == 32 ? waves == 8 ? launch<kMx, 1, 8>(a, t, stream) : launch<kMx, 1, 4>(a, t, stream)
+           : waves == 8 ? launch<kMx, 2, 8>(a, t, stream)
+                        : launch<kMx, 2, 4>(a, t, stream);
 }
 
 }  // namespace mxk

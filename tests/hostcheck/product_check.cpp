@@ -15,7 +15,7 @@
 using namespace mxk;
 
 enum { kNone, kTileL, kTileF32, kSmallL, kAnyL, kMvL };
-static int g_kind, g_packs, g_small_rows;
+static int g_kind, g_packs, g_small_rows, g_waves;
 static MmArgs g_a;
 static MmTable g_t;
 static MvArgs g_mv;
@@ -30,9 +30,9 @@ static hipError_t note(int kind, const MmArgs &a, const MmTable &t)
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t) { return note(kTileL, a, t); }
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t) { return note(kTileF32, a, t); }
 hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t) { return note(kAnyL, a, t); }
-hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, hipStream_t)
+hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, int waves, hipStream_t)
 {
-    g_small_rows = rows;
+    g_small_rows = rows, g_waves = waves;
     return note(kSmallL, a, t);
 }
 hipError_t launch_mm_pack(const MmArgs &, const MmTable &, uint8_t *qa, uint8_t *qb, hipStream_t)
@@ -120,7 +120,7 @@ int main()
         const bool tiles = g_kind == kTileL || g_kind == kTileF32;
         const int64_t tm = tiles ? kMmTileM : g_kind == kSmallL ? g_small_rows : kMmAnyTile;
         const int64_t tn = tiles ? kMmTileN : g_kind == kSmallL ? kMmSmallN : kMmAnyTile;
-        CHECK(g_kind != kSmallL || g_small_rows == 32 || g_small_rows == 64);
+        CHECK(g_kind != kSmallL || ((g_small_rows == 32 || g_small_rows == 64) && (g_waves == 4 || g_waves == 8)));
         CHECK(g_a.dim == dim && g_a.N == cols && g_a.sum_rows == wgrad && g_a.tiled == tiled);
         CHECK(g_t.count == G && g_t.tile0[0] == 0);
         std::vector<char> used(G, 0);

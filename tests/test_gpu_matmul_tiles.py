@@ -79,9 +79,13 @@ def fmt_flags(ea, eb):
 # (M, N, K): parts only; 256 whole tiles and parts; three rounds and parts; one
 # partial round of whole tiles; a single round; short, odd and unaligned rows.
 SIZES = [(1500, 1301, 2064), (4200, 4157, 400), (6200, 8300, 144), (3800, 3800, 208),
-         (4096, 4096, 512), (1, 66000, 1040), (131001, 3, 528), (5000, 4999, 64), (4999, 5000, 32),
-         (1500, 1300, 2065), (2049, 2047, 1151), (4200, 4157, 330), (130, 9000, 4001)]
-
+         (4096, 4096, 512), (257, 16500, 1040), (16501, 259, 528), (5000, 4999, 64), (4999, 5000, 32),
+         (2500, 2300, 2065), (2049, 4095, 1151), (4200, 4157, 330), (700, 9000, 4001)]
+FORMAT_SIZES = [(1500, 1301, 2064), (2500, 2302, 2065)]
+GROUPED = [([1000, 0, 1, 700, 257, 256], 2500, 1040), ([0, 3000, 0], 4050, 1041),
+           ([100] * 40, 4096, 512), ([33, 2900, 5, 0], 3999, 2063)]
+WGRAD = [([1000, 0, 1, 700, 257, 256], 2000, 2500), ([512, 2048, 0, 16], 2100, 2300),
+         ([1, 2, 3, 2000], 2999, 2111), ([128] * 30, 1200, 2048), ([31, 0, 1808, 640], 3777, 2050)]
 
 @pytest.mark.parametrize("out", [0, mx.OUT_F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("tiled", [0, mx.SCALE_TILED], ids=["compact", "tiled"])
@@ -96,7 +100,7 @@ def test_tiles(M, N, K, tiled, out):
     assert_same(y.t, a.values() @ b.values().t(), f"{M}x{N}x{K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(1500, 1301, 2064), (1500, 1302, 2065)])
+@pytest.mark.parametrize("M,N,K", FORMAT_SIZES)
 @pytest.mark.parametrize("ea,eb", [(True, False), (False, True), (True, True)])
 def test_tiles_of_every_format(M, N, K, ea, eb):
     for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
@@ -122,9 +126,7 @@ def test_tiles_accumulate(N):
 
 
 @pytest.mark.parametrize("tiled", [0, mx.SCALE_TILED], ids=["compact", "tiled"])
-@pytest.mark.parametrize("rows,N,K", [([1000, 0, 1, 700, 257, 256], 1500, 1040),
-                                      ([0, 2000, 0], 2050, 1041),
-                                      ([100] * 40, 2048, 512), ([33, 1900, 5, 0], 1999, 2063)])
+@pytest.mark.parametrize("rows,N,K", GROUPED)
 def test_grouped_tiles(rows, N, K, tiled):
     G, M = len(rows), sum(rows)
     for flags in (tiled, tiled | mx.OUT_F32 | mx.A_E5M2):
@@ -137,10 +139,6 @@ def test_grouped_tiles(rows, N, K, tiled):
         y.check("grouped")
         want = torch.cat([a.values(g) @ b.values(g).t() for g in range(G)])
         assert_same(y.t, want, f"rows {rows}")
-
-
-WGRAD = [([1000, 0, 1, 700, 257, 256], 1000, 1500), ([512, 2048, 0, 16], 1100, 1300),
-         ([1, 2, 3, 2000], 2999, 2111), ([128] * 30, 600, 1536), ([31, 0, 1808, 640], 1777, 2050)]
 
 
 @pytest.mark.parametrize("tiled", [0, mx.SCALE_TILED], ids=["compact", "tiled"])
@@ -163,7 +161,7 @@ def test_weight_gradient_tiles(rows, N, K, tiled):
     (40, 262165, 16400, mx.SCALE_TILED),             # B
     (66000, 33000, 48, mx.OUT_F32),                  # the output
     (20, 8200, 524304, 0),                           # B, small products' kernel
-    (262165, 70, 16401, mx.SCALE_TILED)])            # A's copy
+    (262165, 270, 16401, mx.SCALE_TILED)])            # A's copy
 def test_past_32_bits(M, N, K, flags):
     """Sums of up to 524304 exact products stay below 2^24 quarters here: they
     have random signs and a standard deviation of less than 12000."""
@@ -187,7 +185,7 @@ def test_past_32_bits(M, N, K, flags):
 def test_own_workspaces_on_two_streams():
     """Two packed products at a time, each with its own workspace, and the given
     workspace's bytes behind the needed ones untouched."""
-    M, N, K = 1500, 1300, 2065
+    M, N, K = 2500, 2300, 2065
     need = mx.mx_matmul_workspace_size(M, N, K)
     assert need == (M + N) * 2176
     ops = [(Operand([(M, K)], 0, False, 20 + i), Operand([(N, K)], 0, False, 30 + i)) for i in range(2)]
@@ -208,7 +206,7 @@ def test_own_workspaces_on_two_streams():
 def test_captured_with_a_copy_of_the_rows():
     """Graph replays of a packed product and weight gradient, with new operands
     and eager work between them."""
-    rows, N, K = [1000, 0, 333, 367], 1100, 1500
+    rows, N, K = [1000, 0, 333, 767], 2100, 2500
     M, G = sum(rows), len(rows)
     sets = [(Operand([(N, r) for r in rows], 0, False, 40 + i),
              Operand([(K, r) for r in rows], 0, False, 50 + i)) for i in range(3)]
