@@ -214,6 +214,11 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
     const int nb = (a.K + 15) >> 4, nchunk = (a.K + kChunk - 1) / kChunk;
     const int partial = a.K % kChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
     const int stages = (nchunk + Plan::kFit - 1) / Plan::kFit;
+    // Rows some kilobytes apart lie in few of the memory's channels at any one k, and
+    // the workgroups walk along k at about the same pace: neighbouring ones start
+    // at different stages.
+    const int first = (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)stages);
+    auto turned = [&](int st) { return st + first < stages ? st + first : st + first - stages; };
     int from = 0;                                 // the next slot to look at
     int e = 0;
     if (EXPERTS) {
@@ -264,8 +269,8 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
         Aim next(a, e, (int)blockIdx.x * Plan::kRows, 16 * wn + r, g);
 #pragma unroll
         for (int j = 0; j < D; j++)
-            if (ks + j * KS < nchunk)
-                next.fetch(w[j], ks + j * KS);
+            if (turned(0) * Plan::kFit + ks + j * KS < nchunk)
+                next.fetch(w[j], turned(0) * Plan::kFit + ks + j * KS);
         if (EXPERTS)
             __syncthreads();                      // slot[]
 
@@ -324,7 +329,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
             for (int j = 0; j < P; j++)
                 xl[j / TB * kSide * 32 * TT + 16 * (j % TB)] = xv[j];
         };
-        load_tokens(0);
+        load_tokens(turned(0));
         const float sg = a.sg[e];
 
         for (int block = (int)blockIdx.x; block < blocks; block += EXPERTS ? step : blocks) {
@@ -395,23 +400,24 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
                 // tokens that fit one stage stay for all blocks
                 if (stages > 1 || block == (int)blockIdx.x) {
                     __syncthreads();
-                    store_tokens(st);
+                    store_tokens(turned(st));
                     __syncthreads();
                     if (stages > 1 && (st + 1 < stages || more))
-                        load_tokens(st + 1 < stages ? st + 1 : 0);
+                        load_tokens(turned(st + 1 < stages ? st + 1 : 0));
                 }
 #pragma unroll
                 for (int j = 0; j < D; j++) {
-                    const int c = st * Plan::kFit + ks + j * KS;
+                    const int c = turned(st) * Plan::kFit + ks + j * KS;
                     if (c < nchunk)
                         work(w[j], ks + j * KS, c);
                     if (Plan::kDot)
                         __builtin_amdgcn_sched_barrier(0);   // one chunk's fragments at a time
                     // the next stage's chunk, or the next block's
-                    if (c + Plan::kFit < nchunk)
-                        aim.fetch(w[j], c + Plan::kFit);
-                    else if (more && ks + j * KS < nchunk)
-                        next.fetch(w[j], ks + j * KS);
+                    const int ahead = turned(st + 1 < stages ? st + 1 : 0) * Plan::kFit + ks + j * KS;
+                    if (st + 1 < stages && ahead < nchunk)
+                        aim.fetch(w[j], ahead);
+                    else if (st + 1 == stages && more && ahead < nchunk)
+                        next.fetch(w[j], ahead);
                 }
             }
 
