@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
     // Rows some kilobytes apart lie in few of the memory's channels at any one k, and
     // the workgroups walk along k at about the same pace: neighbouring ones start
     // at different stages.
-    const int first = (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)stages);
+    const int first = stages > 1 ? (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)stages) : 0;
     auto turned = [&](int st) { return st + first < stages ? st + first : st + first - stages; };
     int from = 0;                                 // the next slot to look at
     int e = 0;
@@ -528,7 +528,8 @@ hipError_t launch_one(MvArgs a, hipStream_t stream)
     // that weights are always under way.  Otherwise a workgroup per block.
     int64_t nx = blocks;
     if (EXPERTS && a.K <= Plan::kFit * kChunk) {
-        const int64_t fill = 2 * 256 / ny > 1 ? 2 * 256 / ny : 1;
+        const int64_t each_y = a.by_slot ? slots : a.G;      // (zero rows take no time)
+        const int64_t fill = 2 * 256 / each_y > 1 ? 2 * 256 / each_y : 1;
         const int64_t each = (blocks + fill - 1) / fill;
         nx = (blocks + each - 1) / each;
     }
