@@ -351,6 +351,19 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
                 if (chunk >= partial)
                     aim.settle(u, chunk, nb, g);
                 const uint4 *xs = reinterpret_cast<const uint4 *>(lds) + 32 * TT * c;
+                // token fragment f of tile t; columns behind the last token are of any
+                // value and not stored
+                auto tokens = [&](int f, int t) {
+                    return __builtin_bit_cast(
+                        bf16x8_t, xs[4 * f * TT + ((g * TT + (r < TT ? r : 0)) ^ (f & kMix)) + 16 * t]);
+                };
+                // read one fragment ahead of their use
+                bf16x8_t xf[2][TB];
+                if constexpr (!Plan::kDot) {
+#pragma unroll
+                    for (int t = 0; t < TB; t++)
+                        xf[0][t] = tokens(0, t);
+                }
 #pragma unroll
                 for (int b = 0; b < 4; b++) {     // block b of the lane's 4: fragments 2b, 2b + 1
                     const float s = b == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 0)
@@ -376,15 +389,17 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const 
                                 sum[t] = dot2(w3, x.w, sum[t]);
                             }
                         } else {
+                            if (f < 7) {
+#pragma unroll
+                                for (int t = 0; t < TB; t++)
+                                    xf[(f + 1) & 1][t] = tokens(f + 1, t);
+                            }
                             const bf16x8_t wf = weights8(d, s);
 #pragma unroll
-                            for (int t = 0; t < TB; t++) {
-                                // columns behind the last token are of any value
-                                // and not stored
-                                const bf16x8_t xf = __builtin_bit_cast(
-                                    bf16x8_t, xs[4 * f * TT + ((g * TT + (r < TT ? r : 0)) ^ (f & kMix)) + 16 * t]);
-                                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[t], 0, 0, 0);
-                            }
+                            for (int t = 0; t < TB; t++)
+                                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[f & 1][t], acc[t], 0, 0, 0);
+                            if (TB > 1)
+                                __builtin_amdgcn_sched_barrier(0);   // and not all reads first
                         }
                     }
                     if constexpr (Plan::kDot) {
