@@ -1,7 +1,7 @@
 """Python binding of libmxcast (include/mxcast.h): block-scaled quantisation of
-bf16 tensors on MI355X.
+bf16 tensors on MI355X, and the products of what it writes.
 
-Argument marshalling only.  Every step of the cast runs in the HIP kernels of
+Argument marshalling only.  Every step of the casts and products runs in the HIP kernels of
 libmxcast.so; PyTorch provides device memory and the stream.  If the library
 is not built, importing a function raises -- there is no fallback path.
 
@@ -13,7 +13,8 @@ The same names as the C ABI:
     *_workspace_size, nvfp4_matvec, nvfp4_matvec_experts, mx_status_str,
     mx_abi_version
 take torch tensors (bf16 inputs, or int16/uint16 holding bf16 bits, on a ROCm
-device) and return dicts of uint8 / float32 torch tensors on the same device.
+device).  The casts return dicts of uint8 / float32 torch tensors on the same
+device; the products take those and return a bf16 or float32 tensor.
 The MXFP8 casts take the format flags ELEM_E5M2 / SCALE_ROUND_UP and the
 layout flag SCALE_TILED OR-ed into `axis`, as the C ABI does.
 `lib()` returns the raw ctypes library for callers that pass pointers
@@ -632,13 +633,20 @@ def _scale_bytes(rows, cols, flags):
     return rows * nb
 
 
+def _current_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _launch(where, dev, stream, fn, *args):
-    """Calls fn on the tensors' device (made current for the call) and stream."""
+    """Calls fn on the tensors' device (made current for the call) and stream.
+    (The current stream's handle alone: making a torch.cuda.Stream of it takes 2
+    of the 10 microseconds of a call.)"""
+    handle = _current_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(dev, stream))
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev, stream))
+            st = fn(*args, handle)
     if st:
         _check(st, where)
 

@@ -1,13 +1,14 @@
-// mm_any.hip -- products of MXFP8 operands of any shape and alignment.
+// mm_any.hip -- products of MXFP8 operands too small for the other kernels' loads:
+// fewer than 16 bytes of codes or 8 of scales in one of them.
 //
 // Y_g[m][n] = sum_k A_g[m][k] B_g[n][k], each operand's value being its
 // element times 2^(byte - 127) of its 32-element block along k.  (MmMode has the
-// two ways to compute it.)
+// two ways to compute it.)  Such an operand has at most 7 blocks, so time is a
+// launch (3 us) and the output; nothing here is tuned.
 //
-// A workgroup of 4 waves owns 64 x 64 outputs, a wave 32 x 32.  Rows may start
-// at any byte, so the codes come through registers (16-byte loads without
-// alignment; the last, partial chunk of a row byte by byte, zeros behind it)
-// into LDS, 128 k at a time.
+// A workgroup of 4 waves owns 64 x 64 outputs, a wave 32 x 32.  Codes come through
+// registers (16 bytes inside a row, else byte by byte, zeros behind it) into LDS,
+// 128 k at a time.
 #include "launch_mm.h"
 #include "mm_common.h"
 
