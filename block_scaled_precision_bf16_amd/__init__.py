@@ -625,6 +625,29 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _group_rows(group_rows, M=None):
+    """The group sizes as ints, checked as _group_total does."""
+    rows = [int(r) for r in group_rows]
+    if rows and min(rows) < 0 or M is not None and sum(rows) != M:
+        _group_total(rows, M)
+    return rows
+
+
+def _group_scale_bytes(rows, cols, flags):
+    """Bytes of the scales of operands [r][cols], r in rows, one after the other."""
+    nb = -(-cols // 32)
+    if flags & SCALE_TILED:
+        return sum((r + 31) // 32 for r in rows) * -(-nb // 8) * 256
+    return sum(rows) * nb
+
+
+def _group_col_scale_bytes(rows, cols, flags):
+    """The same of their transposed operands [cols][r]."""
+    if flags & SCALE_TILED:
+        return -(-cols // 32) * sum((r + 255) // 256 for r in rows) * 256
+    return cols * sum((r + 31) // 32 for r in rows)
+
+
 def _scale_bytes(rows, cols, flags):
     """Bytes of one operand's scales (none for an operand without elements)."""
     nb = -(-cols // 32)
@@ -711,16 +734,16 @@ def mx_matmul_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, workspace=N
     if qa.dim() != 2:
         raise ValueError(f"qa must be 2-D, got shape {tuple(qa.shape)}")
     (M, K), G, dev = qa.shape, len(group_rows), qa.device
-    _group_total(group_rows, M)
+    rows = _group_rows(group_rows, M)
     if G == 0 or K == 0 or qb.numel() % (G * K):
         raise ValueError(f"qb must hold {G} matrices with rows of {K}, got {qb.numel()} bytes")
     N = qb.numel() // (G * K)
-    _want_bytes(sa, sum(_scale_bytes(int(r), K, flags) for r in group_rows), "sa")
+    _want_bytes(sa, _group_scale_bytes(rows, K, flags), "sa")
     _want_bytes(sb, G * _scale_bytes(N, K, flags), "sb")
     y = _product_out(out, (M, N), flags, dev, stream)
     _on_device(dev, sa, qb, sb)
-    L, rows = lib(), _rows_arg(group_rows)
-    rp = ctypes.addressof(rows)
+    L, table = lib(), (ctypes.c_int64 * G)(*rows)
+    rp = ctypes.addressof(table)
     ws, wp, wn = _product_ws(workspace, L.mx_matmul_grouped_workspace_size(N, K, rp, G, flags), dev,
                              stream)
     _launch("mx_matmul_grouped", dev, stream, L.mx_matmul_grouped, qa.data_ptr(), sa.data_ptr(),
@@ -737,18 +760,18 @@ def mx_matmul_wgrad_grouped(qa, sa, qb, sb, group_rows, flags=0, out=None, works
     for t, name in ((qa, "qa"), (sa, "sa"), (qb, "qb"), (sb, "sb")):
         _codes(t, name)
     G, dev = len(group_rows), qa.device
-    M = sum(int(r) for r in group_rows)
-    _group_total(group_rows, M)
+    rows = _group_rows(group_rows)
+    M = sum(rows)
     if M == 0 or qa.numel() % M or qb.numel() % M:
         raise ValueError(f"qa and qb must hold whole columns of {M} rows, got {qa.numel()} and "
                          f"{qb.numel()} bytes")
     N, K = qa.numel() // M, qb.numel() // M
-    _want_bytes(sa, sum(_scale_bytes(N, int(r), flags) for r in group_rows), "sa")
-    _want_bytes(sb, sum(_scale_bytes(K, int(r), flags) for r in group_rows), "sb")
+    _want_bytes(sa, _group_col_scale_bytes(rows, N, flags), "sa")
+    _want_bytes(sb, _group_col_scale_bytes(rows, K, flags), "sb")
     y = _product_out(out, (G, N, K), flags, dev, stream)
     _on_device(dev, sa, qb, sb)
-    L, rows = lib(), _rows_arg(group_rows)
-    rp = ctypes.addressof(rows)
+    L, table = lib(), (ctypes.c_int64 * G)(*rows)
+    rp = ctypes.addressof(table)
     ws, wp, wn = _product_ws(workspace, L.mx_matmul_wgrad_grouped_workspace_size(N, K, rp, G, flags),
                              dev, stream)
     _launch("mx_matmul_wgrad_grouped", dev, stream, L.mx_matmul_wgrad_grouped, qa.data_ptr(),

@@ -92,9 +92,9 @@ constexpr int kBand = 4;
 __device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int id, int tile_m,
                                           int tile_n)
 {
-    int g = 0;
-    while (id >= t.tile0[g + 1])
-        g++;
+    // (all lanes look at once: one group after the other is a chain of loads)
+    const int L = (int)threadIdx.x & 63;
+    const int g = __popcll(__ballot(L < t.count && id >= t.tile0[L + 1 < t.count ? L + 1 : t.count]));
     const int64_t r0 = t.row0[g], rows = t.rows[g];
     MmTile w;
     w.M = a.sum_rows ? a.dim : rows;
@@ -152,6 +152,22 @@ __device__ __forceinline__ void store_out(const MmArgs &a, int64_t i, float v)
     }
 }
 
+// Outputs i and i + 1, at any element (rows of odd lengths): one store.
+__device__ __forceinline__ void store_out2(const MmArgs &a, int64_t i, float v0, float v1)
+{
+    if (a.out_f32) {
+        float *y = static_cast<float *>(a.y) + i;
+        float2 o = make_float2(0.f, 0.f);
+        if (a.accumulate)
+            __builtin_memcpy(&o, y, 8);
+        o = a.accumulate ? make_float2(o.x + v0, o.y + v1) : make_float2(v0, v1);
+        __builtin_memcpy(y, &o, 8);
+    } else {
+        const uint32_t o = bf16_pair(v0, v1);
+        __builtin_memcpy(static_cast<uint16_t *>(a.y) + i, &o, 4);
+    }
+}
+
 __device__ __forceinline__ uint32_t clip31(int64_t v)
 {
     return (uint32_t)(v < kMaxRecords ? v : kMaxRecords);
@@ -188,6 +204,7 @@ struct ByteRows {
     int64_t last;
     uint32_t lead;             // offset of the tile's first row
 
+    ByteRows() = default;
     // rows of `pitch` bytes from `first` on, of an array that `left` bytes from
     // there on belong to
     __device__ __forceinline__ ByteRows(const uint8_t *array, const uint8_t *first, int64_t left)

@@ -217,16 +217,21 @@ __global__ __launch_bounds__(64 * KW, MT == 1 && KW == 4 ? 3 : 2) void mm_small_
                 part[(wave * MT + i) * 1024 + 64 * e + L] += acc[i][e];
     __syncthreads();
     // register e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4, column r
-    for (int o = tid; o < MT * 1024; o += 64 * KW) {
-        const int i = o >> 10, m = o >> 5 & 31, n = o & 31;
+    for (int o = tid; o < MT * 512; o += 64 * KW) {
+        const int i = o >> 9, m = o >> 4 & 31, n = 2 * (o & 15);
         const int e = (m >> 3) * 4 + (m & 3), lane = n + 32 * (m >> 2 & 1);
-        float v = 0.f;
+        float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < KW / 2; k++)
-            v += part[(k * MT + i) * 1024 + 64 * e + lane];
+        for (int k = 0; k < KW / 2; k++) {
+            const float2 p = *reinterpret_cast<const float2 *>(part + (k * MT + i) * 1024 + 64 * e + lane);
+            v0 += p.x;
+            v1 += p.y;
+        }
         const int64_t row = w.m0 + 32 * i + m, col = w.n0 + n;
-        if (row < w.M && col < a.N)
-            store_out(a, w.y0 + row * a.N + col, v);
+        if (row < w.M && col + 1 < a.N)
+            store_out2(a, w.y0 + row * a.N + col, v0, v1);
+        else if (row < w.M && col < a.N)
+            store_out(a, w.y0 + row * a.N + col, v0);
     }
 }
 

@@ -506,8 +506,7 @@ struct MmKernel {
     }
 
     // Writes the outputs (kMx: bf16, kExact: fp32, with ADD added to what is
-    // there); PAIR: a lane's two neighbouring columns in one store, where rows
-    // start at an even element.
+    // there); PAIR: a lane's two neighbouring columns in one store.
     template <bool PAIR, bool ADD>
     __device__ __forceinline__ void store_form() const
     {
@@ -563,7 +562,9 @@ struct MmKernel {
 
     __device__ __forceinline__ void store() const
     {
-        const bool pair = (a.N & 1) == 0;
+        // (rows of an odd length: pairs at any element, which memory takes, where
+        // none holds the last column alone)
+        const bool pair = (a.N & 1) == 0 || w.n0 + TN <= a.N;
         if (MODE == kMx)
             pair ? store_form<true, false>() : store_form<false, false>();
         else if (a.accumulate)

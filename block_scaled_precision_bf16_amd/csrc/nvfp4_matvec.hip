@@ -572,7 +572,15 @@ hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
     // tokens that a weight matrix meets: all, or an expert's fair share twice over
     const int64_t slots = (int64_t)a.T * a.top;
     const int64_t tokens = a.experts ? (2 * slots + a.G - 1) / a.G : a.T;
-    const int64_t most = slots < tokens ? slots : tokens;
+    int64_t most = slots < tokens ? slots : tokens;
+    // Few rows of many tokens: 16 or 32 at a time, the weights read again (from the
+    // caches) for each, rather than few workgroups.
+    if (!a.experts && a.T > 16) {
+        const int64_t by16 = (((int64_t)a.N + 31) / 32) * ((a.T + 15) / 16);
+        const int64_t by32 = (((int64_t)a.N + 63) / 64) * ((a.T + 31) / 32);
+        most = by16 <= 512 ? 16 : by32 <= 256 ? 32 : 64;
+        most = most > a.T ? a.T : most;
+    }
     return most <= 1    ? launch<1>(a, stream)
            : most <= 2  ? launch<2>(a, stream)
            : most <= 8  ? launch<8>(a, stream)
