@@ -100,16 +100,16 @@ struct Rows {
 };
 
 // Through the wave's own 4 KB of LDS (whose accesses come in order): chunk c of row
-// R lies in slot c ^ R % 8 of the row, so that 8 lanes that are served together
-// use all banks, writing and reading.
+// R lies in slot c ^ (R / 2 mod 8) of the row, so that 16 lanes that are served
+// together use all 64 banks, writing and reading.
 __device__ __forceinline__ void turn(const Rows &rows, const Load &p, int u, Piece &o, uint4 *lds, int lane)
 {
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        lds[64 * i + (lane & 56) + ((lane & 7) ^ (lane >> 3))] = p.q[i];
+        lds[64 * i + (lane & 56) + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))] = p.q[i];
     asm volatile("" ::: "memory");
     const uint4 *row = lds + 8 * (lane & 31);
-    const int h = lane >> 5, x = lane & 7;
+    const int h = lane >> 5, x = lane >> 1 & 7;
 #pragma unroll
     for (int i = 0; i < 2; i++)
         o.f[i] = join(row[(4 * i + h) ^ x], row[(4 * i + 2 + h) ^ x]);

@@ -12,23 +12,24 @@
 //   done with tile t's buffer, and tile t + 1 is there; load tile t + NB
 //   step 1 of tile t:  MFMAs on F1, reads of F0 (step 0 of tile t + 1)
 //
-// LDS holds rows of 128 bytes; 16-byte chunk c of a row sits in slot c ^ s(row),
-// so that the 8 lanes a read serves together take 8 different slots.  The
-// direct loads place lanes' 16 bytes one after the other, so the exchange is
-// done on the global side: a lane loads the chunk that belongs in its slot.
+// LDS holds rows of 128 bytes, two of which use its 64 banks once; 16-byte chunk c of
+// row R sits in slot c ^ (R / 2 mod 8), so that the 16 lanes (rows) a read serves
+// together use all banks.  The direct loads place lanes' 16 bytes one after the other, so
+// the exchange is done on the global side: a lane loads the chunk that belongs in
+// its slot.
 //
 // B's rows are dealt to the lanes in pairs: of two neighbouring 32-column
 // tiles, lane r holds columns 2r (first tile) and 2r + 1 (second), so that the
-// outputs leave as whole 128-byte lines from registers.
+// outputs leave as whole 128-byte lines from registers.  In LDS the first tile's rows
+// come first.
 //
-// Measured: 8192^3 to bf16 in 420 us, 2.6 PFLOP/s (a library's fp8 product without
-// block scales reaches 2.96 on this card); the matrix cores are busy 74% of the
-// time at the clock the power limit leaves them (1.7 - 2.0 GHz), and LDS moves
-// 1536 of a tile's 2048 cycles.  To fp32 (twice the MFMA time) 800 us.  A round
-// of 256 tiles takes 6 us + 1.5 us for 128 k, a last round of 128 x 128 parts,
-// which LDS bounds (768 cycles of reads and writes to 512 of MFMA), 0.55 us for
-// 128 k, one of 256 x 128 parts 1.0 us: 64 tiles of 8192 k take 40 us in parts and
-// 92 us whole.  Two buffers instead of four there: 50 us.
+// Measured: 8192^3 to bf16 in 410 - 440 us, 2.5 - 2.7 PFLOP/s (a library's fp8 product
+// without block scales reaches 2.96 on this card); the matrix cores are busy 70% of
+// the time at the clock that the power limit leaves them (1.7 - 2.0 GHz).  To fp32
+// (twice the MFMA time) 800 us.  A round of 256 tiles takes 8 us + 1.5 us for 128 k;
+// its outputs alone are 34 MB, about 7 us.  A last round of 128 x 128 parts takes
+// 0.55 us for 128 k, one of 256 x 128 parts 1.0 us: 64 tiles of 8192 k take 39 us in
+// parts and 92 us whole.  With two buffers instead of four they take 50 us.
 #pragma once
 
 #include "mm_common.h"
@@ -118,7 +119,7 @@ struct MmKernel {
     uint32_t lds0;                 // its LDS address
     int L, wave, h, r;
     int wm, wn;                    // the wave's rows and columns in the tile
-    uint32_t voff[3];              // A; B's loads of even and odd numbers
+    uint32_t voff[4];              // A's loads of even and odd numbers, and B's
     mm_rsrc_t ra, rb;
     uint32_t last_a, last_b;       // the operands' last rows in the tile
     int nt, phase;                 // tiles of k, the first one
@@ -200,24 +201,25 @@ struct MmKernel {
     __device__ __forceinline__ uint32_t offset(int i) const
     {
         const int nth = is_a(i) ? i : i - kLoadsA;
-        return voff[is_a(i) ? 0 : 1 + (nth & 1)] + 8 * nth * (uint32_t)w.K;
+        const int row = is_a(i) ? 8 * nth : 64 * (nth >> 3) + (nth >> 2 & 1) + 16 * (nth & 3);
+        return voff[(is_a(i) ? 0 : 2) + (nth & 1)] + row * (uint32_t)w.K;
     }
     // The chunk of its row that lane L loads (the slot's exchange, above).
     __device__ __forceinline__ uint32_t chunk(int i) const
     {
-        const int row = row8(i) + (L >> 3);
-        return (uint32_t)((L & 7) ^ ((is_a(i) ? row : row >> 1) & 7));
+        static_assert(kLoadsA % 2 == 0 && TN / 32 % 2 == 0, "rows 16 n + 0 .. 7 by even loads");
+        return (uint32_t)((L & 7) ^ (4 * ((is_a(i) ? i : i - kLoadsA) & 1) + (L >> 4)));
     }
 
     __device__ __forceinline__ i32x8_t frag_a(int t, int s, int i) const
     {
         const uint4 *p = reinterpret_cast<const uint4 *>(lds + buf(t)) + (wm + 32 * i + r) * 8;
-        return join(p[(4 * s + h) ^ (r & 7)], p[(4 * s + 2 + h) ^ (r & 7)]);
+        return join(p[(4 * s + h) ^ (r >> 1 & 7)], p[(4 * s + 2 + h) ^ (r >> 1 & 7)]);
     }
     __device__ __forceinline__ i32x8_t frag_b(int t, int s, int j) const
     {
-        const uint4 *p = reinterpret_cast<const uint4 *>(lds + buf(t)) + (TM + brow(j)) * 8;
-        return join(p[(4 * s + h) ^ (r & 7)], p[(4 * s + 2 + h) ^ (r & 7)]);
+        const uint4 *p = reinterpret_cast<const uint4 *>(lds + buf(t)) + (TM + wn + 32 * j + r) * 8;
+        return join(p[(4 * s + h) ^ (r >> 1 & 7)], p[(4 * s + 2 + h) ^ (r >> 1 & 7)]);
     }
     // One of a step's MT + NT fragments.
     __device__ __forceinline__ void read(Frags &f, int t, int s, int i) const
@@ -434,10 +436,11 @@ struct MmKernel {
         last_a = (uint32_t)(w.M - w.m0 < TM ? w.M - w.m0 : TM) - 1;
         last_b = (uint32_t)(a.N - w.n0 < TN ? a.N - w.n0 : TN) - 1;
 #pragma unroll
-        for (int i = 0; i < 3; i++) {
-            const int l = i == 0 ? 0 : kLoadsA + i - 1;    // the load it is for
-            const int row = row8(l) + (L >> 3) - (i ? TM : 0) - (i == 2 ? 8 : 0);
-            voff[i] = (uint32_t)(row * (int)w.K) + 16 * chunk(l);
+        for (int i = 0; i < 2; i++) {
+            const int ra = 8 * wave * kLoadsA + (L >> 3), p = wave * (TN / 32);
+            const int rb = 64 * (p >> 3) + (p >> 2 & 1) + 2 * (L >> 3);
+            voff[i] = (uint32_t)(ra * (int)w.K) + 16 * chunk(i);
+            voff[2 + i] = (uint32_t)(rb * (int)w.K) + 16 * chunk(kLoadsA + i);
         }
 #pragma unroll
         for (int i = 0; i < MT; i++)
