@@ -151,36 +151,42 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
     // us).
     const int small_m = small32 <= mxk::kMmCUs || most_m <= 32 ? 32 : 64;
     const int64_t small = small_m == 32 ? small32 : small64;
-    double small_bytes = 0;
+    double small_bytes = 1, slow_bytes = 1;
     for (int g = 0; g < G; g++) {
         const int64_t m = a.sum_rows ? a.dim : t.rows[g], k = a.sum_rows ? t.rows[g] : a.dim;
-        small_bytes += (double)(ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN) * (small_m + mxk::kMmSmallN) * k);
+        const double b = (double)(ceil_div(m, small_m) * ceil_div(a.N, mxk::kMmSmallN) * (small_m + mxk::kMmSmallN) * k);
+        small_bytes += b;
+        slow_bytes += b * (k % 16 == 0 ? a.out_f32 ? 1.2 : 1.0 : a.out_f32 ? 2.0 : 1.5);
     }
     p = MmPlan{};
     p.waves = small <= mxk::kMmCUs ? 8 : 4;
-    // Microseconds, as measured (graph replays).  The small kernel: its waves' share
-    // of k, one after the other, and what each workgroup reads for itself, at 14 TB/s
-    // from the caches, partly at the same time; 5.4 ns for each workgroup that does not
-    // start at once.  The tiled one: rounds of tiles, of which the outputs are 8 us (in
-    // fp32 14), and the last, partial one, whose steps in parts take longer than their
-    // share; in fp32 twice the time of a step; the copy of unaligned rows.
-    const double f = a.out_f32 ? 2 : 1;
-    const double lat = (double)ceil_div(most_k, 128) * (a.out_f32 ? 1.2 : 1.0) *
+    // Microseconds, as measured (graph replays).
+    // The small kernel: its waves' share of k, one after the other, and what each
+    // workgroup reads for itself, at 14 TB/s from the caches, partly at the same time;
+    // for each workgroup that does not start at once 5.4 ns, or 9 with its reads; all
+    // that 1.2 times for fp32 outputs, 1.5 (2) times for unaligned rows.
+    const double lat = (double)ceil_div(most_k, 128) *
                        (small_m == 32 ? p.waves == 8 ? 0.10 : 0.14 : p.waves == 8 ? 0.19 : 0.22);
-    const double read = small_bytes / 14e6;
-    const double small_us = 3 + (lat > read ? lat + read / 4 : read + lat / 4) +
-                            (small > mxk::kMmCUs ? 5.4e-3 * (double)(small - mxk::kMmCUs) : 0);
+    const double read = small_bytes / 14e6, each = 9e-3 - read / (double)small;
+    const double more = small > mxk::kMmCUs ? (double)(small - mxk::kMmCUs) : 0;
+    const double small_us = 3 + slow_bytes / small_bytes * ((lat > read ? lat + read / 4 : read + lat / 4) +
+                                                            (each > 5.4e-3 ? each : 5.4e-3) * more);
+    // The tiled one: rounds of tiles, of which the outputs are 8 us (in fp32 14), and the
+    // last, partial one, whose steps in parts take longer than their share; in fp32
+    // twice the time of a step; at least the longest sum; the copy of unaligned rows.
     const int parts = last_parts(big);
     const int64_t last = big % mxk::kMmCUs;
-    const double steps = tile_steps / (double)big;      // a tile's, on average
-    const double round = a.out_f32 ? 14 + 3 * steps : 8 + 1.5 * steps;
-    double tile_us = 4 + (double)(big / mxk::kMmCUs) * round;
-    if (last != 0)
-        tile_us += parts == 4   ? 1 + (a.out_f32 ? 0.8 : 0.5) * steps + f * (double)last / 32
-                   : parts == 2 ? 4 * f + 0.95 * f * steps
-                                : round;
-    if (!rows16)
-        tile_us += 3 + (double)(n.qa + n.qb) / 2e6;
+    auto round = [&](double steps) { return a.out_f32 ? 14 + 3 * steps : 8 + 1.5 * steps; };
+    auto partial = [&](double steps) {
+        const double f = a.out_f32 ? 2 : 1;
+        return parts == 4   ? 1 + (a.out_f32 ? 0.8 : 0.5) * steps + f * (double)last / 32
+               : parts == 2 ? 4 * f + 0.95 * f * steps
+                            : round(steps);
+    };
+    const double steps = tile_steps / (double)big, most = (double)ceil_div(most_k, 128);
+    const double all = (double)(big / mxk::kMmCUs) * round(steps) + (last ? partial(steps) : 0);
+    const double longest = big < mxk::kMmCUs ? partial(most) : round(most);
+    const double tile_us = 4 + (all > longest ? all : longest) + (rows16 ? 0 : 7 + (double)(n.qa + n.qb) / 2e6);
     if (n.qa < 16 || n.qb < 16 || n.sa < 8 || n.sb < 8) {
         p.kind = kAny;
         p.tile_m = p.tile_n = mxk::kMmAnyTile;
