@@ -112,6 +112,7 @@ struct MmPlan {
     MmKind kind;
     int tile_m, tile_n;
     int waves;                 // of a small product's workgroup
+    bool square;               // tiles of 128 x 128
     bool pack;                 // rows are copied to 128-byte boundaries first
     int64_t pack_a, pack_b;    // bytes of the copies
 };
@@ -199,6 +200,15 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
         p.tile_m = mxk::kMmTileM;
         p.tile_n = mxk::kMmTileN;
         p.pack = !rows16;
+        // Tiles of 128 x 128, two workgroups per CU, whose outputs and starts overlap,
+        // where the sums are short (4096 x 8192 outputs with 512 k: 31.6 -> 28.7 us) or
+        // there are few tiles (2048 x 4096 with 2048 k: 24.3 -> 21.6 us); elsewhere their
+        // reads take longer (8192^3: 414 -> 574 us; 2048^2 with 4096 k, where parts
+        // have four buffers: 22.8 -> 26.3 us).
+        p.square = 4 * big <= kMaxTiles &&
+                   (steps <= 4 || (2 * big <= mxk::kMmCUs && steps <= 20));
+        if (p.square)
+            p.tile_m = p.tile_n = mxk::kMmPart;
     }
     if (p.pack) {
         const int64_t rows_a = a.sum_rows ? 0 : (int64_t)n.qa / a.dim, pitch = mxk::mm_pitch(a.dim);
@@ -213,7 +223,8 @@ bool plan_mm(const mxk::MmArgs &a, mxk::MmTable &t, const MmBytes &n, MmPlan &p)
             return false;
     }
     t.tile0[G] = (int32_t)tiles;
-    t.parts = p.kind == kTiles ? parts : 1;
+    t.parts = p.kind == kTiles && !p.square ? parts : 1;
+    t.square = p.square;
     t.whole = (int32_t)(t.parts == 1 ? tiles : tiles - tiles % mxk::kMmCUs);
     return true;
 }

@@ -21,6 +21,7 @@ struct MmTable {
     int32_t count;                      // the groups, in the order of their tiles
     int32_t whole;                      // tiles not taken in parts
     int32_t parts;                      // of each of the others
+    int32_t square;                     // tiles of kMmPart x kMmPart, all whole
     int32_t tile0[kMmMaxGroups + 1];    // first workgroup tile of each
     int32_t rows[kMmMaxGroups];
     int32_t index[kMmMaxGroups];        // its place in the caller's order

@@ -84,7 +84,8 @@ __device__ __forceinline__ mm_rsrc_t rows_rsrc(const uint8_t *p, int64_t rows, i
 }
 constexpr uint32_t kDeadRow = 0xFFFFFFF0u;   // behind every bound: loads zeros
 
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
+// PAIRED: two workgroups share a CU and its LDS.
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool PAIRED = false>
 struct MmKernel {
     static constexpr int MT = TM / 64, NT = TN / 64;      // 32-row tiles of a wave
     static constexpr int kBuf = (TM + TN) * 128;          // bytes of an LDS buffer
@@ -92,7 +93,7 @@ struct MmKernel {
     // LDS buffers: smaller tiles take less time, and have more of them under way.
     // (Compact scales come through registers, which the compiler waits for with
     // all loads: two buffers.)
-    static constexpr int NB = !TILED ? 2 : TM == 128 ? 4 : TN == 128 ? 3 : 2;
+    static constexpr int NB = !TILED || PAIRED ? 2 : TM == 128 ? 4 : TN == 128 ? 3 : 2;
     // Scales of 8 blocks and all rows; of the tiled ones, (NB + 1) / 2 buffers and
     // a wave's share of the loads, which go with those of the first of two tiles.
     static constexpr int kScales = (TM + TN) * 8;
@@ -577,11 +578,11 @@ struct MmKernel {
     }
 };
 
-template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
+template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool PAIRED = false>
 __device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, uint8_t *lds)
 {
     typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
-    MmKernel<MODE, FA, FB, TM, TN, TILED> k{
+    MmKernel<MODE, FA, FB, TM, TN, TILED, PAIRED> k{
         a, w,
         ByteRows<8>(a.sa, w.sa + w.m0 * w.nb, w.sa_left - w.m0 * w.nb),
         ByteRows<8>(a.sb, w.sb + w.n0 * w.nb, w.sb_left - w.n0 * w.nb)};
@@ -621,10 +622,31 @@ __global__ __launch_bounds__(256, 1) void mm_tile_kernel(const MmArgs a, const M
         mm_tile_run<MODE, FA, FB, S, S, TILED>(a, w, mm_lds);
 }
 
+// Tiles of 128 x 128 only, two workgroups per CU.
+template <MmMode MODE, int FA, int FB, bool TILED>
+__global__ __launch_bounds__(256, 2) void mm_square_kernel(const MmArgs a, const MmTable t)
+{
+    extern __shared__ uint8_t mm_lds[];
+    constexpr int S = kMmPart;
+    const MmTile w = mm_tile(a, t, mm_xcd_order((int)blockIdx.x, t.whole), S, S);
+    mm_tile_run<MODE, FA, FB, S, S, TILED, true>(a, w, mm_lds);
+}
+
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED>
 hipError_t launch_mm_tile_one(const MmArgs &a, const MmTable &t, hipStream_t stream)
 {
     constexpr int S = kMmPart;
+    if (t.square) {
+        constexpr int bytes = MmKernel<MODE, FA, FB, S, S, TILED, true>::kLds;
+        const hipError_t e =
+            hipFuncSetAttribute(reinterpret_cast<const void *>(mm_square_kernel<MODE, FA, FB, TILED>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL((mm_square_kernel<MODE, FA, FB, TILED>), dim3((unsigned)t.whole), dim3(256), bytes,
+                           stream, a, t);
+        return hipGetLastError();
+    }
     constexpr int l0 = MmKernel<MODE, FA, FB, TM, TN, TILED>::kLds, l1 = MmKernel<MODE, FA, FB, TM, S, TILED>::kLds,
                   l2 = MmKernel<MODE, FA, FB, S, S, TILED>::kLds;
     constexpr int lds = l0 > l1 ? (l0 > l2 ? l0 : l2) : l1 > l2 ? l1 : l2;

@@ -80,7 +80,7 @@ int main()
         v = step == 0 ? v : step == 1 ? v / 16 * 16 : step == 2 ? v / 128 * 128 : v | 1;
         return v < 1 ? (int64_t)1 : v > top ? top : v;
     };
-    int seen[6] = {0, 0, 0, 0, 0, 0}, packed = 0, parts = 0;
+    int seen[6] = {0, 0, 0, 0, 0, 0}, packed = 0, parts = 0, squares = 0;
     for (int it = 0; it < 20000; it++) {
         const bool wgrad = rng() % 2;
         const int G = it % 3 == 0 ? 1 : 1 + (int)(rng() % 64);
@@ -118,8 +118,10 @@ int main()
         CHECK((g_packs != 0) == (ws != 0) && g_packs <= 1 && (g_packs == 0) == (g_a.packed == 0));
         packed += g_packs;
         const bool tiles = g_kind == kTileL || g_kind == kTileF32;
-        const int64_t tm = tiles ? kMmTileM : g_kind == kSmallL ? g_small_rows : kMmAnyTile;
-        const int64_t tn = tiles ? kMmTileN : g_kind == kSmallL ? kMmSmallN : kMmAnyTile;
+        CHECK(g_t.square == 0 || (tiles && g_t.square == 1 && g_t.parts == 1));
+        squares += g_t.square;
+        const int64_t tm = g_t.square ? kMmPart : tiles ? kMmTileM : g_kind == kSmallL ? g_small_rows : kMmAnyTile;
+        const int64_t tn = g_t.square ? kMmPart : tiles ? kMmTileN : g_kind == kSmallL ? kMmSmallN : kMmAnyTile;
         CHECK(g_kind != kSmallL || ((g_small_rows == 32 || g_small_rows == 64) && (g_waves == 4 || g_waves == 8)));
         CHECK(g_a.dim == dim && g_a.N == cols && g_a.sum_rows == wgrad && g_a.tiled == tiled);
         CHECK(g_t.count == G && g_t.tile0[0] == 0);
@@ -176,7 +178,7 @@ int main()
     }
     for (int k : {kTileL, kTileF32, kSmallL, kAnyL})
         CHECK(seen[k] > 50);
-    CHECK(packed > 50 && parts > 50);
+    CHECK(packed > 50 && parts > 50 && squares > 50);
 
     for (int it = 0; it < 5000; it++) {
         const int64_t top = it % 2 ? 4096 : (int64_t)1 << 23;

@@ -1,6 +1,6 @@
-"""MXFP8 products at sizes that take the tiled kernel: whole rounds of 256 x 256
-tiles, the last tiles in parts of 128 x 128, rows copied to 128-byte boundaries,
-operands and outputs past 2^32 bytes.
+"""MXFP8 products at sizes that take the tiled kernels: whole rounds of 256 x 256
+tiles, the last tiles in parts of 128 x 128 or 256 x 128, tiles of 128 x 128, rows
+copied to 128-byte boundaries, operands and outputs past 2^32 bytes.
 
 Operands are exact ones (see product_util), made on the GPU as codes and scale
 bytes: elements n in {-4 .. 4} and scales 2^-1 .. 2^1, so an output must equal the
@@ -76,14 +76,17 @@ def fmt_flags(ea, eb):
     return (mx.A_E5M2 if ea else 0) | (mx.B_E5M2 if eb else 0)
 
 
-# (M, N, K): parts only; 256 whole tiles and parts; three rounds and parts; one
-# partial round of whole tiles; a single round; short, odd and unaligned rows.
+# (M, N, K): tiles of 128 x 128 (few tiles, short sums), odd and unaligned rows; then
+# parts only, whole rounds and parts, halves, one partial round of whole tiles.
 SIZES = [(1500, 1301, 2064), (4200, 4157, 400), (6200, 8300, 144), (3800, 3800, 208),
          (4096, 4096, 512), (257, 16500, 1040), (16501, 259, 528), (5000, 4999, 64), (4999, 5000, 32),
-         (2500, 2300, 2065), (2049, 4095, 1151), (4200, 4157, 330), (700, 9000, 4001)]
-FORMAT_SIZES = [(1500, 1301, 2064), (2500, 2302, 2065)]
+         (2500, 2300, 2065), (2049, 4095, 1151), (4200, 4157, 330), (700, 9000, 4001),
+         (1500, 1301, 4112), (4200, 4157, 656), (6200, 8300, 640), (5000, 4700, 656),
+         (3800, 3801, 784), (4200, 4158, 801), (5000, 4700, 657)]
+FORMAT_SIZES = [(1500, 1301, 2064), (2500, 2302, 2065), (4200, 4157, 656), (5000, 4700, 657)]
 GROUPED = [([1000, 0, 1, 700, 257, 256], 2500, 1040), ([0, 3000, 0], 4050, 1041),
-           ([100] * 40, 4096, 512), ([33, 2900, 5, 0], 3999, 2063)]
+           ([100] * 40, 4096, 512), ([33, 2900, 5, 0], 3999, 2063),
+           ([3000, 0, 1, 700, 257, 256], 4096, 1040)]
 WGRAD = [([1000, 0, 1, 700, 257, 256], 2000, 2500), ([512, 2048, 0, 16], 2100, 2300),
          ([1, 2, 3, 2000], 2999, 2111), ([128] * 30, 1200, 2048), ([31, 0, 1808, 640], 3777, 2050)]
 
@@ -110,9 +113,9 @@ def test_tiles_of_every_format(M, N, K, ea, eb):
         assert_same(y, a.values() @ b.values().t(), f"{M}x{N}x{K} {f}")
 
 
-@pytest.mark.parametrize("N", [1301, 1302])
-def test_tiles_accumulate(N):
-    M, K = 1500, 2064
+@pytest.mark.parametrize("M,N,K", [(1500, 1301, 2064), (1500, 1302, 2064), (4200, 4157, 656),
+                                   (4200, 4158, 656)])
+def test_tiles_accumulate(M, N, K):
     a, b = Operand([(M, K)], 0, False, 5), Operand([(N, K)], 0, False, 6)
     start = torch.randint(-100, 100, (M, N), device="cuda").float()
     y = Guarded((M, N), torch.float32)
