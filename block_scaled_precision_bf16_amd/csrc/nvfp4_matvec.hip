@@ -136,15 +136,15 @@ __device__ __forceinline__ void zero_rows(const MvArgs &a, const int32_t *slot, 
             store_mv(a, (int64_t)(slot ? slot[t] : p + t) * a.N + n, 0.f);
 }
 
-// Waves per SIMD: two workgroups per CU, one for 64 tokens (136 KB of LDS).
-constexpr int mv_occupancy(int tokens) { return tokens == 64 ? 2 : 4; }
+// Waves per SIMD: two workgroups per CU, or one that takes 136 KB of LDS.
+constexpr int mv_occupancy(int tokens, bool few) { return tokens == 64 || (tokens == 16 && few) ? 2 : 4; }
 
 // How a kernel for up to TT tokens is laid out: KS waves share the chunks of a
 // row, each has D of its chunks under way, a stage holds the tokens of D KS
-// chunks.
-template <int TT, bool EXPERTS>
+// chunks.  FEW: for few rows, all 8 waves share them.
+template <int TT, bool EXPERTS, bool FEW>
 struct MvPlan {
-    static constexpr int KS = TT <= 2 && EXPERTS ? 8 : TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 && !EXPERTS ? 4 : 2;
+    static constexpr int KS = FEW || (TT <= 2 && EXPERTS) ? 8 : TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 && !EXPERTS ? 4 : 2;
     static constexpr int kRows = 16 * WN;                     // weight rows of a block
     static constexpr int kFit = D * KS;                       // chunks of a stage
     static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
@@ -207,10 +207,10 @@ struct Aim {
 // EXPERTS: blockIdx.y is the expert (G: the slots without one, whose rows become zeros)
 // or, with a.by_slot, a slot, whose workgroups serve its expert if no earlier
 // slot has the same; else the tile of TT tokens.
-template <int TT, bool EXPERTS>
-__global__ __launch_bounds__(kMvThreads, mv_occupancy(TT)) void mv_kernel(const MvArgs a)
+template <int TT, bool EXPERTS, bool FEW>
+__global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(const MvArgs a)
 {
-    using Plan = MvPlan<TT, EXPERTS>;
+    using Plan = MvPlan<TT, EXPERTS, FEW>;
     constexpr int TB = (TT + 15) / 16;            // token tiles
     constexpr int KS = Plan::KS, P = Plan::kPieces, D = Plan::D;
     constexpr int kMix = TT == 1 ? 3 : 7;         // within a fragment's 4 TT slots
@@ -530,13 +530,13 @@ __global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
         }
 }
 
-template <int TT, bool EXPERTS>
+template <int TT, bool EXPERTS, bool FEW>
 hipError_t launch_one(MvArgs a, hipStream_t stream)
 {
-    using Plan = MvPlan<TT, EXPERTS>;
+    using Plan = MvPlan<TT, EXPERTS, FEW>;
     const int64_t slots = (int64_t)a.T * a.top, blocks = (a.N + Plan::kRows - 1) / Plan::kRows;
     if (Plan::kLds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(mv_kernel<TT, EXPERTS>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(mv_kernel<TT, EXPERTS, FEW>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, Plan::kLds);
         if (e != hipSuccess)
             return e;
@@ -556,7 +556,7 @@ hipError_t launch_one(MvArgs a, hipStream_t stream)
         const int64_t each = (blocks + fill - 1) / fill;
         nx = (blocks + each - 1) / each;
     }
-    hipLaunchKernelGGL((mv_kernel<TT, EXPERTS>), dim3((unsigned)nx, (unsigned)ny), dim3(kMvThreads),
+    hipLaunchKernelGGL((mv_kernel<TT, EXPERTS, FEW>), dim3((unsigned)nx, (unsigned)ny), dim3(kMvThreads),
                        Plan::kLds, stream, a);
     return hipGetLastError();
 }
@@ -564,7 +564,18 @@ hipError_t launch_one(MvArgs a, hipStream_t stream)
 template <int TT>
 hipError_t launch(const MvArgs &a, hipStream_t stream)
 {
-    return a.experts ? launch_one<TT, true>(a, stream) : launch_one<TT, false>(a, stream);
+    if (a.experts)
+        return launch_one<TT, true, false>(a, stream);
+    // Workgroups of 32 rows that do not fill the CUs: twice as many, of 16 (5 tokens by
+    // 1001 x 4095: 7.9 -> 6.7 us, 4096 x 4096: 7.5 -> 5.8 us; but 16384 x 16384: 38 -> 42
+    // us, and 512 x 512, where there is nothing to share: 4.1 -> 4.6 us).  For 16 tokens
+    // only one of them fits a CU's LDS.
+    if constexpr (TT <= 16) {
+        const int64_t blocks = ((int64_t)a.N + 31) / 32 * (((int64_t)a.T + TT - 1) / TT);
+        if (blocks <= (TT == 16 ? 128 : 255) && a.K >= 1024)
+            return launch_one<TT, false, true>(a, stream);
+    }
+    return launch_one<TT, false, false>(a, stream);
 }
 
 }  // namespace
