@@ -11,8 +11,8 @@
 //
 // 8 waves where those workgroups do not fill the CUs more than once (the same product
 // 10.2 us, 64 x 8192 outputs 22.7 us for 23.3), else 4 (16 experts' 64 rows by 4096 x
-// 2048 each: 24.7 us, with 8 waves 36 us); these 25 us are for 105 MB of weights,
-// 4.3 TB/s.
+// 2048 each: 25 - 29 us with 105 MB of weights, some of them from the MALL, 3.6 - 4.3
+// TB/s; with 8 waves 36 us).
 #include "mm_common.h"
 
 namespace mxk {
