@@ -56,12 +56,12 @@ constexpr int64_t mm_pitch(int64_t K) { return (K + 127) / 128 * 128; }
 // which the last ones go.
 constexpr int kMmTileM = 256, kMmTileN = 256, kMmPart = 128;
 constexpr int kMmCUs = 256;
-// The any-shape kernel's tile, and the columns of the small kernel's (32 or 64
-// rows).
+// The tile of the kernel for tiny operands, and the columns of the small kernel's.
 constexpr int kMmAnyTile = 64, kMmSmallN = 32;
 
 hipError_t launch_mm_tile(const MmArgs &a, const MmTable &t, hipStream_t stream);
 hipError_t launch_mm_tile_f32(const MmArgs &a, const MmTable &t, hipStream_t stream);
+// rows: 32 or 64 of a workgroup's tile; waves: 4 or 8, which share k.
 hipError_t launch_mm_small(const MmArgs &a, const MmTable &t, int rows, int waves, hipStream_t stream);
 hipError_t launch_mm_any(const MmArgs &a, const MmTable &t, hipStream_t stream);
 // Copies the operands' rows to qa and qb, mm_pitch apart.
