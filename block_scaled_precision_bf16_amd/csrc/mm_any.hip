@@ -3,8 +3,9 @@
 //
 // Y_g[m][n] = sum_k A_g[m][k] B_g[n][k], each operand's value being its
 // element times 2^(byte - 127) of its 32-element block along k.  (MmMode has the
-// two ways to compute it.)  Such an operand has at most 7 blocks, so time is a
-// launch (3 us) and the output; nothing here is tuned.
+// two ways to compute it; fp32 outputs all go by mfma_far here.)  Such an operand
+// has at most 7 blocks, so time is a launch (3 us) and the output; nothing here is
+// tuned.
 //
 // A workgroup of 4 waves owns 64 x 64 outputs, a wave 32 x 32.  Codes come through
 // registers (16 bytes inside a row, else byte by byte, zeros behind it) into LDS,
@@ -67,26 +68,11 @@ __global__ __launch_bounds__(256) void mm_any_kernel(const MmArgs a, const MmTab
             const uint4 b0 = lds[1][(wn + r) * 8 + (c0 ^ (r & 7))];
             const uint4 b1 = lds[1][(wn + r) * 8 + (c1 ^ (r & 7))];
             const int64_t blk = k0 / 32 + 2 * s, m = w.m0 + wm + r, n = w.n0 + wn + r;
-            if (MODE == kMx) {
-                // the lane's scale byte is block h's
-                const int sa = scale_byte(w.sa, w.M, w.nb, m, blk + h, a.tiled);
-                const int sb = scale_byte(w.sb, a.N, w.nb, n, blk + h, a.tiled);
-                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a0, a1), join(b0, b1), acc,
-                                                                      FA, FB, 0, sa, 0, sb);
-            } else {
-#pragma unroll
-                for (int p = 0; p < 2; p++) {
-                    const float sa = scale_float(scale_byte(w.sa, w.M, w.nb, m, blk + p, a.tiled));
-                    const float sb = scale_float(scale_byte(w.sb, a.N, w.nb, n, blk + p, a.tiled));
-                    const uint4 ca = p ? a1 : a0, cb = p ? b1 : b0;
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        bf16_of_codes8<FA>(ca.x, ca.y, sa), bf16_of_codes8<FB>(cb.x, cb.y, sb), acc,
-                        0, 0, 0);
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        bf16_of_codes8<FA>(ca.z, ca.w, sa), bf16_of_codes8<FB>(cb.z, cb.w, sb), acc,
-                        0, 0, 0);
-                }
-            }
+            // the lane's scale byte is block h's
+            const uint32_t sa = (uint32_t)scale_byte(w.sa, w.M, w.nb, m, blk + h, a.tiled);
+            const uint32_t sb = (uint32_t)scale_byte(w.sb, a.N, w.nb, n, blk + h, a.tiled);
+            acc = MODE == kMx ? mfma_mx<FA, FB, 0>(join(a0, a1), join(b0, b1), acc, sa, sb)
+                              : mfma_far<FA, FB, 0>(join(a0, a1), join(b0, b1), acc, sa, sb);
         }
     }
     // lane (r, h), register i: row 8 (i / 4) + 4 h + i % 4, column r

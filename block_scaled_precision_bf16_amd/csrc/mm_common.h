@@ -23,9 +23,10 @@ __device__ __forceinline__ i32x8_t join(uint4 a, uint4 b)
 //       exponent and cut below 2^-13 of it (measured; everything beyond those 8
 //       is summed in fp32): an error of the order of 1.5e-5 of the result, 100
 //       times below the rounding of a bf16 output, which is where it is used.
-//   kExact: the codes times their scales as bf16 (exact: at most 4 significant
-//       bits), products exact, sums in fp32, by the bf16 MFMA, 32 x 32 x 16, at
-//       half the rate; for fp32 outputs.
+//   kExact: the codes times their scales as bf16 (at most 4 significant bits: exact
+//       where the power of two fits, see far_block), products exact, sums in fp32, by
+//       the bf16 MFMA, 32 x 32 x 16, at half the rate; for fp32 outputs.  A step with
+//       values that bf16 does not hold goes by mfma_far instead.
 enum MmMode { kMx, kExact };
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -48,6 +49,31 @@ __device__ __forceinline__ bf16x8_t bf16_of_codes8(uint32_t lo, uint32_t hi, flo
     const u32x4v_t v = {bf16_of_codes<F, false>(lo, scale), bf16_of_codes<F, true>(lo, scale),
                         bf16_of_codes<F, false>(hi, scale), bf16_of_codes<F, true>(hi, scale)};
     return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// Whether a block has elements that its scale may take out of what bf16 holds, the
+// multiples of 2^-133 below 2^128: E4M3's are multiples of 2^-9 up to 448 = 1.75 2^8,
+// E5M2's of 2^-16 up to 57344 = 1.75 2^15.  (Scale bytes that the casts write for values
+// near the ends of bf16's range; blocks of zeros, whose byte is 0, are not among them.)
+// NaN blocks are.
+template <int F>
+__device__ __forceinline__ bool far_block(uint4 codes, uint32_t byte)
+{
+    constexpr uint32_t lo = F ? 10 : 3, hi = F ? 239 : 246;
+    return ((codes.x | codes.y | codes.z | codes.w) & 0x7F7F7F7Fu) != 0 && byte - lo > hi - lo;
+}
+
+// Bit 7 of each byte is set where the byte of w lies in 64 .. 191: no block is far if
+// it is in all of them, which is cheaper to look at first.
+__device__ __forceinline__ uint32_t middle_bytes(uint32_t w) { return w ^ (w << 1); }
+// The same bits for the bytes behind the first `live`, blocks behind the rows' ends.
+__device__ __forceinline__ uint32_t dead_bytes(int live)
+{
+    return live >= 4 ? 0 : live <= 0 ? 0x80808080u : 0x80808080u << (8 * live);
+}
+__device__ __forceinline__ bool any_not_middle(uint32_t middle)
+{
+    return __ballot((middle & 0x80808080u) != 0x80808080u) != 0;
 }
 
 // fp32 to bf16 bits, to nearest even, NaN kept.
@@ -242,6 +268,32 @@ template <int FA, int FB, int J>
 __device__ __forceinline__ f32x16_t mfma_mx(i32x8_t a, i32x8_t b, f32x16_t c, uint32_t sa, uint32_t sb)
 {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, FB, J, (int)sa, J, (int)sb);
+}
+
+// c + A B^T over 64 k for fp32 outputs at any scales: the block-scaled MFMA takes the
+// powers of two in their whole range, and with one of each 8 neighbouring k at a time,
+// the others 0 in both operands, it has nothing to align.  8 instructions, 4 times the
+// matrix time of the bf16 ones.
+struct Pick {
+    uint32_t even, odd;        // of the even and odd words of codes
+    __device__ __forceinline__ explicit Pick(int q)
+        : even(q < 4 ? 0xFFu << (8 * q) : 0), odd(q < 4 ? 0 : 0xFFu << (8 * (q - 4)))
+    {
+    }
+    __device__ __forceinline__ i32x8_t of(i32x8_t v) const
+    {
+        const int e = (int)even, o = (int)odd;
+        return v & i32x8_t{e, o, e, o, e, o, e, o};
+    }
+};
+
+template <int FA, int FB, int J>
+__device__ __forceinline__ f32x16_t mfma_far(i32x8_t a, i32x8_t b, f32x16_t c, uint32_t sa, uint32_t sb)
+{
+#pragma unroll 1
+    for (int q = 0; q < 8; q++)
+        c = mfma_mx<FA, FB, J>(Pick(q).of(a), Pick(q).of(b), c, sa, sb);
+    return c;
 }
 
 }  // namespace mxk

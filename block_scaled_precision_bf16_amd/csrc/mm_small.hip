@@ -117,15 +117,58 @@ __device__ __forceinline__ void turn(const Rows &rows, const Load &p, int u, Pie
     o.s = rows.scales(p, u);
 }
 
+// The scale bytes that a lane gives the block-scaled MFMA: blocks h and 2 + h, for steps
+// 0 and 1.
+__device__ __forceinline__ uint32_t lane_scales(uint32_t s, int h)
+{
+    return __builtin_amdgcn_perm(0, s, h ? 0x00000301u : 0x00000200u);
+}
+
+template <int F>
+__device__ __forceinline__ bool far_piece(const Piece &p)
+{
+    bool far = false;
+#pragma unroll
+    for (int b = 0; b < 4; b++)
+        far |= far_block<F>(half_of(p.f[b >> 1], b & 1), (p.s >> (8 * b)) & 255);
+    return far;
+}
+
+// kExact: a piece (of `blocks` blocks, or more) with far blocks goes by mfma_far, and
+// leaves zeros for multiply().
+template <int FA, int FB, int MT>
+__device__ __forceinline__ void multiply_far(Piece (&x)[MT], Piece &y, f32x16_t (&acc)[MT], int h, int blocks)
+{
+    uint32_t middle = middle_bytes(y.s);
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+        middle &= middle_bytes(x[m].s);
+    if (__builtin_expect(!any_not_middle(middle | dead_bytes(blocks)), 1))
+        return;
+    bool far = far_piece<FB>(y);
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+        far |= far_piece<FA>(x[m]);
+    if (__builtin_expect(__ballot(far) == 0, 1))
+        return;
+    const uint32_t sy = lane_scales(y.s, h);
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+        const uint32_t sx = lane_scales(x[m].s, h);
+        acc[m] = mfma_far<FA, FB, 0>(x[m].f[0], y.f[0], acc[m], sx, sy);
+        acc[m] = mfma_far<FA, FB, 1>(x[m].f[1], y.f[1], acc[m], sx, sy);
+        x[m].f[0] = x[m].f[1] = i32x8_t{};
+    }
+    y.f[0] = y.f[1] = i32x8_t{};
+}
+
 // acc += A B^T over a piece: two steps of 64 k.  Chunk 2 s + b of a lane (r, h)
 // holds k 16 h .. + 15 of block 2 s + b.
 template <MmMode MODE, int FA, int FB>
 __device__ __forceinline__ void multiply(const Piece &x, const Piece &y, f32x16_t &acc, int h)
 {
     if constexpr (MODE == kMx) {
-        // the lane's scale bytes: blocks h and 2 + h, for steps 0 and 1
-        const uint32_t sel = h ? 0x00000301u : 0x00000200u;
-        const uint32_t sx = __builtin_amdgcn_perm(0, x.s, sel), sy = __builtin_amdgcn_perm(0, y.s, sel);
+        const uint32_t sx = lane_scales(x.s, h), sy = lane_scales(y.s, h);
         acc = mfma_mx<FA, FB, 0>(x.f[0], y.f[0], acc, sx, sy);
         acc = mfma_mx<FA, FB, 1>(x.f[1], y.f[1], acc, sx, sy);
     } else {
@@ -173,6 +216,8 @@ __global__ __launch_bounds__(64 * KW, MT == 1 && KW == 4 ? 3 : 2) void mm_small_
 #pragma unroll
             for (int m = 0; m < MT; m++)
                 turn(m ? ra1 : ra0, pa[i][m], u, x[m], mine + 256 * (m + 1), L);
+            if constexpr (MODE == kExact)
+                multiply_far<FA, FB, MT>(x, y, acc, h, (int)w.nb - 4 * u);
 #pragma unroll
             for (int m = 0; m < MT; m++)
                 multiply<MODE, FA, FB>(x[m], y, acc[m], h);

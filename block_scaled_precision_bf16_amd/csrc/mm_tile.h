@@ -26,7 +26,7 @@
 // Measured: 8192^3 to bf16 in 410 - 440 us, 2.5 - 2.7 PFLOP/s (a library's fp8 product
 // without block scales reaches 2.96 on this card); the matrix cores are busy 70% of
 // the time at the clock that the power limit leaves them (1.7 - 2.0 GHz).  To fp32
-// (twice the MFMA time) 800 us.  A round of 256 tiles takes 8 us + 1.5 us for 128 k;
+// (twice the MFMA time) 760 us, 11 of which the look for far blocks takes.  A round of 256 tiles takes 8 us + 1.5 us for 128 k;
 // its outputs alone are 34 MB, about 7 us.  A last round of 128 x 128 parts takes
 // 0.55 us for 128 k, one of 256 x 128 parts 1.0 us: 64 tiles of 8192 k take 39 us in
 // parts and 92 us whole.  With two buffers instead of four they take 50 us.
@@ -133,6 +133,8 @@ struct MmKernel {
     // kMx: the words of the lane's blocks (byte j: step j of the next four);
     // kExact: those of even blocks and of odd ones
     uint32_t sa[MT][W], sb[NT][W];
+    int at_a[MT], at_b[NT];        // kExact, tiled: where a lane's words are
+    bool odd_scales;               // kExact: some of them may make a block far (wave-uniform)
     f32x16_t acc[MT][NT];
 
     // Row of B in the workgroup tile that lane r of the wave's column tile j
@@ -231,10 +233,31 @@ struct MmKernel {
             f.a[i - NT] = frag_a(t, s, i - NT);
     }
 
-    // Tiled: the words of the tiles in places t (even) and t + 1.
+    // The words of the tiles in places t (even) and t + 1.
     struct Words {
         uint32_t a[MT][W], b[NT][W];
+        uint32_t middle[W];            // kExact: of those looked at
+
+        __device__ __forceinline__ void look(int i)
+        {
+            if (i < MT * W)
+                middle[i % W] &= middle_bytes(a[i / W][i % W]);
+            else if (i < (MT + NT) * W)
+                middle[i % W] &= middle_bytes(b[i / W - MT][i % W]);
+        }
+        __device__ __forceinline__ void look_at_none()
+        {
+            middle[0] = middle[W - 1] = ~0u;
+        }
     };
+    // (kExact: rows behind the last one, whose elements are zeros, take that one's
+    // words, so that only scales that count are looked at.)
+    __device__ __forceinline__ static int word_at(int row) { return (row >> 5) * 256 + 4 * (row & 31); }
+    __device__ __forceinline__ int word_a(int i) const
+    {
+        return MODE == kExact ? at_a[i] : ((wm >> 5) + i) * 256 + 4 * r;
+    }
+    __device__ __forceinline__ int word_b(int j) const { return MODE == kExact ? at_b[j] : word_at(brow(j)); }
     __device__ __forceinline__ void read_words(Words &o, int t) const
     {
         const uint8_t *p = lds + scale_buf(t);
@@ -243,13 +266,14 @@ struct MmKernel {
             const int at = 128 * (MODE == kMx ? h : k);
 #pragma unroll
             for (int j = 0; j < NT; j++)
-                o.b[j][k] = *reinterpret_cast<const uint32_t *>(p + TM * 8 + (brow(j) >> 5) * 256 + 4 * (brow(j) & 31) + at);
+                o.b[j][k] = *reinterpret_cast<const uint32_t *>(p + TM * 8 + word_b(j) + at);
 #pragma unroll
             for (int i = 0; i < MT; i++)
-                o.a[i][k] = *reinterpret_cast<const uint32_t *>(p + ((wm >> 5) + i) * 256 + 4 * r + at);
+                o.a[i][k] = *reinterpret_cast<const uint32_t *>(p + word_a(i) + at);
         }
     }
-    __device__ __forceinline__ void take_words(const Words &o)
+    // The words of the tiles in places 2 place and 2 place + 1 in use.
+    __device__ __forceinline__ void take_words(const Words &o, int place)
     {
 #pragma unroll
         for (int k = 0; k < W; k++) {
@@ -259,6 +283,12 @@ struct MmKernel {
 #pragma unroll
             for (int j = 0; j < NT; j++)
                 sb[j][k] = o.b[j][k];
+        }
+        if (MODE == kExact) {
+            // (byte j of word k: block 2 j + k)
+            const int live = (int)w.nb - 8 * (turned(2 * place) >> 1);
+            odd_scales = any_not_middle((o.middle[0] | dead_bytes((live + 1) >> 1)) &
+                                        (o.middle[W - 1] | dead_bytes(live >> 1)));
         }
     }
 
@@ -313,16 +343,16 @@ struct MmKernel {
         const uint4 u = rows.fix(make_uint4(v.x, v.y, 0, 0), off, at, n);
         return make_uint2(u.x, u.y);
     }
-    // Compact: the words of the four steps of `place` in use.
-    __device__ __forceinline__ void read_scales(int place)
+    // Compact: the words of the four steps of `place`.
+    __device__ __forceinline__ void read_scales(Words &o, int place) const
     {
         const uint2 *p = reinterpret_cast<const uint2 *>(lds + NB * kBuf) + (place & 1) * (TM + TN);
 #pragma unroll
         for (int i = 0; i < MT; i++)
-            words(sa[i], p[wm + 32 * i + r]);
+            words(o.a[i], p[wm + 32 * i + r]);
 #pragma unroll
         for (int j = 0; j < NT; j++)
-            words(sb[j], p[TM + brow(j)]);
+            words(o.b[j], p[TM + brow(j)]);
     }
     __device__ __forceinline__ void words(uint32_t (&o)[W], uint2 v) const
     {
@@ -331,10 +361,57 @@ struct MmKernel {
             o[W - 1] = __builtin_amdgcn_perm(v.y, v.x, 0x07050301u);
     }
 
+    template <int F, int J>
+    __device__ __forceinline__ static bool far_of(const i32x8_t &f, const uint32_t (&s)[W])
+    {
+        return far_block<F>(make_uint4((uint32_t)f[0], (uint32_t)f[1], (uint32_t)f[2], (uint32_t)f[3]),
+                            (s[0] >> (8 * J)) & 255) ||
+               far_block<F>(make_uint4((uint32_t)f[4], (uint32_t)f[5], (uint32_t)f[6], (uint32_t)f[7]),
+                            (s[W - 1] >> (8 * J)) & 255);
+    }
+    // kExact, a step with odd scales: if it has a far block, its MFMAs as in mfma_far,
+    // and then zeros for the usual ones.  (Those instead of these, in two branches,
+    // spill 1900 registers.)
+    template <int J>
+    __device__ __forceinline__ void step_far(Frags &f)
+    {
+        bool far = false;
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+            far |= far_of<FA, J>(f.a[i], sa[i]);
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            far |= far_of<FB, J>(f.b[j], sb[j]);
+        if (__builtin_expect(__ballot(far) == 0, 1))
+            return;
+#pragma unroll 1
+        for (int q = 0; q < 8; q++) {
+            const Pick pick(q);
+            i32x8_t y[NT];
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                y[j] = pick.of(f.b[j]);
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                const i32x8_t x = pick.of(f.a[i]);
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+                    acc[i][j] = mfma_mx<FA, FB, J>(x, y[j], acc[i][j], h ? sa[i][W - 1] : sa[i][0],
+                                                   h ? sb[j][W - 1] : sb[j][0]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+            f.a[i] = i32x8_t{};
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            f.b[j] = i32x8_t{};
+    }
+
     // The MFMAs of one step on f, with the reads of the next step's fragments
-    // between them.
+    // between them, and in kExact the look at the next scale words.
     template <int J, bool LOAD>
-    __device__ __forceinline__ void step(const Frags &f, Frags &next, int tn, int sn, int tl)
+    __device__ __forceinline__ void step(Frags &f, Frags &next, int tn, int sn, int tl, Words &scales)
     {
         if (MODE == kMx) {
             int k = 0;
@@ -352,6 +429,8 @@ struct MmKernel {
                 }
             return;
         }
+        if (__builtin_expect(odd_scales, 0))
+            step_far<J>(f);
         // four parts of 8 codes per lane: block p, half q.  A part's B
         // fragments and the next A fragment are converted between the MFMAs
         // before them.
@@ -385,6 +464,8 @@ struct MmKernel {
                         for (int k = 0; k < MT + NT; k++)
                             if (k * 4 * MT / (MT + NT) == part * MT + i)
                                 read(next, tn, sn, k);
+                        if (J == 3)
+                            scales.look(part * MT + i);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -409,7 +490,7 @@ struct MmKernel {
     __device__ __forceinline__ void tile(Frags &f0, Frags &f1, Words &next, int t)
     {
         constexpr int odd = J / 2;
-        step<J, false>(f0, f1, t, 1, 0);
+        step<J, false>(f0, f1, t, 1, 0, next);
         wait_and_barrier<loads(odd + 2, odd + NB - 1)>();
         if constexpr (TILED) {
             if (odd)
@@ -418,8 +499,11 @@ struct MmKernel {
                 issue_scales(t + NB);
         } else if (odd) {
             settle_scales();       // fetched before: no more loads than here
+            if (MODE == kExact)
+                read_scales(next, (t >> 1) + 1);
         }
-        step<J + 1, true>(f1, f0, t + 1, 0, t + NB);
+        next.look_at_none();
+        step<J + 1, true>(f1, f0, t + 1, 0, t + NB, next);
     }
 
     __device__ __forceinline__ void run()
@@ -448,6 +532,14 @@ struct MmKernel {
 #pragma unroll
             for (int j = 0; j < NT; j++)
                 acc[i][j] = f32x16_t{};
+        if (TILED && MODE == kExact) {
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+                at_a[i] = word_at(wm + 32 * i + r < (int)last_a ? wm + 32 * i + r : (int)last_a);
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                at_b[j] = word_at(brow(j) < (int)last_b ? brow(j) : (int)last_b);
+        }
         static_assert(TM <= 256 && TN <= 256, "compact scales: a thread per row");
         if constexpr (!TILED) {
             off_a = scale_offset(last_a, 64 * wave + L) + sra.lead;
@@ -478,10 +570,14 @@ struct MmKernel {
             wait_and_barrier<loads(1, NB - 1)>();
             if constexpr (TILED) {
                 read_words(next, 0);
-                take_words(next);
             } else {
-                read_scales(0);
+                read_scales(next, 0);
             }
+            next.look_at_none();
+#pragma unroll
+            for (int i = 0; i < (MT + NT) * W; i++)
+                next.look(i);
+            take_words(next, 0);
 #pragma unroll
             for (int i = 0; i < MT + NT; i++)
                 read(f0, 0, 0, i);
@@ -490,7 +586,7 @@ struct MmKernel {
                 // scale words of two tiles at a time.  Tiled: read from LDS behind
                 // the second one's barrier.  Compact: fetched two tiles earlier, put
                 // into LDS before the first tile's barrier and taken from there
-                // after the second.
+                // after the second's (kMx: after its MFMAs, for the registers).
                 const int place = (t >> 1) + 1;
                 if constexpr (!TILED)
                     write_scales(place);
@@ -498,10 +594,9 @@ struct MmKernel {
                 if constexpr (!TILED)
                     fetch_scales(place + 1);
                 tile<2>(f0, f1, next, t + 1);
-                if constexpr (TILED)
-                    take_words(next);
-                else
-                    read_scales(place);
+                if (!TILED && MODE == kMx)
+                    read_scales(next, place);
+                take_words(next, place);
                 t += 2;
             } while (t < nt);
         }

@@ -1,0 +1,169 @@
+"""MXFP8 products over the whole range of scale bytes, by each kernel.
+
+One operand is dense, the other holds one element a row, so that an output is one
+product and is known exactly without a matrix product.  Bytes of both operands
+come from both ends and the middle of 0 .. 254.  The product (at most 8
+significant bits) has to be right to the bit.  Below 2^-126 it is a multiple of
+2^-149 after one rounding, off by half of that; adding zeros to it is exact, and
+rounding it to bf16 (there a multiple of 2^-133) one more half step.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_bf16_amd as mx
+from product_util import E4M3, E5M2
+from test_gpu_matmul_tiles import tiled_layout
+
+pytestmark = pytest.mark.gpu
+
+ENDS = [*range(0, 13), *range(117, 138), *range(236, 255)]
+# M, N, K of each kernel: operands below one load; small products of 32 rows and 8
+# waves, 32 and 4, 64 and 8, 64 and 4; tiles of 128 x 128, aligned and copied rows;
+# 256 x 256 with a last round in parts of 128 x 128 and of 256 x 128, and copied rows.
+SIZES = [(1, 300, 8), (70, 96, 500), (32, 9000, 160), (130, 2100, 288), (512, 2048, 160),
+         (1500, 1301, 2064), (1500, 1302, 2065), (1500, 1301, 4112), (4200, 4157, 656),
+         (5000, 4700, 657)]
+
+
+def finite_codes(e5m2):
+    t = E5M2 if e5m2 else E4M3
+    return np.flatnonzero(np.isfinite(t)).astype(np.uint8)
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def values(codes, e5m2):
+    return dev(E5M2 if e5m2 else E4M3)[codes.int()]
+
+
+def scale_of(byte):
+    return torch.where(byte == 255, float("nan"), torch.exp2(byte.double() - 127))
+
+
+def operand(s, tiled):
+    return tiled_layout(s) if tiled else s.view(-1)
+
+
+def assert_product(got, want, what):
+    """got: the exact values `want` after one rounding to fp32 and, for bf16 outputs,
+    another to bf16."""
+    f = want.float().to(got.dtype).double()
+    g = got.double()
+    step = 2.0 ** -149 if got.dtype == torch.float32 else 2.0 ** -133
+    ok = (g == f) | (g.isnan() & want.isnan()) | ((want.abs() < 2.0 ** -126) & ((g - want).abs() <= step))
+    if not bool(ok.all()):
+        bad = (~ok).nonzero()
+        i = tuple(bad[0].tolist())
+        raise AssertionError(f"{what}: {len(bad)} of {ok.numel()} wrong, first at {i}: "
+                             f"{got[i].item()} for {want[i].item()}")
+
+
+def multiply(dense, one, dense_is_a, M, N, K, flags):
+    (qd, sd), (qo, so) = dense, one
+    a, b = ((qd, sd), (qo, so)) if dense_is_a else ((qo, so), (qd, sd))
+    y = mx.mx_matmul(a[0], operand(a[1], flags & mx.SCALE_TILED), b[0],
+                     operand(b[1], flags & mx.SCALE_TILED), flags=flags)
+    return y if dense_is_a else y.t()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2", "mixed"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_every_scale_byte(M, N, K, fmt):
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+    for dense_is_a in (True, False):
+        R, C = (M, N) if dense_is_a else (N, M)
+        ed, eo = fmt != "e4m3", fmt == "e5m2"
+        nb = -(-K // 32)
+
+        def pick(table, *shape):
+            t = dev(np.asarray(table, np.uint8))
+            return t[torch.randint(0, len(t), shape, device="cuda", generator=gen)]
+
+        qd, sd = pick(finite_codes(ed), R, K), pick(ENDS, R, nb)
+        at = torch.randint(0, K, (C,), device="cuda", generator=gen)
+        co, so = pick(finite_codes(eo), C), pick(ENDS, C, nb)
+        qo = torch.zeros(C, K, dtype=torch.uint8, device="cuda")
+        cols = torch.arange(C, device="cuda")
+        qo[cols, at] = co
+        want = values(qd[:, at], ed) * scale_of(sd[:, at // 32]) * \
+            (values(co, eo) * scale_of(so[cols, at // 32]))
+        fl = (mx.A_E5M2 if (ed if dense_is_a else eo) else 0) | (mx.B_E5M2 if (eo if dense_is_a else ed) else 0)
+        for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
+            y = multiply((qd, sd), (qo, so), dense_is_a, M, N, K, fl | flags)
+            assert_product(y, want, f"{M}x{N}x{K} {fmt} {dense_is_a} {flags}")
+
+
+def test_nan_blocks_among_far_ones():
+    M, N, K = 300, 200, 400
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    qd = torch.randint(0, 127, (M, K), dtype=torch.uint8, device="cuda", generator=gen)
+    sd = torch.randint(0, 255, (M, 13), dtype=torch.uint8, device="cuda", generator=gen)
+    qd[7, 64:96], sd[7, 2] = 0x7F, 255
+    at = torch.randint(0, K, (N,), device="cuda", generator=gen)
+    qo = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    so = torch.randint(0, 255, (N, 13), dtype=torch.uint8, device="cuda", generator=gen)
+    cols = torch.arange(N, device="cuda")
+    qo[cols, at] = 0x38
+    want = values(qd[:, at], False) * scale_of(sd[:, at // 32]) * scale_of(so[cols, at // 32])
+    want[7] = float("nan")
+    for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
+        assert_product(multiply((qd, sd), (qo, so), True, M, N, K, flags), want, str(flags))
+
+
+def test_largest_values_of_the_round_up_cast():
+    """bf16's largest number rounds up to 2^128 in a block of its own scale: finite
+    products with small operands."""
+    K = 64
+    x = np.full((40, K), 0x7F7F, np.uint16)
+    w = np.full((48, K), 0x0C00 | 0x0080, np.uint16)                # 2^-102
+    for e5 in (0, mx.ELEM_E5M2):
+        c = mx.mx_quantize(dev(x.view(np.int16)), axis=mx.ROWWISE | mx.SCALE_ROUND_UP | e5)
+        d = mx.mx_quantize(dev(w.view(np.int16)), axis=mx.ROWWISE | mx.SCALE_ROUND_UP)
+        a = values(c["q_row"], bool(e5)) * scale_of(c["s_row"]).repeat_interleave(32, 1)
+        b = values(d["q_row"], False) * scale_of(d["s_row"]).repeat_interleave(32, 1)
+        assert bool((a == 2.0 ** 128).all())
+        for flags in (0, mx.OUT_F32):
+            y = mx.mx_matmul(c["q_row"], c["s_row"], d["q_row"], d["s_row"],
+                             flags=flags | (mx.A_E5M2 if e5 else 0))
+            assert_product(y, a @ b.t(), f"{e5} {flags}")
+
+
+def test_grouped_products_and_weight_gradients_of_far_blocks():
+    rows, N, K = [70, 0, 33, 129], 160, 224
+    G, M = len(rows), sum(rows)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    ends = dev(np.asarray(ENDS, np.uint8))
+
+    def pick(*shape):
+        return ends[torch.randint(0, len(ends), shape, device="cuda", generator=gen)]
+
+    def one(n, k):
+        """[n][k] with an element 1 in each row."""
+        q = torch.zeros(n, k, dtype=torch.uint8, device="cuda")
+        at = torch.randint(0, k, (n,), device="cuda", generator=gen)
+        q[torch.arange(n, device="cuda"), at] = 0x38
+        return q, pick(n, -(-k // 32)), at
+
+    def want(q, s, o):
+        n = torch.arange(len(o[2]), device="cuda")
+        return values(q[:, o[2]], False) * scale_of(s[:, o[2] // 32]) * scale_of(o[1][n, o[2] // 32])
+
+    qa, sa = torch.randint(0, 127, (M, K), dtype=torch.uint8, device="cuda", generator=gen), pick(M, K // 32)
+    bs = [one(N, K) for _ in rows]
+    y = mx.mx_matmul_grouped(qa, sa.view(-1), torch.cat([b[0] for b in bs]),
+                             torch.cat([b[1].view(-1) for b in bs]), rows, flags=mx.OUT_F32)
+    parts = torch.split(qa, rows), torch.split(sa, rows)
+    assert_product(y, torch.cat([want(q, s, b) for q, s, b in zip(*parts, bs)]), "by expert")
+
+    ds = [(torch.randint(0, 127, (N, r), dtype=torch.uint8, device="cuda", generator=gen), pick(N, -(-r // 32)))
+          for r in rows]
+    xs = [one(K, r) if r else None for r in rows]
+    dw = mx.mx_matmul_wgrad_grouped(torch.cat([q.view(-1) for q, _ in ds]), torch.cat([s.view(-1) for _, s in ds]),
+                                    torch.cat([x[0].view(-1) for x in xs if x]),
+                                    torch.cat([x[1].view(-1) for x in xs if x]), rows, flags=mx.OUT_F32)
+    for g, r in enumerate(rows):
+        w = want(*ds[g], xs[g]) if r else torch.zeros(N, K, dtype=torch.float64, device="cuda")
+        assert_product(dw[g], w, f"weight gradient {g}")
