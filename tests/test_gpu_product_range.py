@@ -1,11 +1,17 @@
-"""MXFP8 products over the whole range of scale bytes, by each kernel.
+"""MXFP8 products over the whole range of scale bytes and at the border of what the
+8-bit matrix instruction keeps, by each kernel.
 
-One operand is dense, the other holds one element a row, so that an output is one
-product and is known exactly without a matrix product.  Bytes of both operands
-come from both ends and the middle of 0 .. 254.  The product (at most 8
-significant bits) has to be right to the bit.  Below 2^-126 it is a multiple of
-2^-149 after one rounding, off by half of that; adding zeros to it is exact, and
-rounding it to bf16 (there a multiple of 2^-133) one more half step.
+One operand is dense, the other holds one or two elements a row, so that an
+output is one product, or the sum of two, and is known exactly without a matrix
+product:
+  - one element, bytes of both operands from both ends and the middle of 0 .. 254:
+    the product (at most 8 significant bits) has to be right to the bit.  Below
+    2^-126 it is a multiple of 2^-149 after one rounding, off by half of that;
+    adding zeros to it and rounding it to bf16 (there a multiple of 2^-133) are
+    exact, or one more half step;
+  - two elements among 8 neighbouring k, whose products are up to 2^16 apart (17
+    bits of sum): fp32 outputs have to be right to the bit, which sums that drop
+    what is below 2^-13 of the larger one (bf16 outputs) are not.
 """
 import numpy as np
 import pytest
@@ -129,6 +135,32 @@ def test_largest_values_of_the_round_up_cast():
             y = mx.mx_matmul(c["q_row"], c["s_row"], d["q_row"], d["s_row"],
                              flags=flags | (mx.A_E5M2 if e5 else 0))
             assert_product(y, a @ b.t(), f"{e5} {flags}")
+
+
+@pytest.mark.parametrize("far", [False, True], ids=["near", "far"])
+@pytest.mark.parametrize("tiled", [0, mx.SCALE_TILED], ids=["compact", "tiled"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_fp32_outputs_drop_nothing(M, N, K, tiled, far):
+    """Sums of +-2^8 and +-2^-8 (or of two of one size) among 8 neighbouring k."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    nb = -(-K // 32)
+    codes = dev(np.array([int(np.flatnonzero(E4M3 == v)[0]) for v in (16., -16., 2. ** -4, -2. ** -4)],
+                         np.uint8))
+    qd = codes[torch.randint(0, 4, (M, K), device="cuda", generator=gen)]
+    k1 = torch.randint(0, K, (N,), device="cuda", generator=gen)
+    k2 = k1 // 8 * 8 + (k1 % 8 + torch.randint(1, 8, (N,), device="cuda", generator=gen)) % 8
+    k2 = torch.where(k2 < K, k2, k1 // 8 * 8)
+    cols = torch.arange(N, device="cuda")
+    qo = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    qo[cols, k1], qo[cols, k2] = codes[0], codes[2]
+    up = 121 if far else 0            # bytes 248 and 6: the dense operand's blocks are far
+    sd = torch.full((M, nb), 127 + up, dtype=torch.uint8, device="cuda")
+    so = torch.full((N, nb), 127 - up, dtype=torch.uint8, device="cuda")
+    vo = values(qo, False)
+    want = values(qd[:, k1], False) * vo[cols, k1] + \
+        torch.where(k1 == k2, 0.0, values(qd[:, k2], False) * vo[cols, k2])
+    flags = tiled | mx.OUT_F32
+    assert_product(multiply((qd, sd), (qo, so), True, M, N, K, flags), want, f"{M}x{N}x{K}")
 
 
 def test_grouped_products_and_weight_gradients_of_far_blocks():
