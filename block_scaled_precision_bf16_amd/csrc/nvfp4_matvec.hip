@@ -148,8 +148,10 @@ struct MvPlan {
     static constexpr int kRows = 16 * WN;                     // weight rows of a block
     static constexpr int kFit = D * KS;                       // chunks of a stage
     static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
-    // 1 or 2 tokens: dot products on the vector units, which need no scaled
-    // weights: 1.1 (1.6) vector instructions a weight
+    // 1 or 2 tokens: dot products on the vector units.  Their weights carry the power
+    // of two of the block's scale, which the conversion applies, and the block's sum
+    // its significand, so that a sum leaves fp32's range only where one of wholly
+    // scaled weights, as for more tokens, does: 1.1 (1.6) vector instructions a weight
     static constexpr bool kDot = TT <= 2;
     // LDS: a stage's tokens, then the waves' sums of a token tile
     static constexpr int kTokens = kFit * 512 * TT, kLds = kTokens + kMvWaves * 1024;
@@ -381,16 +383,19 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
                                     : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 1)
                                     : b == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.s, 2)
                                              : __builtin_amdgcn_cvt_f32_fp8((int)u.s, 3);
+                    // kDot: s = 2 rest * 2^e (s = 0: rest = 0; NaN: NaN), and the conversion
+                    // takes e from s, whose other bits it does not look at
+                    const float rest = __builtin_amdgcn_frexp_mantf(s);
                     float sum[2] = {0.f, 0.f};
 #pragma unroll
                     for (int f = 2 * b; f < 2 * b + 2; f++) {
                         const uint4 v = u.q[f >> 2];
                         const uint32_t d = (f & 3) == 0 ? v.x : (f & 3) == 1 ? v.y : (f & 3) == 2 ? v.z : v.w;
                         if constexpr (Plan::kDot) {
-                            const bf16x2v_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
-                            const bf16x2v_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
-                            const bf16x2v_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2);
-                            const bf16x2v_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3);
+                            const bf16x2v_t w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0);
+                            const bf16x2v_t w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1);
+                            const bf16x2v_t w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2);
+                            const bf16x2v_t w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3);
 #pragma unroll
                             for (int t = 0; t < TT; t++) {
                                 const uint4 x = xs[4 * f * TT + ((g * TT + t) ^ (f & kMix))];
@@ -416,7 +421,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
                     if constexpr (Plan::kDot) {
 #pragma unroll
                         for (int t = 0; t < TT; t++)
-                            acc[0][t] = __builtin_fmaf(sum[t], s, acc[0][t]);
+                            acc[0][t] = __builtin_fmaf(sum[t], rest, acc[0][t]);
                         if (TT == 2)
                             __builtin_amdgcn_sched_barrier(0);
                     }
@@ -453,6 +458,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
                 for (int t = 0; t < TT; t++) {
                     acc[0][t] += __shfl_xor(acc[0][t], 16);
                     acc[0][t] += __shfl_xor(acc[0][t], 32);
+                    acc[0][t] *= 2.f;            // (rest)
                 }
                 float *part = reinterpret_cast<float *>(lds + Plan::kTokens);
                 __syncthreads();
