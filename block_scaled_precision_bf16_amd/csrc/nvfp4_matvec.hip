@@ -516,27 +516,29 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
 }
 
 // Weights of fewer than 16 bytes of codes or 4 of scales, or fewer than 8 token
-// elements, which the loads above do not fit: a wave per output row, bytes one by one.
-__global__ __launch_bounds__(64) void mv_tiny_kernel(const MvArgs a)
+// elements, which the loads above do not fit: a lane per output, bytes one by one (K is
+// 48 at most).  There may be many outputs: one token of 7 by 2^23 rows.
+constexpr int kTinyThreads = 256;
+__global__ __launch_bounds__(kTinyThreads) void mv_tiny_kernel(const MvArgs a)
 {
-    const int lane = (int)threadIdx.x;
-    const int64_t nb = (a.K + 15) / 16, pitch = (a.K + 1) / 2, slots = a.T * a.top;
-    for (int64_t p = (int64_t)blockIdx.x * 64 + lane; p < slots; p += (int64_t)gridDim.x * 64)
-        for (int64_t n = 0; n < a.N; n++) {
-            const int e = a.experts ? a.experts[p] : 0;
-            float sum = 0.f;
-            if (e >= 0 && e < a.G) {
-                const int64_t row = (int64_t)e * a.N + n;
-                for (int64_t k = 0; k < a.K; k++) {
-                    const uint32_t code = a.qw[row * pitch + (k >> 1)] >> (4 * (k & 1));
-                    const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.sw[row * nb + (k >> 4)], 0);
-                    const f32x2v_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0);
-                    sum += __uint_as_float((uint32_t)a.x[p / a.top * a.K + k] << 16) * (v[0] * s);
-                }
-                sum *= a.sg[e];
+    const int64_t nb = (a.K + 15) / 16, pitch = (a.K + 1) / 2, all = (int64_t)a.T * a.top * a.N;
+    for (int64_t i = (int64_t)blockIdx.x * kTinyThreads + threadIdx.x; i < all;
+         i += (int64_t)gridDim.x * kTinyThreads) {
+        const int64_t p = i / a.N, n = i - p * a.N;
+        const int e = a.experts ? a.experts[p] : 0;
+        float sum = 0.f;
+        if (e >= 0 && e < a.G) {
+            const int64_t row = (int64_t)e * a.N + n;
+            for (int k = 0; k < a.K; k++) {
+                const uint32_t code = a.qw[row * pitch + (k >> 1)] >> (4 * (k & 1));
+                const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.sw[row * nb + (k >> 4)], 0);
+                const f32x2v_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0);
+                sum += __uint_as_float((uint32_t)a.x[p / a.top * a.K + k] << 16) * (v[0] * s);
             }
-            store_mv(a, p * a.N + n, sum);
+            sum *= a.sg[e];
         }
+        store_mv(a, i, sum);
+    }
 }
 
 template <int TT, bool EXPERTS, bool FEW>
@@ -593,8 +595,9 @@ hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
 {
     const int64_t rows = (int64_t)a.G * a.N;
     if (rows * ((a.K + 1) / 2) < 16 || rows * ((a.K + 15) / 16) < 4 || (int64_t)a.T * a.K < 8) {
-        const int64_t n = ((int64_t)a.T * a.top + 63) / 64;
-        hipLaunchKernelGGL(mv_tiny_kernel, dim3((unsigned)(n < 4096 ? n : 4096)), dim3(64), 0, stream, a);
+        const int64_t n = ((int64_t)a.T * a.top * a.N + kTinyThreads - 1) / kTinyThreads;
+        hipLaunchKernelGGL(mv_tiny_kernel, dim3((unsigned)(n < 65536 ? n : 65536)), dim3(kTinyThreads), 0,
+                           stream, a);
         return hipGetLastError();
     }
     // tokens that a weight matrix meets: all, or an expert's fair share twice over
