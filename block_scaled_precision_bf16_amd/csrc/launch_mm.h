@@ -81,6 +81,61 @@ struct MvArgs {
     int32_t by_slot;                    // set by the launcher
 };
 
+constexpr int kMvThreads = 512, kMvWaves = 8;
+constexpr int kMvChunk = 256;          // k of one step of a wave
+
+// How a kernel for up to TT tokens is laid out: KS waves share the chunks of a
+// row, each has D of its chunks under way, a stage holds the tokens of D KS
+// chunks.  FEW: for few rows, all 8 waves share them.
+template <int TT, bool EXPERTS, bool FEW>
+struct MvPlan {
+    static constexpr int KS = FEW || (TT <= 2 && EXPERTS) ? 8 : TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 && !EXPERTS ? 4 : 2;
+    static constexpr int kRows = 16 * WN;                     // weight rows of a block
+    static constexpr int kFit = D * KS;                       // chunks of a stage
+    static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
+    // 1 or 2 tokens: dot products on the vector units.  Their weights carry the power
+    // of two of the block's scale, which the conversion applies, and the block's sum
+    // its significand, so that a sum leaves fp32's range only where one of wholly
+    // scaled weights, as for more tokens, does: 1.1 (1.6) vector instructions a weight
+    static constexpr bool kDot = TT <= 2;
+    // LDS: a stage's tokens, then the waves' sums of a token tile
+    static constexpr int kTokens = kFit * 512 * TT, kLds = kTokens + kMvWaves * 1024;
+};
+
+// The kernel for a product: for up to `tokens` (1, 2, 8, 16, 32, 64) at a time, 0 for
+// operands smaller than its loads; few: for few rows.
+struct MvChoice {
+    int tokens;
+    bool few;
+};
+
+inline MvChoice mv_choose(const MvArgs &a)
+{
+    const int64_t rows = (int64_t)a.G * a.N;
+    if (rows * ((a.K + 1) / 2) < 16 || rows * ((a.K + 15) / 16) < 4 || (int64_t)a.T * a.K < 8)
+        return {0, false};
+    // tokens that a weight matrix meets: all, or an expert's fair share twice over
+    const int64_t slots = (int64_t)a.T * a.top;
+    const int64_t tokens = a.experts ? (2 * slots + a.G - 1) / a.G : a.T;
+    int64_t most = slots < tokens ? slots : tokens;
+    // Few rows of many tokens: 16 or 32 at a time, the weights read again (from the
+    // caches) for each, rather than few workgroups.
+    if (!a.experts && a.T > 16) {
+        const int64_t by16 = (((int64_t)a.N + 31) / 32) * ((a.T + 15) / 16);
+        const int64_t by32 = (((int64_t)a.N + 63) / 64) * ((a.T + 31) / 32);
+        most = by16 <= 512 ? 16 : by32 <= 256 ? 32 : 64;
+        most = most > a.T ? a.T : most;
+    }
+    const int at_once = most <= 1 ? 1 : most <= 2 ? 2 : most <= 8 ? 8 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
+    // Workgroups of 32 rows that do not fill the CUs: twice as many, of 16 (5 tokens by
+    // 1001 x 4095: 7.9 -> 6.7 us, 4096 x 4096: 7.5 -> 5.8 us; but 16384 x 16384: 38 -> 42
+    // us, and 512 x 512, where there is nothing to share: 4.1 -> 4.6 us).  For 16 tokens
+    // only one of them fits a CU's LDS.
+    const int64_t blocks = ((int64_t)a.N + 31) / 32 * (((int64_t)a.T + at_once - 1) / at_once);
+    const bool few = !a.experts && at_once <= 16 && blocks <= (at_once == 16 ? 128 : 255) && a.K >= 1024;
+    return {at_once, few};
+}
+
 hipError_t launch_mv(const MvArgs &a, hipStream_t stream);
 
 }  // namespace mxk

@@ -36,9 +36,6 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2v_t __attribute__((ext_vector_type(2)));
 
-constexpr int kMvThreads = 512, kMvWaves = 8;
-constexpr int kChunk = 256;            // k of one step of a wave
-
 // 8 E2M1 codes times their scale, as bf16 (exact).
 __device__ __forceinline__ bf16x8_t weights8(uint32_t w, float s)
 {
@@ -139,24 +136,6 @@ __device__ __forceinline__ void zero_rows(const MvArgs &a, const int32_t *slot, 
 // Waves per SIMD: two workgroups per CU, or one that takes 136 KB of LDS.
 constexpr int mv_occupancy(int tokens, bool few) { return tokens == 64 || (tokens == 16 && few) ? 2 : 4; }
 
-// How a kernel for up to TT tokens is laid out: KS waves share the chunks of a
-// row, each has D of its chunks under way, a stage holds the tokens of D KS
-// chunks.  FEW: for few rows, all 8 waves share them.
-template <int TT, bool EXPERTS, bool FEW>
-struct MvPlan {
-    static constexpr int KS = FEW || (TT <= 2 && EXPERTS) ? 8 : TT <= 16 ? 4 : 2, WN = kMvWaves / KS, D = TT <= 2 && !EXPERTS ? 4 : 2;
-    static constexpr int kRows = 16 * WN;                     // weight rows of a block
-    static constexpr int kFit = D * KS;                       // chunks of a stage
-    static constexpr int kPieces = kFit * 512 * TT / 16 / kMvThreads;   // of a thread
-    // 1 or 2 tokens: dot products on the vector units.  Their weights carry the power
-    // of two of the block's scale, which the conversion applies, and the block's sum
-    // its significand, so that a sum leaves fp32's range only where one of wholly
-    // scaled weights, as for more tokens, does: 1.1 (1.6) vector instructions a weight
-    static constexpr bool kDot = TT <= 2;
-    // LDS: a stage's tokens, then the waves' sums of a token tile
-    static constexpr int kTokens = kFit * 512 * TT, kLds = kTokens + kMvWaves * 1024;
-};
-
 // Where a workgroup finds the weights of a block of rows.
 struct Aim {
     const uint8_t *q, *s;       // bases a little before the block's first row
@@ -182,7 +161,7 @@ struct Aim {
     // the end, which settle() moves where they belong.
     __device__ __forceinline__ void fetch(Share &w, int c) const
     {
-        const uint32_t o = qoff + c * (kChunk / 2), p = soff + c * (kChunk / 16);
+        const uint32_t o = qoff + c * (kMvChunk / 2), p = soff + c * (kMvChunk / 16);
         __builtin_memcpy(&w.q[0], q + (o < qlast ? o : qlast), 16);
         __builtin_memcpy(&w.q[1], q + (o + 16 < qlast ? o + 16 : qlast), 16);
         __builtin_memcpy(&w.s, s + (p < slast ? p : slast), 4);
@@ -191,12 +170,12 @@ struct Aim {
     // zero tokens, scales there (from block nb on) become 0.
     __device__ __forceinline__ void settle(Share &w, int c, int nb, int g) const
     {
-        const int o = (int)(qoff + c * (kChunk / 2) - qlast), p = (int)(soff + c * (kChunk / 16) - slast);
+        const int o = (int)(qoff + c * (kMvChunk / 2) - qlast), p = (int)(soff + c * (kMvChunk / 16) - slast);
         if (o > 0)
             w.q[0] = shift_down(w.q[0], o < 15 ? o : 15);
         if (o + 16 > 0)
             w.q[1] = shift_down(w.q[1], o + 16 < 15 ? o + 16 : 15);
-        const int keep = nb - c * (kChunk / 16) - 4 * g;
+        const int keep = nb - c * (kMvChunk / 16) - 4 * g;
         uint32_t v = p > 0 ? (p < 4 ? w.s >> (8 * p) : 0) : w.s;
         if (keep < 4)
             v = keep <= 0 ? 0 : v & ((1u << (8 * keep)) - 1);
@@ -221,8 +200,8 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
     __shared__ int32_t wave_count[kMvWaves];
 
     const int blocks = (a.N + Plan::kRows - 1) / Plan::kRows, step = (int)gridDim.x;
-    const int nb = (a.K + 15) >> 4, nchunk = (a.K + kChunk - 1) / kChunk;
-    const int partial = a.K % kChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
+    const int nb = (a.K + 15) >> 4, nchunk = (a.K + kMvChunk - 1) / kMvChunk;
+    const int partial = a.K % kMvChunk ? nchunk - 1 : nchunk;    // the first chunk to settle
     const int stages = (nchunk + Plan::kFit - 1) / Plan::kFit;
     // Rows some kilobytes apart lie in few of the memory's channels at any one k, and
     // the workgroups walk along k at about the same pace: neighbouring ones start
@@ -299,7 +278,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
         // tokens (TT < 16: TT tokens of 16 / TT chunks), TB times over.
         constexpr int kSide = TT < 16 ? 16 / TT : 1;
         const int q = tid & 31, c_side = (tid >> 5) / (TT < 16 ? TT : 16);
-        const int xk = c_side * kChunk + 8 * q;
+        const int xk = c_side * kMvChunk + 8 * q;
         int64_t xo[TB];                           // element offset in x
 #pragma unroll
         for (int b = 0; b < TB; b++) {
@@ -315,16 +294,16 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
         auto load_tokens = [&](int st) {
 #pragma unroll
             for (int j = 0; j < P; j++) {
-                const int64_t o = xo[j % TB] + (st * Plan::kFit + j / TB * kSide) * kChunk;
+                const int64_t o = xo[j % TB] + (st * Plan::kFit + j / TB * kSide) * kMvChunk;
                 __builtin_memcpy(&xv[j], a.x + (o < x_end ? o : x_end), 16);
             }
         };
         auto store_tokens = [&](int st) {
-            if ((st + 1) * Plan::kFit * kChunk > a.K) {
+            if ((st + 1) * Plan::kFit * kMvChunk > a.K) {
                 // what lies behind a row's end becomes 0
 #pragma unroll
                 for (int j = 0; j < P; j++) {
-                    const int k0 = (st * Plan::kFit + j / TB * kSide) * kChunk;
+                    const int k0 = (st * Plan::kFit + j / TB * kSide) * kMvChunk;
                     const int64_t d = 2 * (xo[j % TB] + k0 - x_end);
                     const int keep = a.K - k0 - xk;
                     uint4 v = xv[j];
@@ -561,7 +540,7 @@ hipError_t launch_one(MvArgs a, hipStream_t stream)
     // workgroup's blocks: then as many workgroups as fit the CUs (two each), so
     // that weights are always under way.  Otherwise a workgroup per block.
     int64_t nx = blocks;
-    if (EXPERTS && a.K <= Plan::kFit * kChunk) {
+    if (EXPERTS && a.K <= Plan::kFit * kMvChunk) {
         const int64_t each_y = a.by_slot ? slots : a.G;      // (zero rows take no time)
         const int64_t fill = 2 * 256 / each_y > 1 ? 2 * 256 / each_y : 1;
         const int64_t each = (blocks + fill - 1) / fill;
@@ -573,17 +552,12 @@ hipError_t launch_one(MvArgs a, hipStream_t stream)
 }
 
 template <int TT>
-hipError_t launch(const MvArgs &a, hipStream_t stream)
+hipError_t launch(const MvArgs &a, bool few, hipStream_t stream)
 {
     if (a.experts)
         return launch_one<TT, true, false>(a, stream);
-    // Workgroups of 32 rows that do not fill the CUs: twice as many, of 16 (5 tokens by
-    // 1001 x 4095: 7.9 -> 6.7 us, 4096 x 4096: 7.5 -> 5.8 us; but 16384 x 16384: 38 -> 42
-    // us, and 512 x 512, where there is nothing to share: 4.1 -> 4.6 us).  For 16 tokens
-    // only one of them fits a CU's LDS.
     if constexpr (TT <= 16) {
-        const int64_t blocks = ((int64_t)a.N + 31) / 32 * (((int64_t)a.T + TT - 1) / TT);
-        if (blocks <= (TT == 16 ? 128 : 255) && a.K >= 1024)
+        if (few)
             return launch_one<TT, false, true>(a, stream);
     }
     return launch_one<TT, false, false>(a, stream);
@@ -593,31 +567,19 @@ hipError_t launch(const MvArgs &a, hipStream_t stream)
 
 hipError_t launch_mv(const MvArgs &a, hipStream_t stream)
 {
-    const int64_t rows = (int64_t)a.G * a.N;
-    if (rows * ((a.K + 1) / 2) < 16 || rows * ((a.K + 15) / 16) < 4 || (int64_t)a.T * a.K < 8) {
+    const MvChoice c = mv_choose(a);
+    if (c.tokens == 0) {
         const int64_t n = ((int64_t)a.T * a.top * a.N + kTinyThreads - 1) / kTinyThreads;
         hipLaunchKernelGGL(mv_tiny_kernel, dim3((unsigned)(n < 65536 ? n : 65536)), dim3(kTinyThreads), 0,
                            stream, a);
         return hipGetLastError();
     }
-    // tokens that a weight matrix meets: all, or an expert's fair share twice over
-    const int64_t slots = (int64_t)a.T * a.top;
-    const int64_t tokens = a.experts ? (2 * slots + a.G - 1) / a.G : a.T;
-    int64_t most = slots < tokens ? slots : tokens;
-    // Few rows of many tokens: 16 or 32 at a time, the weights read again (from the
-    // caches) for each, rather than few workgroups.
-    if (!a.experts && a.T > 16) {
-        const int64_t by16 = (((int64_t)a.N + 31) / 32) * ((a.T + 15) / 16);
-        const int64_t by32 = (((int64_t)a.N + 63) / 64) * ((a.T + 31) / 32);
-        most = by16 <= 512 ? 16 : by32 <= 256 ? 32 : 64;
-        most = most > a.T ? a.T : most;
-    }
-    return most <= 1    ? launch<1>(a, stream)
-           : most <= 2  ? launch<2>(a, stream)
-           : most <= 8  ? launch<8>(a, stream)
-           : most <= 16 ? launch<16>(a, stream)
-           : most <= 32 ? launch<32>(a, stream)
-                        : launch<64>(a, stream);
+    return c.tokens == 1    ? launch<1>(a, c.few, stream)
+           : c.tokens == 2  ? launch<2>(a, c.few, stream)
+           : c.tokens == 8  ? launch<8>(a, c.few, stream)
+           : c.tokens == 16 ? launch<16>(a, c.few, stream)
+           : c.tokens == 32 ? launch<32>(a, c.few, stream)
+                            : launch<64>(a, c.few, stream);
 }
 
 }  // namespace mxk

@@ -18,18 +18,14 @@ import pytest
 import torch
 
 import block_scaled_precision_bf16_amd as mx
+from product_cases import PRODUCTS
 from product_util import E4M3, E5M2
 from test_gpu_matmul_tiles import tiled_layout
 
 pytestmark = pytest.mark.gpu
 
 ENDS = [*range(0, 13), *range(117, 138), *range(236, 255)]
-# M, N, K of each kernel: operands below one load; small products of 32 rows and 8
-# waves, 32 and 4, 64 and 8, 64 and 4; tiles of 128 x 128, aligned and copied rows;
-# 256 x 256 with a last round in parts of 128 x 128 and of 256 x 128, and copied rows.
-SIZES = [(1, 300, 8), (70, 96, 500), (32, 9000, 160), (130, 2100, 288), (512, 2048, 160),
-         (1500, 1301, 2064), (1500, 1302, 2065), (1500, 1301, 4112), (4200, 4157, 656),
-         (5000, 4700, 657)]
+SIZES = [size for size, _ in PRODUCTS]       # each kernel
 
 
 def finite_codes(e5m2):
