@@ -60,18 +60,6 @@ struct Share {
     uint32_t s;
 };
 
-// v shifted down by d bytes (d < 16; anything above leaves any codes).
-__device__ __forceinline__ uint4 shift_down(uint4 v, uint32_t d)
-{
-    if (d & 8)
-        v = make_uint4(v.z, v.w, 0, 0);
-    if (d & 4)
-        v = make_uint4(v.y, v.z, v.w, 0);
-    const uint32_t b = d & 3;
-    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, b), __builtin_amdgcn_alignbyte(v.z, v.y, b),
-                      __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0, v.w, b));
-}
-
 __device__ __forceinline__ void store_mv(const MvArgs &a, int64_t i, float v)
 {
     if (a.out_f32)
@@ -172,9 +160,9 @@ struct Aim {
     {
         const int o = (int)(qoff + c * (kMvChunk / 2) - qlast), p = (int)(soff + c * (kMvChunk / 16) - slast);
         if (o > 0)
-            w.q[0] = shift_down(w.q[0], o < 15 ? o : 15);
+            w.q[0] = bytes_down(w.q[0], o < 15 ? o : 15);
         if (o + 16 > 0)
-            w.q[1] = shift_down(w.q[1], o + 16 < 15 ? o + 16 : 15);
+            w.q[1] = bytes_down(w.q[1], o + 16 < 15 ? o + 16 : 15);
         const int keep = nb - c * (kMvChunk / 16) - 4 * g;
         uint32_t v = p > 0 ? (p < 4 ? w.s >> (8 * p) : 0) : w.s;
         if (keep < 4)
@@ -183,8 +171,9 @@ struct Aim {
     }
 };
 
-// A workgroup takes row block blockIdx.x, with EXPERTS also + gridDim.x, ...
-// (which costs registers, and gains where a workgroup's own work is short).
+// A workgroup takes row block blockIdx.x, with EXPERTS and tokens that fit one stage
+// also + gridDim.x, ... (which costs registers, and gains where a workgroup's own work
+// is short).
 // EXPERTS: blockIdx.y is the expert (G: the slots without one, whose rows become zeros)
 // or, with a.by_slot, a slot, whose workgroups serve its expert if no earlier
 // slot has the same; else the tile of TT tokens.
@@ -308,7 +297,7 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
                     const int keep = a.K - k0 - xk;
                     uint4 v = xv[j];
                     if (d > 0)
-                        v = shift_down(v, d < 15 ? (uint32_t)d : 15);
+                        v = bytes_down(v, d < 15 ? (uint32_t)d : 15);
                     const uint32_t half = keep & 1 ? 0xFFFFu : 0;
                     v.x &= keep >= 2 ? ~0u : keep > 0 ? half : 0;
                     v.y &= keep >= 4 ? ~0u : keep > 2 ? half : 0;
@@ -412,8 +401,8 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
                     __syncthreads();
                     store_tokens(turned(st));
                     __syncthreads();
-                    if (stages > 1 && (st + 1 < stages || more))
-                        load_tokens(turned(st + 1 < stages ? st + 1 : 0));
+                    if (st + 1 < stages)
+                        load_tokens(turned(st + 1));
                 }
 #pragma unroll
                 for (int j = 0; j < D; j++) {
