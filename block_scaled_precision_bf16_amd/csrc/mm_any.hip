@@ -45,6 +45,8 @@ __global__ __launch_bounds__(256) void mm_any_kernel(const MmArgs a, const MmTab
     __shared__ uint4 lds[2][kT * kBK / 16];
     const int tid = (int)threadIdx.x, L = tid & 63, wave = tid >> 6;
     const MmTile w = mm_tile(a, t, (int)blockIdx.x, kT, kT);
+    if (nothing_to_add(a, w))
+        return;
     const int h = L >> 5, r = L & 31;
     const int wm = 32 * (wave >> 1), wn = 32 * (wave & 1);
 

@@ -152,6 +152,13 @@ __device__ __forceinline__ MmTile mm_tile(const MmArgs &a, const MmTable &t, int
     return w;
 }
 
+// A tile without a sum whose outputs keep what they hold, to the bit (-0 + 0 is 0): an
+// empty group's gradient with MX_OUT_ACCUMULATE.
+__device__ __forceinline__ bool nothing_to_add(const MmArgs &a, const MmTile &w)
+{
+    return a.accumulate && w.K == 0;
+}
+
 // Scale byte of (row, blk) of an operand [rows][nb]; 0 (2^-127) outside it,
 // where every element is 0.
 __device__ __forceinline__ int scale_byte(const uint8_t *s, int64_t rows, int64_t nb, int64_t row,

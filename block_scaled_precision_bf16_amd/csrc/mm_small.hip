@@ -192,6 +192,8 @@ __global__ __launch_bounds__(64 * KW, MT == 1 && KW == 4 ? 3 : 2) void mm_small_
     const int tid = (int)threadIdx.x, L = tid & 63, h = L >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const MmTile w = mm_tile(a, t, (int)blockIdx.x, 32 * MT, 32);
+    if (nothing_to_add(a, w))
+        return;
     const int pieces = (int)((w.K + 127) >> 7), whole = (int)(w.K >> 7);
     f32x16_t acc[MT];
 #pragma unroll

@@ -676,6 +676,8 @@ struct MmKernel {
 template <MmMode MODE, int FA, int FB, int TM, int TN, bool TILED, bool PAIRED = false>
 __device__ __forceinline__ void mm_tile_run(const MmArgs &a, const MmTile &w, uint8_t *lds)
 {
+    if (nothing_to_add(a, w))
+        return;
     typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
     MmKernel<MODE, FA, FB, TM, TN, TILED, PAIRED> k{
         a, w,
