@@ -195,3 +195,37 @@ def test_grouped_products_and_weight_gradients_of_far_blocks():
     for g, r in enumerate(rows):
         w = want(*ds[g], xs[g]) if r else torch.zeros(N, K, dtype=torch.float64, device="cuda")
         assert_product(dw[g], w, f"weight gradient {g}")
+
+
+@pytest.mark.parametrize("far", [False, True], ids=["near", "far"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_infinite_and_nan_elements(M, N, K, far):
+    """E5M2 has infinities, and both formats NaNs, which the casts do not write but an
+    operand may hold: +-Inf times a number, NaN times anything, in the rows that hold
+    them only."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    nb = -(-K // 32)
+    qa = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    qb = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    at = K // 2
+    qb[:, at] = 0x38 | (torch.randint(0, 2, (N,), device="cuda", generator=gen) * 0x80).byte()   # +-1
+    qa[:, at] = 0x3C                                                  # E5M2 1
+    kinds = dev(np.array([0x3C, 0x7C, 0xFC, 0x7D, 0xFF], np.uint8))   # 1, Inf, -Inf, NaN, NaN
+    which = torch.randint(0, 5, (M,), device="cuda", generator=gen)
+    which[-1] = 1
+    qa[:, at] = kinds[which]
+    up = 121 if far else 0
+    sa = torch.full((M, nb), 127 + up, dtype=torch.uint8, device="cuda")
+    sb = torch.full((N, nb), 127 - up, dtype=torch.uint8, device="cuda")
+    a = dev(np.array([1, np.inf, -np.inf, np.nan, np.nan]))[which]
+    want = a[:, None] * values(qb[:, at], False)[None]
+    for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
+        y = multiply((qa, sa), (qb, sb), True, M, N, K, flags | mx.A_E5M2)
+        assert_product(y, want, f"{M}x{N}x{K} {flags}")
+    qa[:, at] = 0x38
+    qa[0, at] = 0x7F                                                  # E4M3 NaN
+    want = torch.ones(M, 1, dtype=torch.float64, device="cuda") * values(qb[:, at], False)[None]
+    want[0] = float("nan")
+    for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
+        y = multiply((qa, sa), (qb, sb), True, M, N, K, flags)
+        assert_product(y, want, f"{M}x{N}x{K} {flags} E4M3")
