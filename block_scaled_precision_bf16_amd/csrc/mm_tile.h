@@ -23,11 +23,14 @@
 // outputs leave as whole 128-byte lines from registers.  In LDS the first tile's rows
 // come first.
 //
-// Measured: 8192^3 to bf16 in 410 - 440 us, 2.5 - 2.7 PFLOP/s (a library's fp8 product
-// without block scales reaches 2.96 on this card); the matrix cores are busy 70% of
-// the time at the clock that the power limit leaves them (1.7 - 2.0 GHz).  To fp32
-// (twice the MFMA time) 760 us, 11 of which the look for far blocks takes.  A round of 256 tiles takes 8 us + 1.5 us for 128 k;
-// its outputs alone are 34 MB, about 7 us.  A last round of 128 x 128 parts takes
+// Measured: 8192^3 to bf16 in 440 - 460 us back to back, by the card, 2.4 - 2.5 PFLOP/s
+// (a library's fp8 product without block scales reaches 2.8 - 2.96), 397 in short
+// bursts; the matrix cores are busy 70% of the time at the clock that the power limit
+// leaves them (1.7 - 2.0 GHz).  To fp32 (twice the MFMA time) 762 us in bursts, of which
+// the look for far blocks takes 11; with one in every step it takes 3.4 times as long,
+// with zeros for half of A's rows, whose scale bytes have to be told from those, 9 %
+// longer.  A round of 256 tiles takes 8 us + 1.5 us for 128 k; its outputs alone are 34
+// MB, about 7 us.  A last round of 128 x 128 parts takes
 // 0.55 us for 128 k, one of 256 x 128 parts 1.0 us: 64 tiles of 8192 k take 39 us in
 // parts and 92 us whole.  With two buffers instead of four they take 50 us.
 #pragma once

@@ -20,12 +20,12 @@
 // which the fragments want them, a stage of chunks at a time.  The KS partial
 // sums are added through LDS in a fixed order.
 //
-// Measured, 16384 x 16384 (151 MB of weights, some of them from the MALL): 1 token 30 us,
-// 5.1 TB/s; 16 tokens 42 us (from HBM alone, 131072 rows: 3.4 TB/s, where 1 token
-// reaches 4.4 and a plain sum over memory 4.0); the vector units are busy 53% of the
-// time, and waves wait for weights and at the stages' barriers.  32 tokens 52 us, 64
-// tokens 72 us, where the conversions, the reads of the tokens from LDS and the MFMAs
-// come one after the other in too few waves.  One token by 14336 x 4096: 9.7 us, of
+// Measured, 16384 x 16384 (151 MB of weights, some of them from the MALL): 1 token 31 us,
+// 4.9 TB/s; 16 tokens 41 - 43 us (from HBM alone, 131072 rows: 3.4 TB/s, where 1 token
+// reaches 4.4 and the absmax pass, which only reads, 6.8 - 7.2); the vector units are
+// busy 53% of the time, and waves wait for weights and at the stages' barriers.  32
+// tokens 50 us, 64 tokens 69 us, where the conversions, the reads of the tokens from LDS and the MFMAs
+// come one after the other in too few waves.  One token by 14336 x 4096: 9.8 us, of
 // which 3.2 are an empty launch's.
 #include "launch_mm.h"
 #include "mm_common.h"
@@ -195,7 +195,8 @@ __global__ __launch_bounds__(kMvThreads, mv_occupancy(TT, FEW)) void mv_kernel(c
     // Rows some kilobytes apart lie in few of the memory's channels at any one k, and
     // the workgroups walk along k at about the same pace: neighbouring ones start
     // at different stages.  (Not where a workgroup lives for a few chunks only: one
-    // token through 2 of 8 experts 10.4 -> 10.0 us without.)
+    // token through 2 of 8 experts of 5120 x 4096 11.3 -> 11.0 us without, of 4096 x
+    // 14336 19.7 -> 19.0, of 4096 x 8192 13.2 -> 13.4.)
     const int first = (TT <= 2 && EXPERTS) || stages <= 1
                           ? 0
                           : (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)stages);
