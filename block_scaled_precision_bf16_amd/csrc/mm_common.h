@@ -71,6 +71,7 @@ __device__ __forceinline__ uint32_t dead_bytes(int live)
 {
     return live >= 4 ? 0 : live <= 0 ? 0x80808080u : 0x80808080u << (8 * live);
 }
+// Whether a lane's bits of both, all its words' ANDed, say that a byte is elsewhere.
 __device__ __forceinline__ bool any_not_middle(uint32_t middle)
 {
     return __ballot((middle & 0x80808080u) != 0x80808080u) != 0;

@@ -24,9 +24,9 @@
 // 4.9 TB/s; 16 tokens 41 - 43 us (from HBM alone, 131072 rows: 3.4 TB/s, where 1 token
 // reaches 4.4 and the absmax pass, which only reads, 6.8 - 7.2); the vector units are
 // busy 53% of the time, and waves wait for weights and at the stages' barriers.  32
-// tokens 50 us, 64 tokens 69 us, where the conversions, the reads of the tokens from LDS and the MFMAs
-// come one after the other in too few waves.  One token by 14336 x 4096: 9.8 us, of
-// which 3.2 are an empty launch's.
+// tokens 50 us, 64 tokens 69 us, where the conversions, the reads of the tokens from
+// LDS and the MFMAs come one after the other in too few waves.  One token by 14336 x
+// 4096: 9.8 us, of which 3.2 are an empty launch's.
 #include "launch_mm.h"
 #include "mm_common.h"
 

@@ -229,3 +229,22 @@ def test_infinite_and_nan_elements(M, N, K, far):
     for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
         y = multiply((qa, sa), (qb, sb), True, M, N, K, flags)
         assert_product(y, want, f"{M}x{N}x{K} {flags} E4M3")
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_nan_blocks_of_zeros(M, N, K):
+    """A block's scale alone makes it NaN, whatever its elements."""
+    nb = -(-K // 32)
+    for e5m2 in (False, True):
+        q = torch.full((M, K), 0x3C if e5m2 else 0x38, dtype=torch.uint8, device="cuda")
+        s = torch.full((M, nb), 127, dtype=torch.uint8, device="cuda")
+        qo = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+        qo[:, 0] = 0x38
+        so = torch.full((N, nb), 127, dtype=torch.uint8, device="cuda")
+        q[M - 1, 32 * (nb - 1):], s[M - 1, nb - 1] = 0, 255
+        so[0, nb // 2], qo[0, 32 * (nb // 2):32 * (nb // 2) + 32] = 255, 0
+        want = torch.ones(M, N, dtype=torch.float64, device="cuda")
+        want[M - 1], want[:, 0] = float("nan"), float("nan")
+        for flags in (0, mx.SCALE_TILED, mx.OUT_F32, mx.OUT_F32 | mx.SCALE_TILED):
+            y = multiply((q, s), (qo, so), True, M, N, K, flags | (mx.A_E5M2 if e5m2 else 0))
+            assert_product(y, want, f"{M}x{N}x{K} {e5m2} {flags}")
