@@ -10,8 +10,9 @@ The same names as the C ABI:
     mx_quantize_grouped_workspace_size, mx_grouped_scale_size, mx_quantize_gated,
     mx_fused_values, mx_absmax_bf16, nvfp4_quantize_transpose,
     mx_matmul, mx_matmul_grouped, mx_matmul_wgrad_grouped, their
-    *_workspace_size, nvfp4_matvec, nvfp4_matvec_experts, mx_status_str,
-    mx_abi_version
+    *_workspace_size, nvfp4_matvec, nvfp4_matvec_experts, mx_rmsnorm,
+    mx_rmsnorm_backward, moe_route, moe_route_backward, moe_sort, moe_gather,
+    moe_combine, moe_combine_backward, mx_status_str, mx_abi_version
 take torch tensors (bf16 inputs, or int16/uint16 holding bf16 bits, on a ROCm
 device).  The casts return dicts of uint8 / float32 torch tensors on the same
 device; the products take those and return a bf16 or float32 tensor.
@@ -36,6 +37,8 @@ GATED_SWIGLU, GATED_GEGLU = 1, 2
 OP_GATED, OP_DGATED = 0x100, 0x200
 # flags of the products (with SCALE_TILED): operand formats, output type
 A_E5M2, B_E5M2, OUT_F32, ACCUMULATE = 4, 32, 64, 128
+# flags of the router (its logits' type, ROUTE_F32 in the C ABI, comes from the tensor)
+ROUTE_SIGMOID, ROUTE_RENORM, ROUTE_GROUP_PAIR, _ROUTE_F32 = 1, 2, 4, 8
 (MX_OK, MX_ERR_NULL, MX_ERR_ENUM, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_WORKSPACE,
  MX_ERR_ALIAS, MX_ERR_HIP, MX_ERR_UNSUPPORTED) = range(9)
 
@@ -48,6 +51,9 @@ EXPORTS = ("mx_quantize", "mx_quantize_workspace_size", "mx_quantize_noalloc", "
            "mx_matmul", "mx_matmul_grouped", "mx_matmul_wgrad_grouped",
            "mx_matmul_workspace_size", "mx_matmul_grouped_workspace_size",
            "mx_matmul_wgrad_grouped_workspace_size", "nvfp4_matvec", "nvfp4_matvec_experts",
+           "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size",
+           "moe_route", "moe_route_backward", "moe_sort", "moe_sort_rows", "moe_sort_workspace_size",
+           "moe_gather", "moe_combine", "moe_combine_backward",
            "mx_status_str", "mx_abi_version")
 
 
@@ -134,6 +140,24 @@ def lib():
         L.nvfp4_matvec_experts.restype = ctypes.c_int
         L.nvfp4_matvec_experts.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, ctypes.c_int, _i64,
                                            _i64, ctypes.c_uint, _vp, _vp]
+        u32, f32, sz = ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
+        for name, args in (
+                ("mx_rmsnorm", [_vp] * 3 + [_i64, _i64, f32, u32] + [_vp] * 10),
+                ("mx_rmsnorm_backward", [_vp] * 7 + [_i64, _i64] + [_vp] * 3 + [sz, _vp]),
+                ("moe_route", [_vp] * 2 + [_i64] * 5 + [f32, u32] + [_vp] * 4),
+                ("moe_route_backward", [_vp] * 4 + [_i64] * 3 + [f32, u32] + [_vp] * 2),
+                ("moe_sort", [_vp] + [_i64] * 5 + [_vp] * 4 + [sz, _vp]),
+                ("moe_gather", [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp]),
+                ("moe_combine", [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp]),
+                ("moe_combine_backward", [_vp, _vp, _i64, _i64] + [_vp] * 3 + [_i64, _i64] + [_vp] * 3)):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
+        L.mx_rmsnorm_backward_workspace_size.restype = sz
+        L.mx_rmsnorm_backward_workspace_size.argtypes = [_i64, _i64]
+        L.moe_sort_rows.restype = _i64
+        L.moe_sort_rows.argtypes = [_i64] * 4
+        L.moe_sort_workspace_size.restype = sz
+        L.moe_sort_workspace_size.argtypes = [_i64] * 3
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ctypes.c_int]
         L.mx_abi_version.restype = ctypes.c_int
@@ -826,3 +850,268 @@ def nvfp4_matvec_experts(x, experts, qw, sw, sg, flags=0, out=None, stream=None)
             experts.data_ptr(), T, top, qw.data_ptr(), sw.data_ptr(), sg.data_ptr(), G, N, K, flags,
             y.data_ptr())
     return y
+
+
+# ---- the norm before a product, the router, and the rows' way to the experts ----
+
+I32 = torch.int32
+
+
+def _want(t, shape, dtypes, name, dev):
+    """An input: a contiguous tensor of this shape and one of these types, on dev."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous tensor {tuple(shape)} on {dev}; got "
+                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _new(out, name, shape, dtype, dev, stream):
+    """Output `name`: out's, of this many elements, or a new one."""
+    t = None if out is None else out.get(name)
+    if t is None:
+        return _empty(shape, dtype, dev, stream)
+    n = 1
+    for d in shape:
+        n *= d
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"out[{name!r}] must be a tensor")
+    ok = t.dtype == dtype or (dtype == BF16 and t.dtype in _BF16_BITS)
+    if not ok or t.numel() != n or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"out[{name!r}] must be a contiguous {dtype} tensor of {n} elements on {dev}; "
+                         f"got {t.dtype}, {t.numel()} elements on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gpu(dev):
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a ROCm (cuda) device, got {dev}")
+
+
+def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, checkpoint=False,
+               out=None, stream=None):
+    """h = x + residual (x itself without), y = h rstd weight with rstd =
+    (mean h^2 + eps)^(-1/2) of each row, for bf16 x [M][K], and the MXFP8 casts
+    of y that `axis` asks for (0: none; flags as for mx_quantize).  Returns {h, y,
+    rstd, q_row, s_row, q_col, s_col, q_h, s_h}, None where not requested: y with
+    want_y (default: without casts), q_h and s_h, an 8-bit copy of h for
+    mx_rmsnorm_backward, with `checkpoint`.  Without a residual h is x."""
+    x = _2d(x, "x")
+    (M, K), dev = x.shape, x.device
+    rp = None if residual is None else _want(residual, x.shape, _BF16_BITS, "residual", dev)
+    wp = None if weight is None else _want(weight, (K,), _BF16_BITS, "weight", dev)
+    o = dict.fromkeys(("h", "y", "rstd", "q_row", "s_row", "q_col", "s_col", "q_h", "s_h"))
+    if residual is not None:
+        o["h"] = _new(out, "h", (M, K), BF16, dev, stream)
+    if want_y or (want_y is None and not axis):
+        o["y"] = _new(out, "y", (M, K), BF16, dev, stream)
+    o["rstd"] = _new(out, "rstd", (M,), F32, dev, stream)
+    if axis:
+        for name, (shape, dtype) in _mx_need(M, K, axis).items():
+            o[name] = _new(out, name, shape, dtype, dev, stream)
+    if checkpoint:
+        o["q_h"] = _new(out, "q_h", (M, K), U8, dev, stream)
+        o["s_h"] = _new(out, "s_h", (M, -(-K // 32)), U8, dev, stream)
+    _gpu(dev)
+    _launch("mx_rmsnorm", dev, stream, lib().mx_rmsnorm, x.data_ptr(), rp, wp, M, K, eps, axis,
+            _at(o["h"]), _at(o["y"]), _at(o["q_row"]), _at(o["s_row"]), _at(o["q_col"]),
+            _at(o["s_col"]), _at(o["q_h"]), _at(o["s_h"]), o["rstd"].data_ptr())
+    if residual is None:
+        o["h"] = x
+    return o
+
+
+def mx_rmsnorm_backward_workspace_size(M: int, K: int) -> int:
+    return lib().mx_rmsnorm_backward_workspace_size(M, K)
+
+
+def mx_rmsnorm_backward(dy, rstd, weight=None, h=None, q_h=None, s_h=None, dres=None,
+                        want_dweight=True, out=None, workspace=None, stream=None):
+    """Gradients of mx_rmsnorm from dy, the gradient of y, the forward's rstd, and
+    its h or the 8-bit copy q_h, s_h.  Returns {dh, dweight}: dh bf16 [M][K], the
+    gradient of x and of the residual, with dres (that of h itself, from the
+    residual stream) added; dweight float32 [K] (None without want_dweight)."""
+    dy = _2d(dy, "dy")
+    (M, K), dev = dy.shape, dy.device
+    if (h is None) == (q_h is None) or (q_h is None) != (s_h is None):
+        raise ValueError("mx_rmsnorm_backward takes either h or q_h and s_h")
+    rp = _want(rstd, (M,), (F32,), "rstd", dev)
+    hp = None if h is None else _want(h, dy.shape, _BF16_BITS, "h", dev)
+    qp = None if q_h is None else _want(q_h, dy.shape, (U8,), "q_h", dev)
+    sp = None if s_h is None else _want(s_h, (M, -(-K // 32)), (U8,), "s_h", dev)
+    wp = None if weight is None else _want(weight, (K,), _BF16_BITS, "weight", dev)
+    dp = None if dres is None else _want(dres, dy.shape, _BF16_BITS, "dres", dev)
+    o = dict(dh=_new(out, "dh", (M, K), BF16, dev, stream), dweight=None)
+    ws, pp, pn = None, None, 0
+    L = lib()
+    if want_dweight:
+        o["dweight"] = _new(out, "dweight", (K,), F32, dev, stream)
+        ws, pp, pn = _product_ws(workspace, L.mx_rmsnorm_backward_workspace_size(M, K), dev, stream)
+    _gpu(dev)
+    _launch("mx_rmsnorm_backward", dev, stream, L.mx_rmsnorm_backward, dy.data_ptr(), hp, qp, sp, rp,
+            wp, dp, M, K, o["dh"].data_ptr(), _at(o["dweight"]), pp, pn)
+    return o
+
+
+def _logits(t):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (BF16, F32):
+        raise TypeError("logits must be a bfloat16 or float32 tensor")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"logits must be a contiguous 2-D tensor, got {tuple(t.shape)}")
+    return _ROUTE_F32 if t.dtype == F32 else 0
+
+
+def moe_route(logits, top, bias=None, flags=0, groups=1, top_groups=1, scale=1.0, want_scores=False,
+              out=None, stream=None):
+    """Each token's `top` experts from its logits [T][E] (bf16 or float32), by
+    softmax scores (sigmoid with ROUTE_SIGMOID) plus bias (float32 [E]), within the
+    best top_groups of `groups` groups.  Returns {experts (int32 [T][top], -1:
+    none), weights (float32 [T][top]: the scores without the bias, divided by their
+    sum with ROUTE_RENORM, times scale), scores (float32 [T][E] with want_scores)}."""
+    f32 = _logits(logits)
+    (T, E), dev = logits.shape, logits.device
+    bp = None if bias is None else _want(bias, (E,), (F32,), "bias", dev)
+    o = dict(experts=_new(out, "experts", (T, top), I32, dev, stream),
+             weights=_new(out, "weights", (T, top), F32, dev, stream),
+             scores=_new(out, "scores", (T, E), F32, dev, stream) if want_scores else None)
+    _gpu(dev)
+    _launch("moe_route", dev, stream, lib().moe_route, logits.data_ptr(), bp, T, E, top, groups,
+            top_groups, scale, flags | f32, o["experts"].data_ptr(), o["weights"].data_ptr(),
+            _at(o["scores"]))
+    return o
+
+
+def moe_route_backward(dweights, logits, experts, flags=0, scale=1.0, dscores=None, out=None,
+                       stream=None):
+    """The gradient of moe_route's logits (a tensor of their shape and type; `out`
+    may hold it) from those of its weights and, with dscores, of its scores; flags
+    and scale as in the forward."""
+    f32 = _logits(logits)
+    (T, E), dev = logits.shape, logits.device
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise ValueError("experts must be a tensor [T][top]")
+    top = experts.shape[1]
+    ep = _want(experts, (T, top), (I32,), "experts", dev)
+    wp = _want(dweights, (T, top), (F32,), "dweights", dev)
+    sp = None if dscores is None else _want(dscores, (T, E), (F32,), "dscores", dev)
+    o = _new({"out": out}, "out", (T, E), logits.dtype, dev, stream)
+    _gpu(dev)
+    _launch("moe_route_backward", dev, stream, lib().moe_route_backward, logits.data_ptr(), ep, wp, sp,
+            T, E, top, scale, flags | f32, o.data_ptr())
+    return o
+
+
+def moe_sort_rows(T: int, top: int, E: int, align: int = 1) -> int:
+    return lib().moe_sort_rows(T, top, E, align)
+
+
+def moe_sort_workspace_size(T: int, top: int, E: int) -> int:
+    return lib().moe_sort_workspace_size(T, top, E)
+
+
+def _slots_2d(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype != I32 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [T][top]")
+    return t
+
+
+def moe_sort(experts, E, align=1, rows=None, out=None, workspace=None, stream=None):
+    """The order of the slots (token, choice) of experts int32 [T][top] by expert,
+    each expert's rows from a multiple of `align` on.  Returns {counts int32 [E],
+    pos int32 [T][top] (each slot's row or -1), slots int32 [rows] (each row's slot
+    or -1)}; rows: by default moe_sort_rows(T, top, E, align), the most there can
+    be.  group_rows[e] of the grouped casts and products is counts[e] rounded up to
+    align."""
+    T, top = _slots_2d(experts, "experts").shape
+    dev, L = experts.device, lib()
+    rows = L.moe_sort_rows(T, top, E, align) if rows is None else int(rows)
+    o = dict(counts=_new(out, "counts", (E,), I32, dev, stream),
+             pos=_new(out, "pos", (T, top), I32, dev, stream),
+             slots=_new(out, "slots", (rows,), I32, dev, stream))
+    ws, wp, wn = _product_ws(workspace, L.moe_sort_workspace_size(T, top, E), dev, stream)
+    _gpu(dev)
+    _launch("moe_sort", dev, stream, L.moe_sort, experts.data_ptr(), T, top, E, align, rows,
+            o["counts"].data_ptr(), o["pos"].data_ptr(), o["slots"].data_ptr(), wp, wn)
+    return o
+
+
+def moe_gather(x, slots, top, out=None, stream=None):
+    """Row r of the result [rows][...] is row slots[r] // top of x [T][...] (any
+    type), or zeros where slots[r] names no slot."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous tensor [T][...]")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D tensor")
+    dev, T, rows = x.device, x.shape[0], slots.shape[0]
+    sp = _want(slots, (rows,), (I32,), "slots", dev)
+    o = _new({"out": out}, "out", (rows, *x.shape[1:]), x.dtype, dev, stream)
+    width = x.element_size()
+    for d in x.shape[1:]:
+        width *= d
+    _gpu(dev)
+    _launch("moe_gather", dev, stream, lib().moe_gather, x.data_ptr(), T, top, sp, rows, width,
+            o.data_ptr())
+    return o
+
+
+def _rows_and_slots(y, weights, pos):
+    """(T, top, rows, K) of experts' rows y: [rows][K] with pos [T][top], or
+    [T][top][K]."""
+    y = _bf16_bits(y)
+    if pos is None:
+        if y.dim() != 3:
+            raise ValueError(f"without pos y must be [T][top][K], got {tuple(y.shape)}")
+        T, top, K = y.shape
+        rows = T * top
+    else:
+        T, top = _slots_2d(pos, "pos").shape
+        if y.dim() != 2:
+            raise ValueError(f"y must be [rows][K], got {tuple(y.shape)}")
+        rows, K = y.shape
+    dev = y.device
+    pp = None if pos is None else _want(pos, (T, top), (I32,), "pos", dev)
+    wp = None if weights is None else _want(weights, (T, top), (F32,), "weights", dev)
+    return T, top, rows, K, pp, wp
+
+
+def moe_combine(y, weights=None, pos=None, out=None, stream=None):
+    """out[t] = sum_j weights[t][j] y[pos[t][j]] (bf16 [T][K]) of the experts' rows
+    y bf16 [rows][K]; a pos that names no row adds nothing.  Without pos y is
+    [T][top][K], as nvfp4_matvec_experts returns it; without weights they are 1."""
+    T, top, rows, K, pp, wp = _rows_and_slots(y, weights, pos)
+    dev = y.device
+    o = _new({"out": out}, "out", (T, K), BF16, dev, stream)
+    _gpu(dev)
+    _launch("moe_combine", dev, stream, lib().moe_combine, y.data_ptr(), rows, K, pp, wp, T, top,
+            o.data_ptr())
+    return o
+
+
+def moe_combine_backward(dout, y, weights=None, pos=None, slots=None, want_dweights=True, out=None,
+                         stream=None):
+    """Gradients of moe_combine from that of its output, dout bf16 [T][K]: {dy (of
+    y's shape, zeros in rows without a slot), dweights (float32 [T][top])}.  With
+    pos, slots as moe_sort returned it."""
+    T, top, rows, K, pp, wp = _rows_and_slots(y, weights, pos)
+    dev = y.device
+    if (pos is None) != (slots is None):
+        raise ValueError("pos and slots go together")
+    gp = _want(dout, (T, K), _BF16_BITS, "dout", dev)
+    sp = None if slots is None else _want(slots, (rows,), (I32,), "slots", dev)
+    o = dict(dy=_new(out, "dy", tuple(y.shape), BF16, dev, stream),
+             dweights=_new(out, "dweights", (T, top), F32, dev, stream) if want_dweights else None)
+    _gpu(dev)
+    _launch("moe_combine_backward", dev, stream, lib().moe_combine_backward, gp, y.data_ptr(), rows, K,
+            pp, sp, wp, T, top, o["dy"].data_ptr(), _at(o["dweights"]))
+    return o

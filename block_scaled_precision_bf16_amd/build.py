@@ -15,6 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxcast.so")
 SOURCES = ["api.cpp", "mx_cast.hip", "mx_cast_any.hip", "nvfp4.hip", "nvfp4_any.hip",
            "api_matmul.cpp", "mm_any.hip", "mm_tile.hip", "mm_tile_f32.hip", "mm_small.hip", "mm_pack.hip", "nvfp4_matvec.hip",
+           "api_norm.cpp", "norm.hip", "mx_cast_norm.hip", "api_moe.cpp", "moe_route.hip", "moe_rows.hip",
            *[f"mx_cast_{kind}_{fmt}.hip" for kind in ("fmt", "grp", "rag")
              for fmt in ("e4m3", "e5m2", "e4m3_up", "e5m2_up")]]
 

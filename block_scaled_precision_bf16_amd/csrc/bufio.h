@@ -53,6 +53,25 @@ __device__ __forceinline__ uint4 buf_load16(rsrc_t r, uint32_t off)
 }
 
 template <int AUX = 0>
+__device__ __forceinline__ uint2 buf_load8(rsrc_t r, uint32_t off)
+{
+    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, AUX);
+    return make_uint2(v[0], v[1]);
+}
+
+template <int AUX = 0>
+__device__ __forceinline__ uint32_t buf_load4(rsrc_t r, uint32_t off)
+{
+    return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, AUX);
+}
+
+template <int AUX = 0>
+__device__ __forceinline__ uint32_t buf_load1(rsrc_t r, uint32_t off)
+{
+    return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, AUX);
+}
+
+template <int AUX = 0>
 __device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, uint4 v)
 {
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{v.x, v.y, v.z, v.w}, r, (int)off, 0, AUX);

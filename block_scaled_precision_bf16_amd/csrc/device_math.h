@@ -414,6 +414,14 @@ __device__ __forceinline__ uint32_t dgated_pair(uint32_t g, uint32_t dy, uint32_
                       dgated_value<OP>(bf16_hi(g), bf16_hi(dy), bf16_hi(l), gate_half));
 }
 
+// The norm's output of a packed pair: each element times its column's weight (16
+// significant bits at most, exact in fp32), times its row's rstd, rounded once to
+// fp32 and then to bf16.
+__device__ __forceinline__ uint32_t norm_pair(uint32_t h, float rstd, uint32_t w)
+{
+    return bf16x2_rne((bf16_lo(h) * bf16_lo(w)) * rstd, (bf16_hi(h) * bf16_hi(w)) * rstd);
+}
+
 // ---------------------------------------------------------------------------
 // Cross-lane max within aligned groups of 2 / 4 lanes (DPP quad permutes,
 // no LDS traffic).

@@ -11,7 +11,8 @@ namespace mxk {
 enum Op : int {
     OP_PLAIN = 0, OP_GELU = 1, OP_DGELU = 2, OP_SWIGLU = 3, OP_GEGLU = 4,
     OP_DSILU = 5,                    // dsilu(x) * grad
-    OP_DSWIGLU = 6, OP_DGEGLU = 7    // gated backward: [d_gate | d_linear]
+    OP_DSWIGLU = 6, OP_DGEGLU = 7,   // gated backward: [d_gate | d_linear]
+    OP_NORM = 8                      // (x row_scale[row]) aux[column] (launch_norm.h)
 };
 
 // MX format variants, as flags (the same bits as the ABI's flags beside the
@@ -175,7 +176,7 @@ inline int any_walk_len(const int64_t *rows, int groups, int64_t K)
 
 struct MxArgs {
     const uint16_t *x;     // input (gated: [M][2N] with the linear half at lin_off)
-    const uint16_t *aux;   // grad for dGELU, else unused
+    const uint16_t *aux;   // grad for dGELU, the norm's weight (or null), else unused
     int64_t M, K;          // rows and columns of the quantised tensor
     int64_t ldx;           // row stride of x in elements
     int64_t lin_off;       // gated: column offset of the linear half
@@ -186,6 +187,7 @@ struct MxArgs {
     int group, groups_m;   // sub-tiles per workgroup walk, walks along M
     int tiled;             // scales in the GEMM-ready tile layout (walks of >= 2 sub-tiles)
     int qcol_nt;           // plain cast with both outputs: transposed stores non-temporal
+    const float *row_scale = nullptr;   // OP_NORM: the rows' reciprocal root mean squares
 };
 
 // The plain cast's transposed stores are non-temporal only for a transposed

@@ -1,0 +1,407 @@
+// moe_rows.hip -- the tokens' rows to their experts and back (gfx950): a stable
+// sort of the slots (token, choice) by expert, the rows in that order, and the
+// weighted sum of the experts' rows with its gradients.
+//
+// The sort counts.  A workgroup's slots are taken in order, a run of them by each
+// wave; a wave counts 64 slots at a time, the lanes of one expert found by a
+// ballot for each bit of its index, so that ranks are those of the slots' order
+// and nothing depends on the order of atomics.  Few slots take one workgroup and
+// one launch; more, three: counts of each workgroup, sums over the workgroups and
+// experts, ranks.
+//
+// The rest moves rows and is bound by memory: 16-byte accesses wherever the rows'
+// length allows, several in flight for each lane.
+#include "bufio.h"
+#include "device_math.h"
+#include "launch_moe.h"
+#include "wave.h"
+
+namespace mxk {
+
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortE = 1024;
+
+// Lanes of the wave whose e is this lane's (e < 2^bits).
+__device__ __forceinline__ uint64_t same_lanes(int e, int bits)
+{
+    uint64_t m = ~0ull;
+    for (int b = 0; b < bits; b++) {
+        const bool one = (e >> b) & 1;
+        const uint64_t v = __builtin_amdgcn_ballot_w64(one);
+        m &= one ? v : ~v;
+    }
+    return m;
+}
+
+// Rank of this lane's slot among its expert's slots of the run so far, whose
+// counts are in cnt (one wave's own); -1 without an expert (e = E).
+__device__ __forceinline__ int rank_and_count(int32_t *cnt, int e, int E, int bits, int lane)
+{
+    const uint64_t m = same_lanes(e, bits);
+    const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
+    int at = -1;
+    if (e < E)
+        at = cnt[e] + before;
+    __builtin_amdgcn_wave_barrier();
+    if (e < E && before == 0)
+        cnt[e] += __builtin_popcountll(m);
+    __builtin_amdgcn_wave_barrier();
+    return at;
+}
+
+__device__ __forceinline__ int expert_of(const SortArgs &a, int64_t slot, int64_t end)
+{
+    int e = a.E;
+    if (slot < end) {
+        const int v = a.experts[slot];
+        e = v >= 0 && v < a.E ? v : a.E;
+    }
+    return e;
+}
+
+// Sum of v over the workgroup's threads before this one (red: a word per wave),
+// and over all of them.
+__device__ __forceinline__ int before_sum(int v, int32_t *red, int waves, int &total)
+{
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    int s = v;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(s, d, 64);
+        s += lane >= d ? o : 0;
+    }
+    if (lane == 63)
+        red[wave] = s;
+    __syncthreads();
+    int base = 0;
+    total = 0;
+    for (int w = 0; w < waves; w++) {
+        base += w < wave ? red[w] : 0;
+        total += red[w];
+    }
+    __syncthreads();
+    return base + s - v;
+}
+
+// -1 in the rows between expert e's last and the next expert's first, for the
+// workgroup's share of the experts, and behind the last one's (from `total` on).
+__device__ __forceinline__ void fill_rows(const SortArgs &a, const int32_t *start, const int32_t *counts,
+                                          int64_t total, int block, int blocks)
+{
+    if (a.align > 1)
+        for (int e = block; e < a.E; e += blocks) {
+            const int64_t from = (int64_t)start[e] + counts[e], to = e + 1 < a.E ? start[e + 1] : total;
+            for (int64_t r = from + threadIdx.x; r < to; r += blockDim.x)
+                a.slots[r] = -1;
+        }
+    for (int64_t r = total + (int64_t)block * blockDim.x + threadIdx.x; r < a.rows;
+         r += (int64_t)blocks * blockDim.x)
+        a.slots[r] = -1;
+}
+
+__device__ __forceinline__ int index_bits(int E) { return 32 - __builtin_clz((unsigned)E); }
+
+// One workgroup sorts all slots: its waves' counts in LDS, their sums, the ranks.
+// The waves' slots are taken twice (they are in the caches the second time).
+__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(SortArgs a)
+{
+    extern __shared__ int32_t lds[];                  // [waves][E], start [E], counts [E]
+    __shared__ int32_t red[kSortWaves];
+    int32_t *const start = lds + kSortWaves * a.E, *const counts = start + a.E;
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, bits = index_bits(a.E);
+    const int64_t run = a.chunk / kSortWaves, first = wave * run;
+    const int64_t end = first + run < a.N ? first + run : a.N;
+    int32_t *const cnt = lds + wave * a.E;
+    for (int i = threadIdx.x; i < kSortWaves * a.E; i += kSortThreads)
+        lds[i] = 0;
+    __syncthreads();
+    for (int64_t s = first; s < end; s += 64)
+        rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+    __syncthreads();
+    // each thread's experts are neighbours, so that the threads' sums are in order
+    const int per = (a.E + kSortThreads - 1) / kSortThreads, e0 = (int)threadIdx.x * per;
+    int mine = 0;
+    for (int e = e0; e < e0 + per && e < a.E; e++) {
+        int n = 0;
+        for (int w = 0; w < kSortWaves; w++) {
+            const int c = lds[w * a.E + e];
+            lds[w * a.E + e] = n;
+            n += c;
+        }
+        counts[e] = n;
+        a.counts[e] = n;
+        mine += (n + a.align - 1) / a.align * a.align;
+    }
+    int total;
+    int at = before_sum(mine, red, kSortWaves, total);
+    for (int e = e0; e < e0 + per && e < a.E; e++) {
+        start[e] = at;
+        for (int w = 0; w < kSortWaves; w++)
+            lds[w * a.E + e] += at;
+        at += (counts[e] + a.align - 1) / a.align * a.align;
+    }
+    __syncthreads();
+    for (int64_t s = first; s < end; s += 64) {
+        const int row = rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+        if (s + lane < end) {
+            a.pos[s + lane] = row;
+            if (row >= 0)
+                a.slots[row] = (int32_t)(s + lane);
+        }
+    }
+    fill_rows(a, start, counts, total, 0, 1);
+}
+
+// Counts of each workgroup's slots: ws[block][E].
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a)
+{
+    __shared__ int32_t cnt[kSortE];
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads)
+        cnt[e] = 0;
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * a.chunk;
+    const int64_t end = first + a.chunk < a.N ? first + a.chunk : a.N;
+    for (int64_t s = first + threadIdx.x; s < end; s += kSortThreads) {
+        const int e = expert_of(a, s, end);
+        if (e < a.E)
+            atomicAdd(&cnt[e], 1);   // sums of ones: the same in any order
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads)
+        a.ws[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+}
+
+// Thread e: sums over the workgroups before each, in place; the experts' counts;
+// their first rows in ws[blocks].
+__global__ __launch_bounds__(kSortE) void sort_sum_kernel(SortArgs a)
+{
+    __shared__ int32_t red[kSortE / 64];
+    const int e = (int)threadIdx.x;
+    int n = 0;
+    if (e < a.E) {
+        for (int b = 0; b < a.blocks; b++) {
+            const int c = a.ws[(int64_t)b * a.E + e];
+            a.ws[(int64_t)b * a.E + e] = n;
+            n += c;
+        }
+        a.counts[e] = n;
+    }
+    int total;
+    const int at = before_sum((n + a.align - 1) / a.align * a.align, red, kSortE / 64, total);
+    if (e < a.E)
+        a.ws[(int64_t)a.blocks * a.E + e] = at;
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a)
+{
+    extern __shared__ int32_t lds[];                  // [waves][E]
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, bits = index_bits(a.E);
+    const int64_t run = a.chunk / kSortWaves, first = (int64_t)blockIdx.x * a.chunk + wave * run;
+    const int64_t end = first + run < a.N ? first + run : a.N;
+    const int32_t *const start = a.ws + (int64_t)a.blocks * a.E;
+    int32_t *const cnt = lds + wave * a.E;
+    for (int i = threadIdx.x; i < kSortWaves * a.E; i += kSortThreads)
+        lds[i] = 0;
+    __syncthreads();
+    for (int64_t s = first; s < end; s += 64)
+        rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+        int n = start[e] + a.ws[(int64_t)blockIdx.x * a.E + e];
+        for (int w = 0; w < kSortWaves; w++) {
+            const int c = lds[w * a.E + e];
+            lds[w * a.E + e] = n;
+            n += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t s = first; s < end; s += 64) {
+        const int row = rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+        if (s + lane < end) {
+            a.pos[s + lane] = row;
+            if (row >= 0)
+                a.slots[row] = (int32_t)(s + lane);
+        }
+    }
+    const int64_t total = (int64_t)start[a.E - 1] +
+                          (a.counts[a.E - 1] + a.align - 1) / a.align * (int64_t)a.align;
+    fill_rows(a, start, a.counts, total, (int)blockIdx.x, (int)gridDim.x);
+}
+
+hipError_t launch_sort(const SortArgs &a, hipStream_t s)
+{
+    const size_t lds = (size_t)kSortWaves * a.E * sizeof(int32_t);
+    if (!a.ws) {
+        hipLaunchKernelGGL(sort_alone_kernel, dim3(1), dim3(kSortThreads),
+                           lds + 2 * (size_t)a.E * sizeof(int32_t), s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, s, a);
+    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSortE), 0, s, a);
+    hipLaunchKernelGGL(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads), lds, s, a);
+    return hipGetLastError();
+}
+
+// ---- rows ---------------------------------------------------------------------
+
+// Row blockIdx.y * n + ... of out; V: the widest access that every row allows.
+template <class V>
+__global__ __launch_bounds__(256) void gather_kernel(GatherArgs a)
+{
+    const int64_t n = a.row_bytes / (int64_t)sizeof(V);
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const int32_t slot = a.slots[r];
+        V *const o = reinterpret_cast<V *>(a.out + r * a.row_bytes);
+        if (slot < 0 || slot >= a.T * a.top) {
+            for (int64_t i = threadIdx.x; i < n; i += 256)
+                o[i] = V{};
+            continue;
+        }
+        const V *const x = reinterpret_cast<const V *>(a.x + (int64_t)(slot / a.top) * a.row_bytes);
+        for (int64_t i = threadIdx.x; i < n; i += 256)
+            o[i] = x[i];
+    }
+}
+
+hipError_t launch_gather(const GatherArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.rows < 65536 ? a.rows : 65536));
+    if (a.row_bytes % 16 == 0)
+        hipLaunchKernelGGL(gather_kernel<u32x4_t>, grid, dim3(256), 0, s, a);
+    else if (a.row_bytes % 4 == 0)
+        hipLaunchKernelGGL(gather_kernel<uint32_t>, grid, dim3(256), 0, s, a);
+    else if (a.row_bytes % 2 == 0)
+        hipLaunchKernelGGL(gather_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(gather_kernel<uint8_t>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Row of slot s in y, or -1.
+__device__ __forceinline__ int64_t row_of_slot(const CombineArgs &a, int64_t s)
+{
+    if (!a.pos)
+        return s;
+    const int32_t r = a.pos[s];
+    return r >= 0 && r < a.rows ? r : -1;
+}
+
+// E elements at p as fp32 (E = 8: one 16-byte access; E = 1), and back.
+template <int E>
+__device__ __forceinline__ void load_elems(const uint16_t *p, float (&v)[E])
+{
+    if constexpr (E == 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int d = 0; d < 4; d++) {
+            v[2 * d] = bf16_lo(w[d]);
+            v[2 * d + 1] = bf16_hi(w[d]);
+        }
+    } else {
+        v[0] = bf16_lo(p[0]);
+    }
+}
+template <int E>
+__device__ __forceinline__ void store_elems(uint16_t *p, const float (&v)[E])
+{
+    if constexpr (E == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                                   bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    else
+        p[0] = (uint16_t)(bf16x2_rne(v[0], 0.0f) & 0xFFFFu);
+}
+
+// One group of E elements of one token per thread.
+template <int E>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int64_t parts)
+{
+    for (int64_t b = blockIdx.x; b < a.T * parts; b += gridDim.x) {
+        const int64_t t = b / parts, c = (b - t * parts) * 256 + threadIdx.x;
+        if (c * E >= a.K)
+            continue;
+        float acc[E];
+#pragma unroll
+        for (int d = 0; d < E; d++)
+            acc[d] = 0.0f;
+        for (int j = 0; j < a.top; j++) {
+            const int64_t s = t * a.top + j, r = row_of_slot(a, s);
+            if (r < 0)
+                continue;
+            const float w = a.weights ? a.weights[s] : 1.0f;
+            float v[E];
+            load_elems<E>(a.y + r * a.K + c * E, v);
+#pragma unroll
+            for (int d = 0; d < E; d++)
+                acc[d] = __builtin_fmaf(w, v[d], acc[d]);
+        }
+        store_elems<E>(a.out + t * a.K + c * E, acc);
+    }
+}
+
+hipError_t launch_combine(const CombineArgs &a, hipStream_t s)
+{
+    const int64_t per = a.K % 8 == 0 ? 2048 : 256, parts = (a.K + per - 1) / per;
+    const dim3 grid((unsigned)(a.T * parts < (1 << 22) ? a.T * parts : 1 << 22));
+    if (a.K % 8 == 0)
+        hipLaunchKernelGGL(combine_kernel<8>, grid, dim3(256), 0, s, a, parts);
+    else
+        hipLaunchKernelGGL(combine_kernel<1>, grid, dim3(256), 0, s, a, parts);
+    return hipGetLastError();
+}
+
+// A wave per slot, then a wave per 64 rows for those without a slot.
+template <int E>
+__global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a)
+{
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), N = a.T * a.top;
+    if (w < N) {
+        const int64_t r = row_of_slot(a, w), t = w / a.top;
+        float dot = 0.0f;
+        if (r >= 0) {
+            const float wt = a.weights ? a.weights[w] : 1.0f;
+            const bool mine = !a.slots || a.slots[r] == w;   // the row's only writer
+            for (int64_t k = lane * E; k < a.K; k += 64 * E) {
+                float g[E], y[E], o[E];
+                load_elems<E>(a.dout + t * a.K + k, g);
+                load_elems<E>(a.y + r * a.K + k, y);
+#pragma unroll
+                for (int d = 0; d < E; d++) {
+                    dot = __builtin_fmaf(g[d], y[d], dot);
+                    o[d] = wt * g[d];
+                }
+                if (mine)
+                    store_elems<E>(a.out + r * a.K + k, o);
+            }
+            dot = wave_sum(dot);
+        }
+        if (a.dweights && lane == 0)
+            a.dweights[w] = dot;
+        return;
+    }
+    if (!a.slots)
+        return;
+    const int64_t r0 = (w - N) * 64;
+    const bool empty = r0 + lane < a.rows && a.slots[r0 + lane] == -1;
+    uint64_t m = __builtin_amdgcn_ballot_w64(empty);
+    float zero[E] = {};
+    while (m) {
+        const int64_t r = r0 + __builtin_ctzll(m);
+        m &= m - 1;
+        for (int64_t k = lane * E; k < a.K; k += 64 * E)
+            store_elems<E>(a.out + r * a.K + k, zero);
+    }
+}
+
+hipError_t launch_combine_back(const CombineArgs &a, hipStream_t s)
+{
+    const int64_t waves = a.T * a.top + (a.slots ? (a.rows + 63) / 64 : 0);
+    const dim3 grid((unsigned)((waves + 3) / 4));
+    if (a.K % 8 == 0)
+        hipLaunchKernelGGL(combine_back_kernel<8>, grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(combine_back_kernel<1>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace mxk

@@ -191,6 +191,28 @@ __device__ __forceinline__ void load_tile(const MxArgs &a, const LaneAt &l, int 
     const rsrc_t rx = make_rsrc(a.x, 2 * tile, 2 * total);
     const uint32_t rs = (uint32_t)(2 * a.ldx);
     const uint32_t off = live ? (uint32_t)l.row * rs + (uint32_t)(2 * kColsPerLane * l.cl) : kDead;
+    if constexpr (OP == OP_NORM) {
+        // this lane's 8 weights and the row scales of its 16 rows (those past M
+        // read as 0, as their elements do)
+        uint4 wt = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        if (a.aux)
+            wt = buf_load16(make_rsrc(a.aux, 2 * (int64_t)tk * kTileK, 2 * a.K),
+                            live ? (uint32_t)(2 * kColsPerLane * l.cl) : kDead);
+        const rsrc_t rr = make_rsrc(a.row_scale, 4 * (int64_t)tm * kTileM, 4 * a.M);
+        float sc[kRowsPerLane];
+#pragma unroll
+        for (int r = 0; r < kRowsPerLane; r++)
+            sc[r] = f32_bits(buf_load4(rr, live ? (uint32_t)(4 * (l.row + r)) : kDead));
+#pragma unroll
+        for (int r = 0; r < kRowsPerLane; r++) {
+            const uint4 v = buf_load16<XA>(rx, off + r * rs);
+            w[r][0] = norm_pair(v.x, sc[r], wt.x);
+            w[r][1] = norm_pair(v.y, sc[r], wt.y);
+            w[r][2] = norm_pair(v.z, sc[r], wt.z);
+            w[r][3] = norm_pair(v.w, sc[r], wt.w);
+        }
+        return;
+    }
     rsrc_t rb = rx;
     uint32_t rbs = rs, boff = off;
     if constexpr (OP == OP_DGELU || OP == OP_DSILU) {

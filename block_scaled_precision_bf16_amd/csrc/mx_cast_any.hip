@@ -113,6 +113,17 @@ __device__ __forceinline__ void any_load(const MxArgs &a, const AnyView &v, int6
             const uint32_t p = pack2(e[2 * i], e[2 * i + 1]);
             w[i] = fused_pair<OP>(p, p);
         }
+    } else if constexpr (OP == OP_NORM) {
+        // the column's weight, and the row scales (0 past the last row; one
+        // address for all lanes of a wave)
+        const uint32_t wt = !a.aux ? 0x3F803F80u : col_ok ? (uint32_t)a.aux[k] * 0x10001u : 0u;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const float s0 = m + 2 * i < v.M ? a.row_scale[m + 2 * i] : 0.0f;
+            const float s1 = m + 2 * i + 1 < v.M ? a.row_scale[m + 2 * i + 1] : 0.0f;
+            w[i] = bf16x2_rne((bf16_lo(e[2 * i]) * bf16_lo(wt)) * s0,
+                              (bf16_lo(e[2 * i + 1]) * bf16_lo(wt)) * s1);
+        }
     } else {
         // second operand: the linear half (gated) or grad (dGELU, dSiLU)
         constexpr bool gated = OP == OP_SWIGLU || OP == OP_GEGLU;
@@ -384,6 +395,7 @@ hipError_t launch_mx_cast_any(int op, unsigned axis, unsigned fmt, bool dbias, c
     case OP_DSILU: return launch_any_op<OP_DSILU>(axis, fmt, dbias, a, gt, s);
     case OP_DSWIGLU: return launch_any_op<OP_DSWIGLU>(axis, fmt, false, a, gt, s);
     case OP_DGEGLU: return launch_any_op<OP_DGEGLU>(axis, fmt, false, a, gt, s);
+    case OP_NORM: return launch_any_op<OP_NORM>(axis, fmt, false, a, gt, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -25,7 +25,11 @@
  *     the round-up scale rule, GEMM-ready scale tiles, any row count and row
  *     length (partial edge blocks);
  *   - products of the casts' outputs: MXFP8 matrix products, dense and grouped
- *     by expert, with their gradients, and NVFP4 matrix-vector products.
+ *     by expert, with their gradients, and NVFP4 matrix-vector products;
+ *   - what stands around them in a transformer layer: the root-mean-square norm
+ *     whose output the casts take, the router whose experts the products go
+ *     through, and the way of the tokens' rows to the experts and back, each
+ *     with its gradients.
  *
  * Numerics (the pages name these formats but do not define their
  * arithmetic; these are the readings the library implements bit-exactly):
@@ -552,6 +556,190 @@ mx_status nvfp4_matvec(const void *x, int64_t T, const uint8_t *qw, const uint8_
 mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T, int64_t top,
                                const uint8_t *qw, const uint8_t *sw, const float *sg, int G,
                                int64_t N, int64_t K, unsigned flags, void *y, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of a residual stream, with the casts of its output:
+ *   h[m][k]  = bf16(fl32(x + residual)); x itself without a residual
+ *   rstd[m]  = (mean_k h[m][k]^2 + eps)^(-1/2), the sum in fp32 in a fixed order
+ *   y[m][k]  = bf16(fl32((h weight) rstd)), where fp32 holds h weight exactly
+ * and the MXFP8 casts of y, exactly as mx_quantize casts that tensor.
+ *   x, residual  device, bf16 [M][K]; residual may be NULL
+ *   weight     device, bf16 [K]; NULL: ones
+ *   M, K       as for mx_quantize.  K a multiple of 8 up to 16384 keeps a row in
+ *              registers, any other K reads it twice
+ *   eps        finite and not negative (MX_ERR_ENUM otherwise)
+ *   axis_mask  0 (no casts), or as for mx_quantize, flags included
+ *   h          bf16 [M][K], required iff there is a residual
+ *   y          bf16 [M][K] or NULL (not written: the casts do not need it)
+ *   q_row, s_row, q_col, s_col  as for mx_quantize
+ *   q_h, s_h   NULL, or an 8-bit copy of h for the backward: the row-wise MXFP8
+ *              cast of h with E4M3 elements, MX_SCALE_ROUND_UP and compact
+ *              scales, [M][K] and [M][ceil(K/32)], whatever axis_mask says.  It
+ *              is the activation checkpoint of mx_rmsnorm_backward, at half of
+ *              h's memory; one step of its elements is 2^-3 of their binade
+ *   rstd       fp32 [M]
+ * A row that holds Inf or NaN, or whose squares' sum passes fp32, gets what these
+ * formulas give in fp32 (a NaN or 0 rstd).  Errors as for mx_quantize.
+ */
+mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, int64_t M, int64_t K,
+                     float eps, unsigned axis_mask, void *h, void *y, uint8_t *q_row,
+                     uint8_t *s_row, uint8_t *q_col, uint8_t *s_col, uint8_t *q_h, uint8_t *s_h,
+                     float *rstd, hipStream_t stream);
+
+/*
+ * Gradients of mx_rmsnorm.  With xhat = h rstd, g = dy weight and
+ * c[m] = mean_k(g xhat):
+ *   dh[m][k]    = bf16(dres + rstd (g - xhat c))     the gradient of x, and the
+ *                 same of the residual
+ *   dweight[k]  = sum_m dy xhat
+ * sums in fp32 in a fixed order (results are run-to-run identical).
+ *   dy         device, bf16 [M][K]: the gradient of y
+ *   h          bf16 [M][K], or NULL: then
+ *   q_h, s_h   the forward's 8-bit copy is read in its place (NULL with h)
+ *   rstd       fp32 [M], of the forward
+ *   weight     bf16 [K] or NULL
+ *   dres       bf16 [M][K], the gradient that arrives at h from the residual
+ *              stream, or NULL
+ *   dh         bf16 [M][K]
+ *   dweight    fp32 [K], or NULL: not computed
+ *   workspace, workspace_bytes  device scratch of at least
+ *              mx_rmsnorm_backward_workspace_size() bytes with dweight
+ *              (per-workgroup partial sums; NULL and 0 without)
+ * MX_ERR_NULL also for both or neither of h and q_h.
+ */
+mx_status mx_rmsnorm_backward(const void *dy, const void *h, const uint8_t *q_h, const uint8_t *s_h,
+                              const float *rstd, const void *weight, const void *dres, int64_t M,
+                              int64_t K, void *dh, float *dweight, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+size_t mx_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
+
+/*
+ * A router: each token's experts and their weights, from its logits.
+ *   p[t][e]   = softmax over e of logits[t], or with MX_ROUTE_SIGMOID the
+ *               logistic function of each
+ *   key[t][e] = p + bias[e] (bias NULL: 0).  An expert whose logit or bias is
+ *               -Inf is masked: it is never chosen
+ *   groups    the E experts are `groups` runs of E / groups; a group's score is
+ *             its best key, or with MX_ROUTE_GROUP_PAIR the sum of its two best
+ *             (of its one, where it has one); the top_groups best groups stay.
+ *             groups = 1: all of them
+ *   experts   the `top` best keys of these, best first; equal keys, and equal
+ *             groups, the lowest index first.  Keys are compared in 64 bits;
+ *             without a bias, and where no two are added, by the logits
+ *             themselves, exactly
+ *   weights   p of the chosen ones (without the bias), with MX_ROUTE_RENORM
+ *             divided by their sum (0 where that is 0), times scale
+ * A slot that no expert is left for (fewer unmasked ones than `top`) gets expert
+ * -1 and weight 0, which nvfp4_matvec_experts and moe_sort take as no expert.  A
+ * token with a NaN among its p or keys gets experts -1 and weights NaN.
+ *   logits    device, [T][E]: bf16, or fp32 with MX_ROUTE_F32
+ *   bias      device, fp32 [E] or NULL
+ *   T, E      1 <= T <= 2^23, 1 <= E <= 1024, T * E <= 2^40
+ *   top       1 <= top <= 64, top <= E; 1 <= groups <= 64 divides E,
+ *             1 <= top_groups <= groups
+ *   scale     finite
+ *   experts   int32 [T][top];  weights  fp32 [T][top]
+ *   scores    fp32 [T][E], p itself (for a balance loss), or NULL
+ * Errors: MX_ERR_ENUM for an unknown flag or a scale that is not finite,
+ * MX_ERR_SHAPE for a size outside these; the others as for the casts (logits,
+ * experts, weights and scores 16-byte aligned, bias 4-byte).
+ */
+#define MX_ROUTE_SIGMOID 1u
+#define MX_ROUTE_RENORM 2u
+#define MX_ROUTE_GROUP_PAIR 4u
+#define MX_ROUTE_F32 8u
+mx_status moe_route(const void *logits, const float *bias, int64_t T, int64_t E, int64_t top,
+                    int64_t groups, int64_t top_groups, float scale, unsigned flags,
+                    int32_t *experts, float *weights, float *scores, hipStream_t stream);
+
+/*
+ * The gradient of a router's logits (the choice itself has none, nor has the
+ * bias): from the gradients of the weights and, with dscores, of the scores.
+ *   logits, T, E, top, scale, flags  as for moe_route (MX_ROUTE_GROUP_PAIR may
+ *             be set and changes nothing)
+ *   experts   int32 [T][top] as moe_route chose them; an index outside 0 .. E - 1
+ *             is no expert, one named twice counts twice
+ *   dweights  fp32 [T][top];  dscores  fp32 [T][E] or NULL
+ *   dlogits   [T][E], of the logits' type
+ * The gradients of a token whose p hold a NaN are NaN; those of masked experts 0.
+ */
+mx_status moe_route_backward(const void *logits, const int32_t *experts, const float *dweights,
+                             const float *dscores, int64_t T, int64_t E, int64_t top, float scale,
+                             unsigned flags, void *dlogits, hipStream_t stream);
+
+/*
+ * The order of the tokens' rows by expert.  A slot is a (token, choice) pair, in
+ * the order of experts[T][top]; each expert's rows are its slots in that order,
+ * the experts one after the other, each from a multiple of `align` rows on (the
+ * rows that mx_quantize_grouped and mx_matmul_grouped take, with group_rows[e] =
+ * counts[e] rounded up to align).
+ *   experts   device, int32 [T][top]; an index outside 0 .. E - 1 is no expert
+ *   T, top    >= 1, top <= 64, T * top <= 2^23;  1 <= E <= 1024;  1 <= align <= 4096
+ *   rows      rows the caller has room for: at least moe_sort_rows(T, top, E,
+ *             align), at most 2^24
+ *   counts    int32 [E]: the slots of each expert (padding not among them)
+ *   pos       int32 [T][top]: each slot's row, -1 without an expert
+ *   slots     int32 [rows]: each row's slot; -1 for padding and for rows behind
+ *             the last expert's
+ *   workspace, workspace_bytes  device scratch of at least
+ *             moe_sort_workspace_size() bytes (0 for few slots: NULL and 0 then)
+ * Errors as for the products (every pointer 16-byte aligned).
+ */
+mx_status moe_sort(const int32_t *experts, int64_t T, int64_t top, int64_t E, int64_t align,
+                   int64_t rows, int32_t *counts, int32_t *pos, int32_t *slots, void *workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
+/* The most rows that T * top slots of E experts can take, T * top +
+ * min(E, T * top) * (align - 1), and moe_sort's workspace in bytes (each 0 for
+ * invalid arguments). */
+int64_t moe_sort_rows(int64_t T, int64_t top, int64_t E, int64_t align);
+size_t moe_sort_workspace_size(int64_t T, int64_t top, int64_t E);
+
+/*
+ * The tokens' rows in that order: row r of out is row slots[r] / top of x, or
+ * zeros where slots[r] is outside 0 .. T * top - 1.  Rows are bytes of any type
+ * (bf16, or the codes and compact scales of a row-wise cast).
+ *   x         device, [T] rows of row_bytes;  out  [rows] of them
+ *   slots     device, int32 [rows], as moe_sort gives it; any values
+ *   T, top    as for moe_sort; 1 <= rows <= 2^24; 1 <= row_bytes <= 2^24,
+ *             row_bytes * max(rows, T) <= 2^41
+ * Its gradient is moe_combine without weights.
+ */
+mx_status moe_gather(const void *x, int64_t T, int64_t top, const int32_t *slots, int64_t rows,
+                     int64_t row_bytes, void *out, hipStream_t stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t][k] = bf16(sum_j weights[t][j] y[pos[t][j]][k]), summed in fp32 in the
+ * order of j; a slot whose pos is outside 0 .. rows - 1 adds nothing.
+ *   y         device, bf16 [rows][K]
+ *   pos       int32 [T][top], as moe_sort gives it (any values), or NULL: slot i
+ *             is row i, the layout of nvfp4_matvec_experts' output; rows = T * top
+ *             then
+ *   weights   fp32 [T][top] or NULL (ones)
+ *   T, top, rows  as for moe_gather; K and the products T * K, rows * K as for
+ *             mx_quantize
+ *   out       bf16 [T][K]
+ */
+mx_status moe_combine(const void *y, int64_t rows, int64_t K, const int32_t *pos,
+                      const float *weights, int64_t T, int64_t top, void *out, hipStream_t stream);
+
+/*
+ * Its gradients:
+ *   dy[r][k]       = bf16(weights[s] dout[t][k]) for the row r of slot s = (t, j)
+ *   dweights[t][j] = sum_k dout[t][k] y[r][k], in fp32; 0 for a slot without a row
+ *   pos, slots  device, both as moe_sort gives them, or both NULL (slot i is row
+ *             i, rows = T * top).  A row whose slot is -1 gets zeros.  Row r is
+ *             its slot's where pos[slots[r]] is r again; a row for which that is
+ *             not so is left as it was (moe_sort gives none)
+ *   weights   fp32 [T][top] or NULL (ones)
+ *   dy        bf16 [rows][K]
+ *   dweights  fp32 [T][top], or NULL: not computed
+ */
+mx_status moe_combine_backward(const void *dout, const void *y, int64_t rows, int64_t K,
+                               const int32_t *pos, const int32_t *slots, const float *weights,
+                               int64_t T, int64_t top, void *dy, float *dweights,
+                               hipStream_t stream);
 
 /* Static string naming a status code. */
 const char *mx_status_str(int status);
