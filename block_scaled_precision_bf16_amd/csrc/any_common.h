@@ -21,12 +21,6 @@
 
 namespace mxk {
 
-template <int AUX = 0>
-__device__ __forceinline__ uint32_t buf_load2(rsrc_t r, uint32_t off)
-{
-    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, AUX);
-}
-
 __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) { return lo | (hi << 16); }
 
 // Low bits of the absolute byte address p + off.

@@ -66,6 +66,12 @@ __device__ __forceinline__ uint32_t buf_load4(rsrc_t r, uint32_t off)
 }
 
 template <int AUX = 0>
+__device__ __forceinline__ uint32_t buf_load2(rsrc_t r, uint32_t off)
+{
+    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, AUX);
+}
+
+template <int AUX = 0>
 __device__ __forceinline__ uint32_t buf_load1(rsrc_t r, uint32_t off)
 {
     return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, AUX);

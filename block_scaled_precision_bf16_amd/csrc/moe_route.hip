@@ -7,10 +7,12 @@
 //   dp_j = (scale / s) (dw_j - sum_i dw_i p_i / s) for the chosen ones, plus the
 //   scores' own gradient
 //
-// One wave per token; lane l holds the experts l NPL .. l NPL + NPL - 1, so that
-// the lowest lane among equal keys, and there the first, is the lowest index.  The
-// bytes (4 an expert) take less time than the instructions: the exponentials and
-// `top` maxima over the wave bound it.
+// Up to 256 experts: four tokens a wave, 16 lanes each; lane l of them holds the
+// experts l NPL .. l NPL + NPL - 1, so that the lowest lane among equal keys, and
+// there the first, is the lowest index.  More experts, and groups that are not a
+// power of two of such lanes, take a wave per token.  The bytes (4 an expert) take
+// less time than the instructions: the exponentials and `top` maxima bound it.
+#include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"
 #include "wave.h"
@@ -19,39 +21,68 @@ namespace mxk {
 
 constexpr int kRouteWaves = 4;
 
-__device__ __forceinline__ float minus_inf(float) { return -__builtin_inff(); }
-__device__ __forceinline__ double minus_inf(double) { return -__builtin_inf(); }
-
+// NPL floats from element `at` on (0 past the descriptor's end; multiples of 4:
+// groups of 4, wholly inside or outside).
 template <int NPL>
-__device__ __forceinline__ void load_logits(const void *p, int64_t t, int E, int lane, int f32,
-                                            float (&x)[NPL])
+__device__ __forceinline__ void load_floats(rsrc_t r, uint32_t at, bool fours, float (&x)[NPL])
 {
+    if (NPL % 4 == 0 && fours) {
 #pragma unroll
-    for (int i = 0; i < NPL; i++) {
-        const int e = lane * NPL + i;
-        x[i] = -__builtin_inff();
-        if (e < E)
-            x[i] = f32 ? static_cast<const float *>(p)[t * E + e]
-                       : bf16_lo(static_cast<const uint16_t *>(p)[t * E + e]);
+        for (int i = 0; i + 3 < NPL; i += 4) {
+            const uint4 v = buf_load16(r, 4 * (at + i));
+            x[i] = f32_bits(v.x), x[i + 1] = f32_bits(v.y), x[i + 2] = f32_bits(v.z), x[i + 3] = f32_bits(v.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            x[i] = f32_bits(buf_load4(r, 4 * (at + i)));
     }
+}
+
+// Logits of `rows` tokens from t on: this lane's NPL from expert e0 of token
+// t + row on, -Inf past the last expert and the last token.
+template <int NPL>
+__device__ __forceinline__ void load_logits(const void *p, int64_t t, int64_t rows, int row, int e0, int E,
+                                            int f32, float (&x)[NPL])
+{
+    const int size = f32 ? 4 : 2;
+    const rsrc_t r = make_rsrc(static_cast<const char *>(p) + t * E * size, 0, rows * E * size);
+    const uint32_t at = (uint32_t)(row * E + e0);
+    if (f32) {
+        load_floats<NPL>(r, at, E % 4 == 0, x);
+    } else if (NPL % 4 == 0 && E % 4 == 0) {   // rows of whole 8 bytes
+#pragma unroll
+        for (int i = 0; i + 3 < NPL; i += 4) {
+            const uint2 v = buf_load8(r, 2 * (at + i));
+            x[i] = bf16_lo(v.x), x[i + 1] = bf16_hi(v.x), x[i + 2] = bf16_lo(v.y), x[i + 3] = bf16_hi(v.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            x[i] = bf16_lo(buf_load2(r, 2 * (at + i)));
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; i++)
+        x[i] = row < rows && e0 + i < E ? x[i] : -__builtin_inff();
 }
 
 __device__ __forceinline__ float exp_nonpos(float a) { return exp32_nonpos(a); }
 __device__ __forceinline__ double exp_nonpos(double a) { return exp(a); }
+__device__ __forceinline__ float rcp12(float d) { return rcp_1_2(d); }   // d in [1, 2]
+__device__ __forceinline__ double rcp12(double d) { return 1.0 / d; }
 
-// Scores of a token in type F: softmax (those of -Inf logits 0, all of them where
+// Scores of a token in type F (ROW: one for each row of 16 lanes): softmax (those of -Inf logits 0, all of them where
 // every logit is) or sigmoid (q: 1 - p); NaN where they have no value.
-template <class F, int NPL>
+template <class F, int NPL, bool ROW>
 __device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, F (&p)[NPL], F (&q)[NPL])
 {
     if (sigmoid) {
 #pragma unroll
         for (int i = 0; i < NPL; i++) {
-            const F z = (F)x[i], e = exp_nonpos(z < F(0) ? z : -z), r = F(1) / (F(1) + e);
-            p[i] = z >= F(0) ? r : e * r;
-            q[i] = z >= F(0) ? e * r : r;
-            if (x[i] != x[i])
-                p[i] = q[i] = (F)x[i];
+            const F z = (F)x[i], e = exp_nonpos(z < F(0) ? z : -z), r = rcp12(F(1) + e), s = e * r;
+            const bool up = z >= F(0), nan = x[i] != x[i];
+            p[i] = nan ? z : up ? r : s;
+            q[i] = nan ? z : up ? s : r;
         }
         return;
     }
@@ -59,228 +90,704 @@ __device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, F
 #pragma unroll
     for (int i = 1; i < NPL; i++)
         m = __builtin_fmaxf(m, x[i]);
-    m = wave_max(m);
+    m = ROW ? row_max(m) : wave_max(m);
+    m = m == -__builtin_inff() ? 0.0f : m;   // then every exponential is 0 (or NaN)
     F sum = F(0);
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
-        p[i] = m == -__builtin_inff() && x[i] == x[i] ? F(0) : exp_nonpos((F)x[i] - (F)m);
+        p[i] = exp_nonpos((F)x[i] - (F)m);
         sum += p[i];
     }
-    sum = wave_sum(sum);
+    sum = ROW ? row_sum(sum) : wave_sum(sum);
     const F inv = sum > F(0) ? F(1) / sum : sum;
 #pragma unroll
     for (int i = 0; i < NPL; i++)
         p[i] *= inv;
 }
 
-// Key: float where the logits themselves give the order, double where scores are
-// added to a bias or to each other.
-template <int NPL, class Key>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a)
+// fp32 keys as unsigned numbers of the same order, -0 as 0; 0 stands for none (a
+// masked expert).
+__device__ __forceinline__ uint32_t order_of(float k)
 {
-    __shared__ Key keys[kRouteWaves][64 * NPL];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= a.T)
-        return;
-    const Key low = minus_inf(Key(0));
-    float x[NPL], pf[NPL];
-    Key key[NPL];
-    load_logits<NPL>(a.logits, t, a.E, lane, a.f32, x);
-    bool nan = false;
-    {
-        Key p[NPL], q[NPL];
-        scores_of<Key, NPL>(x, a.sigmoid != 0, p, q);
+    const uint32_t u = bits_f32(k + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_of(uint32_t o)
+{
+    return o == 0u ? -__builtin_inff() : f32_bits(o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
+}
+
+// How far two fp32 keys have to be apart for their order to be that of the exact
+// ones.  p <= 1 is off by less than 2^-19 (a softmax's exponent by 2^-24 |x - m|,
+// which e^-|x - m| makes less than 2^-25, the exponential, sum and quotient by 30
+// roundings at most), the bias' addition by 2^-24 of the key, the sum of a group's
+// two by twice that and its own rounding; two such values by 2^-17 + 2^-21 |key|.
+__device__ __forceinline__ float key_margin(float k) { return 0x1p-17f + 0x1p-21f * __builtin_fabsf(k); }
+
+// What a token's choice leaves: lane j's expert (-1: none) of slot j; sure: that
+// keys off by their rounding give the same choice.
+struct Choice {
+    int expert;
+    bool sure;
+};
+
+// A group's best key and second best, of two parts' best and second.
+template <class K>
+__device__ __forceinline__ void merge_two(K &best, K &second, K b, K s)
+{
+    const K low = best < b ? best : b;
+    second = second > s ? second : s;
+    second = second > low ? second : low;
+    best = best > b ? best : b;
+}
+
+template <int CTRL>
+__device__ __forceinline__ void merge_step(uint32_t &best, uint32_t &second)
+{
+    merge_two(best, second, dpp<CTRL>(0u, best), dpp<CTRL>(0u, second));
+}
+
+// The best groups: key = 0 in the others.  False where groups are too close to be
+// told apart (CERT).  Where a group is a power of two of lanes, at most 16, these
+// find its score among themselves; otherwise lane g reads group g's keys from LDS,
+// one after the other.
+template <int NPL, bool CERT>
+__device__ __forceinline__ bool keep_groups(const RouteArgs &a, int lane, uint32_t *keys,
+                                            uint32_t (&key)[NPL])
+{
+    const int S = a.E / a.groups, L = S / NPL;
+    // e / S for e, S <= 1024, by a reciprocal that is less than 2^-20 too large
+    const uint32_t inv = (1u << 20) / (uint32_t)S + 1;
+    const bool lanes = S % NPL == 0 && (L & (L - 1)) == 0 && L <= 16;
+    uint32_t first = 0u, second = 0u;
+    int group = lane;                  // whose score this lane has
+    if (lanes) {
 #pragma unroll
-        for (int i = 0; i < NPL; i++) {
-            const int e = lane * NPL + i;
-            pf[i] = (float)p[i];
-            key[i] = (Key)x[i];
-            float b = 0.0f;
-            if constexpr (sizeof(Key) == 8) {
-                b = a.bias && e < a.E ? a.bias[e] : 0.0f;
-                key[i] = p[i] + (Key)b;
-            }
-            nan = nan || (e < a.E && (pf[i] != pf[i] || key[i] != key[i]));
-            if (x[i] == -__builtin_inff() || b == -__builtin_inff())
-                key[i] = low;
-            if (a.scores && e < a.E)
-                a.scores[t * a.E + e] = pf[i];
+        for (int i = 0; i < NPL; i++)
+            merge_two(first, second, key[i], 0u);
+        if (L >= 2)
+            merge_step<kDppXor1>(first, second);
+        if (L >= 4)
+            merge_step<kDppXor2>(first, second);
+        if (L >= 8)
+            merge_step<kDppHalfMirror>(first, second);
+        if (L >= 16)
+            merge_step<kDppMirror>(first, second);
+        group = (int)(((uint32_t)(lane * NPL) * inv) >> 20);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            keys[lane * NPL + i] = key[i];
+        __builtin_amdgcn_wave_barrier();
+        if (lane < a.groups)
+            for (int j = 0; j < S; j++)
+                merge_two(first, second, keys[lane * S + j], 0u);
+    }
+    float best = key_of(first);
+    if (a.pair && second != 0u)
+        best += key_of(second);
+    const float margin = key_margin(best);
+    int rank = 0, near = 0;
+    for (int g = 0; g < a.groups; g++) {
+        const float k = from_lane(best, lanes ? g * L : g);
+        if constexpr (CERT) {          // equal ones are near: their order does not matter
+            rank += k > best ? 1 : 0;
+            near += __builtin_fabsf(k - best) <= margin ? 1 : 0;
+        } else {
+            rank += k > best || (k == best && g < group) ? 1 : 0;
         }
     }
-    const bool bad = __builtin_amdgcn_ballot_w64(nan) != 0;
+    if (lanes) {
+        const bool kept = rank < a.top_groups;
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            key[i] = kept ? key[i] : 0u;
+    } else {
+        const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && rank < a.top_groups);
+#pragma unroll
+        for (int i = 0; i < NPL; i++) {
+            const uint32_t g = ((uint32_t)(lane * NPL + i) * inv) >> 20;
+            key[i] = (kept >> (g & 63)) & 1 ? key[i] : 0u;
+        }
+    }
+    return !CERT ||
+           __builtin_amdgcn_ballot_w64(group < a.groups && (near > 1 || best == __builtin_inff())) == 0;
+}
 
-    if (a.groups > 1 && !bad) {
+// A lane's keys, largest first and of equal ones the lowest index first; the
+// indices within the lane as bytes of `at`.
+struct Sorted4 {
+    uint32_t k0, k1, k2, k3, at;
+};
+
+__device__ __forceinline__ void in_order(uint32_t &a, uint32_t &b, uint32_t &i, uint32_t &j)
+{
+    const bool up = b > a;
+    const uint32_t k = up ? b : a, n = up ? j : i;
+    b = up ? a : b;
+    j = up ? i : j;
+    a = k;
+    i = n;
+}
+
+template <int NPL>
+__device__ __forceinline__ Sorted4 sort_lane(const uint32_t (&key)[NPL])
+{
+    Sorted4 s{key[0], 0u, 0u, 0u, 0u};
+    uint32_t i0 = 0, i1 = 1, i2 = 2, i3 = 3;
+    if constexpr (NPL >= 2) {
+        s.k1 = key[1];
+        in_order(s.k0, s.k1, i0, i1);
+    }
+    if constexpr (NPL == 4) {
+        s.k2 = key[2];
+        s.k3 = key[3];
+        in_order(s.k1, s.k2, i1, i2);
+        in_order(s.k2, s.k3, i2, i3);
+        in_order(s.k0, s.k1, i0, i1);
+        in_order(s.k1, s.k2, i1, i2);
+        in_order(s.k0, s.k1, i0, i1);
+    }
+    s.at = i0 | i1 << 8 | i2 << 16 | i3 << 24;
+    return s;
+}
+
+// The `top` best keys, a maximum over the wave for each.  With up to 4 keys a lane
+// they are sorted first, so that a round looks at one and the lane that had it
+// moves up; with more, a round looks at all of them.  CERT: `sure` tells whether
+// each key is far enough from the next one.
+template <int NPL, bool CERT>
+__device__ __forceinline__ Choice choose32(const RouteArgs &a, int lane, uint32_t *keys,
+                                           uint32_t (&key)[NPL])
+{
+    Choice c{-1, true};
+    if (a.groups > 1)
+        c.sure = keep_groups<NPL, CERT>(a, lane, keys, key);
+    Sorted4 s{};
+    if constexpr (NPL <= 4)
+        s = sort_lane<NPL>(key);
+    uint32_t got = 0u, extra = 0u;        // lane j: the key of slot j; the first one left over
+    for (int j = 0;; j++) {
+        uint32_t best, at;
+        if constexpr (NPL <= 4) {
+            best = s.k0;
+            at = s.at & 0xFFu;
+        } else {
+            best = key[0];
+            at = 0;
+#pragma unroll
+            for (int i = 1; i < NPL; i++) {
+                const bool more = key[i] > best;
+                best = more ? key[i] : best;
+                at = more ? (uint32_t)i : at;
+            }
+        }
+        const uint32_t m = wave_max(best);
+        if (j == a.top) {
+            extra = m;
+            break;
+        }
+        if (m == 0u)
+            break;
+        const int owner = __builtin_ctzll(__builtin_amdgcn_ballot_w64(best == m));
+        const int i = __builtin_amdgcn_readlane((int)at, owner);
+        const bool slot = lane == j, mine = lane == owner;
+        c.expert = slot ? owner * NPL + i : c.expert;
+        if constexpr (CERT)
+            got = slot ? m : got;
+        else if (j + 1 == a.top)
+            break;
+        if constexpr (NPL <= 4) {
+            s.k0 = mine ? s.k1 : s.k0;
+            s.k1 = mine ? s.k2 : s.k1;
+            s.k2 = mine ? s.k3 : s.k2;
+            s.k3 = mine ? 0u : s.k3;
+            s.at = mine ? s.at >> 8 : s.at;
+        } else {
+#pragma unroll
+            for (int n = 0; n < NPL; n++)
+                key[n] = mine && n == i ? 0u : key[n];
+        }
+    }
+    if constexpr (CERT) {
+        const uint32_t below = (uint32_t)__shfl_down((int)got, 1, 64);
+        const float k = key_of(got), n = key_of(lane == a.top - 1 ? extra : below);
+        const bool close = lane < a.top && got != 0u && !(k - n > key_margin(k));
+        c.sure = c.sure && __builtin_amdgcn_ballot_w64(close) == 0;
+    }
+    return c;
+}
+
+// The same in 64 bits, for the few tokens whose fp32 keys do not tell, by a whole
+// wave: lane j's expert is slot j's.
+template <int NPL>
+__device__ __forceinline__ int choose64(const RouteArgs &a, int lane, double *keys, const float (&x)[NPL],
+                                        const float (&bias)[NPL])
+{
+    const double low = -__builtin_inf();
+    double key[NPL], q[NPL];
+    scores_of<double, NPL, false>(x, a.sigmoid != 0, key, q);
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
+        key[i] = masked ? low : key[i] + (double)bias[i];
+    }
+    if (a.groups > 1) {
         const int S = a.E / a.groups;
 #pragma unroll
         for (int i = 0; i < NPL; i++)
-            keys[wave][lane * NPL + i] = key[i];
+            keys[lane * NPL + i] = key[i];
         __builtin_amdgcn_wave_barrier();
-        // lane g: group g's score
-        Key best = low, second = low;
+        double best = low, second = low;
         if (lane < a.groups)
-            for (int j = 0; j < S; j++) {
-                const Key k = keys[wave][lane * S + j];
-                second = k > best ? best : max_of(second, k);
-                best = max_of(best, k);
-            }
+            for (int j = 0; j < S; j++)
+                merge_two(best, second, keys[lane * S + j], low);
         if (a.pair && second > low)
             best += second;
         int rank = 0;
         for (int g = 0; g < a.groups; g++) {
-            const Key k = from_lane(best, g);
+            const double k = from_lane(best, g);
             rank += k > best || (k == best && g < lane) ? 1 : 0;
         }
         const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && rank < a.top_groups);
-        // e / S for e, S <= 1024, by a reciprocal that is less than 2^-20 too large
-        const uint32_t inv = (1u << 20) / (uint32_t)S + 1;
 #pragma unroll
-        for (int i = 0; i < NPL; i++) {
-            const uint32_t g = ((uint32_t)(lane * NPL + i) * inv) >> 20;
-            if (!((kept >> (g & 63)) & 1))
+        for (int i = 0; i < NPL; i++)
+            if (!((kept >> (((lane * NPL + i) / S) & 63)) & 1))
                 key[i] = low;
-        }
     }
-
-    int chosen = -1;
-    float w = 0.0f;
-    for (int j = 0; j < a.top && !bad; j++) {
-        Key best = key[0];
-        float bp = pf[0];
-        int bi = 0;
+    int expert = -1;
+    for (int j = 0; j < a.top; j++) {
+        double best = key[0];
+        int at = 0;
 #pragma unroll
         for (int i = 1; i < NPL; i++) {
             const bool more = key[i] > best;
             best = more ? key[i] : best;
-            bp = more ? pf[i] : bp;
-            bi = more ? i : bi;
+            at = more ? i : at;
         }
-        const Key m = wave_max(best);
+        const double m = wave_max(best);
         if (m == low)
             break;
         const int owner = __builtin_ctzll(__builtin_amdgcn_ballot_w64(best == m));
-        const int e = __builtin_amdgcn_readlane(lane * NPL + bi, owner);
-        const float p = from_lane(bp, owner);
+        const int i = __builtin_amdgcn_readlane(at, owner);
+        expert = lane == j ? owner * NPL + i : expert;
+#pragma unroll
+        for (int n = 0; n < NPL; n++)
+            key[n] = lane == owner && n == i ? low : key[n];
+    }
+    return expert;
+}
+
+// VALUE: keys are scores plus a bias, or a group's two are added; otherwise the
+// logits give the order.  Such scores are compared in fp32 first, and only where
+// two of those that decide are within their rounding of each other (about one
+// token in a hundred) once more in 64 bits.
+template <int NPL, bool VALUE>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a)
+{
+    __shared__ double lds[kRouteWaves][64 * NPL];
+    __shared__ float ps[kRouteWaves][64 * NPL];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+    if (t >= a.T)
+        return;
+    float x[NPL], p[NPL], q[NPL], bias[NPL];
+    load_logits<NPL>(a.logits, t, 1, 0, lane * NPL, a.E, a.f32, x);
+    if (VALUE && a.bias)
+        load_floats<NPL>(make_rsrc(a.bias, 0, 4 * a.E), lane * NPL, a.E % 4 == 0, bias);
+    else
+        for (int i = 0; i < NPL; i++)
+            bias[i] = 0.0f;
+    scores_of<float, NPL, false>(x, a.sigmoid != 0, p, q);
+    uint32_t key[NPL];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        const float k = VALUE ? p[i] + bias[i] : x[i];
+        const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
+        key[i] = masked ? 0u : order_of(k);
+        nan |= (p[i] != p[i]) | (k != k);
+        ps[wave][lane * NPL + i] = p[i];
+    }
+    if (a.scores) {
 #pragma unroll
         for (int i = 0; i < NPL; i++)
-            key[i] = lane == owner && i == bi ? low : key[i];
-        chosen = lane == j ? e : chosen;
-        w = lane == j ? p : w;
+            if (lane * NPL + i < a.E)
+                a.scores[t * a.E + lane * NPL + i] = p[i];
     }
+    const bool bad = __builtin_amdgcn_ballot_w64(nan) != 0;
+    int expert = -1;
+    if (!bad) {
+        const Choice c = choose32<NPL, VALUE>(a, lane, reinterpret_cast<uint32_t *>(lds[wave]), key);
+        expert = c.expert;
+        if (VALUE && !c.sure)
+            expert = choose64<NPL>(a, lane, lds[wave], x, bias);
+    }
+    __builtin_amdgcn_wave_barrier();
+    float w = expert >= 0 ? ps[wave][expert] : 0.0f;
     if (a.renorm) {
         const float s = wave_sum(w);
         w = s > 0.0f ? w / s : 0.0f;
     }
     w *= a.scale;
     if (lane < a.top) {
-        a.experts[t * a.top + lane] = chosen;
+        a.experts[t * a.top + lane] = expert;
         a.weights[t * a.top + lane] = bad ? __builtin_nanf("") : w;
     }
 }
 
-template <int NPL>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackArgs a)
+// ---- four tokens a wave -----------------------------------------------------
+
+// Whether 16 lanes of NPL experts find the groups' scores among themselves.
+__host__ __device__ inline bool groups_of_lanes(int E, int groups, int npl)
 {
-    __shared__ float ps[kRouteWaves][64 * NPL];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= a.T)
-        return;
-    float x[NPL], p[NPL], q[NPL], dp[NPL];
-    load_logits<NPL>(a.logits, t, a.E, lane, a.f32, x);
-    scores_of<float, NPL>(x, a.sigmoid != 0, p, q);
+    const int S = E / groups, L = S / npl;
+    return groups == 1 || (S % npl == 0 && (L & (L - 1)) == 0 && L <= 16);
+}
+
+// As keep_groups, for the rows of 16 lanes; the return value is the row's.
+template <int NPL, bool CERT>
+__device__ __forceinline__ bool keep_groups16(const RouteArgs &a, int lane, uint32_t (&key)[NPL])
+{
+    const int L = a.E / a.groups / NPL, group = (lane & 15) / L;   // L a power of two
+    uint32_t first = 0u, second = 0u;
 #pragma unroll
-    for (int i = 0; i < NPL; i++) {
-        const int e = lane * NPL + i;
-        ps[wave][e] = p[i];
-        dp[i] = a.dscores && e < a.E ? a.dscores[t * a.E + e] : 0.0f;
-    }
-    __builtin_amdgcn_wave_barrier();
-    // lane j: the gradient of chosen slot j's p
-    int e = -1;
-    float d = 0.0f, pj = 0.0f;
-    if (lane < a.top) {
-        e = a.experts[t * a.top + lane];
-        if (e >= 0 && e < a.E) {
-            pj = ps[wave][e];
-            d = a.scale * a.dweights[t * a.top + lane];
+    for (int i = 0; i < NPL; i++)
+        merge_two(first, second, key[i], 0u);
+    if (L >= 2)
+        merge_step<kDppXor1>(first, second);
+    if (L >= 4)
+        merge_step<kDppXor2>(first, second);
+    if (L >= 8)
+        merge_step<kDppHalfMirror>(first, second);
+    if (L >= 16)
+        merge_step<kDppMirror>(first, second);
+    float best = key_of(first);
+    if (a.pair && second != 0u)
+        best += key_of(second);
+    const float margin = key_margin(best);
+    int rank = 0, near = 0;
+    for (int g = 0; g < a.groups; g++) {
+        const float k = __shfl(best, (lane & 48) + g * L, 64);
+        if constexpr (CERT) {
+            rank += k > best ? 1 : 0;
+            near += __builtin_fabsf(k - best) <= margin ? 1 : 0;
+        } else {
+            rank += k > best || (k == best && g < group) ? 1 : 0;
         }
     }
+    const bool kept = rank < a.top_groups;
+#pragma unroll
+    for (int i = 0; i < NPL; i++)
+        key[i] = kept ? key[i] : 0u;
+    if constexpr (!CERT)
+        return true;
+    const uint64_t m = __builtin_amdgcn_ballot_w64(group < a.groups && (near > 1 || best == __builtin_inff()));
+    return ((m >> (lane & 48)) & 0xFFFF) == 0;
+}
+
+template <int NPL, bool VALUE>
+__global__ __launch_bounds__(64 * kRouteWaves) void route16_kernel(RouteArgs a)
+{
+    constexpr int LISTS = (NPL + 3) / 4, PER = NPL < 4 ? NPL : 4, WIDE = (NPL + 3) / 4;
+    __shared__ float ps[kRouteWaves][4][16 * NPL];
+    __shared__ uint2 found[kRouteWaves][4][65];   // expert and key of each slot, and the next key
+    __shared__ double lds[VALUE ? kRouteWaves : 1][VALUE ? 64 * WIDE : 1];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = lane >> 4, l = lane & 15;
+    const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4;
+    if (t0 >= a.T)
+        return;
+    const int64_t rows = a.T - t0 < 4 ? a.T - t0 : 4;
+    float x[NPL], p[NPL], q[NPL], bias[NPL];
+    load_logits<NPL>(a.logits, t0, rows, row, l * NPL, a.E, a.f32, x);
+    if (VALUE && a.bias)
+        load_floats<NPL>(make_rsrc(a.bias, 0, 4 * a.E), l * NPL, a.E % 4 == 0, bias);
+    else
+        for (int i = 0; i < NPL; i++)
+            bias[i] = 0.0f;
+    scores_of<float, NPL, true>(x, a.sigmoid != 0, p, q);
+    uint32_t key[NPL];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        const float k = VALUE ? p[i] + bias[i] : x[i];
+        const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
+        key[i] = masked ? 0u : order_of(k);
+        nan |= (p[i] != p[i]) | (k != k);
+        ps[wave][row][l * NPL + i] = p[i];
+    }
+    if (a.scores && row < rows) {
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            if (l * NPL + i < a.E)
+                a.scores[(t0 + row) * a.E + l * NPL + i] = p[i];
+    }
+    const bool bad = ((__builtin_amdgcn_ballot_w64(nan) >> (lane & 48)) & 0xFFFF) != 0;
+#pragma unroll
+    for (int i = 0; i < NPL; i++)
+        key[i] = bad ? 0u : key[i];
+    bool sure = true;
+    if (a.groups > 1)
+        sure = keep_groups16<NPL, VALUE>(a, lane, key);
+
+    // each lane's keys as sorted lists of up to 4; a round takes the largest head
+    // of the row's lists, the first among equal ones, and moves that list up
+    Sorted4 list[LISTS];
+#pragma unroll
+    for (int c = 0; c < LISTS; c++) {
+        uint32_t part[PER];
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            part[i] = key[c * 4 + i];
+        list[c] = sort_lane<PER>(part);
+    }
+    const int rounds = a.top + (VALUE ? 1 : 0);
+    int n = 0;
+    for (int j = 0; j < rounds; j++) {
+        uint32_t best = list[0].k0, at = list[0].at;
+        int which = 0;
+#pragma unroll
+        for (int c = 1; c < LISTS; c++) {
+            const bool more = list[c].k0 > best;
+            best = more ? list[c].k0 : best;
+            at = more ? list[c].at : at;
+            which = more ? c : which;
+        }
+        const uint32_t m = row_max(best);
+        if (__builtin_amdgcn_ballot_w64(m != 0u) == 0)
+            break;
+        const uint32_t who = (uint32_t)(__builtin_amdgcn_ballot_w64(best == m) >> (lane & 48));
+        const bool mine = m != 0u && (int)__builtin_ctz(who | 0x10000u) == l;
+        if (mine)
+            found[wave][row][j] = make_uint2((uint32_t)(l * NPL + which * 4) + (at & 0xFFu), m);
+        n += m != 0u ? 1 : 0;
+#pragma unroll
+        for (int c = 0; c < LISTS; c++) {
+            const bool up = mine && which == c;
+            list[c].k0 = up ? list[c].k1 : list[c].k0;
+            list[c].k1 = up ? list[c].k2 : list[c].k1;
+            list[c].k2 = up ? list[c].k3 : list[c].k2;
+            list[c].k3 = up ? 0u : list[c].k3;
+            list[c].at = up ? list[c].at >> 8 : list[c].at;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (VALUE) {
+        bool close = false;
+        for (int s = l; s < a.top && s < n; s += 16) {
+            const float k = key_of(found[wave][row][s].y);
+            const float next = s + 1 < n ? key_of(found[wave][row][s + 1].y) : -__builtin_inff();
+            close |= !(k - next > key_margin(k));
+        }
+        uint64_t again = __builtin_amdgcn_ballot_w64(!bad && (close || !sure) && row < rows);
+        while (again) {
+            // the wave takes this row's token alone, in 64 bits
+            const int r = __builtin_ctzll(again) >> 4;
+            again &= ~(0xFFFFull << (16 * r));
+            float xw[WIDE], bw[WIDE];
+            load_logits<WIDE>(a.logits, t0 + r, 1, 0, lane * WIDE, a.E, a.f32, xw);
+            if (a.bias)
+                load_floats<WIDE>(make_rsrc(a.bias, 0, 4 * a.E), lane * WIDE, a.E % 4 == 0, bw);
+            else
+                for (int i = 0; i < WIDE; i++)
+                    bw[i] = 0.0f;
+            const int e = choose64<WIDE>(a, lane, lds[wave], xw, bw);
+            __builtin_amdgcn_wave_barrier();
+            if (lane < a.top)
+                found[wave][r][lane].x = (uint32_t)e;
+            const int count = __builtin_popcountll(__builtin_amdgcn_ballot_w64(e >= 0));
+            n = row == r ? count : n;
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+    float sum = 0.0f;
+    if (a.renorm) {
+        for (int s = l; s < a.top && s < n; s += 16)
+            sum += ps[wave][row][found[wave][row][s].x];
+        sum = row_sum(sum);
+    }
+    if (row >= rows)
+        return;
+    for (int s = l; s < a.top; s += 16) {
+        const int64_t o = (t0 + row) * a.top + s;
+        const int e = s < n ? (int)found[wave][row][s].x : -1;
+        float w = e >= 0 ? ps[wave][row][e] : 0.0f;
+        if (a.renorm)
+            w = sum > 0.0f ? w / sum : 0.0f;
+        a.experts[o] = e;
+        a.weights[o] = bad ? __builtin_nanf("") : w * a.scale;
+    }
+}
+
+// ---- the logits' gradient -------------------------------------------------------
+
+// ROW: four tokens a wave, 16 lanes each; otherwise one.
+template <int NPL, bool ROW>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackArgs a)
+{
+    constexpr int TOKENS = ROW ? 4 : 1, LANES = 64 / TOKENS;
+    __shared__ float ps[kRouteWaves][TOKENS][LANES * NPL];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = ROW ? lane >> 4 : 0, l = lane & (LANES - 1);
+    const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TOKENS;
+    if (t0 >= a.T)
+        return;
+    const int64_t rows = a.T - t0 < TOKENS ? a.T - t0 : TOKENS, t = t0 + row;
+    const auto sum_of = [](float v) { return ROW ? row_sum(v) : wave_sum(v); };
+    float x[NPL], p[NPL], q[NPL], dp[NPL];
+    load_logits<NPL>(a.logits, t0, rows, row, l * NPL, a.E, a.f32, x);
+    if (a.dscores)
+        load_floats<NPL>(make_rsrc(a.dscores + t0 * a.E, 0, 4 * rows * a.E), row * a.E + l * NPL,
+                         a.E % 4 == 0, dp);
+    scores_of<float, NPL, ROW>(x, a.sigmoid != 0, p, q);
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        ps[wave][row][l * NPL + i] = p[i];
+        dp[i] = a.dscores && l * NPL + i < a.E ? dp[i] : 0.0f;
+    }
+    __builtin_amdgcn_wave_barrier();
     // sum over the experts of p times their dp.  With normalised weights the
     // chosen ones' part is 0 (the weights do not change when all p grow alike), so
     // that experts that were not chosen get no gradient from rounding
     float all = 0.0f;
-    if (!a.sigmoid) {
+    if (!a.sigmoid && a.dscores) {
 #pragma unroll
         for (int i = 0; i < NPL; i++)
             all += p[i] * dp[i];
-        all = wave_sum(all);
+        all = sum_of(all);
     }
-    if (a.renorm) {
-        const float s = wave_sum(pj);
-        const float c = wave_sum(d * pj);
-        d = s > 0.0f ? (d - c / s) / s : 0.0f;
-    } else if (!a.sigmoid) {
-        all += wave_sum(d * pj);
+    // slots s0 + l: the chosen p's sum, and that of p times its gradient
+    float sp = 0.0f, sd = 0.0f;
+    for (int s = l; s < a.top; s += LANES) {
+        const int e = row < rows ? a.experts[t * a.top + s] : -1;
+        const bool is = e >= 0 && e < a.E;
+        const float pj = is ? ps[wave][row][e] : 0.0f;
+        sp += pj;
+        sd += is ? a.scale * a.dweights[t * a.top + s] * pj : 0.0f;
     }
-    for (int j = 0; j < a.top; j++) {
-        const int ej = __builtin_amdgcn_readlane(e, j);
-        const float dj = from_lane(d, j);
+    sp = sum_of(sp);
+    sd = sum_of(sd);
+    if (!a.renorm && !a.sigmoid)
+        all += sd;
+    for (int s0 = 0; s0 < a.top; s0 += LANES) {
+        const int s = s0 + l;
+        const int e = row < rows && s < a.top ? a.experts[t * a.top + s] : -1;
+        float d = e >= 0 && e < a.E ? a.scale * a.dweights[t * a.top + s] : 0.0f;
+        if (a.renorm)
+            d = sp > 0.0f ? (d - sd / sp) / sp : 0.0f;
+        const int n = a.top - s0 < LANES ? a.top - s0 : LANES;
+        for (int j = 0; j < n; j++) {
+            const int ej = __shfl(e, (lane & ~(LANES - 1)) + j, 64);
+            const float dj = __shfl(d, (lane & ~(LANES - 1)) + j, 64);
 #pragma unroll
-        for (int i = 0; i < NPL; i++)
-            dp[i] += lane * NPL + i == ej ? dj : 0.0f;
+            for (int i = 0; i < NPL; i++)
+                dp[i] += l * NPL + i == ej ? dj : 0.0f;
+        }
+    }
+    if (row >= rows)
+        return;
+    float o[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; i++)
+        o[i] = a.sigmoid ? dp[i] * (p[i] * q[i]) : p[i] * (dp[i] - all);
+    if (NPL % 4 == 0 && a.E % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i + 3 < NPL; i += 4) {
+            const int64_t at = t * a.E + l * NPL + i;
+            if (l * NPL + i >= a.E)
+                continue;
+            if (a.f32)
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.dlogits) + at) =
+                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dlogits) + at) =
+                    make_uint2(bf16x2_rne(o[i], o[i + 1]), bf16x2_rne(o[i + 2], o[i + 3]));
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
-        const int k = lane * NPL + i;
-        if (k >= a.E)
+        const int e = l * NPL + i;
+        if (e >= a.E)
             continue;
-        const float o = a.sigmoid ? dp[i] * (p[i] * q[i]) : p[i] * (dp[i] - all);
         if (a.f32)
-            static_cast<float *>(a.dlogits)[t * a.E + k] = o;
+            static_cast<float *>(a.dlogits)[t * a.E + e] = o[i];
         else
-            static_cast<uint16_t *>(a.dlogits)[t * a.E + k] = (uint16_t)(bf16x2_rne(o, 0.0f) & 0xFFFFu);
+            static_cast<uint16_t *>(a.dlogits)[t * a.E + e] = (uint16_t)(bf16x2_rne(o[i], 0.0f) & 0xFFFFu);
     }
 }
 
 template <int NPL>
-static void launch_npl(const RouteArgs &a, hipStream_t s)
+static void launch_npl(const RouteArgs &a, bool value, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-    if (a.bias || (a.pair && a.groups > 1))
-        hipLaunchKernelGGL((route_kernel<NPL, double>), grid, block, 0, s, a);
+    if (value)
+        hipLaunchKernelGGL((route_kernel<NPL, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((route_kernel<NPL, float>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((route_kernel<NPL, false>), grid, block, 0, s, a);
+}
+
+template <int NPL>
+static void launch_npl16(const RouteArgs &a, bool value, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.T + 4 * kRouteWaves - 1) / (4 * kRouteWaves))), block(64 * kRouteWaves);
+    if (value)
+        hipLaunchKernelGGL((route16_kernel<NPL, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((route16_kernel<NPL, false>), grid, block, 0, s, a);
 }
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 {
-    if (a.E <= 64)
-        launch_npl<1>(a, s);
-    else if (a.E <= 128)
-        launch_npl<2>(a, s);
-    else if (a.E <= 256)
-        launch_npl<4>(a, s);
-    else if (a.E <= 512)
-        launch_npl<8>(a, s);
-    else
-        launch_npl<16>(a, s);
+    const bool value = a.bias || (a.pair && a.groups > 1);
+    const int npl = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 128 ? 8 : 16;
+    if (a.E <= 256 && groups_of_lanes(a.E, a.groups, npl)) {
+        switch (npl) {
+        case 1: launch_npl16<1>(a, value, s); break;
+        case 2: launch_npl16<2>(a, value, s); break;
+        case 4: launch_npl16<4>(a, value, s); break;
+        case 8: launch_npl16<8>(a, value, s); break;
+        default: launch_npl16<16>(a, value, s);
+        }
+    } else if (a.E <= 64) {
+        launch_npl<1>(a, value, s);
+    } else if (a.E <= 128) {
+        launch_npl<2>(a, value, s);
+    } else if (a.E <= 256) {
+        launch_npl<4>(a, value, s);
+    } else if (a.E <= 512) {
+        launch_npl<8>(a, value, s);
+    } else {
+        launch_npl<16>(a, value, s);
+    }
     return hipGetLastError();
+}
+
+template <int NPL, bool ROW>
+static void launch_back(const RouteBackArgs &a, hipStream_t s)
+{
+    const int64_t per = kRouteWaves * (ROW ? 4 : 1);
+    hipLaunchKernelGGL((route_back_kernel<NPL, ROW>), dim3((unsigned)((a.T + per - 1) / per)),
+                       dim3(64 * kRouteWaves), 0, s, a);
 }
 
 hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-    if (a.E <= 64)
-        hipLaunchKernelGGL(route_back_kernel<1>, grid, block, 0, s, a);
+    if (a.E <= 16)
+        launch_back<1, true>(a, s);
+    else if (a.E <= 32)
+        launch_back<2, true>(a, s);
+    else if (a.E <= 64)
+        launch_back<4, true>(a, s);
     else if (a.E <= 128)
-        hipLaunchKernelGGL(route_back_kernel<2>, grid, block, 0, s, a);
+        launch_back<8, true>(a, s);
     else if (a.E <= 256)
-        hipLaunchKernelGGL(route_back_kernel<4>, grid, block, 0, s, a);
+        launch_back<16, true>(a, s);
     else if (a.E <= 512)
-        hipLaunchKernelGGL(route_back_kernel<8>, grid, block, 0, s, a);
+        launch_back<8, false>(a, s);
     else
-        hipLaunchKernelGGL(route_back_kernel<16>, grid, block, 0, s, a);
+        launch_back<16, false>(a, s);
     return hipGetLastError();
 }
 

@@ -87,10 +87,11 @@ __device__ __forceinline__ int before_sum(int v, int32_t *red, int waves, int &t
 __device__ __forceinline__ void fill_rows(const SortArgs &a, const int32_t *start, const int32_t *counts,
                                           int64_t total, int block, int blocks)
 {
-    if (a.align > 1)
-        for (int e = block; e < a.E; e += blocks) {
+    if (a.align > 1)   // 16 threads for each expert
+        for (int e = block * (int)(blockDim.x / 16) + (int)(threadIdx.x >> 4); e < a.E;
+             e += blocks * (int)(blockDim.x / 16)) {
             const int64_t from = (int64_t)start[e] + counts[e], to = e + 1 < a.E ? start[e + 1] : total;
-            for (int64_t r = from + threadIdx.x; r < to; r += blockDim.x)
+            for (int64_t r = from + (threadIdx.x & 15); r < to; r += 16)
                 a.slots[r] = -1;
         }
     for (int64_t r = total + (int64_t)block * blockDim.x + threadIdx.x; r < a.rows;

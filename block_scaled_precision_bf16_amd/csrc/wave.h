@@ -74,4 +74,44 @@ __device__ __forceinline__ T wave_max(T v)
     return from_lane(v, 63);
 }
 
+// The same over each row of 16 lanes, in every lane of it.
+template <class T>
+__device__ __forceinline__ T row_sum(T v)
+{
+    v += dpp<kDppXor1>(T(0), v);
+    v += dpp<kDppXor2>(T(0), v);
+    v += dpp<kDppHalfMirror>(T(0), v);
+    v += dpp<kDppMirror>(T(0), v);
+    return v;
+}
+template <class T>
+__device__ __forceinline__ T row_max(T v)
+{
+    v = max_of(v, dpp<kDppXor1>(v, v));
+    v = max_of(v, dpp<kDppXor2>(v, v));
+    v = max_of(v, dpp<kDppHalfMirror>(v, v));
+    v = max_of(v, dpp<kDppMirror>(v, v));
+    return v;
+}
+
+// Of unsigned numbers (0 is neutral, which lets each step be one instruction).
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max_u32(v, dpp<kDppXor1>(0u, v));
+    v = max_u32(v, dpp<kDppXor2>(0u, v));
+    v = max_u32(v, dpp<kDppHalfMirror>(0u, v));
+    return max_u32(v, dpp<kDppMirror>(0u, v));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max_u32(v, dpp<kDppXor1>(0u, v));
+    v = max_u32(v, dpp<kDppXor2>(0u, v));
+    v = max_u32(v, dpp<kDppHalfMirror>(0u, v));
+    v = max_u32(v, dpp<kDppMirror>(0u, v));
+    v = max_u32(v, dpp<kDppBcast15, 0xA>(0u, v));
+    v = max_u32(v, dpp<kDppBcast31, 0xC>(0u, v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 }  // namespace mxk
