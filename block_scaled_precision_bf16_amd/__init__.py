@@ -684,12 +684,16 @@ def _current_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 def _launch(where, dev, stream, fn, *args):
     """Calls fn on the tensors' device (made current for the call) and stream.
     (The current stream's handle alone: making a torch.cuda.Stream of it takes 2
     of the 10 microseconds of a call.)"""
     handle = _current_stream(dev.index) if stream is None else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -857,8 +861,15 @@ def nvfp4_matvec_experts(x, experts, qw, sw, sg, flags=0, out=None, stream=None)
 I32 = torch.int32
 
 
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+_F32, _U8, _I32 = (F32,), (U8,), (I32,)
+
+
 def _want(t, shape, dtypes, name, dev):
-    """An input: a contiguous tensor of this shape and one of these types, on dev."""
+    """The address of an input, a contiguous tensor of this shape and one of these
+    types on dev (None for None)."""
+    if t is None:
+        return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype not in dtypes:
@@ -869,25 +880,32 @@ def _want(t, shape, dtypes, name, dev):
     return t.data_ptr()
 
 
-_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+def _new(like, out, stream):
+    """A function of (name, shape, dtype) that gives outputs on the device of `like`:
+    out's tensor of that name, of as many elements, or a new one (of the pool of the
+    stream that works on it)."""
+    if out is None and stream is None:
+        empty = like.new_empty
+        return lambda name, shape, dtype: empty(shape, dtype=dtype)
+    dev = like.device
 
+    def take(name, shape, dtype):
+        t = None if out is None else out.get(name)
+        if t is None:
+            return _empty(shape, dtype, dev, stream)
+        n = 1
+        for d in shape:
+            n *= d
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"out[{name!r}] must be a tensor")
+        ok = t.dtype == dtype or (dtype == BF16 and t.dtype in _BF16_BITS)
+        if not ok or t.numel() != n or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"out[{name!r}] must be a contiguous {dtype} tensor of {n} elements on "
+                             f"{dev}; got {t.dtype}, {t.numel()} elements on {t.device}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+        return t
 
-def _new(out, name, shape, dtype, dev, stream):
-    """Output `name`: out's, of this many elements, or a new one."""
-    t = None if out is None else out.get(name)
-    if t is None:
-        return _empty(shape, dtype, dev, stream)
-    n = 1
-    for d in shape:
-        n *= d
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"out[{name!r}] must be a tensor")
-    ok = t.dtype == dtype or (dtype == BF16 and t.dtype in _BF16_BITS)
-    if not ok or t.numel() != n or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"out[{name!r}] must be a contiguous {dtype} tensor of {n} elements on {dev}; "
-                         f"got {t.dtype}, {t.numel()} elements on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t
+    return take
 
 
 def _at(t):
@@ -909,21 +927,24 @@ def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, che
     mx_rmsnorm_backward, with `checkpoint`.  Without a residual h is x."""
     x = _2d(x, "x")
     (M, K), dev = x.shape, x.device
-    rp = None if residual is None else _want(residual, x.shape, _BF16_BITS, "residual", dev)
-    wp = None if weight is None else _want(weight, (K,), _BF16_BITS, "weight", dev)
-    o = dict.fromkeys(("h", "y", "rstd", "q_row", "s_row", "q_col", "s_col", "q_h", "s_h"))
+    rp = _want(residual, x.shape, _BF16_BITS, "residual", dev)
+    wp = _want(weight, (K,), _BF16_BITS, "weight", dev)
+    o = {"h": None, "y": None, "rstd": None, "q_row": None, "s_row": None, "q_col": None,
+         "s_col": None, "q_h": None, "s_h": None}
+    new = _new(x, out, stream)
     if residual is not None:
-        o["h"] = _new(out, "h", (M, K), BF16, dev, stream)
+        o["h"] = new("h", (M, K), BF16)
     if want_y or (want_y is None and not axis):
-        o["y"] = _new(out, "y", (M, K), BF16, dev, stream)
-    o["rstd"] = _new(out, "rstd", (M,), F32, dev, stream)
+        o["y"] = new("y", (M, K), BF16)
+    o["rstd"] = new("rstd", (M,), F32)
     if axis:
         for name, (shape, dtype) in _mx_need(M, K, axis).items():
-            o[name] = _new(out, name, shape, dtype, dev, stream)
+            o[name] = new(name, shape, dtype)
     if checkpoint:
-        o["q_h"] = _new(out, "q_h", (M, K), U8, dev, stream)
-        o["s_h"] = _new(out, "s_h", (M, -(-K // 32)), U8, dev, stream)
-    _gpu(dev)
+        o["q_h"] = new("q_h", (M, K), U8)
+        o["s_h"] = new("s_h", (M, -(-K // 32)), U8)
+    if dev.index is None:
+        _gpu(dev)
     _launch("mx_rmsnorm", dev, stream, lib().mx_rmsnorm, x.data_ptr(), rp, wp, M, K, eps, axis,
             _at(o["h"]), _at(o["y"]), _at(o["q_row"]), _at(o["s_row"]), _at(o["q_col"]),
             _at(o["s_col"]), _at(o["q_h"]), _at(o["s_h"]), o["rstd"].data_ptr())
@@ -946,19 +967,21 @@ def mx_rmsnorm_backward(dy, rstd, weight=None, h=None, q_h=None, s_h=None, dres=
     (M, K), dev = dy.shape, dy.device
     if (h is None) == (q_h is None) or (q_h is None) != (s_h is None):
         raise ValueError("mx_rmsnorm_backward takes either h or q_h and s_h")
-    rp = _want(rstd, (M,), (F32,), "rstd", dev)
-    hp = None if h is None else _want(h, dy.shape, _BF16_BITS, "h", dev)
-    qp = None if q_h is None else _want(q_h, dy.shape, (U8,), "q_h", dev)
-    sp = None if s_h is None else _want(s_h, (M, -(-K // 32)), (U8,), "s_h", dev)
-    wp = None if weight is None else _want(weight, (K,), _BF16_BITS, "weight", dev)
-    dp = None if dres is None else _want(dres, dy.shape, _BF16_BITS, "dres", dev)
-    o = dict(dh=_new(out, "dh", (M, K), BF16, dev, stream), dweight=None)
+    rp = _want(rstd, (M,), _F32, "rstd", dev)
+    hp = _want(h, dy.shape, _BF16_BITS, "h", dev)
+    qp = _want(q_h, dy.shape, _U8, "q_h", dev)
+    sp = _want(s_h, (M, -(-K // 32)), _U8, "s_h", dev)
+    wp = _want(weight, (K,), _BF16_BITS, "weight", dev)
+    dp = _want(dres, dy.shape, _BF16_BITS, "dres", dev)
+    new = _new(dy, out, stream)
+    o = dict(dh=new("dh", (M, K), BF16), dweight=None)
     ws, pp, pn = None, None, 0
     L = lib()
     if want_dweight:
-        o["dweight"] = _new(out, "dweight", (K,), F32, dev, stream)
+        o["dweight"] = new("dweight", (K,), F32)
         ws, pp, pn = _product_ws(workspace, L.mx_rmsnorm_backward_workspace_size(M, K), dev, stream)
-    _gpu(dev)
+    if dev.index is None:
+        _gpu(dev)
     _launch("mx_rmsnorm_backward", dev, stream, L.mx_rmsnorm_backward, dy.data_ptr(), hp, qp, sp, rp,
             wp, dp, M, K, o["dh"].data_ptr(), _at(o["dweight"]), pp, pn)
     return o
@@ -981,11 +1004,13 @@ def moe_route(logits, top, bias=None, flags=0, groups=1, top_groups=1, scale=1.0
     sum with ROUTE_RENORM, times scale), scores (float32 [T][E] with want_scores)}."""
     f32 = _logits(logits)
     (T, E), dev = logits.shape, logits.device
-    bp = None if bias is None else _want(bias, (E,), (F32,), "bias", dev)
-    o = dict(experts=_new(out, "experts", (T, top), I32, dev, stream),
-             weights=_new(out, "weights", (T, top), F32, dev, stream),
-             scores=_new(out, "scores", (T, E), F32, dev, stream) if want_scores else None)
-    _gpu(dev)
+    bp = _want(bias, (E,), _F32, "bias", dev)
+    new = _new(logits, out, stream)
+    o = dict(experts=new("experts", (T, top), I32),
+             weights=new("weights", (T, top), F32),
+             scores=new("scores", (T, E), F32) if want_scores else None)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_route", dev, stream, lib().moe_route, logits.data_ptr(), bp, T, E, top, groups,
             top_groups, scale, flags | f32, o["experts"].data_ptr(), o["weights"].data_ptr(),
             _at(o["scores"]))
@@ -1002,11 +1027,12 @@ def moe_route_backward(dweights, logits, experts, flags=0, scale=1.0, dscores=No
     if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
         raise ValueError("experts must be a tensor [T][top]")
     top = experts.shape[1]
-    ep = _want(experts, (T, top), (I32,), "experts", dev)
-    wp = _want(dweights, (T, top), (F32,), "dweights", dev)
-    sp = None if dscores is None else _want(dscores, (T, E), (F32,), "dscores", dev)
-    o = _new({"out": out}, "out", (T, E), logits.dtype, dev, stream)
-    _gpu(dev)
+    ep = _want(experts, (T, top), _I32, "experts", dev)
+    wp = _want(dweights, (T, top), _F32, "dweights", dev)
+    sp = _want(dscores, (T, E), _F32, "dscores", dev)
+    o = _new(logits, None if out is None else {"out": out}, stream)("out", (T, E), logits.dtype)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_route_backward", dev, stream, lib().moe_route_backward, logits.data_ptr(), ep, wp, sp,
             T, E, top, scale, flags | f32, o.data_ptr())
     return o
@@ -1036,11 +1062,13 @@ def moe_sort(experts, E, align=1, rows=None, out=None, workspace=None, stream=No
     T, top = _slots_2d(experts, "experts").shape
     dev, L = experts.device, lib()
     rows = L.moe_sort_rows(T, top, E, align) if rows is None else int(rows)
-    o = dict(counts=_new(out, "counts", (E,), I32, dev, stream),
-             pos=_new(out, "pos", (T, top), I32, dev, stream),
-             slots=_new(out, "slots", (rows,), I32, dev, stream))
+    new = _new(experts, out, stream)
+    o = dict(counts=new("counts", (E,), I32),
+             pos=new("pos", (T, top), I32),
+             slots=new("slots", (rows,), I32))
     ws, wp, wn = _product_ws(workspace, L.moe_sort_workspace_size(T, top, E), dev, stream)
-    _gpu(dev)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_sort", dev, stream, L.moe_sort, experts.data_ptr(), T, top, E, align, rows,
             o["counts"].data_ptr(), o["pos"].data_ptr(), o["slots"].data_ptr(), wp, wn)
     return o
@@ -1054,12 +1082,13 @@ def moe_gather(x, slots, top, out=None, stream=None):
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D tensor")
     dev, T, rows = x.device, x.shape[0], slots.shape[0]
-    sp = _want(slots, (rows,), (I32,), "slots", dev)
-    o = _new({"out": out}, "out", (rows, *x.shape[1:]), x.dtype, dev, stream)
+    sp = _want(slots, (rows,), _I32, "slots", dev)
+    o = _new(x, None if out is None else {"out": out}, stream)("out", (rows, *x.shape[1:]), x.dtype)
     width = x.element_size()
     for d in x.shape[1:]:
         width *= d
-    _gpu(dev)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_gather", dev, stream, lib().moe_gather, x.data_ptr(), T, top, sp, rows, width,
             o.data_ptr())
     return o
@@ -1080,8 +1109,8 @@ def _rows_and_slots(y, weights, pos):
             raise ValueError(f"y must be [rows][K], got {tuple(y.shape)}")
         rows, K = y.shape
     dev = y.device
-    pp = None if pos is None else _want(pos, (T, top), (I32,), "pos", dev)
-    wp = None if weights is None else _want(weights, (T, top), (F32,), "weights", dev)
+    pp = _want(pos, (T, top), _I32, "pos", dev)
+    wp = _want(weights, (T, top), _F32, "weights", dev)
     return T, top, rows, K, pp, wp
 
 
@@ -1091,8 +1120,9 @@ def moe_combine(y, weights=None, pos=None, out=None, stream=None):
     [T][top][K], as nvfp4_matvec_experts returns it; without weights they are 1."""
     T, top, rows, K, pp, wp = _rows_and_slots(y, weights, pos)
     dev = y.device
-    o = _new({"out": out}, "out", (T, K), BF16, dev, stream)
-    _gpu(dev)
+    o = _new(y, None if out is None else {"out": out}, stream)("out", (T, K), BF16)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_combine", dev, stream, lib().moe_combine, y.data_ptr(), rows, K, pp, wp, T, top,
             o.data_ptr())
     return o
@@ -1108,10 +1138,12 @@ def moe_combine_backward(dout, y, weights=None, pos=None, slots=None, want_dweig
     if (pos is None) != (slots is None):
         raise ValueError("pos and slots go together")
     gp = _want(dout, (T, K), _BF16_BITS, "dout", dev)
-    sp = None if slots is None else _want(slots, (rows,), (I32,), "slots", dev)
-    o = dict(dy=_new(out, "dy", tuple(y.shape), BF16, dev, stream),
-             dweights=_new(out, "dweights", (T, top), F32, dev, stream) if want_dweights else None)
-    _gpu(dev)
+    sp = _want(slots, (rows,), _I32, "slots", dev)
+    new = _new(y, out, stream)
+    o = dict(dy=new("dy", tuple(y.shape), BF16),
+             dweights=new("dweights", (T, top), F32) if want_dweights else None)
+    if dev.index is None:
+        _gpu(dev)
     _launch("moe_combine_backward", dev, stream, lib().moe_combine_backward, gp, y.data_ptr(), rows, K,
             pp, sp, wp, T, top, o["dy"].data_ptr(), _at(o["dweights"]))
     return o

@@ -176,10 +176,10 @@ int64_t moe_sort_rows(int64_t T, int64_t top, int64_t E, int64_t align)
 
 size_t moe_sort_workspace_size(int64_t T, int64_t top, int64_t E)
 {
-    if (!sort_size(T, top, E, 1) || T * top <= mxk::kSortAlone)
+    if (!sort_size(T, top, E, 1) || T * top <= mxk::kSortFew)
         return 0;
     const int64_t chunk = mxk::sort_chunk(T * top), blocks = (T * top + chunk - 1) / chunk;
-    return (size_t)((blocks + 1) * E) * sizeof(int32_t);
+    return (size_t)(blocks * E) * sizeof(int32_t);
 }
 
 mx_status moe_sort(const int32_t *experts, int64_t T, int64_t top, int64_t E, int64_t align,

@@ -36,18 +36,19 @@ struct SortArgs {
     int E, align;
     int64_t rows;
     int32_t *counts, *pos, *slots;
-    int32_t *ws;                    // [blocks + 1][E], or null for one workgroup
+    int32_t *ws;                    // [blocks][E], or null for one launch
     int blocks, chunk;              // workgroups and slots of each
 };
 
-// Slots up to which one workgroup sorts alone; beyond, workgroups of 512 threads
-// take a whole number of 512 slots each, at least 2048, and are at most 256.
-constexpr int64_t kSortAlone = 8192;
+// Slots up to which one launch sorts, in up to 16 workgroups of 1024 threads and a
+// whole number of 1024 slots each; beyond, workgroups of 512 threads take a whole
+// number of 512 slots, at least 2048, and are at most 256.
+constexpr int64_t kSortFew = 32768;
 constexpr int kSortThreads = 512;
 inline int64_t sort_chunk(int64_t N)
 {
-    if (N <= kSortAlone)
-        return (N + kSortThreads - 1) / kSortThreads * kSortThreads;
+    if (N <= kSortFew)
+        return 1024 * ((N + 16 * 1024 - 1) / (16 * 1024));
     const int64_t per = (N + 256 * kSortThreads - 1) / (256 * kSortThreads);
     return kSortThreads * (per < 4 ? 4 : per);
 }

@@ -35,7 +35,8 @@ __device__ __forceinline__ uint64_t same_lanes(int e, int bits)
 
 // Rank of this lane's slot among its expert's slots of the run so far, whose
 // counts are in cnt (one wave's own); -1 without an expert (e = E).
-__device__ __forceinline__ int rank_and_count(int32_t *cnt, int e, int E, int bits, int lane)
+template <class C>
+__device__ __forceinline__ int rank_and_count(C *cnt, int e, int E, int bits, int lane)
 {
     const uint64_t m = same_lanes(e, bits);
     const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
@@ -44,7 +45,7 @@ __device__ __forceinline__ int rank_and_count(int32_t *cnt, int e, int E, int bi
         at = cnt[e] + before;
     __builtin_amdgcn_wave_barrier();
     if (e < E && before == 0)
-        cnt[e] += __builtin_popcountll(m);
+        cnt[e] = (C)(cnt[e] + __builtin_popcountll(m));
     __builtin_amdgcn_wave_barrier();
     return at;
 }
@@ -101,55 +102,190 @@ __device__ __forceinline__ void fill_rows(const SortArgs &a, const int32_t *star
 
 __device__ __forceinline__ int index_bits(int E) { return 32 - __builtin_clz((unsigned)E); }
 
-// One workgroup sorts all slots: its waves' counts in LDS, their sums, the ranks.
-// The waves' slots are taken twice (they are in the caches the second time).
-__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(SortArgs a)
+// One workgroup of 64 WAVES threads sorts up to 64 WAVES RUN slots: a wave's run,
+// 64 at a time, with each slot's rank within the run kept in registers; the runs'
+// counts (16 bits) summed over the waves and the experts; the rows.
+template <int WAVES, int RUN>
+__global__ __launch_bounds__(64 * WAVES) void sort_alone_kernel(SortArgs a)
 {
-    extern __shared__ int32_t lds[];                  // [waves][E], start [E], counts [E]
-    __shared__ int32_t red[kSortWaves];
-    int32_t *const start = lds + kSortWaves * a.E, *const counts = start + a.E;
+    extern __shared__ int32_t lds[];                  // start [E], counts [E], runs [WAVES][E]
+    __shared__ int32_t red[WAVES];
+    constexpr int THREADS = 64 * WAVES;
+    int32_t *const start = lds, *const counts = lds + a.E;
+    uint16_t *const runs = reinterpret_cast<uint16_t *>(counts + a.E);
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, bits = index_bits(a.E);
-    const int64_t run = a.chunk / kSortWaves, first = wave * run;
-    const int64_t end = first + run < a.N ? first + run : a.N;
-    int32_t *const cnt = lds + wave * a.E;
-    for (int i = threadIdx.x; i < kSortWaves * a.E; i += kSortThreads)
-        lds[i] = 0;
-    __syncthreads();
-    for (int64_t s = first; s < end; s += 64)
-        rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+    const int64_t first = (int64_t)wave * (64 * RUN);
+    const int64_t end = first + 64 * RUN < a.N ? first + 64 * RUN : a.N;
+    uint16_t *const cnt = runs + wave * a.E;
+    int e[RUN], rank[RUN];
+#pragma unroll
+    for (int i = 0; i < RUN; i++)
+        e[i] = expert_of(a, first + 64 * i + lane, end);
+    for (int i = lane; i < a.E; i += 64)
+        cnt[i] = 0;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < RUN; i++)
+        rank[i] = first + 64 * i < end ? rank_and_count(cnt, e[i], a.E, bits, lane) : -1;
     __syncthreads();
     // each thread's experts are neighbours, so that the threads' sums are in order
-    const int per = (a.E + kSortThreads - 1) / kSortThreads, e0 = (int)threadIdx.x * per;
+    const int per = (a.E + THREADS - 1) / THREADS, e0 = (int)threadIdx.x * per;
     int mine = 0;
-    for (int e = e0; e < e0 + per && e < a.E; e++) {
+    for (int k = e0; k < e0 + per && k < a.E; k++) {
         int n = 0;
-        for (int w = 0; w < kSortWaves; w++) {
-            const int c = lds[w * a.E + e];
-            lds[w * a.E + e] = n;
+#pragma unroll
+        for (int w = 0; w < WAVES; w++) {
+            const int c = runs[w * a.E + k];
+            runs[w * a.E + k] = (uint16_t)n;
             n += c;
         }
-        counts[e] = n;
-        a.counts[e] = n;
+        counts[k] = n;
+        a.counts[k] = n;
         mine += (n + a.align - 1) / a.align * a.align;
     }
     int total;
-    int at = before_sum(mine, red, kSortWaves, total);
-    for (int e = e0; e < e0 + per && e < a.E; e++) {
-        start[e] = at;
-        for (int w = 0; w < kSortWaves; w++)
-            lds[w * a.E + e] += at;
-        at += (counts[e] + a.align - 1) / a.align * a.align;
+    int at = before_sum(mine, red, WAVES, total);
+    for (int k = e0; k < e0 + per && k < a.E; k++) {
+        start[k] = at;
+        at += (counts[k] + a.align - 1) / a.align * a.align;
     }
     __syncthreads();
-    for (int64_t s = first; s < end; s += 64) {
-        const int row = rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
+#pragma unroll
+    for (int i = 0; i < RUN; i++) {
+        const int64_t s = first + 64 * i + lane;
+        if (s >= end)
+            continue;
+        const int row = rank[i] < 0 ? -1 : start[e[i]] + cnt[e[i]] + rank[i];
+        a.pos[s] = row;
+        if (row >= 0)
+            a.slots[row] = (int32_t)s;
+    }
+    fill_rows(a, start, counts, total, 0, 1);
+}
+
+// Rows of a workgroup's slots, its waves' runs of a.chunk / WAVES one after the
+// other from `first` on: base[e], the row of the first of expert e's among them;
+// runs: 16-bit counts [WAVES][E], any values.  Each run is ranked twice where it is
+// longer than RUN 64 (the first ranks are not kept), once otherwise.
+template <int WAVES>
+__device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, const int32_t *base,
+                                            uint16_t *runs)
+{
+    constexpr int THREADS = 64 * WAVES;
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, bits = index_bits(a.E);
+    const int64_t run = a.chunk / WAVES, from = first + wave * run;
+    const int64_t end = from + run < a.N ? from + run : a.N;
+    uint16_t *const cnt = runs + wave * a.E;
+    for (int k = lane; k < a.E; k += 64)
+        cnt[k] = 0;
+    __builtin_amdgcn_wave_barrier();
+    int e = expert_of(a, from + lane, end), rank = -1;
+    for (int64_t s = from; s < end; s += 64) {
+        const int next = expert_of(a, s + 64 + lane, end);
+        rank = rank_and_count(cnt, e, a.E, bits, lane);
+        e = run > 64 ? next : e;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.E; k += THREADS) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; w++) {
+            const int c = runs[w * a.E + k];
+            runs[w * a.E + k] = (uint16_t)n;
+            n += c;
+        }
+    }
+    __syncthreads();
+    if (run > 64)
+        e = expert_of(a, from + lane, end);
+    for (int64_t s = from; s < end; s += 64) {
+        const int next = run > 64 ? expert_of(a, s + 64 + lane, end) : a.E;
+        if (run > 64)
+            rank = rank_and_count(cnt, e, a.E, bits, lane);
+        else if (rank >= 0)
+            rank += cnt[e];
         if (s + lane < end) {
+            const int row = rank < 0 ? -1 : base[e] + rank;
             a.pos[s + lane] = row;
             if (row >= 0)
                 a.slots[row] = (int32_t)(s + lane);
         }
+        e = next;
     }
-    fill_rows(a, start, counts, total, 0, 1);
+}
+
+// Up to 16 workgroups in one launch: each counts all slots (wave w those of
+// workgroup w), so that it knows what comes before its own.
+constexpr int kFewWaves = 16, kFewCopies = 8;
+// Few experts: neighbouring lanes count in arrays of their own, or they would queue
+// for the same words.
+__host__ __device__ inline int few_copies(int E) { return E <= 64 ? kFewCopies : 1; }
+__global__ __launch_bounds__(64 * kFewWaves) void sort_few_kernel(SortArgs a)
+{
+    extern __shared__ int32_t lds[];       // base [E], start [E], counts [E], runs [16 copies][E] (16 bits)
+    __shared__ int32_t red[kFewWaves];
+    constexpr int THREADS = 64 * kFewWaves;
+    const int E2 = (a.E + 1) & ~1;
+    int32_t *const base = lds, *const start = base + E2, *const counts = start + E2;
+    uint32_t *const words = reinterpret_cast<uint32_t *>(counts + E2);
+    uint16_t *const runs = reinterpret_cast<uint16_t *>(words);
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, me = (int)blockIdx.x;
+    const int copies = few_copies(a.E);
+    for (int i = threadIdx.x; i < kFewWaves * copies * E2 / 2; i += THREADS)
+        words[i] = 0;
+    __syncthreads();
+    const int64_t from = (int64_t)wave * a.chunk;
+    const int64_t end = from + a.chunk < a.N ? from + a.chunk : a.N;
+    for (int64_t s = from; s < end; s += 8 * 64) {
+        int e[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            e[i] = expert_of(a, s + 64 * i + lane, end);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (e[i] < a.E)            // sums of ones: the same in any order
+                atomicAdd(&words[((wave * copies + (lane & (copies - 1))) * E2 + e[i]) >> 1],
+                          1u << (16 * (e[i] & 1)));
+    }
+    __syncthreads();
+    // the copies into the first one, two counts a word (none passes 16 bits)
+    for (int i = threadIdx.x; copies > 1 && i < kFewWaves * E2 / 2; i += THREADS) {
+        const int w = i / (E2 / 2);
+        uint32_t *const at = words + w * copies * (E2 / 2) + (i - w * (E2 / 2));
+        uint32_t v = at[0];
+#pragma unroll
+        for (int c = 1; c < kFewCopies; c++)
+            v += at[c * (E2 / 2)];
+        at[0] = v;
+    }
+    __syncthreads();
+    // each thread's experts are neighbours, so that the threads' sums are in order
+    const int per = (a.E + THREADS - 1) / THREADS, e0 = (int)threadIdx.x * per;
+    int mine = 0;
+    for (int k = e0; k < e0 + per && k < a.E; k++) {
+        int n = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; w++) {
+            const int c = runs[w * copies * E2 + k];
+            before += w < me ? c : 0;
+            n += c;
+        }
+        base[k] = before;
+        counts[k] = n;
+        if (me == 0)
+            a.counts[k] = n;
+        mine += (n + a.align - 1) / a.align * a.align;
+    }
+    int total;
+    int at = before_sum(mine, red, kFewWaves, total);
+    for (int k = e0; k < e0 + per && k < a.E; k++) {
+        start[k] = at;
+        base[k] += at;
+        at += (counts[k] + a.align - 1) / a.align * a.align;
+    }
+    __syncthreads();
+    place_slots<kFewWaves>(a, (int64_t)me * a.chunk, base, runs);
+    fill_rows(a, start, counts, total, me, (int)gridDim.x);
 }
 
 // Counts of each workgroup's slots: ws[block][E].
@@ -171,95 +307,92 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a)
         a.ws[(int64_t)blockIdx.x * a.E + e] = cnt[e];
 }
 
-// Thread e: sums over the workgroups before each, in place; the experts' counts;
-// their first rows in ws[blocks].
-__global__ __launch_bounds__(kSortE) void sort_sum_kernel(SortArgs a)
-{
-    __shared__ int32_t red[kSortE / 64];
-    const int e = (int)threadIdx.x;
-    int n = 0;
-    if (e < a.E) {
-        for (int b = 0; b < a.blocks; b++) {
-            const int c = a.ws[(int64_t)b * a.E + e];
-            a.ws[(int64_t)b * a.E + e] = n;
-            n += c;
-        }
-        a.counts[e] = n;
-    }
-    int total;
-    const int at = before_sum((n + a.align - 1) / a.align * a.align, red, kSortE / 64, total);
-    if (e < a.E)
-        a.ws[(int64_t)a.blocks * a.E + e] = at;
-}
-
+// Each workgroup adds all workgroups' counts, those before it apart.
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a)
 {
-    extern __shared__ int32_t lds[];                  // [waves][E]
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, bits = index_bits(a.E);
-    const int64_t run = a.chunk / kSortWaves, first = (int64_t)blockIdx.x * a.chunk + wave * run;
-    const int64_t end = first + run < a.N ? first + run : a.N;
-    const int32_t *const start = a.ws + (int64_t)a.blocks * a.E;
-    int32_t *const cnt = lds + wave * a.E;
-    for (int i = threadIdx.x; i < kSortWaves * a.E; i += kSortThreads)
-        lds[i] = 0;
+    extern __shared__ int32_t lds[];       // base [E], start [E], counts [E], runs [waves][E] (16 bits)
+    __shared__ int32_t red[kSortWaves];
+    int32_t *const base = lds, *const start = base + a.E, *const counts = start + a.E;
+    const int per = (a.E + kSortThreads - 1) / kSortThreads, e0 = (int)threadIdx.x * per;
+    const int me = (int)blockIdx.x;
+    // a thread's share: experts k, k + 512, .. when they are many, or a part of the
+    // workgroups' counts of one expert when they are few
+    for (int k = threadIdx.x; k < a.E; k += kSortThreads)
+        base[k] = counts[k] = 0;
     __syncthreads();
-    for (int64_t s = first; s < end; s += 64)
-        rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-        int n = start[e] + a.ws[(int64_t)blockIdx.x * a.E + e];
-        for (int w = 0; w < kSortWaves; w++) {
-            const int c = lds[w * a.E + e];
-            lds[w * a.E + e] = n;
+    const int parts = a.E >= kSortThreads ? 1 : kSortThreads / a.E;
+    const int part = parts == 1 ? 0 : (int)threadIdx.x / a.E;
+    for (int k = parts == 1 ? (int)threadIdx.x : (int)threadIdx.x - part * a.E; k < a.E && part < parts;
+         k += parts == 1 ? kSortThreads : a.E) {
+        int n = 0, before = 0;
+#pragma unroll 8
+        for (int b = part; b < a.blocks; b += parts) {
+            const int c = a.ws[(int64_t)b * a.E + k];
+            before += b < me ? c : 0;
             n += c;
         }
+        atomicAdd(&counts[k], n);      // whole numbers: the same in any order
+        atomicAdd(&base[k], before);
     }
     __syncthreads();
-    for (int64_t s = first; s < end; s += 64) {
-        const int row = rank_and_count(cnt, expert_of(a, s + lane, end), a.E, bits, lane);
-        if (s + lane < end) {
-            a.pos[s + lane] = row;
-            if (row >= 0)
-                a.slots[row] = (int32_t)(s + lane);
-        }
+    int mine = 0;
+    for (int k = e0; k < e0 + per && k < a.E; k++)
+        mine += (counts[k] + a.align - 1) / a.align * a.align;
+    int total;
+    int at = before_sum(mine, red, kSortWaves, total);
+    for (int k = e0; k < e0 + per && k < a.E; k++) {
+        start[k] = at;
+        base[k] += at;
+        at += (counts[k] + a.align - 1) / a.align * a.align;
+        if (me == 0)
+            a.counts[k] = counts[k];
     }
-    const int64_t total = (int64_t)start[a.E - 1] +
-                          (a.counts[a.E - 1] + a.align - 1) / a.align * (int64_t)a.align;
-    fill_rows(a, start, a.counts, total, (int)blockIdx.x, (int)gridDim.x);
+    __syncthreads();
+    place_slots<kSortWaves>(a, (int64_t)me * a.chunk, base, reinterpret_cast<uint16_t *>(counts + a.E));
+    fill_rows(a, start, counts, total, me, (int)gridDim.x);
 }
 
 hipError_t launch_sort(const SortArgs &a, hipStream_t s)
 {
-    const size_t lds = (size_t)kSortWaves * a.E * sizeof(int32_t);
-    if (!a.ws) {
-        hipLaunchKernelGGL(sort_alone_kernel, dim3(1), dim3(kSortThreads),
-                           lds + 2 * (size_t)a.E * sizeof(int32_t), s, a);
-        return hipGetLastError();
+    const size_t sums = 3 * (size_t)((a.E + 1) & ~1) * sizeof(int32_t);
+    const size_t run = (size_t)((a.E + 1) & ~1) * sizeof(uint16_t);
+    if (a.N <= 1024) {
+        hipLaunchKernelGGL((sort_alone_kernel<4, 4>), dim3(1), dim3(256), sums + 4 * run, s, a);
+    } else if (!a.ws) {
+        hipLaunchKernelGGL(sort_few_kernel, dim3(a.blocks), dim3(64 * kFewWaves), sums + few_copies(a.E) * kFewWaves * run,
+                           s, a);
+    } else {
+        hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, s, a);
+        hipLaunchKernelGGL(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads), sums + kSortWaves * run,
+                           s, a);
     }
-    hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, s, a);
-    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSortE), 0, s, a);
-    hipLaunchKernelGGL(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads), lds, s, a);
     return hipGetLastError();
 }
 
 // ---- rows ---------------------------------------------------------------------
 
-// Row blockIdx.y * n + ... of out; V: the widest access that every row allows.
+// Rows of out by workgroups, four pieces a thread under way at once; V: the widest
+// access that every row allows.
 template <class V>
 __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a)
 {
     const int64_t n = a.row_bytes / (int64_t)sizeof(V);
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int32_t slot = a.slots[r];
+        const bool live = slot >= 0 && slot < a.T * a.top;
         V *const o = reinterpret_cast<V *>(a.out + r * a.row_bytes);
-        if (slot < 0 || slot >= a.T * a.top) {
-            for (int64_t i = threadIdx.x; i < n; i += 256)
-                o[i] = V{};
-            continue;
+        const V *const x =
+            reinterpret_cast<const V *>(a.x + (live ? (int64_t)(slot / a.top) * a.row_bytes : 0));
+        for (int64_t i = threadIdx.x; i < n; i += 4 * 256) {
+            V v[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                v[j] = live && i + 256 * j < n ? x[i + 256 * j] : V{};
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (i + 256 * j < n)
+                    __builtin_nontemporal_store(v[j], &o[i + 256 * j]);
         }
-        const V *const x = reinterpret_cast<const V *>(a.x + (int64_t)(slot / a.top) * a.row_bytes);
-        for (int64_t i = threadIdx.x; i < n; i += 256)
-            o[i] = x[i];
     }
 }
 

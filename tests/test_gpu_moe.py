@@ -315,7 +315,9 @@ def check_sort(ex, E, align, more=0):
 
 
 @pytest.mark.parametrize("T,top,E", [(1, 1, 1), (1, 8, 8), (3, 2, 5), (64, 1, 64), (65, 1, 2), (128, 4, 16),
-                                     (1000, 8, 256), (1024, 8, 1024), (1025, 8, 7), (4096, 4, 8),
+                                     (1000, 8, 256), (1024, 8, 1024), (1025, 8, 7), (4096, 4, 8), (4097, 4, 9),
+                                     (128, 8, 256), (129, 8, 1024), (512, 8, 31), (513, 8, 64), (2048, 8, 1000),
+                                     (2049, 8, 5), (4096, 8, 128), (4097, 8, 1000), (8193, 8, 300), (65536, 1, 3),
                                      (5000, 3, 1000), (20001, 8, 64), (70000, 7, 33), (8193, 1, 1)])
 def test_sort(T, top, E):
     check_sort(experts_of(T, T, top, E), E, 1)

@@ -209,10 +209,10 @@ def test_sort_sizes():
     for bad in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 65, 1, 1), (1, 1, 0, 1), (1, 1, 1025, 1), (1, 1, 1, 0),
                 (1, 1, 1, 4097), (1 << 23, 2, 1, 1), (-1, 1, 1, 1)):
         assert rows(*bad) == 0
-    assert size(1024, 8, 64) == 0 and size(1025, 8, 64) > 0 and size(0, 8, 64) == 0
-    for t in (1025, 4096, 1 << 17, 1 << 20):
-        blocks = size(t, 8, 64) // 256 - 1
-        assert 1 <= blocks <= 256 and size(t, 8, 64) == 256 * (blocks + 1)
+    assert size(4096, 8, 64) == 0 and size(4097, 8, 64) > 0 and size(0, 8, 64) == 0
+    for t in (4097, 1 << 17, 1 << 20):
+        blocks = size(t, 8, 64) // 256
+        assert 1 <= blocks <= 256 and size(t, 8, 64) == 256 * blocks
 
 
 def test_gather_errors():
