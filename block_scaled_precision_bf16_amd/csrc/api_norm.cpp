@@ -83,6 +83,7 @@ mx_status norm_columns(const void *h, const void *weight, int64_t M, int64_t K, 
     a.q_col = q_col;
     a.s_col = s_col;
     a.tiled = (axis_mask & MX_SCALE_TILED) != 0;
+    a.qcol_nt = mxk::norm_streams(M, K);
     mxk::GroupTable gt{};
     gt.count = 1;
     gt.row0[1] = M;
@@ -158,6 +159,7 @@ mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, in
     a.s_h = s_h;
     a.rstd = rstd;
     a.tiled = tiled;
+    a.stream = mxk::norm_streams(M, K);
     const hipError_t e =
         mxk::launch_norm(axis_mask & (MX_ELEM_E5M2 | MX_SCALE_ROUND_UP), a, stream);
     if (e != hipSuccess || !col)
@@ -205,6 +207,7 @@ mx_status mx_rmsnorm_backward(const void *dy, const void *h, const uint8_t *q_h,
     a.dh = static_cast<uint16_t *>(dh);
     a.partials = dweight ? static_cast<float *>(workspace) : nullptr;
     a.dweight = dweight;
+    a.stream = mxk::norm_streams(M, K);
     return from_hip(mxk::launch_norm_back(a, stream));
 }
 

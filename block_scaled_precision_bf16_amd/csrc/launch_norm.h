@@ -18,6 +18,7 @@ struct NormArgs {
     uint8_t *q_h, *s_h;            // 8-bit copy of h, may be null
     float *rstd;
     int tiled;                     // s_row in the tile layout
+    int stream;                    // too large for the caches: norm_streams
 };
 
 struct NormBackArgs {
@@ -28,7 +29,17 @@ struct NormBackArgs {
     int64_t M, K;
     uint16_t *dh;
     float *partials, *dweight;     // both null: no weight gradient
+    int stream;                    // too large for the caches: norm_streams
 };
+
+// Tensors of more than 64 MiB, which with the others of a call pass the 256 MiB
+// of the last cache: what is read or written once goes by non-temporal accesses,
+// which leaves that cache to h, the input of the column-wise casts (16384 x 7168
+// with both casts and the checkpoint 259 -> 209 us, 8192 x 7168 120 -> 102 us, 16384
+// x 8192 row-wise 182 -> 151 us).  4096 x 7168, 56 MiB, takes 60.5 and 61.1 us, and
+// smaller ones are still in the caches from the kernel that wrote them (1024 x 7168:
+// 24.0 and 29.9 us).
+inline bool norm_streams(int64_t M, int64_t K) { return 2 * M * K > int64_t(1) << 26; }
 
 // A row in registers: a lane holds 1 or 2 chunks of 8 elements, chunk c of the
 // row in lane c mod threads, in whole waves, 1024 threads at most.
@@ -45,13 +56,17 @@ inline NormShape norm_shape(int64_t K)
     return NormShape{chunks, (int)((n + 64 * chunks - 1) / (64 * chunks)) * 64};
 }
 
-// Workgroups of the backward kernel, each of which leaves one row of partial
-// weight gradients; of the two-pass kernels: row slices.
+// The backward kernel's workgroups: as many rows at a time as 512 threads hold (a
+// row's elements stay with the same threads, whose weight gradients they are), one
+// workgroup a CU or two where a row takes at most 256 threads, each of which leaves
+// one row of partial sums.  The two-pass kernels: row slices.
+inline int norm_back_rows(const NormShape &s) { return s.threads >= 512 ? 1 : 512 / s.threads; }
 inline int64_t norm_back_parts(int64_t M, int64_t K)
 {
     const NormShape s = norm_shape(K);
-    const int64_t most = s.chunks == 0 ? 64 : 256 * (s.threads <= 512 ? 2 : 1);
-    return M < most ? M : most;
+    const int64_t turns = s.chunks == 0 ? M : (M + norm_back_rows(s) - 1) / norm_back_rows(s);
+    const int64_t most = s.chunks == 0 ? 64 : 256;
+    return turns < most ? turns : most;
 }
 
 hipError_t launch_norm(unsigned fmt, const NormArgs &a, hipStream_t s);

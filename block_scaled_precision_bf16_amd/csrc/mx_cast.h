@@ -61,6 +61,9 @@ __device__ __forceinline__ float half_value(uint32_t w, int hi)
 // non-temporal as well; the row scales keep the default policy (non-temporal
 // row scales, 8-byte pieces of lines that other workgroups complete, cost
 // ~15%), and so does the transposed output alone (non-temporal: 26% slower).
+// The norm's transposed output is non-temporal where its input is too large for
+// the caches otherwise (qcol_nt; 16384 x 7168: 226 -> 209 us with the kernel
+// before it), but not where its rows share lines with other workgroups'.
 // The policies change timing only, never results.
 template <int OP, bool ROW, bool COL>
 struct Policy {
@@ -69,7 +72,7 @@ struct Policy {
         plain || OP == OP_DGELU || OP == OP_DSILU || OP == OP_DSWIGLU ? kNT : 0;
     static constexpr int q_row = plain ? kSC1 : 0;       // row-wise stores
     static constexpr int s_row = 0;
-    static constexpr int q_col = both ? kNT : 0;         // transposed stores
+    static constexpr int q_col = both || OP == OP_NORM ? kNT : 0;   // transposed stores
     static constexpr int s_col = both ? kNT : 0;
 };
 
@@ -507,7 +510,8 @@ __device__ __forceinline__ void tile_step(const MxArgs &a, const LaneAt &l,
     }
     __syncthreads();
     if constexpr (COL && RAG) {
-        col_flush_q_rag<Policy<OP, ROW, COL>::q_col>(a, *st, tm, tk, g, g == 0, g + 1 == n);
+        col_flush_q_rag<OP == OP_NORM ? 0 : Policy<OP, ROW, COL>::q_col>(a, *st, tm, tk, g, g == 0,
+                                                                      g + 1 == n);
     } else if constexpr (COL) {
         // the non-temporal transposed stores pay off only for outputs too
         // large to be absorbed by the caches (the host decides: qcol_nt)
@@ -600,8 +604,14 @@ __device__ __forceinline__ void mx_cast_walk(const MxArgs &a, int rg, int tk)
             tile_step<OP, FMT, ROW, COL, DBIAS, RAG>(a, l, w, srow, st, tm0 + g, tk, g, n, dsum);
         }
     }
-    if constexpr (COL)
+    if constexpr (COL && OP == OP_NORM && !RAG) {
+        if (a.qcol_nt)
+            col_flush_s<kNT>(a, *st, rg, tk, n);
+        else
+            col_flush_s<0>(a, *st, rg, tk, n);
+    } else if constexpr (COL) {
         col_flush_s<Policy<OP, ROW, COL>::s_col>(a, *st, rg, tk, n);
+    }
 
     if constexpr (DBIAS) {
         // per-lane sums (rows in order, sub-tiles in order), then the 8
@@ -658,6 +668,10 @@ __device__ __forceinline__ void job_of(const MxArgs &a, int &rg, int &tk)
     const int job = xcd_tile((int)blockIdx.x, (int)gridDim.x);
     rg = job / a.tiles_k;
     tk = job - rg * a.tiles_k;
+    // the norm's kernel before this one has just written h: its last rows first,
+    // while the caches still hold them
+    if constexpr (OP == OP_NORM)
+        rg = a.groups_m - 1 - rg;
 }
 
 template <int OP, int FMT, bool ROW, bool COL, bool DBIAS>

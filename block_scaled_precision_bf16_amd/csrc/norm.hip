@@ -33,9 +33,10 @@ __device__ __forceinline__ int64_t row_of(int64_t step, int b, int n)
     return step * n + at;
 }
 
-// Sum over the workgroup, the same in every thread; red: one float per wave,
-// another one for the next call.
-__device__ __forceinline__ float block_sum(float v, float *red, int waves)
+// Sum over `waves` waves of the workgroup, from wave `first` on, the same in each of
+// their threads; red: a float for each wave of the workgroup, others for the next
+// call.
+__device__ __forceinline__ float block_sum(float v, float *red, int waves, int first = 0)
 {
     v = wave_sum(v);
     if (waves == 1)
@@ -43,9 +44,9 @@ __device__ __forceinline__ float block_sum(float v, float *red, int waves)
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
-    float s = red[0];
+    float s = red[first];
     for (int i = 1; i < waves; i++)
-        s += red[i];
+        s += red[first + i];
     return s;
 }
 
@@ -77,7 +78,7 @@ __device__ __forceinline__ uint32_t block_mag(const uint32_t (&m)[4])
 
 // MXFP8 of a lane's 8 elements of row r, chunk c: codes to q (the row's
 // descriptor), the scale byte returned.
-template <int FMT>
+template <int FMT, int AUX>
 __device__ __forceinline__ uint32_t cast8(rsrc_t q, const uint32_t (&w)[4], uint32_t c)
 {
     uint32_t m[4];
@@ -88,7 +89,7 @@ __device__ __forceinline__ uint32_t cast8(rsrc_t q, const uint32_t (&w)[4], uint
     uint2 o = encode8_row<FMT>(w, m, sb);
     if (sb == 0xFFu)
         o.x = o.y = 0x7F7F7F7Fu;
-    buf_store8(q, 8 * c, o);
+    buf_store8<AUX>(q, 8 * c, o);
     return sb;
 }
 
@@ -134,7 +135,7 @@ struct NormRow {
     uint4 x[CH], r[CH];
 };
 
-template <int CH>
+template <int CH, int AUX>
 __device__ __forceinline__ void norm_load(const NormArgs &a, int64_t row, NormRow<CH> &v)
 {
     // a row outside the tensor reads as zeros, without traffic
@@ -145,13 +146,14 @@ __device__ __forceinline__ void norm_load(const NormArgs &a, int64_t row, NormRo
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const uint32_t off = 16 * (threadIdx.x + i * blockDim.x);
-        v.x[i] = buf_load16(dx, off);
+        v.x[i] = buf_load16<AUX>(dx, off);
         if (a.res)
-            v.r[i] = buf_load16(dr, off);
+            v.r[i] = buf_load16<AUX>(dr, off);
     }
 }
 
-template <int FMT, int CH>
+// NT: the policy of what is read and written once (kNT or 0).
+template <int FMT, int CH, int NT>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 
     NormRow<CH> next;
     int64_t row = row_of(0, (int)blockIdx.x, n);
-    norm_load(a, row, next);
+    norm_load<CH, NT>(a, row, next);
     for (int64_t step = 0; row < rows; step++) {
         uint32_t h[CH][4];
         float s0 = 0.0f, s1 = 0.0f;
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
             }
         }
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
-        norm_load(a, after, next);
+        norm_load<CH, NT>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
         const float rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), a.K, a.eps);
 
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
             if (a.h)
                 buf_store16(rh, 16 * c, make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]));
             if (a.q_h)
-                store_scales(rks, cast8<kFmtRoundUp>(rk, h[i], c), c, nb, quad);
+                store_scales(rks, cast8<kFmtRoundUp, NT>(rk, h[i], c), c, nb, quad);
             if (!a.y && !a.q_row)
                 continue;
             uint32_t y[4] = {norm_pair(h[i][0], rstd, wt[i].x), norm_pair(h[i][1], rstd, wt[i].y),
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
             if (a.y)
                 buf_store16(ry, 16 * c, make_uint4(y[0], y[1], y[2], y[3]));
             if (a.q_row) {
-                const uint32_t sb = cast8<FMT>(rq, y, c);
+                const uint32_t sb = cast8<FMT, NT>(rq, y, c);
                 if (tiled)
                     store_scales_tiled(a.s_row + (row >> 5) * 256, live ? sb : 0u, c, (uint32_t)row, RT,
                                        CT);
@@ -311,12 +313,13 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
         hipLaunchKernelGGL(norm_any_kernel<FMT>, grid, dim3(256), 0, s, a);
         return hipGetLastError();
     }
-    const int64_t most = 256 * (n.threads <= 64 ? 16 : 2048 / n.threads);
+    // 1024 threads a CU, whose next rows are on their way meanwhile (2048 x 8192: 21.4
+    // us, with twice as many that take two rows each 23.2, with half 26.2)
+    const int64_t most = 256 * (1024 / n.threads);
     const dim3 grid((unsigned)(rows < most ? rows : most)), block(n.threads);
-    switch (n.chunks) {
-    case 1: hipLaunchKernelGGL((norm_kernel<FMT, 1>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((norm_kernel<FMT, 2>), grid, block, 0, s, a); break;
-    }
+    auto *const kernel = n.chunks == 1 ? (a.stream ? norm_kernel<FMT, 1, kNT> : norm_kernel<FMT, 1, 0>)
+                                       : (a.stream ? norm_kernel<FMT, 2, kNT> : norm_kernel<FMT, 2, 0>);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -353,8 +356,10 @@ struct BackRow {
     float rstd;
 };
 
-template <int CH, bool CK>
-__device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, BackRow<CH, CK> &v)
+// Row `row` of a group of n threads, of which this is the tid-th.
+template <int CH, bool CK, int AUX>
+__device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, uint32_t tid, uint32_t n,
+                                          BackRow<CH, CK> &v)
 {
     const bool live = row < a.M;
     const int64_t at = live ? row * a.K : 0, len = live ? a.K : 0, nb = (a.K + 31) >> 5;
@@ -363,44 +368,55 @@ __device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, Ba
     v.rstd = live ? a.rstd[row] : 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        const uint32_t c = threadIdx.x + i * blockDim.x;
-        v.dy[i] = buf_load16(rd, 16 * c);
+        const uint32_t c = tid + i * n;
+        v.dy[i] = buf_load16<AUX>(rd, 16 * c);
         if constexpr (CK) {
-            v.q[i] = buf_load8(rh, 8 * c);
+            v.q[i] = buf_load8<AUX>(rh, 8 * c);
             v.s[i] = buf_load1(make_rsrc(a.s_h + (live ? row * nb : 0), 0, live ? nb : 0), c >> 2);
         } else {
-            v.h[i] = buf_load16(rh, 16 * c);
+            v.h[i] = buf_load16<AUX>(rh, 16 * c);
         }
         if (a.dres)
-            v.dres[i] = buf_load16(rr, 16 * c);
+            v.dres[i] = buf_load16<AUX>(rr, 16 * c);
     }
 }
 
-// T: the most threads of a workgroup (1024 leave 128 registers a lane, of which
-// the 8-bit copy's variant spills 4; 512 leave all that it wants).
-template <int CH, bool CK, int T>
-__global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a)
+// Groups of n threads, a whole number of waves each, take a row each; ROWS is
+// whether there may be more than one.  NT: what is read once is read non-temporally,
+// and dh written through the caches (SC1), for tensors that do not fit them; from
+// the 8-bit copy dh's default policy is faster (16384 x 7168: 143 us and 150, from
+// bf16 158 and 149).  T: the most threads of a workgroup (1024 leave 128 registers a
+// lane, of which the 8-bit copy's variant spills 4).
+template <int CH, bool CK, bool NT, bool ROWS, int T>
+__global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
 {
+    constexpr int IN = NT ? kNT : 0, OUT = NT && !CK ? kSC1 : 0;
     __shared__ float red[2][16];
-    const int waves = (int)blockDim.x >> 6, n = (int)gridDim.x;
+    __shared__ __align__(16) float4 parts[ROWS ? 2 * CH * T / 2 : 1];
+    const uint32_t n = ROWS ? blockDim.x / rows : blockDim.x;
+    const uint32_t group = ROWS ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / n)) : 0u;
+    const uint32_t tid = threadIdx.x - group * n;
+    const int waves = (int)n >> 6, step_rows = (int)gridDim.x * rows;
     uint32_t wt[CH][4];
     float dw[CH][8];
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         uint4 w = make_uint4(kOnes, kOnes, kOnes, kOnes);
         if (a.w)
-            w = buf_load16(make_rsrc(a.w, 0, 2 * a.K), 16 * (threadIdx.x + i * blockDim.x));
+            w = buf_load16(make_rsrc(a.w, 0, 2 * a.K), 16 * (tid + i * n));
         wt[i][0] = w.x; wt[i][1] = w.y; wt[i][2] = w.z; wt[i][3] = w.w;
 #pragma unroll
         for (int d = 0; d < 8; d++)
             dw[i][d] = 0.0f;
     }
     BackRow<CH, CK> next;
-    back_load(a, blockIdx.x, next);
+    int64_t row = (int64_t)blockIdx.x * rows + group;
+    back_load<CH, CK, IN>(a, row, tid, n, next);
     int step = 0;
-    for (int64_t row = blockIdx.x; row < a.M; row += n, step ^= 1) {
+    // all groups of the workgroup take as many turns: they share barriers
+    for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < a.M; row0 += step_rows, row += step_rows, step ^= 1) {
         const BackRow<CH, CK> v = next;
-        back_load(a, row + n, next);
+        back_load<CH, CK, IN>(a, row + step_rows, tid, n, next);
         __builtin_amdgcn_sched_barrier(0);
         float g[CH][8], xh[CH][8], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -438,8 +454,9 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a)
                 dw[i][2 * d + 1] = __builtin_fmaf(y1, xh[i][2 * d + 1], dw[i][2 * d + 1]);
             }
         }
-        const float c = block_sum(s0 + s1, red[step], waves) / (float)a.K;
-        const rsrc_t ro = make_rsrc(a.dh + row * a.K, 0, 2 * a.K);
+        const float c = block_sum(s0 + s1, red[step], waves, (int)group * waves) / (float)a.K;
+        const bool live = row < a.M;
+        const rsrc_t ro = make_rsrc(a.dh + (live ? row * a.K : 0), 0, live ? 2 * a.K : 0);
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t dr[4] = {v.dres[i].x, v.dres[i].y, v.dres[i].z, v.dres[i].w};
@@ -454,15 +471,41 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a)
                 }
                 o[d] = bf16x2_rne(e0, e1);
             }
-            buf_store16(ro, 16 * (threadIdx.x + i * blockDim.x), make_uint4(o[0], o[1], o[2], o[3]));
+            buf_store16<OUT>(ro, 16 * (tid + i * n), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
     if (!a.partials)
         return;
+    if constexpr (ROWS) {
+        // the groups' sums, halves to halves: group g adds that of g + half
+        for (int left = rows; left > 1;) {
+            const int half = (left + 1) / 2;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2 * CH; i++)
+                if ((int)group >= half && (int)group < left)
+                    parts[(i * (rows / 2) + group - half) * n + tid] =
+                        make_float4(dw[i / 2][4 * (i & 1)], dw[i / 2][4 * (i & 1) + 1],
+                                    dw[i / 2][4 * (i & 1) + 2], dw[i / 2][4 * (i & 1) + 3]);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2 * CH; i++)
+                if ((int)group < left - half) {
+                    const float4 p = parts[(i * (rows / 2) + group) * n + tid];
+                    dw[i / 2][4 * (i & 1)] += p.x;
+                    dw[i / 2][4 * (i & 1) + 1] += p.y;
+                    dw[i / 2][4 * (i & 1) + 2] += p.z;
+                    dw[i / 2][4 * (i & 1) + 3] += p.w;
+                }
+            left = half;
+        }
+        if (group != 0)
+            return;
+    }
     const rsrc_t rp = make_rsrc(a.partials + (int64_t)blockIdx.x * a.K, 0, 4 * a.K);
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        const uint32_t off = 32 * (threadIdx.x + i * blockDim.x);
+        const uint32_t off = 32 * (tid + i * n);
 #pragma unroll
         for (int q = 0; q < 2; q++)
             buf_store16(rp, off + 16 * q,
@@ -537,19 +580,21 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial
     }
 }
 
-template <int CH, int T>
-static void launch_back(const NormBackArgs &a, unsigned grid, unsigned block, hipStream_t s)
+template <int CH, bool ROWS, int T>
+static void launch_back(const NormBackArgs &a, unsigned grid, int threads, int rows, hipStream_t s)
 {
-    if (a.h)
-        hipLaunchKernelGGL((norm_back_kernel<CH, false, T>), dim3(grid), dim3(block), 0, s, a);
-    else
-        hipLaunchKernelGGL((norm_back_kernel<CH, true, T>), dim3(grid), dim3(block), 0, s, a);
+    auto *const kernel = a.h ? (a.stream ? norm_back_kernel<CH, false, true, ROWS, T>
+                                         : norm_back_kernel<CH, false, false, ROWS, T>)
+                             : (a.stream ? norm_back_kernel<CH, true, true, ROWS, T>
+                                         : norm_back_kernel<CH, true, false, ROWS, T>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads * rows), 0, s, a, rows);
 }
 
 hipError_t launch_norm_back(const NormBackArgs &a, hipStream_t s)
 {
     const NormShape n = norm_shape(a.K);
     const unsigned parts = (unsigned)norm_back_parts(a.M, a.K);
+    const int rows = norm_back_rows(n);
     switch (n.chunks) {
     case 0:
         hipLaunchKernelGGL(norm_back_any_kernel, dim3((unsigned)(a.M < 2048 ? a.M : 2048)), dim3(256), 0,
@@ -558,8 +603,11 @@ hipError_t launch_norm_back(const NormBackArgs &a, hipStream_t s)
             hipLaunchKernelGGL(norm_dweight_any_kernel, dim3((unsigned)((a.K + 255) / 256), parts),
                                dim3(256), 0, s, a);
         break;
-    case 1: launch_back<1, 512>(a, parts, n.threads, s); break;
-    default: (n.threads <= 512 ? launch_back<2, 512> : launch_back<2, 1024>)(a, parts, n.threads, s);
+    case 1: launch_back<1, true, 512>(a, parts, n.threads, rows, s); break;
+    default:
+        (rows > 1           ? launch_back<2, true, 512>
+         : n.threads <= 512 ? launch_back<2, false, 512>
+                            : launch_back<2, false, 1024>)(a, parts, n.threads, rows, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.partials)
