@@ -66,20 +66,60 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t t, int64_t ro
         x[i] = row < rows && e0 + i < E ? x[i] : -__builtin_inff();
 }
 
-__device__ __forceinline__ float exp_nonpos(float a) { return exp32_nonpos(a); }
-__device__ __forceinline__ double exp_nonpos(double a) { return exp(a); }
-__device__ __forceinline__ float rcp12(float d) { return rcp_1_2(d); }   // d in [1, 2]
-__device__ __forceinline__ double rcp12(double d) { return 1.0 / d; }
+// e^a for a <= 0 and 1 / d for 1 <= d <= 2 in the three arithmetics of the scores:
+// float; double as far as the keys' fixed point needs it, off by less than 2^-36
+// (Cody and Waite's reduction, the exponential's series to r^9, |r| <= ln(2) / 2;
+// the hardware's reciprocal, measured good to 2^-24, and one Newton step); and double.
+struct Quick {
+    typedef double type;
+    static __device__ __forceinline__ double exp_nonpos(double a)
+    {
+        const double c = __builtin_fmax(a, -1100.0);    // 0 already; NaN: the last select
+        const double n = __builtin_rint(c * 1.44269504088896340736);
+        double r = __builtin_fma(n, -0.69314718036912381649, c);   // ln 2 in 33 bits
+        r = __builtin_fma(n, -1.9082149292705877e-10, r);          // and the rest
+        double p = 1.0 / 362880.0;
+        p = __builtin_fma(p, r, 1.0 / 40320.0);
+        p = __builtin_fma(p, r, 1.0 / 5040.0);
+        p = __builtin_fma(p, r, 1.0 / 720.0);
+        p = __builtin_fma(p, r, 1.0 / 120.0);
+        p = __builtin_fma(p, r, 1.0 / 24.0);
+        p = __builtin_fma(p, r, 1.0 / 6.0);
+        p = __builtin_fma(p, r, 0.5);
+        p = __builtin_fma(p, r, 1.0);
+        p = __builtin_fma(p, r, 1.0);
+        p = __builtin_ldexp(p, (int)n);
+        return a != a ? a : p;
+    }
+    static __device__ __forceinline__ double rcp(double d)
+    {
+        const double r = __builtin_amdgcn_rcp(d);
+        return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    }
+};
+struct Single {
+    typedef float type;
+    static __device__ __forceinline__ float exp_nonpos(float a) { return exp32_nonpos(a); }
+    static __device__ __forceinline__ float rcp(float d) { return rcp_1_2(d); }
+};
+struct Full {
+    typedef double type;
+    static __device__ __forceinline__ double exp_nonpos(double a) { return exp(a); }
+    static __device__ __forceinline__ double rcp(double d) { return 1.0 / d; }
+};
 
-// Scores of a token in type F (ROW: one for each row of 16 lanes): softmax (those of -Inf logits 0, all of them where
-// every logit is) or sigmoid (q: 1 - p); NaN where they have no value.
-template <class F, int NPL, bool ROW>
-__device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, F (&p)[NPL], F (&q)[NPL])
+// Scores of a token in arithmetic A (ROW: one for each row of 16 lanes): softmax
+// (those of -Inf logits 0, all of them where every logit is) or sigmoid (q: 1 - p);
+// NaN where they have no value.
+template <class A, int NPL, bool ROW>
+__device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, typename A::type (&p)[NPL],
+                                          typename A::type (&q)[NPL])
 {
+    typedef typename A::type F;
     if (sigmoid) {
 #pragma unroll
         for (int i = 0; i < NPL; i++) {
-            const F z = (F)x[i], e = exp_nonpos(z < F(0) ? z : -z), r = rcp12(F(1) + e), s = e * r;
+            const F z = (F)x[i], e = A::exp_nonpos(z < F(0) ? z : -z), r = A::rcp(F(1) + e), s = e * r;
             const bool up = z >= F(0), nan = x[i] != x[i];
             p[i] = nan ? z : up ? r : s;
             q[i] = nan ? z : up ? s : r;
@@ -95,7 +135,7 @@ __device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, F
     F sum = F(0);
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
-        p[i] = exp_nonpos((F)x[i] - (F)m);
+        p[i] = A::exp_nonpos((F)x[i] - (F)m);
         sum += p[i];
     }
     sum = ROW ? row_sum(sum) : wave_sum(sum);
@@ -105,24 +145,41 @@ __device__ __forceinline__ void scores_of(const float (&x)[NPL], bool sigmoid, F
         p[i] *= inv;
 }
 
-// fp32 keys as unsigned numbers of the same order, -0 as 0; 0 stands for none (a
-// masked expert).
+// Keys as unsigned numbers of the same order; 0 stands for none (a masked expert).
+// Logits as keys: their bits, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float k)
 {
     const uint32_t u = bits_f32(k + 0.0f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float key_of(uint32_t o)
+// Scores plus a bias: fixed point, 2^-28 apart where no |bias| passes 1 (in general
+// 2^(e - 29) where 1 + |bias| < 2^e for all of them), between 1 and 2^30 + 1.  They
+// are cut, and the scores are off by far less than a step, so that keys 2 apart are
+// in order, and sums of two 3 apart.
+constexpr uint32_t kFixedZero = (1u << 29) + 1u;   // a key of 0
+struct Fixed {
+    double mul;
+    bool infinite;      // a bias of +Inf: 64 bits decide
+};
+template <int NPL, bool ROW>
+__device__ __forceinline__ Fixed fixed_point(const float (&bias)[NPL])
 {
-    return o == 0u ? -__builtin_inff() : f32_bits(o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
+    float most = 0.0f;
+    bool inf = false;
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        const float b = __builtin_fabsf(bias[i]);
+        inf |= bias[i] == __builtin_inff();
+        most = b < __builtin_inff() ? __builtin_fmaxf(most, b) : most;
+    }
+    most = ROW ? row_max(most) : wave_max(most);
+    const int e = __builtin_amdgcn_frexp_exp(1.0 + (double)most);   // 1 + most < 2^e
+    return Fixed{__builtin_ldexp(1.0, 29 - e), __builtin_amdgcn_ballot_w64(inf) != 0};
 }
-
-// How far two fp32 keys have to be apart for their order to be that of the exact
-// ones.  p <= 1 is off by less than 2^-19 (a softmax's exponent by 2^-24 |x - m|,
-// which e^-|x - m| makes less than 2^-25, the exponential, sum and quotient by 30
-// roundings at most), the bias' addition by 2^-24 of the key, the sum of a group's
-// two by twice that and its own rounding; two such values by 2^-17 + 2^-21 |key|.
-__device__ __forceinline__ float key_margin(float k) { return 0x1p-17f + 0x1p-21f * __builtin_fabsf(k); }
+__device__ __forceinline__ uint32_t order_of(double k, const Fixed &f)
+{
+    return (uint32_t)__builtin_fma(k, f.mul, (double)(kFixedZero - 1)) + 1u;
+}
 
 // What a token's choice leaves: lane j's expert (-1: none) of slot j; sure: that
 // keys off by their rounding give the same choice.
@@ -146,6 +203,45 @@ __device__ __forceinline__ void merge_step(uint32_t &best, uint32_t &second)
 {
     merge_two(best, second, dpp<CTRL>(0u, best), dpp<CTRL>(0u, second));
 }
+// Over groups of L lanes, a power of two up to 16.
+__device__ __forceinline__ void merge_lanes(int L, uint32_t &best, uint32_t &second)
+{
+    if (L >= 2)
+        merge_step<kDppXor1>(best, second);
+    if (L >= 4)
+        merge_step<kDppXor2>(best, second);
+    if (L >= 8)
+        merge_step<kDppHalfMirror>(best, second);
+    if (L >= 16)
+        merge_step<kDppMirror>(best, second);
+}
+
+// Score of a group whose two best keys (fixed point) are added; a missing one adds
+// nothing.  0 without any.
+__device__ __forceinline__ uint32_t pair_score(uint32_t first, uint32_t second)
+{
+    const uint32_t more = second != 0u ? second - kFixedZero : 0u;   // may be negative
+    return first != 0u ? first + more + (1u << 30) : 0u;
+}
+
+// Rank of the score `mine` of group `group` among all; get(g) is group g's.  CERT:
+// near tells whether another one is too close to be told apart.
+template <bool CERT, class G>
+__device__ __forceinline__ int group_rank(int groups, uint32_t mine, int group, G get, bool &near)
+{
+    int rank = 0, close = 0;
+    for (int g = 0; g < groups; g++) {
+        const uint32_t k = get(g);
+        if constexpr (CERT) {          // equal ones are close: their order does not matter
+            rank += k > mine ? 1 : 0;
+            close += k - mine + 2u <= 4u ? 1 : 0;
+        } else {
+            rank += k > mine || (k == mine && g < group) ? 1 : 0;
+        }
+    }
+    near = CERT && close > 1 && mine != 0u;
+    return rank;
+}
 
 // The best groups: key = 0 in the others.  False where groups are too close to be
 // told apart (CERT).  Where a group is a power of two of lanes, at most 16, these
@@ -165,14 +261,7 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs &a, int lane, uint32
 #pragma unroll
         for (int i = 0; i < NPL; i++)
             merge_two(first, second, key[i], 0u);
-        if (L >= 2)
-            merge_step<kDppXor1>(first, second);
-        if (L >= 4)
-            merge_step<kDppXor2>(first, second);
-        if (L >= 8)
-            merge_step<kDppHalfMirror>(first, second);
-        if (L >= 16)
-            merge_step<kDppMirror>(first, second);
+        merge_lanes(L, first, second);
         group = (int)(((uint32_t)(lane * NPL) * inv) >> 20);
     } else {
 #pragma unroll
@@ -183,20 +272,11 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs &a, int lane, uint32
             for (int j = 0; j < S; j++)
                 merge_two(first, second, keys[lane * S + j], 0u);
     }
-    float best = key_of(first);
-    if (a.pair && second != 0u)
-        best += key_of(second);
-    const float margin = key_margin(best);
-    int rank = 0, near = 0;
-    for (int g = 0; g < a.groups; g++) {
-        const float k = from_lane(best, lanes ? g * L : g);
-        if constexpr (CERT) {          // equal ones are near: their order does not matter
-            rank += k > best ? 1 : 0;
-            near += __builtin_fabsf(k - best) <= margin ? 1 : 0;
-        } else {
-            rank += k > best || (k == best && g < group) ? 1 : 0;
-        }
-    }
+    const uint32_t score = a.pair ? pair_score(first, second) : first;
+    bool near;
+    const int rank = group_rank<CERT>(
+        a.groups, score, group,
+        [&](int g) { return (uint32_t)__builtin_amdgcn_readlane((int)score, lanes ? g * L : g); }, near);
     if (lanes) {
         const bool kept = rank < a.top_groups;
 #pragma unroll
@@ -210,8 +290,7 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs &a, int lane, uint32
             key[i] = (kept >> (g & 63)) & 1 ? key[i] : 0u;
         }
     }
-    return !CERT ||
-           __builtin_amdgcn_ballot_w64(group < a.groups && (near > 1 || best == __builtin_inff())) == 0;
+    return !CERT || __builtin_amdgcn_ballot_w64(group < a.groups && near) == 0;
 }
 
 // A lane's keys, largest first and of equal ones the lowest index first; the
@@ -311,8 +390,7 @@ __device__ __forceinline__ Choice choose32(const RouteArgs &a, int lane, uint32_
     }
     if constexpr (CERT) {
         const uint32_t below = (uint32_t)__shfl_down((int)got, 1, 64);
-        const float k = key_of(got), n = key_of(lane == a.top - 1 ? extra : below);
-        const bool close = lane < a.top && got != 0u && !(k - n > key_margin(k));
+        const bool close = lane < a.top && got != 0u && got - (lane == a.top - 1 ? extra : below) < 2u;
         c.sure = c.sure && __builtin_amdgcn_ballot_w64(close) == 0;
     }
     return c;
@@ -326,7 +404,7 @@ __device__ __forceinline__ int choose64(const RouteArgs &a, int lane, double *ke
 {
     const double low = -__builtin_inf();
     double key[NPL], q[NPL];
-    scores_of<double, NPL, false>(x, a.sigmoid != 0, key, q);
+    scores_of<Full, NPL, false>(x, a.sigmoid != 0, key, q);
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
         const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
@@ -378,10 +456,42 @@ __device__ __forceinline__ int choose64(const RouteArgs &a, int lane, double *ke
     return expert;
 }
 
+// This lane's keys and scores (fp32) of a token, and whether one of them is NaN.
 // VALUE: keys are scores plus a bias, or a group's two are added; otherwise the
-// logits give the order.  Such scores are compared in fp32 first, and only where
-// two of those that decide are within their rounding of each other (about one
-// token in a hundred) once more in 64 bits.
+// logits give the order.  Such keys are compared in fixed point first, and only where
+// two of those that decide are within its steps of each other (about one token in
+// 10^5, and those with equal keys) once more in 64 bits.
+template <int NPL, bool VALUE, bool ROW>
+__device__ __forceinline__ bool keys_of(const RouteArgs &a, const float (&x)[NPL], const float (&bias)[NPL],
+                                        float (&p)[NPL], uint32_t (&key)[NPL], bool &infinite)
+{
+    bool nan = false;
+    infinite = false;
+    if constexpr (VALUE) {
+        const Fixed f = fixed_point<NPL, ROW>(bias);
+        infinite = f.infinite;
+        double s[NPL], q[NPL];
+        scores_of<Quick, NPL, ROW>(x, a.sigmoid != 0, s, q);
+#pragma unroll
+        for (int i = 0; i < NPL; i++) {
+            const double k = s[i] + (double)bias[i];
+            const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
+            p[i] = (float)s[i];
+            key[i] = masked ? 0u : order_of(k, f);
+            nan |= k != k;
+        }
+    } else {
+        float q[NPL];
+        scores_of<Single, NPL, ROW>(x, a.sigmoid != 0, p, q);
+#pragma unroll
+        for (int i = 0; i < NPL; i++) {
+            key[i] = x[i] == -__builtin_inff() ? 0u : order_of(x[i]);
+            nan |= (p[i] != p[i]) | (x[i] != x[i]);
+        }
+    }
+    return nan;
+}
+
 template <int NPL, bool VALUE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a)
 {
@@ -391,24 +501,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a)
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
     if (t >= a.T)
         return;
-    float x[NPL], p[NPL], q[NPL], bias[NPL];
+    float x[NPL], p[NPL], bias[NPL];
     load_logits<NPL>(a.logits, t, 1, 0, lane * NPL, a.E, a.f32, x);
     if (VALUE && a.bias)
         load_floats<NPL>(make_rsrc(a.bias, 0, 4 * a.E), lane * NPL, a.E % 4 == 0, bias);
     else
         for (int i = 0; i < NPL; i++)
             bias[i] = 0.0f;
-    scores_of<float, NPL, false>(x, a.sigmoid != 0, p, q);
     uint32_t key[NPL];
-    bool nan = false;
+    bool infinite;
+    const bool nan = keys_of<NPL, VALUE, false>(a, x, bias, p, key, infinite);
 #pragma unroll
-    for (int i = 0; i < NPL; i++) {
-        const float k = VALUE ? p[i] + bias[i] : x[i];
-        const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
-        key[i] = masked ? 0u : order_of(k);
-        nan |= (p[i] != p[i]) | (k != k);
+    for (int i = 0; i < NPL; i++)
         ps[wave][lane * NPL + i] = p[i];
-    }
     if (a.scores) {
 #pragma unroll
         for (int i = 0; i < NPL; i++)
@@ -420,7 +525,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a)
     if (!bad) {
         const Choice c = choose32<NPL, VALUE>(a, lane, reinterpret_cast<uint32_t *>(lds[wave]), key);
         expert = c.expert;
-        if (VALUE && !c.sure)
+        if (VALUE && (infinite || !c.sure))
             expert = choose64<NPL>(a, lane, lds[wave], x, bias);
     }
     __builtin_amdgcn_wave_barrier();
@@ -454,35 +559,19 @@ __device__ __forceinline__ bool keep_groups16(const RouteArgs &a, int lane, uint
 #pragma unroll
     for (int i = 0; i < NPL; i++)
         merge_two(first, second, key[i], 0u);
-    if (L >= 2)
-        merge_step<kDppXor1>(first, second);
-    if (L >= 4)
-        merge_step<kDppXor2>(first, second);
-    if (L >= 8)
-        merge_step<kDppHalfMirror>(first, second);
-    if (L >= 16)
-        merge_step<kDppMirror>(first, second);
-    float best = key_of(first);
-    if (a.pair && second != 0u)
-        best += key_of(second);
-    const float margin = key_margin(best);
-    int rank = 0, near = 0;
-    for (int g = 0; g < a.groups; g++) {
-        const float k = __shfl(best, (lane & 48) + g * L, 64);
-        if constexpr (CERT) {
-            rank += k > best ? 1 : 0;
-            near += __builtin_fabsf(k - best) <= margin ? 1 : 0;
-        } else {
-            rank += k > best || (k == best && g < group) ? 1 : 0;
-        }
-    }
+    merge_lanes(L, first, second);
+    const uint32_t score = a.pair ? pair_score(first, second) : first;
+    bool near;
+    const int rank = group_rank<CERT>(
+        a.groups, score, group,
+        [&](int g) { return (uint32_t)__shfl((int)score, (lane & 48) + g * L, 64); }, near);
     const bool kept = rank < a.top_groups;
 #pragma unroll
     for (int i = 0; i < NPL; i++)
         key[i] = kept ? key[i] : 0u;
     if constexpr (!CERT)
         return true;
-    const uint64_t m = __builtin_amdgcn_ballot_w64(group < a.groups && (near > 1 || best == __builtin_inff()));
+    const uint64_t m = __builtin_amdgcn_ballot_w64(group < a.groups && near);
     return ((m >> (lane & 48)) & 0xFFFF) == 0;
 }
 
@@ -499,24 +588,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route16_kernel(RouteArgs a)
     if (t0 >= a.T)
         return;
     const int64_t rows = a.T - t0 < 4 ? a.T - t0 : 4;
-    float x[NPL], p[NPL], q[NPL], bias[NPL];
+    float x[NPL], p[NPL], bias[NPL];
     load_logits<NPL>(a.logits, t0, rows, row, l * NPL, a.E, a.f32, x);
     if (VALUE && a.bias)
         load_floats<NPL>(make_rsrc(a.bias, 0, 4 * a.E), l * NPL, a.E % 4 == 0, bias);
     else
         for (int i = 0; i < NPL; i++)
             bias[i] = 0.0f;
-    scores_of<float, NPL, true>(x, a.sigmoid != 0, p, q);
     uint32_t key[NPL];
-    bool nan = false;
+    bool infinite;
+    const bool nan = keys_of<NPL, VALUE, true>(a, x, bias, p, key, infinite);
 #pragma unroll
-    for (int i = 0; i < NPL; i++) {
-        const float k = VALUE ? p[i] + bias[i] : x[i];
-        const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
-        key[i] = masked ? 0u : order_of(k);
-        nan |= (p[i] != p[i]) | (k != k);
+    for (int i = 0; i < NPL; i++)
         ps[wave][row][l * NPL + i] = p[i];
-    }
     if (a.scores && row < rows) {
 #pragma unroll
         for (int i = 0; i < NPL; i++)
@@ -527,9 +611,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route16_kernel(RouteArgs a)
 #pragma unroll
     for (int i = 0; i < NPL; i++)
         key[i] = bad ? 0u : key[i];
-    bool sure = true;
+    bool sure = !infinite;
     if (a.groups > 1)
-        sure = keep_groups16<NPL, VALUE>(a, lane, key);
+        sure = sure & keep_groups16<NPL, VALUE>(a, lane, key);
 
     // each lane's keys as sorted lists of up to 4; a round takes the largest head
     // of the row's lists, the first among equal ones, and moves that list up
@@ -576,9 +660,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route16_kernel(RouteArgs a)
     if constexpr (VALUE) {
         bool close = false;
         for (int s = l; s < a.top && s < n; s += 16) {
-            const float k = key_of(found[wave][row][s].y);
-            const float next = s + 1 < n ? key_of(found[wave][row][s + 1].y) : -__builtin_inff();
-            close |= !(k - next > key_margin(k));
+            const uint32_t next = s + 1 < n ? found[wave][row][s + 1].y : 0u;
+            close |= found[wave][row][s].y - next < 2u;
         }
         uint64_t again = __builtin_amdgcn_ballot_w64(!bad && (close || !sure) && row < rows);
         while (again) {
@@ -640,7 +723,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackA
     if (a.dscores)
         load_floats<NPL>(make_rsrc(a.dscores + t0 * a.E, 0, 4 * rows * a.E), row * a.E + l * NPL,
                          a.E % 4 == 0, dp);
-    scores_of<float, NPL, ROW>(x, a.sigmoid != 0, p, q);
+    scores_of<Single, NPL, ROW>(x, a.sigmoid != 0, p, q);
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
         ps[wave][row][l * NPL + i] = p[i];
