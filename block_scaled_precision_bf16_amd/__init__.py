@@ -933,9 +933,9 @@ def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, che
          "s_col": None, "q_h": None, "s_h": None}
     new = _new(x, out, stream)
     if residual is not None:
-        o["h"] = new("h", (M, K), BF16)
+        o["h"] = new("h", x.shape, BF16)
     if want_y or (want_y is None and not axis):
-        o["y"] = new("y", (M, K), BF16)
+        o["y"] = new("y", x.shape, BF16)
     o["rstd"] = new("rstd", (M,), F32)
     if axis:
         for name, (shape, dtype) in _mx_need(M, K, axis).items():

@@ -32,14 +32,14 @@ struct NormBackArgs {
     int stream;                    // too large for the caches: norm_streams
 };
 
-// Tensors of more than 64 MiB, which with the others of a call pass the 256 MiB
-// of the last cache: what is read or written once goes by non-temporal accesses,
-// which leaves that cache to h, the input of the column-wise casts (16384 x 7168
-// with both casts and the checkpoint 259 -> 209 us, 8192 x 7168 120 -> 102 us, 16384
-// x 8192 row-wise 182 -> 151 us).  4096 x 7168, 56 MiB, takes 60.5 and 61.1 us, and
-// smaller ones are still in the caches from the kernel that wrote them (1024 x 7168:
-// 24.0 and 29.9 us).
-inline bool norm_streams(int64_t M, int64_t K) { return 2 * M * K > int64_t(1) << 26; }
+// Tensors of 32 MiB and more, of which a call's do not stay in the 256 MiB of the
+// last cache until they are used again: what is read or written once goes by
+// non-temporal accesses (16384 x 7168 with both casts and the checkpoint 251 -> 247
+// us, 8192 x 7168 with both casts 125 -> 102 us, 4096 x 8192 row-wise 46 -> 41 us,
+// 2048 x 8192 23.6 -> 23.1 us; the backward of 4096 x 7168 50 -> 44 us).  Smaller ones
+// may still be there from the kernel that wrote them (backward of 1024 x 8192: 19.3
+// and 21.1 us).
+inline bool norm_streams(int64_t M, int64_t K) { return 2 * M * K >= int64_t(1) << 25; }
 
 // A row in registers: a lane holds 1 or 2 chunks of 8 elements, chunk c of the
 // row in lane c mod threads, in whole waves, 1024 threads at most.

@@ -76,8 +76,8 @@ struct Quick {
     {
         const double c = __builtin_fmax(a, -1100.0);    // 0 already; NaN: the last select
         const double n = __builtin_rint(c * 1.44269504088896340736);
-        double r = __builtin_fma(n, -0.69314718036912381649, c);   // ln 2 in 33 bits
-        r = __builtin_fma(n, -1.9082149292705877e-10, r);          // and the rest
+        double r = __builtin_fma(n, -0.693359375, c);              // 355/512
+        r = __builtin_fma(n, 2.1219444005469058277e-4, r);         // ln 2 - 355/512
         double p = 1.0 / 362880.0;
         p = __builtin_fma(p, r, 1.0 / 40320.0);
         p = __builtin_fma(p, r, 1.0 / 5040.0);

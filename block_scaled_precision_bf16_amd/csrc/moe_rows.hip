@@ -419,7 +419,7 @@ __device__ __forceinline__ int64_t row_of_slot(const CombineArgs &a, int64_t s)
     return r >= 0 && r < a.rows ? r : -1;
 }
 
-// E elements at p as fp32 (E = 8: one 16-byte access; E = 1), and back; NT: read
+// E elements at p as fp32 (E = 8: one 16-byte access; E = 1), and back; NT:
 // non-temporally.
 template <int E, bool NT = false>
 __device__ __forceinline__ void load_elems(const uint16_t *p, float (&v)[E])
@@ -437,13 +437,17 @@ __device__ __forceinline__ void load_elems(const uint16_t *p, float (&v)[E])
         v[0] = bf16_lo(p[0]);
     }
 }
-template <int E>
+template <int E, bool NT = false>
 __device__ __forceinline__ void store_elems(uint16_t *p, const float (&v)[E])
 {
-    if constexpr (E == 8)
-        *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
-                                                   bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-    else
+    if constexpr (E == 8) {
+        const u32x4_t u = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                           bf16x2_rne(v[6], v[7])};
+        if constexpr (NT)
+            __builtin_nontemporal_store(u, reinterpret_cast<u32x4_t *>(p));
+        else
+            *reinterpret_cast<u32x4_t *>(p) = u;
+    } else
         p[0] = (uint16_t)(bf16x2_rne(v[0], 0.0f) & 0xFFFFu);
 }
 
@@ -485,8 +489,9 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Rows of more than 64 MiB are read non-temporally, which leaves the caches to the
-// tokens' rows that are read once for each slot (16384 rows of 7168: 117 -> 97 us).
+// Rows of more than 64 MiB are read and written non-temporally, which leaves the
+// caches to the tokens' rows that are read once for each slot (16384 rows of 7168: 117
+// -> 108 us; 4100 of them 39 us both ways; 2050, still in the caches, 24.9 and 27.5 us).
 static bool rows_stream(const CombineArgs &a) { return 2 * a.rows * a.K > int64_t(1) << 26; }
 
 // A wave per slot, then a wave per 64 rows for those without a slot.
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a)
                     o[d] = wt * g[d];
                 }
                 if (mine)
-                    store_elems<E>(a.out + r * a.K + k, o);
+                    store_elems<E, NT>(a.out + r * a.K + k, o);
             }
             dot = wave_sum(dot);
         }
