@@ -42,16 +42,17 @@ struct NormBackArgs {
 inline bool norm_streams(int64_t M, int64_t K) { return 2 * M * K >= int64_t(1) << 25; }
 
 // A row in registers: a lane holds 1 or 2 chunks of 8 elements, chunk c of the
-// row in lane c mod threads, in whole waves, 1024 threads at most.
+// row in lane c mod threads, in whole waves, 1024 threads at most.  Longer rows are
+// read twice.
 constexpr int64_t kNormMaxRow = 16384;
 struct NormShape {
-    int chunks, threads;   // chunks per lane; 0: the two-pass kernel
+    int chunks, threads;   // chunks per lane; 0: the two-pass kernels
 };
 inline NormShape norm_shape(int64_t K)
 {
-    if (K % 8 != 0 || K > kNormMaxRow)
-        return NormShape{0, 256};
-    const int64_t n = K / 8;
+    if (K > kNormMaxRow)
+        return NormShape{0, 512};
+    const int64_t n = (K + 7) / 8;
     const int chunks = n <= 64 ? 1 : 2;
     return NormShape{chunks, (int)((n + 64 * chunks - 1) / (64 * chunks)) * 64};
 }

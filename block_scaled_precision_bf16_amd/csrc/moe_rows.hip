@@ -9,11 +9,12 @@
 // one launch; more, three: counts of each workgroup, sums over the workgroups and
 // experts, ranks.
 //
-// The rest moves rows and is bound by memory: 16-byte accesses wherever the rows'
-// length allows, several in flight for each lane.
+// The rest moves rows and is bound by memory: 16-byte accesses, at any byte, several
+// in flight for each lane.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"
+#include "rows.h"
 #include "wave.h"
 
 namespace mxk {
@@ -371,42 +372,44 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t s)
 
 // ---- rows ---------------------------------------------------------------------
 
-// Rows of out by workgroups, four pieces a thread under way at once; V: the widest
-// access that every row allows.
-template <class V>
-__global__ __launch_bounds__(256) void gather_kernel(GatherArgs a)
+// Rows of out, `per` threads (a power of two) to each, four pieces of 16 bytes a
+// thread under way at once; a row's last bytes one by one.
+__global__ __launch_bounds__(256) void gather_kernel(GatherArgs a, int per)
 {
-    const int64_t n = a.row_bytes / (int64_t)sizeof(V);
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const int64_t n = a.row_bytes >> 4;
+    const int rows = 256 / per, tid = (int)threadIdx.x & (per - 1);
+    for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < a.rows; r0 += (int64_t)gridDim.x * rows) {
+        const int64_t r = r0 + threadIdx.x / per;
+        if (r >= a.rows)
+            break;
         const int32_t slot = a.slots[r];
         const bool live = slot >= 0 && slot < a.T * a.top;
-        V *const o = reinterpret_cast<V *>(a.out + r * a.row_bytes);
-        const V *const x =
-            reinterpret_cast<const V *>(a.x + (live ? (int64_t)(slot / a.top) * a.row_bytes : 0));
-        for (int64_t i = threadIdx.x; i < n; i += 4 * 256) {
-            V v[4];
+        uint8_t *const ob = a.out + r * a.row_bytes;
+        const uint8_t *const xb = a.x + (live ? (int64_t)(slot / a.top) * a.row_bytes : 0);
+        u32x4_bytes *const o = reinterpret_cast<u32x4_bytes *>(ob);
+        const u32x4_bytes *const x = reinterpret_cast<const u32x4_bytes *>(xb);
+        for (int64_t i = tid; i < n; i += 4 * per) {
+            u32x4_t v[4];
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                v[j] = live && i + 256 * j < n ? x[i + 256 * j] : V{};
+                v[j] = live && i + per * j < n ? (u32x4_t)x[i + per * j] : u32x4_t{};
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                if (i + 256 * j < n)
-                    __builtin_nontemporal_store(v[j], &o[i + 256 * j]);
+                if (i + per * j < n)
+                    __builtin_nontemporal_store((u32x4_bytes)v[j], &o[i + per * j]);
         }
+        for (int64_t i = 16 * n + tid; i < a.row_bytes; i += per)
+            ob[i] = live ? xb[i] : (uint8_t)0;
     }
 }
 
 hipError_t launch_gather(const GatherArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.rows < 65536 ? a.rows : 65536));
-    if (a.row_bytes % 16 == 0)
-        hipLaunchKernelGGL(gather_kernel<u32x4_t>, grid, dim3(256), 0, s, a);
-    else if (a.row_bytes % 4 == 0)
-        hipLaunchKernelGGL(gather_kernel<uint32_t>, grid, dim3(256), 0, s, a);
-    else if (a.row_bytes % 2 == 0)
-        hipLaunchKernelGGL(gather_kernel<uint16_t>, grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(gather_kernel<uint8_t>, grid, dim3(256), 0, s, a);
+    int per = 1;
+    while (per < 256 && 16 * (int64_t)per < a.row_bytes)
+        per *= 2;
+    const int64_t blocks = (a.rows + 256 / per - 1) / (256 / per);
+    hipLaunchKernelGGL(gather_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, a, per);
     return hipGetLastError();
 }
 
@@ -419,73 +422,60 @@ __device__ __forceinline__ int64_t row_of_slot(const CombineArgs &a, int64_t s)
     return r >= 0 && r < a.rows ? r : -1;
 }
 
-// E elements at p as fp32 (E = 8: one 16-byte access; E = 1), and back; NT:
-// non-temporally.
-template <int E, bool NT = false>
-__device__ __forceinline__ void load_elems(const uint16_t *p, float (&v)[E])
+__device__ __forceinline__ void widen(uint4 u, float (&v)[8])
 {
-    if constexpr (E == 8) {
-        const u32x4_t *const q = reinterpret_cast<const u32x4_t *>(p);
-        const u32x4_t u = NT ? __builtin_nontemporal_load(q) : *q;
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int d = 0; d < 4; d++) {
-            v[2 * d] = bf16_lo(w[d]);
-            v[2 * d + 1] = bf16_hi(w[d]);
-        }
-    } else {
-        v[0] = bf16_lo(p[0]);
+    for (int d = 0; d < 4; d++) {
+        v[2 * d] = bf16_lo(w[d]);
+        v[2 * d + 1] = bf16_hi(w[d]);
     }
 }
-template <int E, bool NT = false>
-__device__ __forceinline__ void store_elems(uint16_t *p, const float (&v)[E])
+__device__ __forceinline__ uint4 narrow(const float (&v)[8])
 {
-    if constexpr (E == 8) {
-        const u32x4_t u = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
-                           bf16x2_rne(v[6], v[7])};
-        if constexpr (NT)
-            __builtin_nontemporal_store(u, reinterpret_cast<u32x4_t *>(p));
-        else
-            *reinterpret_cast<u32x4_t *>(p) = u;
-    } else
-        p[0] = (uint16_t)(bf16x2_rne(v[0], 0.0f) & 0xFFFFu);
+    return make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                      bf16x2_rne(v[6], v[7]));
 }
 
-// One group of E elements of one token per thread.
-template <int E>
+// One chunk of 8 elements of one token per thread; four rows' loads under way.
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int64_t parts)
 {
     for (int64_t b = blockIdx.x; b < a.T * parts; b += gridDim.x) {
         const int64_t t = b / parts, c = (b - t * parts) * 256 + threadIdx.x;
-        if (c * E >= a.K)
+        if (8 * c >= a.K)
             continue;
-        float acc[E];
+        float acc[8] = {};
+        for (int j0 = 0; j0 < a.top; j0 += 4) {
+            int64_t r[4];
+            float w[4];
+            uint4 y[4];
 #pragma unroll
-        for (int d = 0; d < E; d++)
-            acc[d] = 0.0f;
-        for (int j = 0; j < a.top; j++) {
-            const int64_t s = t * a.top + j, r = row_of_slot(a, s);
-            if (r < 0)
-                continue;
-            const float w = a.weights ? a.weights[s] : 1.0f;
-            float v[E];
-            load_elems<E>(a.y + r * a.K + c * E, v);
+            for (int j = 0; j < 4; j++) {
+                const int64_t s = t * a.top + j0 + j;
+                r[j] = j0 + j < a.top ? row_of_slot(a, s) : -1;
+                w[j] = a.weights && r[j] >= 0 ? a.weights[s] : 1.0f;
+            }
 #pragma unroll
-            for (int d = 0; d < E; d++)
-                acc[d] = __builtin_fmaf(w, v[d], acc[d]);
+            for (int j = 0; j < 4; j++)
+                y[j] = load_chunk<false>(a.y + (r[j] < 0 ? 0 : r[j]) * a.K, c, r[j] < 0 ? 0 : a.K);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float v[8];
+                widen(y[j], v);
+#pragma unroll
+                for (int d = 0; d < 8; d++)
+                    acc[d] = r[j] < 0 ? acc[d] : __builtin_fmaf(w[j], v[d], acc[d]);
+            }
         }
-        store_elems<E>(a.out + t * a.K + c * E, acc);
+        store_chunk<false>(a.out + t * a.K, c, a.K, narrow(acc));
     }
 }
 
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s)
 {
-    const int64_t per = a.K % 8 == 0 ? 2048 : 256, parts = (a.K + per - 1) / per;
+    const int64_t parts = (a.K + 2047) / 2048;
     const dim3 grid((unsigned)(a.T * parts < (1 << 22) ? a.T * parts : 1 << 22));
-    if (a.K % 8 == 0)
-        hipLaunchKernelGGL(combine_kernel<8>, grid, dim3(256), 0, s, a, parts);
-    else
-        hipLaunchKernelGGL(combine_kernel<1>, grid, dim3(256), 0, s, a, parts);
+    hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, s, a, parts);
     return hipGetLastError();
 }
 
@@ -494,60 +484,75 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s)
 // -> 108 us; 4100 of them 39 us both ways; 2050, still in the caches, 24.9 and 27.5 us).
 static bool rows_stream(const CombineArgs &a) { return 2 * a.rows * a.K > int64_t(1) << 26; }
 
-// A wave per slot, then a wave per 64 rows for those without a slot.
-template <int E, bool NT>
-__global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a)
+// First a wave per kZeroRows rows for those without a slot (first, and few to a wave:
+// the rows behind the last expert's lie together, and a wave that has 64 of them
+// ends long after all others), then a wave per slot.
+constexpr int kZeroRows = 8;
+
+template <bool NT>
+__global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a, int64_t zeros)
 {
     const int lane = (int)threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), N = a.T * a.top;
-    if (w < N) {
-        const int64_t r = row_of_slot(a, w), t = w / a.top;
-        float dot = 0.0f;
-        if (r >= 0) {
-            const float wt = a.weights ? a.weights[w] : 1.0f;
-            const bool mine = !a.slots || a.slots[r] == w;   // the row's only writer
-            for (int64_t k = lane * E; k < a.K; k += 64 * E) {
-                float g[E], y[E], o[E];
-                load_elems<E>(a.dout + t * a.K + k, g);
-                load_elems<E, NT>(a.y + r * a.K + k, y);
-#pragma unroll
-                for (int d = 0; d < E; d++) {
-                    dot = __builtin_fmaf(g[d], y[d], dot);
-                    o[d] = wt * g[d];
-                }
-                if (mine)
-                    store_elems<E, NT>(a.out + r * a.K + k, o);
-            }
-            dot = wave_sum(dot);
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), s = w - zeros;
+    if (s < 0) {
+        const int64_t r0 = w * kZeroRows;
+        const bool empty = lane < kZeroRows && r0 + lane < a.rows && a.slots[r0 + lane] == -1;
+        for (uint64_t m = __builtin_amdgcn_ballot_w64(empty); m; m &= m - 1) {
+            uint16_t *const out = a.out + (r0 + __builtin_ctzll(m)) * a.K;
+            int64_t c = lane;
+            for (; 8 * c + 8 <= a.K; c += 64)
+                put_chunk<NT>(out, c, make_uint4(0u, 0u, 0u, 0u));
+            if (8 * c < a.K)
+                store_chunk<false>(out, c, a.K, make_uint4(0u, 0u, 0u, 0u));
         }
-        if (a.dweights && lane == 0)
-            a.dweights[w] = dot;
         return;
     }
-    if (!a.slots)
+    if (s >= a.T * a.top)
         return;
-    const int64_t r0 = (w - N) * 64;
-    const bool empty = r0 + lane < a.rows && a.slots[r0 + lane] == -1;
-    uint64_t m = __builtin_amdgcn_ballot_w64(empty);
-    float zero[E] = {};
-    while (m) {
-        const int64_t r = r0 + __builtin_ctzll(m);
-        m &= m - 1;
-        for (int64_t k = lane * E; k < a.K; k += 64 * E)
-            store_elems<E>(a.out + r * a.K + k, zero);
+    const int64_t r = row_of_slot(a, s), t = s / a.top;
+    float dot = 0.0f;
+    if (r >= 0) {
+        const float wt = a.weights ? a.weights[s] : 1.0f;
+        const bool mine = !a.slots || a.slots[r] == s;   // the row's only writer
+        const uint16_t *const gr = a.dout + t * a.K, *const yr = a.y + r * a.K;
+        uint16_t *const out = a.out + r * a.K;
+        const auto chunk = [&](uint4 gw, uint4 yw) {
+            float g[8], y[8], o[8];
+            widen(gw, g);
+            widen(yw, y);
+#pragma unroll
+            for (int d = 0; d < 8; d++) {
+                dot = __builtin_fmaf(g[d], y[d], dot);
+                o[d] = wt * g[d];
+            }
+            return narrow(o);
+        };
+        // whole chunks, then the rest
+        int64_t c = lane;
+        for (; 8 * c + 8 <= a.K; c += 64) {
+            const uint4 o = chunk(whole_chunk<false>(gr, c), whole_chunk<NT>(yr, c));
+            if (mine)
+                put_chunk<NT>(out, c, o);
+        }
+        if (8 * c < a.K) {
+            const uint4 o = chunk(load_chunk<false>(gr, c, a.K), load_chunk<false>(yr, c, a.K));
+            if (mine)
+                store_chunk<false>(out, c, a.K, o);
+        }
+        dot = wave_sum(dot);
     }
+    if (a.dweights && lane == 0)
+        a.dweights[s] = dot;
 }
 
 hipError_t launch_combine_back(const CombineArgs &a, hipStream_t s)
 {
-    const int64_t waves = a.T * a.top + (a.slots ? (a.rows + 63) / 64 : 0);
-    const dim3 grid((unsigned)((waves + 3) / 4));
-    if (a.K % 8 != 0)
-        hipLaunchKernelGGL((combine_back_kernel<1, false>), grid, dim3(256), 0, s, a);
-    else if (rows_stream(a))
-        hipLaunchKernelGGL((combine_back_kernel<8, true>), grid, dim3(256), 0, s, a);
+    const int64_t zeros = a.slots ? (a.rows + kZeroRows - 1) / kZeroRows : 0;
+    const dim3 grid((unsigned)((zeros + a.T * a.top + 3) / 4));
+    if (rows_stream(a))
+        hipLaunchKernelGGL(combine_back_kernel<true>, grid, dim3(256), 0, s, a, zeros);
     else
-        hipLaunchKernelGGL((combine_back_kernel<8, false>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL(combine_back_kernel<false>, grid, dim3(256), 0, s, a, zeros);
     return hipGetLastError();
 }
 

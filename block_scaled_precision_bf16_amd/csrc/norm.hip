@@ -18,6 +18,7 @@
 #include "device_math.h"
 #include "launch_norm.h"
 #include "mx_cast.h"
+#include "rows.h"
 #include "wave.h"
 
 namespace mxk {
@@ -76,10 +77,10 @@ __device__ __forceinline__ uint32_t block_mag(const uint32_t (&m)[4])
     return max_xor2(max_xor1(lo > hi ? lo : hi));
 }
 
-// MXFP8 of a lane's 8 elements of row r, chunk c: codes to q (the row's
-// descriptor), the scale byte returned.
-template <int FMT, int AUX>
-__device__ __forceinline__ uint32_t cast8(rsrc_t q, const uint32_t (&w)[4], uint32_t c)
+// MXFP8 of a lane's 8 elements, chunk c of a row: codes to q, the scale byte
+// returned.
+template <int FMT, int AUX, bool AL>
+__device__ __forceinline__ uint32_t cast8(const Row<AL, uint8_t> &q, const uint32_t (&w)[4], uint32_t c)
 {
     uint32_t m[4];
 #pragma unroll
@@ -89,7 +90,7 @@ __device__ __forceinline__ uint32_t cast8(rsrc_t q, const uint32_t (&w)[4], uint
     uint2 o = encode8_row<FMT>(w, m, sb);
     if (sb == 0xFFu)
         o.x = o.y = 0x7F7F7F7Fu;
-    buf_store8<AUX>(q, 8 * c, o);
+    row_store<AUX>(q, c, o);
     return sb;
 }
 
@@ -130,175 +131,168 @@ __device__ __forceinline__ void store_scales_tiled(uint8_t *s, uint32_t sb, uint
                                       ((b & 7) >> 1)) = (uint16_t)two;
 }
 
+// Where a row's outputs go: none of them past the last row.
+template <bool AL>
+struct NormOut {
+    Row<AL, uint16_t> h, y;
+    Row<AL, uint8_t> q, k;          // codes of y, of h
+    rsrc_t s, ks;                   // their compact scales
+};
+
+template <bool AL>
+__device__ __forceinline__ NormOut<AL> norm_out(const NormArgs &a, int64_t row, uint32_t nb)
+{
+    const bool live = row < a.M;
+    const int64_t at = row * a.K, len = live ? a.K : 0, sat = live ? row * nb : 0;
+    NormOut<AL> o;
+    o.h = row_at<AL>(a.h, at, a.h ? len : 0);
+    o.y = row_at<AL>(a.y, at, a.y ? len : 0);
+    o.q = row_at<AL>(a.q_row, at, a.q_row ? len : 0);
+    o.k = row_at<AL>(a.q_h, at, a.q_h ? len : 0);
+    o.s = make_rsrc(a.s_row + sat, 0, a.s_row && live && !a.tiled ? nb : 0);
+    o.ks = make_rsrc(a.s_h + sat, 0, a.s_h && live ? nb : 0);
+    return o;
+}
+
+// The outputs of chunk c of a row; every lane of a wave takes part.
+template <int FMT, int NT, bool AL>
+__device__ __forceinline__ void norm_write(const NormArgs &a, const NormOut<AL> &o, int64_t row, uint32_t c,
+                                           uint32_t nb, const uint32_t (&h)[4], float rstd, uint4 wt)
+{
+    const bool quad = (nb & 3) == 0;
+    if (a.q_h)
+        store_scales(o.ks, cast8<kFmtRoundUp, NT>(o.k, h, c), c, nb, quad);
+    if (!a.y && !a.q_row)
+        return;
+    const uint32_t y[4] = {norm_pair(h[0], rstd, wt.x), norm_pair(h[1], rstd, wt.y),
+                           norm_pair(h[2], rstd, wt.z), norm_pair(h[3], rstd, wt.w)};
+    if (a.y)
+        row_store<0>(o.y, c, make_uint4(y[0], y[1], y[2], y[3]));
+    if (!a.q_row)
+        return;
+    const uint32_t sb = cast8<FMT, NT>(o.q, y, c);
+    const uint32_t RT = (uint32_t)((a.M + 31) >> 5);
+    if (a.tiled)
+        store_scales_tiled(a.s_row + (row >> 5) * 256, row < a.M ? sb : 0u, c, (uint32_t)row, RT, (nb + 7) >> 3);
+    else
+        store_scales(o.s, sb, c, nb, quad);
+}
+
+__device__ __forceinline__ void norm_sum(const uint32_t (&x)[4], const uint4 *r, uint32_t (&h)[4], float &s0,
+                                         float &s1)
+{
+    const uint32_t rr[4] = {r ? r->x : 0u, r ? r->y : 0u, r ? r->z : 0u, r ? r->w : 0u};
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        h[d] = r ? add_pair(x[d], rr[d]) : x[d];
+        s0 = __builtin_fmaf(bf16_lo(h[d]), bf16_lo(h[d]), s0);
+        s1 = __builtin_fmaf(bf16_hi(h[d]), bf16_hi(h[d]), s1);
+    }
+}
+
 template <int CH>
 struct NormRow {
     uint4 x[CH], r[CH];
 };
 
-template <int CH, int AUX>
+// A row outside the tensor reads as zeros, without traffic.
+template <int CH, int AUX, bool AL>
 __device__ __forceinline__ void norm_load(const NormArgs &a, int64_t row, NormRow<CH> &v)
 {
-    // a row outside the tensor reads as zeros, without traffic
-    const bool live = row < a.M;
-    const rsrc_t rx = make_rsrc(a.x, 0, 0), none = rx;
-    const rsrc_t dx = live ? make_rsrc(a.x + row * a.K, 0, 2 * a.K) : none;
-    const rsrc_t dr = live && a.res ? make_rsrc(a.res + row * a.K, 0, 2 * a.K) : none;
+    const int64_t at = row * a.K, len = row < a.M ? a.K : 0;
+    const Row<AL, const uint16_t> x = row_at<AL>(a.x, at, len), r = row_at<AL>(a.res, at, a.res ? len : 0);
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        const uint32_t off = 16 * (threadIdx.x + i * blockDim.x);
-        v.x[i] = buf_load16<AUX>(dx, off);
+        v.x[i] = row_load<AUX>(x, threadIdx.x + i * blockDim.x);
         if (a.res)
-            v.r[i] = buf_load16<AUX>(dr, off);
+            v.r[i] = row_load<AUX>(r, threadIdx.x + i * blockDim.x);
     }
 }
 
-// NT: the policy of what is read and written once (kNT or 0).
-template <int FMT, int CH, int NT>
+// Rows that the tile layout pads to have scales of 0.
+__device__ __forceinline__ int64_t norm_rows(const NormArgs &a)
+{
+    return a.tiled && a.s_row ? (a.M + 31) & ~(int64_t)31 : a.M;
+}
+
+// NT: the policy of what is read and written once (kNT or 0); AL: K is a multiple of
+// 8.
+template <int FMT, int CH, int NT, bool AL>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
     const int waves = (int)blockDim.x >> 6, n = (int)gridDim.x;
-    const uint32_t nb = (uint32_t)((a.K + 31) >> 5), RT = (uint32_t)((a.M + 31) >> 5), CT = (nb + 7) >> 3;
-    const bool tiled = a.tiled && a.s_row, quad = (nb & 3) == 0;
-    const int64_t rows = tiled ? 32 * (int64_t)RT : a.M;   // of padding, scales of 0
+    const uint32_t nb = (uint32_t)((a.K + 31) >> 5);
+    const int64_t rows = norm_rows(a);
+    const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     uint4 wt[CH];
 #pragma unroll
     for (int i = 0; i < CH; i++)
-        wt[i] = a.w ? buf_load16(make_rsrc(a.w, 0, 2 * a.K), 16 * (threadIdx.x + i * blockDim.x))
-                    : make_uint4(kOnes, kOnes, kOnes, kOnes);
+        wt[i] = a.w ? row_load<0>(w, threadIdx.x + i * blockDim.x) : make_uint4(kOnes, kOnes, kOnes, kOnes);
 
     NormRow<CH> next;
     int64_t row = row_of(0, (int)blockIdx.x, n);
-    norm_load<CH, NT>(a, row, next);
+    norm_load<CH, NT, AL>(a, row, next);
     for (int64_t step = 0; row < rows; step++) {
         uint32_t h[CH][4];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
-            h[i][0] = next.x[i].x; h[i][1] = next.x[i].y; h[i][2] = next.x[i].z; h[i][3] = next.x[i].w;
-            if (a.res) {
-                h[i][0] = add_pair(h[i][0], next.r[i].x);
-                h[i][1] = add_pair(h[i][1], next.r[i].y);
-                h[i][2] = add_pair(h[i][2], next.r[i].z);
-                h[i][3] = add_pair(h[i][3], next.r[i].w);
-            }
-#pragma unroll
-            for (int d = 0; d < 4; d++) {
-                s0 = __builtin_fmaf(bf16_lo(h[i][d]), bf16_lo(h[i][d]), s0);
-                s1 = __builtin_fmaf(bf16_hi(h[i][d]), bf16_hi(h[i][d]), s1);
-            }
+            const uint32_t x[4] = {next.x[i].x, next.x[i].y, next.x[i].z, next.x[i].w};
+            norm_sum(x, a.res ? &next.r[i] : nullptr, h[i], s0, s1);
         }
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
-        norm_load<CH, NT>(a, after, next);
+        norm_load<CH, NT, AL>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
         const float rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), a.K, a.eps);
-
-        const bool live = row < a.M;
-        const int64_t at = live ? row * a.K : 0, len = live ? a.K : 0;
-        if (live && threadIdx.x == 0)
+        if (row < a.M && threadIdx.x == 0)
             a.rstd[row] = rstd;
-        const rsrc_t rh = make_rsrc(a.h + at, 0, a.h ? 2 * len : 0);
-        const rsrc_t ry = make_rsrc(a.y + at, 0, a.y ? 2 * len : 0);
-        const rsrc_t rq = make_rsrc(a.q_row + at, 0, a.q_row ? len : 0);
-        const rsrc_t rk = make_rsrc(a.q_h + at, 0, a.q_h ? len : 0);
-        const rsrc_t rks = make_rsrc(a.s_h + (live ? row * nb : 0), 0, a.s_h && live ? nb : 0);
-        const rsrc_t rs = make_rsrc(a.s_row + (live ? row * nb : 0), 0, live && !tiled ? nb : 0);
+        const NormOut<AL> o = norm_out<AL>(a, row, nb);
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t c = threadIdx.x + i * blockDim.x;
             if (a.h)
-                buf_store16(rh, 16 * c, make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]));
-            if (a.q_h)
-                store_scales(rks, cast8<kFmtRoundUp, NT>(rk, h[i], c), c, nb, quad);
-            if (!a.y && !a.q_row)
-                continue;
-            uint32_t y[4] = {norm_pair(h[i][0], rstd, wt[i].x), norm_pair(h[i][1], rstd, wt[i].y),
-                             norm_pair(h[i][2], rstd, wt[i].z), norm_pair(h[i][3], rstd, wt[i].w)};
-            if (a.y)
-                buf_store16(ry, 16 * c, make_uint4(y[0], y[1], y[2], y[3]));
-            if (a.q_row) {
-                const uint32_t sb = cast8<FMT, NT>(rq, y, c);
-                if (tiled)
-                    store_scales_tiled(a.s_row + (row >> 5) * 256, live ? sb : 0u, c, (uint32_t)row, RT,
-                                       CT);
-                else
-                    store_scales(rs, sb, c, nb, quad);
-            }
+                row_store<0>(o.h, c, make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]));
+            norm_write<FMT, NT, AL>(a, o, row, c, nb, h[i], rstd, wt[i]);
         }
         row = after;
     }
 }
 
-// Any row length, rows at any byte: lane by lane over the columns, in two passes
-// over the row (the second finds it in the caches).  Columns past K count as 0.
+// Rows of any length, in two passes: the second finds the row in the caches (and
+// each thread what it wrote itself).
 template <int FMT>
-__device__ __forceinline__ void any_cast(uint8_t *q, uint32_t y, int64_t k, int64_t K, uint32_t &sb)
-{
-    uint32_t mag = y & 0x7FFFu;
-    mag = max_xor2(max_xor1(mag));
-    const uint32_t a = dpp<kDppHalfMirror>(0u, mag);
-    mag = mag > a ? mag : a;
-    const uint32_t b = dpp<kDppMirror>(0u, mag);
-    mag = mag > b ? mag : b;
-    const uint32_t c = (uint32_t)__shfl_xor((int)mag, 16, 64);
-    mag = mag > c ? mag : c;
-    sb = scale_byte<FMT>(mag);
-    const uint32_t code = mx_pair<FMT, false>(y, y & 0x7FFFu, sat_limit2<FMT>(sb), e8m0_operand(sb), 0u);
-    if (k < K)
-        q[k] = (uint8_t)(sb == 0xFFu ? 0x7Fu : code);
-}
-
-template <int FMT>
-__global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
+__global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
-    const int64_t K = a.K, nb = (K + 31) >> 5, RT = (a.M + 31) >> 5, CT = (nb + 7) >> 3;
-    const bool tiled = a.tiled && a.s_row;
-    const int64_t rows = tiled ? 32 * RT : a.M;
+    const uint32_t nb = (uint32_t)((a.K + 31) >> 5), chunks = (uint32_t)((a.K + 7) >> 3);
+    // whole waves, which cover the tile layout's padding blocks too
+    const uint32_t upto = (chunks + 63) & ~63u;
+    const int64_t rows = norm_rows(a);
+    const Row<false, const uint16_t> w = row_at<false>(a.w, 0, a.w ? a.K : 0);
     int step = 0;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, step ^= 1) {
-        const bool live = row < a.M;
-        const int64_t at = row * K;
-        float s = 0.0f;
-        for (int64_t k = threadIdx.x; live && k < K; k += 256) {
-            uint32_t v = a.x[at + k];
-            if (a.res) {
-                v = bf16x2_rne(bf16_lo(v) + bf16_lo(a.res[at + k]), 0.0f) & 0xFFFFu;
-                a.h[at + k] = (uint16_t)v;
-            }
-            s = __builtin_fmaf(bf16_lo(v), bf16_lo(v), s);
+        const int64_t at = row * a.K, len = row < a.M ? a.K : 0;
+        const Row<false, const uint16_t> x = row_at<false>(a.x, at, len), r = row_at<false>(a.res, at, a.res ? len : 0);
+        const NormOut<false> o = norm_out<false>(a, row, nb);
+        float s0 = 0.0f, s1 = 0.0f;
+        for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
+            const uint4 v = row_load<0>(x, c), q = row_load<0>(r, c);
+            const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+            norm_sum(xw, a.res ? &q : nullptr, h, s0, s1);
+            if (a.h)
+                row_store<0>(o.h, c, make_uint4(h[0], h[1], h[2], h[3]));
         }
-        const float rstd = rstd_of(block_sum(s, red[step], 4), K, a.eps);
-        if (live && threadIdx.x == 0)
+        const float rstd = rstd_of(block_sum(s0 + s1, red[step], 8), a.K, a.eps);
+        if (row < a.M && threadIdx.x == 0)
             a.rstd[row] = rstd;
-        const uint16_t *src = a.res ? a.h : a.x;
-        // whole blocks of 32 lanes, and the tile layout's padding blocks
-        const int64_t upto = tiled ? 256 * CT : 32 * nb;
-        for (int64_t k = threadIdx.x; k < ((upto + 63) & ~63); k += 256) {
-            const bool in = live && k < K;
-            const uint32_t h = in ? src[at + k] : 0u, wt = !a.w ? 0x3F80u : in ? a.w[k] : 0u;
-            const uint32_t y = in ? norm_pair(h, rstd, wt) & 0xFFFFu : 0u;
-            const int64_t b = k >> 5;
-            uint32_t sb;
-            if (a.y && in)
-                a.y[at + k] = (uint16_t)y;
-            if (a.q_h) {
-                any_cast<kFmtRoundUp>(a.q_h + at, h, k, live ? K : 0, sb);
-                if (live && (k & 31) == 0 && b < nb)
-                    a.s_h[row * nb + b] = (uint8_t)sb;
-            }
-            if (!a.q_row)
-                continue;
-            any_cast<FMT>(a.q_row + at, y, k, live ? K : 0, sb);
-            if ((k & 31) != 0)
-                continue;
-            if (tiled) {
-                if (b < 8 * CT)
-                    a.s_row[((b >> 3) * RT + (row >> 5)) * 256 + 4 * (32 * (b & 1) + (row & 31)) +
-                            ((b & 7) >> 1)] = (uint8_t)sb;
-            } else if (live && b < nb) {
-                a.s_row[row * nb + b] = (uint8_t)sb;
-            }
+        const Row<false, const uint16_t> hr = a.h ? row_at<false>((const uint16_t *)a.h, at, len) : x;
+        for (uint32_t c = threadIdx.x; c < upto; c += 512) {
+            const uint4 v = row_load<0>(hr, c);
+            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+            norm_write<FMT, 0, false>(a, o, row, c, nb, h, rstd,
+                                      a.w ? row_load<0>(w, c) : make_uint4(kOnes, kOnes, kOnes, kOnes));
         }
     }
 }
@@ -308,18 +302,21 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
 {
     const NormShape n = norm_shape(a.K);
     const int64_t rows = a.tiled && a.s_row ? (a.M + 31) / 32 * 32 : a.M;
-    if (n.chunks == 0) {
-        const dim3 grid((unsigned)(rows < 2048 ? rows : 2048));
-        hipLaunchKernelGGL(norm_any_kernel<FMT>, grid, dim3(256), 0, s, a);
-        return hipGetLastError();
-    }
     // 1024 threads a CU, whose next rows are on their way meanwhile (2048 x 8192: 21.4
     // us, with twice as many that take two rows each 23.2, with half 26.2)
-    const int64_t most = 256 * (1024 / n.threads);
+    const int64_t most = 256 * (n.chunks == 0 ? 4 : 1024 / n.threads);
     const dim3 grid((unsigned)(rows < most ? rows : most)), block(n.threads);
-    auto *const kernel = n.chunks == 1 ? (a.stream ? norm_kernel<FMT, 1, kNT> : norm_kernel<FMT, 1, 0>)
-                                       : (a.stream ? norm_kernel<FMT, 2, kNT> : norm_kernel<FMT, 2, 0>);
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, a);
+    if (n.chunks == 0)
+        hipLaunchKernelGGL(norm_long_kernel<FMT>, grid, block, 0, s, a);
+    else if (a.K % 8 != 0)
+        hipLaunchKernelGGL((a.stream ? norm_kernel<FMT, 2, kNT, false> : norm_kernel<FMT, 2, 0, false>), grid,
+                           block, 0, s, a);
+    else if (n.chunks == 1)
+        hipLaunchKernelGGL((a.stream ? norm_kernel<FMT, 1, kNT, true> : norm_kernel<FMT, 1, 0, true>), grid,
+                           block, 0, s, a);
+    else
+        hipLaunchKernelGGL((a.stream ? norm_kernel<FMT, 2, kNT, true> : norm_kernel<FMT, 2, 0, true>), grid,
+                           block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -357,27 +354,51 @@ struct BackRow {
 };
 
 // Row `row` of a group of n threads, of which this is the tid-th.
-template <int CH, bool CK, int AUX>
+template <int CH, bool CK, int AUX, bool AL>
 __device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, uint32_t tid, uint32_t n,
                                           BackRow<CH, CK> &v)
 {
     const bool live = row < a.M;
-    const int64_t at = live ? row * a.K : 0, len = live ? a.K : 0, nb = (a.K + 31) >> 5;
-    const rsrc_t rd = make_rsrc(a.dy + at, 0, 2 * len), rr = make_rsrc(a.dres + at, 0, a.dres ? 2 * len : 0);
-    const rsrc_t rh = CK ? make_rsrc(a.q_h + at, 0, len) : make_rsrc(a.h + at, 0, 2 * len);
+    const int64_t at = row * a.K, len = live ? a.K : 0, nb = (a.K + 31) >> 5;
+    const Row<AL, const uint16_t> dy = row_at<AL>(a.dy, at, len), dres = row_at<AL>(a.dres, at, a.dres ? len : 0);
+    const Row<AL, const uint16_t> h = row_at<AL>(a.h, at, CK ? 0 : len);
+    const Row<AL, const uint8_t> q = row_at<AL>(a.q_h, at, CK ? len : 0);
+    const rsrc_t s = make_rsrc(a.s_h + (CK && live ? row * nb : 0), 0, CK && live ? nb : 0);
     v.rstd = live ? a.rstd[row] : 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const uint32_t c = tid + i * n;
-        v.dy[i] = buf_load16<AUX>(rd, 16 * c);
+        v.dy[i] = row_load<AUX>(dy, c);
         if constexpr (CK) {
-            v.q[i] = buf_load8<AUX>(rh, 8 * c);
-            v.s[i] = buf_load1(make_rsrc(a.s_h + (live ? row * nb : 0), 0, live ? nb : 0), c >> 2);
+            v.q[i] = row_load<AUX>(q, c);
+            v.s[i] = buf_load1(s, c >> 2);
         } else {
-            v.h[i] = buf_load16<AUX>(rh, 16 * c);
+            v.h[i] = row_load<AUX>(h, c);
         }
         if (a.dres)
-            v.dres[i] = buf_load16<AUX>(rr, 16 * c);
+            v.dres[i] = row_load<AUX>(dres, c);
+    }
+}
+
+// The 8 values of h of a chunk: bf16 words, or codes with their block's scale byte.
+__device__ __forceinline__ void h_values(uint4 h, float (&v)[8])
+{
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        v[2 * d] = bf16_lo(w[d]);
+        v[2 * d + 1] = bf16_hi(w[d]);
+    }
+}
+__device__ __forceinline__ void h_values(uint2 q, uint32_t s, float (&v)[8])
+{
+    float lo[4], hi[4];
+    e4m3x4_values(q.x, e8m0_operand(s), lo);
+    e4m3x4_values(q.y, e8m0_operand(s), hi);
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        v[d] = lo[d];
+        v[4 + d] = hi[d];
     }
 }
 
@@ -387,7 +408,7 @@ __device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, ui
 // the 8-bit copy dh's default policy is faster (16384 x 7168: 143 us and 150, from
 // bf16 158 and 149).  T: the most threads of a workgroup (1024 leave 128 registers a
 // lane, of which the 8-bit copy's variant spills 4).
-template <int CH, bool CK, bool NT, bool ROWS, int T>
+template <int CH, bool CK, bool NT, bool AL, bool ROWS, int T>
 __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
 {
     constexpr int IN = NT ? kNT : 0, OUT = NT && !CK ? kSC1 : 0;
@@ -396,61 +417,32 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
     const uint32_t n = ROWS ? blockDim.x / rows : blockDim.x;
     const uint32_t group = ROWS ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / n)) : 0u;
     const uint32_t tid = threadIdx.x - group * n;
-    const int waves = (int)n >> 6, step_rows = (int)gridDim.x * rows;
+    const int waves = (int)n >> 6;
+    const int64_t step_rows = (int64_t)gridDim.x * rows;
     uint32_t wt[CH][4];
     float dw[CH][8];
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         uint4 w = make_uint4(kOnes, kOnes, kOnes, kOnes);
         if (a.w)
-            w = buf_load16(make_rsrc(a.w, 0, 2 * a.K), 16 * (tid + i * n));
+            w = row_load<0>(row_at<AL>(a.w, 0, a.K), tid + i * n);
         wt[i][0] = w.x; wt[i][1] = w.y; wt[i][2] = w.z; wt[i][3] = w.w;
 #pragma unroll
         for (int d = 0; d < 8; d++)
             dw[i][d] = 0.0f;
     }
-    // two rows under way, one where registers are short (2001 x 5120 from the 8-bit
-    // copy 22.3 -> 21.5 us, 16384 x 7168 155.4 -> 153.8 us)
-    constexpr bool TWO = T <= 512;
-    BackRow<CH, CK> next, after;
-    int64_t row = (int64_t)blockIdx.x * rows + group;
-    back_load<CH, CK, IN>(a, row, tid, n, next);
-    if constexpr (TWO)
-        back_load<CH, CK, IN>(a, row + step_rows, tid, n, after);
-    int step = 0;
-    // all groups of the workgroup take as many turns: they share barriers
-    for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < a.M; row0 += step_rows, row += step_rows, step ^= 1) {
-        const BackRow<CH, CK> v = next;
-        if constexpr (TWO) {
-            next = after;
-            back_load<CH, CK, IN>(a, row + 2 * (int64_t)step_rows, tid, n, after);
-        } else {
-            back_load<CH, CK, IN>(a, row + step_rows, tid, n, next);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    // one turn: a row whose loads are done; all groups of the workgroup take as many
+    // (they share barriers)
+    const auto turn = [&](const BackRow<CH, CK> &v, int64_t row, int step) {
         float g[CH][8], xh[CH][8], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t dy[4] = {v.dy[i].x, v.dy[i].y, v.dy[i].z, v.dy[i].w};
             float hv[8];
-            if constexpr (CK) {
-                float lo[4], hi[4];
-                const float sc = e8m0_operand(v.s[i]);
-                e4m3x4_values(v.q[i].x, sc, lo);
-                e4m3x4_values(v.q[i].y, sc, hi);
-#pragma unroll
-                for (int d = 0; d < 4; d++) {
-                    hv[d] = lo[d];
-                    hv[4 + d] = hi[d];
-                }
-            } else {
-                const uint32_t h[4] = {v.h[i].x, v.h[i].y, v.h[i].z, v.h[i].w};
-#pragma unroll
-                for (int d = 0; d < 4; d++) {
-                    hv[2 * d] = bf16_lo(h[d]);
-                    hv[2 * d + 1] = bf16_hi(h[d]);
-                }
-            }
+            if constexpr (CK)
+                h_values(v.q[i], v.s[i], hv);
+            else
+                h_values(v.h[i], hv);
 #pragma unroll
             for (int d = 0; d < 4; d++) {
                 const float y0 = bf16_lo(dy[d]), y1 = bf16_hi(dy[d]);
@@ -465,8 +457,7 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
             }
         }
         const float c = block_sum(s0 + s1, red[step], waves, (int)group * waves) / (float)a.K;
-        const bool live = row < a.M;
-        const rsrc_t ro = make_rsrc(a.dh + (live ? row * a.K : 0), 0, live ? 2 * a.K : 0);
+        const Row<AL, uint16_t> ro = row_at<AL>(a.dh, row * a.K, row < a.M ? a.K : 0);
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t dr[4] = {v.dres[i].x, v.dres[i].y, v.dres[i].z, v.dres[i].w};
@@ -481,7 +472,43 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
                 }
                 o[d] = bf16x2_rne(e0, e1);
             }
-            buf_store16<OUT>(ro, 16 * (tid + i * n), make_uint4(o[0], o[1], o[2], o[3]));
+            row_store<OUT>(ro, tid + i * n, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    };
+    const int64_t all = a.M + (int64_t)group;   // rows `row` < all: the workgroup's turns
+    int64_t row = (int64_t)blockIdx.x * rows + group;
+    if constexpr (T <= 512 && AL) {
+        // three sets of registers in turn: two rows are under way while one is worked
+        // on
+        BackRow<CH, CK> v0, v1, v2;
+        back_load<CH, CK, IN, AL>(a, row, tid, n, v0);
+        back_load<CH, CK, IN, AL>(a, row + step_rows, tid, n, v1);
+        for (int step = 0; row < all;) {
+            back_load<CH, CK, IN, AL>(a, row + 2 * step_rows, tid, n, v2);
+            __builtin_amdgcn_sched_barrier(0);
+            turn(v0, row, step);
+            row += step_rows, step ^= 1;
+            if (row >= all)
+                break;
+            back_load<CH, CK, IN, AL>(a, row + 2 * step_rows, tid, n, v0);
+            __builtin_amdgcn_sched_barrier(0);
+            turn(v1, row, step);
+            row += step_rows, step ^= 1;
+            if (row >= all)
+                break;
+            back_load<CH, CK, IN, AL>(a, row + 2 * step_rows, tid, n, v1);
+            __builtin_amdgcn_sched_barrier(0);
+            turn(v2, row, step);
+            row += step_rows, step ^= 1;
+        }
+    } else {
+        BackRow<CH, CK> next;
+        back_load<CH, CK, IN, AL>(a, row, tid, n, next);
+        for (int step = 0; row < all; row += step_rows, step ^= 1) {
+            const BackRow<CH, CK> v = next;
+            back_load<CH, CK, IN, AL>(a, row + step_rows, tid, n, next);
+            __builtin_amdgcn_sched_barrier(0);
+            turn(v, row, step);
         }
     }
     if (!a.partials)
@@ -516,6 +543,12 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const uint32_t off = 32 * (tid + i * n);
+        if constexpr (!AL) {
+#pragma unroll
+            for (int d = 0; d < 8; d++)
+                buf_store4(rp, off + 4 * d, bits_f32(dw[i][d]));
+            continue;
+        }
 #pragma unroll
         for (int q = 0; q < 2; q++)
             buf_store16(rp, off + 16 * q,
@@ -524,49 +557,74 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
     }
 }
 
-// h's element of a row (bf16, or the 8-bit copy's value).
-__device__ __forceinline__ float any_h(const NormBackArgs &a, int64_t row, int64_t k)
+// Rows of any length.  Chunk c of a row: g = dy w and xhat.
+__device__ __forceinline__ void long_chunk(const NormBackArgs &a, int64_t row, uint32_t c, float rstd, uint4 dyw,
+                                           float (&dy)[8], float (&g)[8], float (&xh)[8])
 {
+    const int64_t at = row * a.K;
+    h_values(dyw, dy);
     if (a.h)
-        return bf16_lo(a.h[row * a.K + k]);
-    float v[4];
-    e4m3x4_values(a.q_h[row * a.K + k], e8m0_operand(a.s_h[row * ((a.K + 31) >> 5) + (k >> 5)]), v);
-    return v[0];
+        h_values(load_chunk<false>(a.h + at, c, a.K), xh);
+    else
+        h_values(load_codes<false>(a.q_h + at, c, a.K), a.s_h[row * ((a.K + 31) >> 5) + (c >> 2)], xh);
+    float w[8];
+    h_values(a.w ? load_chunk<false>(a.w, c, a.K) : make_uint4(kOnes, kOnes, kOnes, kOnes), w);
+#pragma unroll
+    for (int d = 0; d < 8; d++) {
+        xh[d] *= rstd;
+        g[d] = dy[d] * w[d];
+    }
 }
 
-__global__ __launch_bounds__(256) void norm_back_any_kernel(NormBackArgs a)
+__global__ __launch_bounds__(512) void norm_back_long_kernel(NormBackArgs a)
 {
     __shared__ float red[2][16];
+    const uint32_t chunks = (uint32_t)((a.K + 7) >> 3);
     int step = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, step ^= 1) {
         const float rstd = a.rstd[row];
-        float s = 0.0f;
-        for (int64_t k = threadIdx.x; k < a.K; k += 256) {
-            const float g = bf16_lo(a.dy[row * a.K + k]) * (a.w ? bf16_lo(a.w[k]) : 1.0f);
-            s = __builtin_fmaf(g, any_h(a, row, k) * rstd, s);
+        const uint16_t *const dyr = a.dy + row * a.K;
+        float s = 0.0f, dy[8], g[8], xh[8];
+        for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
+            long_chunk(a, row, c, rstd, load_chunk<false>(dyr, c, a.K), dy, g, xh);
+#pragma unroll
+            for (int d = 0; d < 8; d++)
+                s = __builtin_fmaf(g[d], xh[d], s);
         }
-        const float c = block_sum(s, red[step], 4) / (float)a.K;
-        for (int64_t k = threadIdx.x; k < a.K; k += 256) {
-            const float g = bf16_lo(a.dy[row * a.K + k]) * (a.w ? bf16_lo(a.w[k]) : 1.0f);
-            float e = rstd * __builtin_fmaf(-(any_h(a, row, k) * rstd), c, g);
+        const float mean = block_sum(s, red[step], 8) / (float)a.K;
+        for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
+            long_chunk(a, row, c, rstd, load_chunk<false>(dyr, c, a.K), dy, g, xh);
+            float r[8] = {};
             if (a.dres)
-                e += bf16_lo(a.dres[row * a.K + k]);
-            a.dh[row * a.K + k] = (uint16_t)(bf16x2_rne(e, 0.0f) & 0xFFFFu);
+                h_values(load_chunk<false>(a.dres + row * a.K, c, a.K), r);
+            uint32_t o[4];
+#pragma unroll
+            for (int d = 0; d < 4; d++)
+                o[d] = bf16x2_rne(rstd * __builtin_fmaf(-xh[2 * d], mean, g[2 * d]) + r[2 * d],
+                                  rstd * __builtin_fmaf(-xh[2 * d + 1], mean, g[2 * d + 1]) + r[2 * d + 1]);
+            store_chunk<false>(a.dh + row * a.K, c, a.K, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
 
-// Partial weight gradients of any row length: slice blockIdx.y of the rows,
-// one column per thread.
-__global__ __launch_bounds__(256) void norm_dweight_any_kernel(NormBackArgs a)
+// Their partial weight gradients: slice blockIdx.y of the rows, a chunk per thread.
+__global__ __launch_bounds__(256) void norm_dweight_long_kernel(NormBackArgs a)
 {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= a.K)
+    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
+    if (8 * (int64_t)c >= a.K)
         return;
-    float s = 0.0f;
-    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y)
-        s = __builtin_fmaf(bf16_lo(a.dy[row * a.K + k]), any_h(a, row, k) * a.rstd[row], s);
-    a.partials[(int64_t)blockIdx.y * a.K + k] = s;
+    float sum[8] = {};
+    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+        float dy[8], g[8], xh[8];
+        long_chunk(a, row, c, a.rstd[row], load_chunk<false>(a.dy + row * a.K, c, a.K), dy, g, xh);
+#pragma unroll
+        for (int d = 0; d < 8; d++)
+            sum[d] = __builtin_fmaf(dy[d], xh[d], sum[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < 8; d++)
+        if (8 * (int64_t)c + d < a.K)
+            a.partials[(int64_t)blockIdx.y * a.K + 8 * (int64_t)c + d] = sum[d];
 }
 
 // dweight[k] = sum of partials[p][k]: 32 columns by 32 slices of p a workgroup,
@@ -592,13 +650,13 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial
     }
 }
 
-template <int CH, bool ROWS, int T>
+template <int CH, bool AL, bool ROWS, int T>
 static void launch_back(const NormBackArgs &a, unsigned grid, int threads, int rows, hipStream_t s)
 {
-    auto *const kernel = a.h ? (a.stream ? norm_back_kernel<CH, false, true, ROWS, T>
-                                         : norm_back_kernel<CH, false, false, ROWS, T>)
-                             : (a.stream ? norm_back_kernel<CH, true, true, ROWS, T>
-                                         : norm_back_kernel<CH, true, false, ROWS, T>);
+    auto *const kernel = a.h ? (a.stream ? norm_back_kernel<CH, false, true, AL, ROWS, T>
+                                         : norm_back_kernel<CH, false, false, AL, ROWS, T>)
+                             : (a.stream ? norm_back_kernel<CH, true, true, AL, ROWS, T>
+                                         : norm_back_kernel<CH, true, false, AL, ROWS, T>);
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads * rows), 0, s, a, rows);
 }
 
@@ -607,19 +665,20 @@ hipError_t launch_norm_back(const NormBackArgs &a, hipStream_t s)
     const NormShape n = norm_shape(a.K);
     const unsigned parts = (unsigned)norm_back_parts(a.M, a.K);
     const int rows = norm_back_rows(n);
-    switch (n.chunks) {
-    case 0:
-        hipLaunchKernelGGL(norm_back_any_kernel, dim3((unsigned)(a.M < 2048 ? a.M : 2048)), dim3(256), 0,
-                           s, a);
+    const bool al = a.K % 8 == 0;
+    if (n.chunks == 0) {
+        hipLaunchKernelGGL(norm_back_long_kernel, dim3((unsigned)(a.M < 1024 ? a.M : 1024)), dim3(512), 0, s, a);
         if (a.partials)
-            hipLaunchKernelGGL(norm_dweight_any_kernel, dim3((unsigned)((a.K + 255) / 256), parts),
-                               dim3(256), 0, s, a);
-        break;
-    case 1: launch_back<1, true, 512>(a, parts, n.threads, rows, s); break;
-    default:
-        (rows > 1           ? launch_back<2, true, 512>
-         : n.threads <= 512 ? launch_back<2, false, 512>
-                            : launch_back<2, false, 1024>)(a, parts, n.threads, rows, s);
+            hipLaunchKernelGGL(norm_dweight_long_kernel, dim3((unsigned)((a.K + 2047) / 2048), parts), dim3(256),
+                               0, s, a);
+    } else if (rows > 1) {
+        (!al             ? launch_back<2, false, true, 512>
+         : n.chunks == 1 ? launch_back<1, true, true, 512>
+                         : launch_back<2, true, true, 512>)(a, parts, n.threads, rows, s);
+    } else if (n.threads <= 512) {
+        (al ? launch_back<2, true, false, 512> : launch_back<2, false, false, 512>)(a, parts, n.threads, rows, s);
+    } else {
+        (al ? launch_back<2, true, false, 1024> : launch_back<2, false, false, 1024>)(a, parts, n.threads, rows, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.partials)

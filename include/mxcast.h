@@ -565,8 +565,8 @@ mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T,
  * and the MXFP8 casts of y, exactly as mx_quantize casts that tensor.
  *   x, residual  device, bf16 [M][K]; residual may be NULL
  *   weight     device, bf16 [K]; NULL: ones
- *   M, K       as for mx_quantize.  K a multiple of 8 up to 16384 keeps a row in
- *              registers, any other K reads it twice
+ *   M, K       as for mx_quantize.  Rows of up to 16384 are held in registers, longer
+ *              ones read twice
  *   eps        finite and not negative (MX_ERR_ENUM otherwise)
  *   axis_mask  0 (no casts), or as for mx_quantize, flags included
  *   h          bf16 [M][K], required iff there is a residual

@@ -441,7 +441,7 @@ def test_combine_backward(T, top, E, align, K):
         assert np.all(np.abs(f64(o["dy"]) - dy) <= (2.0 ** -8 + 2 * HALF) * np.abs(dy))
         assert np.all(f64(o["dy"])[~live] == 0)
         prod = np.where((pos >= 0)[:, :, None], y[np.maximum(pos, 0)], 0.0) * dout[:, None, :]
-        adds = -(-K // 64) + 8              # a lane's products in a line, 6 steps over the wave
+        adds = 8 * -(-K // 512) + 7         # a lane's products in a line, 8 of every 512; 6 over the wave
         assert np.all(np.abs(f64(o["dweights"]) - prod.sum(2)) <= adds * HALF * np.abs(prod).sum(2) + 1e-38)
     y3 = normal(generator(K), T, top, K)
     o = mx.moe_combine_backward(c["dout"].cuda(), y3.cuda(), c["w"].cuda())

@@ -6,8 +6,8 @@ Rounding of a sum of positive terms: a term passes through at most `chain` fp32
 additions, each off by 2^-24 of what it adds up to, so the sum is off by at most
 chain 2^-24 of itself.  A row in registers adds 16 elements in two chains of 8 (with
 their squares' exact product inside the FMA), 1, 6 steps over the wave and up to
-15 over the waves: 30.  The two-pass kernel adds ceil(K / 256) in a line, then 6 and
-3."""
+15 over the waves: 30.  A longer one is added by 512 threads, 8 of every 4096 each in
+a line, then 6 steps and 8."""
 import numpy as np
 import pytest
 import torch
@@ -25,7 +25,7 @@ EPS = 1e-5
 
 
 def chain(K):
-    return 30 if K % 8 == 0 and K <= 16384 else -(-K // 256) + 9
+    return 30 if K <= 16384 else 8 * -(-K // 4096) + 15
 
 
 def spec(M, K, axis, residual, y, ckpt):
