@@ -456,7 +456,7 @@ __device__ __forceinline__ int choose64(const RouteArgs &a, int lane, double *ke
     return expert;
 }
 
-// This lane's keys and scores (fp32) of a token, and whether one of them is NaN.
+// This lane's keys and scores (fp32) of a token, and whether an unmasked one is NaN.
 // VALUE: keys are scores plus a bias, or a group's two are added; otherwise the
 // logits give the order.  Such keys are compared in fixed point first, and only where
 // two of those that decide are within its steps of each other (about one token in
@@ -478,15 +478,16 @@ __device__ __forceinline__ bool keys_of(const RouteArgs &a, const float (&x)[NPL
             const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
             p[i] = (float)s[i];
             key[i] = masked ? 0u : order_of(k, f);
-            nan |= k != k;
+            nan |= !masked & (k != k);
         }
     } else {
         float q[NPL];
         scores_of<Single, NPL, ROW>(x, a.sigmoid != 0, p, q);
 #pragma unroll
         for (int i = 0; i < NPL; i++) {
-            key[i] = x[i] == -__builtin_inff() ? 0u : order_of(x[i]);
-            nan |= (p[i] != p[i]) | (x[i] != x[i]);
+            const bool masked = x[i] == -__builtin_inff();
+            key[i] = masked ? 0u : order_of(x[i]);
+            nan |= !masked & ((p[i] != p[i]) | (x[i] != x[i]));
         }
     }
     return nan;
@@ -727,7 +728,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackA
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
         ps[wave][row][l * NPL + i] = p[i];
-        dp[i] = a.dscores && l * NPL + i < a.E ? dp[i] : 0.0f;
+        // (a masked expert's score has no gradient, whatever stands in its place)
+        dp[i] = a.dscores && x[i] != -__builtin_inff() ? dp[i] : 0.0f;
     }
     __builtin_amdgcn_wave_barrier();
     // sum over the experts of p times their dp.  With normalised weights the

@@ -604,7 +604,8 @@ mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, in
  *   dweight    fp32 [K], or NULL: not computed
  *   workspace, workspace_bytes  device scratch of at least
  *              mx_rmsnorm_backward_workspace_size() bytes with dweight
- *              (per-workgroup partial sums; NULL and 0 without)
+ *              (per-workgroup partial sums; NULL and 0 without).  Calls that may
+ *              overlap in time need workspaces of their own
  * MX_ERR_NULL also for both or neither of h and q_h.
  */
 mx_status mx_rmsnorm_backward(const void *dy, const void *h, const uint8_t *q_h, const uint8_t *s_h,
@@ -631,7 +632,8 @@ size_t mx_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
  *             divided by their sum (0 where that is 0), times scale
  * A slot that no expert is left for (fewer unmasked ones than `top`) gets expert
  * -1 and weight 0, which nvfp4_matvec_experts and moe_sort take as no expert.  A
- * token with a NaN among its p or keys gets experts -1 and weights NaN.
+ * token with a NaN among the keys of its unmasked experts gets experts -1 and
+ * weights NaN; what stands in masked places does not matter.
  *   logits    device, [T][E]: bf16, or fp32 with MX_ROUTE_F32
  *   bias      device, fp32 [E] or NULL
  *   T, E      1 <= T <= 2^23, 1 <= E <= 1024, T * E <= 2^40
@@ -661,7 +663,8 @@ mx_status moe_route(const void *logits, const float *bias, int64_t T, int64_t E,
  *             is no expert, one named twice counts twice
  *   dweights  fp32 [T][top];  dscores  fp32 [T][E] or NULL
  *   dlogits   [T][E], of the logits' type
- * The gradients of a token whose p hold a NaN are NaN; those of masked experts 0.
+ * Where p is NaN so is the gradient; a masked logit (-Inf) has gradient 0, whatever
+ * stands in its dscores.
  */
 mx_status moe_route_backward(const void *logits, const int32_t *experts, const float *dweights,
                              const float *dscores, int64_t T, int64_t E, int64_t top, float scale,
@@ -682,7 +685,8 @@ mx_status moe_route_backward(const void *logits, const int32_t *experts, const f
  *   slots     int32 [rows]: each row's slot; -1 for padding and for rows behind
  *             the last expert's
  *   workspace, workspace_bytes  device scratch of at least
- *             moe_sort_workspace_size() bytes (0 for few slots: NULL and 0 then)
+ *             moe_sort_workspace_size() bytes (0 for few slots: NULL and 0 then);
+ *             calls that may overlap in time need workspaces of their own
  * Errors as for the products (every pointer 16-byte aligned).
  */
 mx_status moe_sort(const int32_t *experts, int64_t T, int64_t top, int64_t E, int64_t align,

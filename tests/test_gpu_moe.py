@@ -86,7 +86,7 @@ def logits_of(g, T, E, dtype=F32, masked=0.0, scale=2.0):
 ROUTES = [(1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (5, 4, 4, 2, 1), (33, 64, 6, 8, 3), (17, 40, 5, 4, 2),
           (9, 128, 8, 8, 4), (6, 160, 6, 8, 3), (7, 256, 8, 8, 4), (64, 256, 1, 1, 1), (3, 500, 10, 5, 2),
           (5, 512, 8, 16, 4), (3, 1024, 64, 32, 8), (4, 1000, 33, 1, 1), (130, 63, 7, 1, 1),
-          (2, 64, 64, 64, 9), (3, 65, 65 - 1, 1, 1), (3, 1023, 9, 3, 1), (2, 96, 8, 48, 20)]
+          (2, 64, 64, 64, 9), (3, 65, 65 - 1, 1, 1), (3, 1023, 9, 3, 1), (2, 96, 8, 48, 20), (2, 1024, 64, 64, 64)]
 
 
 @pytest.mark.parametrize("T,E,top,groups,kept", ROUTES)
@@ -178,6 +178,51 @@ def test_route_nan_stays_in_its_row(E, flags):
         assert bool((o["experts"][1] == -1).all()) and bool(o["weights"][1].isnan().all())
 
 
+@pytest.mark.parametrize("E,groups", [(32, 4), (256, 8), (300, 5)])
+def test_route_of_nan_in_masked_places(E, groups):
+    """A NaN bias of an expert whose logit is -Inf, a NaN logit of one whose bias is
+    (by sigmoid scores, which stand alone): neither is seen."""
+    g = generator(E)
+    l = logits_of(g, 20, E)
+    bias = torch.randn(E, generator=g) * 0.1
+    l[:, 3] = float("-inf")
+    bias[3] = float("nan")
+    bias[7] = float("-inf")
+    l2, b2 = l.clone(), bias.clone()
+    b2[3] = 0.0
+    for flags in (0, mx.ROUTE_SIGMOID, mx.ROUTE_SIGMOID | mx.ROUTE_GROUP_PAIR | mx.ROUTE_RENORM):
+        if flags & mx.ROUTE_SIGMOID:
+            l[:, 7] = float("nan")
+        a = mx.moe_route(l.cuda(), 5, bias=bias.cuda(), flags=flags, groups=groups, top_groups=2)
+        b = mx.moe_route(l2.cuda(), 5, bias=b2.cuda(), flags=flags, groups=groups, top_groups=2)
+        assert bool((a["experts"] >= 0).all())
+        assert torch.equal(a["experts"], b["experts"]) and torch.equal(a["weights"], b["weights"])
+
+
+def test_route_with_an_infinite_bias():
+    """+Inf: those experts first, the lowest index first among them; -Inf: never."""
+    g = generator(3)
+    for E in (16, 256, 300):
+        l = logits_of(g, 6, E)
+        bias = torch.zeros(E)
+        bias[9] = bias[5] = float("inf")
+        bias[2] = float("-inf")
+        for flags in (0, mx.ROUTE_SIGMOID):
+            o = mx.moe_route(l.cuda(), 4, bias=bias.cuda(), flags=flags)
+            assert bool((o["experts"][:, 0] == 5).all()) and bool((o["experts"][:, 1] == 9).all())
+            assert not bool((o["experts"] == 2).any()) and bool(o["weights"].isfinite().all())
+
+
+def test_route_with_large_biases():
+    """Keys of every magnitude: the fixed point's steps grow with the largest bias."""
+    g = generator(8)
+    for scale in (1e-6, 30.0, 1e6, 1e30, 3e38):
+        l, bias = logits_of(g, 50, 64), torch.randn(64, generator=g) * min(scale, 1e37)
+        bias[0] = scale
+        check_route(l, 6, bias, flags=mx.ROUTE_SIGMOID)
+        check_route(l, 6, bias, groups=8, top_groups=3, flags=mx.ROUTE_GROUP_PAIR if scale < 1e37 else 0)
+
+
 def grad64(l, ex, dw, ds, flags, scale):
     p = scores64(l, flags & mx.ROUTE_SIGMOID)
     T, E = l.shape
@@ -250,6 +295,19 @@ def test_route_backward_of_other_experts():
     for flags in range(4):
         d = check_route_back(l, ex, flags, 1.0, seed=flags)
         assert np.all(d[2] == 0)
+
+
+@pytest.mark.parametrize("E", [16, 256, 600])
+@pytest.mark.parametrize("flags", [0, 1, 2, 3])
+def test_route_backward_ignores_masked_places(E, flags):
+    g = generator(E + flags)
+    l = logits_of(g, 10, E, masked=0.4)
+    ex = mx.moe_route(l.cuda(), 4, flags=flags)["experts"]
+    dw, ds = torch.randn(10, 4, generator=g).cuda(), torch.randn(10, E, generator=g)
+    clean = mx.moe_route_backward(dw, l.cuda(), ex, flags=flags, dscores=ds.cuda())
+    ds[l == float("-inf")] = float("nan")
+    o = mx.moe_route_backward(dw, l.cuda(), ex, flags=flags, dscores=ds.cuda())
+    assert torch.equal(o, clean) and bool((o[l.cuda() == float("-inf")] == 0).all())
 
 
 @pytest.mark.parametrize("flags", [0, 1, 2, 3])
@@ -470,6 +528,27 @@ def test_combine_backward_of_other_orders():
     assert np.all(np.abs(dw - want) <= 1e-5)
 
 
+def test_combine_backward_without_dweights():
+    c = rows_case(40, 3, 5, 4, 72, 3)
+    args = (c["dout"].cuda(), c["y"].cuda(), c["w"].cuda())
+    a = mx.moe_combine_backward(*args, pos=c["pos"], slots=c["slots"])
+    b = mx.moe_combine_backward(*args, pos=c["pos"], slots=c["slots"], want_dweights=False)
+    assert b["dweights"] is None and torch.equal(a["dy"], b["dy"])
+
+
+def test_codes_and_scales_take_the_same_way():
+    """A row-wise cast's codes and compact scales, moved instead of bf16 rows: the cast
+    of the moved rows."""
+    g = generator(15)
+    T, top, K = 70, 2, 200
+    x = normal(g, T, K).cuda()
+    s = mx.moe_sort(experts_of(5, T, top, 4, none=0.1).cuda(), 4, align=16)
+    c = mx.mx_quantize(x, axis=mx.ROWWISE)
+    want = mx.mx_quantize(mx.moe_gather(x, s["slots"], top), axis=mx.ROWWISE)
+    assert torch.equal(mx.moe_gather(c["q_row"], s["slots"], top), want["q_row"])
+    assert torch.equal(mx.moe_gather(c["s_row"], s["slots"], top), want["s_row"])
+
+
 def test_gather_and_combine_are_each_others_gradient():
     """<combine(y, 1), g> = <y, gather(g)> in 64 bits, on whole numbers (exact)."""
     g = generator(14)
@@ -480,6 +559,30 @@ def test_gather_and_combine_are_each_others_gradient():
     a = (f64(mx.moe_combine(y, pos=s["pos"])) * f64(d)).sum()
     b = (f64(y) * f64(mx.moe_gather(d, s["slots"], top))).sum()
     assert a == b
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^32 bytes of rows: the last ones, there and back."""
+    T, top, K, R = 131200, 2, 8200, 262400
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[-3:] = torch.arange(3 * K, device="cuda").view(3, K).to(BF16)
+    w = torch.ones(T, top, device="cuda")
+    w[-3:, 1] = 2.0
+    ex = torch.zeros(T, top, dtype=I32, device="cuda")
+    ex[:, 1] = 1
+    s = mx.moe_sort(ex, 2)
+    assert s["slots"].numel() == R and s["pos"][-1].tolist() == [T - 1, R - 1]
+    xs = mx.moe_gather(x, s["slots"], top)
+    assert torch.equal(xs[T - 3:T], x[-3:]) and torch.equal(xs[-3:], x[-3:])
+    assert not bool(xs[T:-3].any()) and not bool(xs[:T - 3].any())
+    out = mx.moe_combine(xs, w, s["pos"])
+    assert torch.equal(out[-3:], (3 * x[-3:].float()).to(BF16)) and not bool(out[:-3].any())
+    b = mx.moe_combine_backward(x, xs, w, pos=s["pos"], slots=s["slots"])
+    assert torch.equal(b["dy"][-3:], (2 * x[-3:].float()).to(BF16))
+    assert torch.equal(b["dy"][T - 3:T], x[-3:]) and not bool(b["dy"][T:-3].any())
+    want = (x[-3:].double() ** 2).sum(1)
+    adds = 8 * -(-K // 512) + 7
+    assert bool(((b["dweights"][-3:].double() - want[:, None]).abs() <= adds * HALF * want[:, None]).all())
 
 
 # ---- together, streams, graphs -----------------------------------------------------------

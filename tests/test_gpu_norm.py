@@ -187,6 +187,60 @@ def test_norm_backward_without_dweight():
         assert b["dweight"] is None and torch.equal(a["dh"], b["dh"])
 
 
+@pytest.mark.parametrize("K", [256, 100])
+def test_norm_backward_of_special_rows(K):
+    """A row that holds Inf or NaN has NaN gradients, from bf16 and from the 8-bit copy,
+    and leaves the other rows' alone."""
+    g = generator(K)
+    x, dy = normal(g, 9, K), normal(g, 9, K)
+    def grads(x, **src):
+        f = mx.mx_rmsnorm(x.cuda(), eps=EPS, checkpoint=True)
+        a = mx.mx_rmsnorm_backward(dy.cuda(), f["rstd"], h=f["h"])["dh"]
+        b = mx.mx_rmsnorm_backward(dy.cuda(), f["rstd"], q_h=f["q_h"], s_h=f["s_h"])["dh"]
+        return a, b
+    clean = grads(x)
+    x[2, K - 1] = float("nan")
+    x[5, 0] = float("nan")
+    for a, c in zip(grads(x), clean):
+        assert bool(a[2].isnan().all()) and bool(a[5].isnan().all())
+        for r in (0, 1, 3, 4, 6, 7, 8):
+            assert torch.equal(a[r], c[r]), r
+
+
+def same_rows(M, K, **kw):
+    """The last rows of a tensor past 2^31 elements against the same rows alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    n = 64
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    x[-n:] = torch.randn(n, K, generator=g, device="cuda").to(BF16)
+    x[:-n] = 1.0
+    return x, n
+
+
+def test_norm_past_32_bit_offsets():
+    """2^31 elements and more, with every output: the last rows as when they are alone,
+    and the last row blocks of the column-wise cast likewise."""
+    M, K = 262208, 8200             # 2.15e9 elements, a multiple of 32 rows
+    x, n = same_rows(M, K)
+    w = torch.linspace(0.5, 2.0, K, device="cuda").to(BF16)
+    o = mx.mx_rmsnorm(x, w, axis=3, want_y=True, checkpoint=True)
+    tail = x[-n:].clone()
+    t = mx.mx_rmsnorm(tail, w, axis=3, want_y=True, checkpoint=True)
+    for k in ("y", "rstd", "q_row", "s_row", "q_h", "s_h"):
+        assert torch.equal(o[k][-n:], t[k]), k
+    assert torch.equal(o["q_col"][:, -n:], t["q_col"]) and torch.equal(o["s_col"][:, -2:], t["s_col"])
+    del o["q_col"], o["q_row"], o["y"]
+    dy = torch.zeros_like(x)
+    dy[-n:] = tail.flip(0)
+    a = mx.mx_rmsnorm_backward(dy, o["rstd"], w, q_h=o["q_h"], s_h=o["s_h"])
+    b = mx.mx_rmsnorm_backward(dy[-n:].clone(), t["rstd"], w, q_h=t["q_h"], s_h=t["s_h"])
+    assert torch.equal(a["dh"][-n:], b["dh"]) and not bool(a["dh"][:-n].any())
+    # zeros, and the same 64 rows in other workgroups: fp32 sums of 64 terms
+    mag = (dy[-n:].float() * tail.float() * t["rstd"][:, None]).abs().sum(0)
+    assert bool(((a["dweight"] - b["dweight"]).abs() <= 128 * HALF * mag + 1e-38).all())
+
+
 @pytest.mark.parametrize("K", [24, 15])
 def test_norm_backward_against_differences(K):
     """dh and dweight against central differences of sum(dy y) in 64 bits: the
