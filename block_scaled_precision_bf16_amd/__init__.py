@@ -885,8 +885,15 @@ def _new(like, out, stream):
     out's tensor of that name, of as many elements, or a new one (of the pool of the
     stream that works on it)."""
     if out is None and stream is None:
-        empty = like.new_empty
-        return lambda name, shape, dtype: empty(shape, dtype=dtype)
+        empty, bf16 = like.new_empty, like.dtype == BF16
+        same = like.shape
+
+        def give(name, shape, dtype):
+            if shape is same and bf16 and dtype is BF16:      # the fastest of torch's ways
+                return torch.empty_like(like)
+            return empty(shape, dtype=dtype)
+
+        return give
     dev = like.device
 
     def take(name, shape, dtype):
@@ -917,6 +924,13 @@ def _gpu(dev):
         raise ValueError(f"tensors must be on a ROCm (cuda) device, got {dev}")
 
 
+def _scales_of(rows, cols, axis):
+    """Shape of one direction's scales, as _scale_shape gives it."""
+    if axis & SCALE_TILED:
+        return (_scale_bytes(rows, cols, axis),)
+    return (rows, -(-cols // 32))
+
+
 def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, checkpoint=False,
                out=None, stream=None):
     """h = x + residual (x itself without), y = h rstd weight with rstd =
@@ -926,31 +940,29 @@ def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, che
     want_y (default: without casts), q_h and s_h, an 8-bit copy of h for
     mx_rmsnorm_backward, with `checkpoint`.  Without a residual h is x."""
     x = _2d(x, "x")
-    (M, K), dev = x.shape, x.device
-    rp = _want(residual, x.shape, _BF16_BITS, "residual", dev)
+    shape, dev = x.shape, x.device
+    M, K = shape
+    rp = _want(residual, shape, _BF16_BITS, "residual", dev)
     wp = _want(weight, (K,), _BF16_BITS, "weight", dev)
-    o = {"h": None, "y": None, "rstd": None, "q_row": None, "s_row": None, "q_col": None,
-         "s_col": None, "q_h": None, "s_h": None}
+    h = y = q_row = s_row = q_col = s_col = q_h = s_h = None
     new = _new(x, out, stream)
     if residual is not None:
-        o["h"] = new("h", x.shape, BF16)
+        h = new("h", shape, BF16)
     if want_y or (want_y is None and not axis):
-        o["y"] = new("y", x.shape, BF16)
-    o["rstd"] = new("rstd", (M,), F32)
-    if axis:
-        for name, (shape, dtype) in _mx_need(M, K, axis).items():
-            o[name] = new(name, shape, dtype)
+        y = new("y", shape, BF16)
+    rstd = new("rstd", (M,), F32)
+    if axis & ROWWISE:
+        q_row, s_row = new("q_row", shape, U8), new("s_row", _scales_of(M, K, axis), U8)
+    if axis & COLWISE:
+        q_col, s_col = new("q_col", (K, M), U8), new("s_col", _scales_of(K, M, axis), U8)
     if checkpoint:
-        o["q_h"] = new("q_h", (M, K), U8)
-        o["s_h"] = new("s_h", (M, -(-K // 32)), U8)
+        q_h, s_h = new("q_h", shape, U8), new("s_h", (M, -(-K // 32)), U8)
     if dev.index is None:
         _gpu(dev)
-    _launch("mx_rmsnorm", dev, stream, lib().mx_rmsnorm, x.data_ptr(), rp, wp, M, K, eps, axis,
-            _at(o["h"]), _at(o["y"]), _at(o["q_row"]), _at(o["s_row"]), _at(o["q_col"]),
-            _at(o["s_col"]), _at(o["q_h"]), _at(o["s_h"]), o["rstd"].data_ptr())
-    if residual is None:
-        o["h"] = x
-    return o
+    _launch("mx_rmsnorm", dev, stream, lib().mx_rmsnorm, x.data_ptr(), rp, wp, M, K, eps, axis, _at(h),
+            _at(y), _at(q_row), _at(s_row), _at(q_col), _at(s_col), _at(q_h), _at(s_h), rstd.data_ptr())
+    return {"h": x if h is None else h, "y": y, "rstd": rstd, "q_row": q_row, "s_row": s_row,
+            "q_col": q_col, "s_col": s_col, "q_h": q_h, "s_h": s_h}
 
 
 def mx_rmsnorm_backward_workspace_size(M: int, K: int) -> int:
