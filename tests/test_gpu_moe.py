@@ -427,6 +427,20 @@ def test_gather(dtype, width):
         assert torch.equal(o.cpu().view(U8), want.view(U8))
 
 
+@pytest.mark.parametrize("T,top,rows", [(9000, 2, 140000), (9000, 4, 140000), (8100, 2, 20001)])
+def test_gather_of_many_rows(T, top, rows):
+    """Both orders of the rows, more of them than the grid has workgroups."""
+    g = torch.Generator("cuda").manual_seed(rows + top)
+    x = torch.randint(0, 256, (T, 8192), generator=g, device="cuda", dtype=torch.int32).to(U8)
+    slots = torch.randint(-2, T * top + 2, (rows,), generator=g, device="cuda", dtype=I32)
+    o = mx.moe_gather(x, slots, top)
+    live = (slots >= 0) & (slots < T * top)
+    at = (slots // top).clamp(0, T - 1).long()
+    for r in range(0, rows, 10000):
+        want = torch.where(live[r:r + 10000, None], x[at[r:r + 10000]], x.new_zeros(()))
+        assert torch.equal(o[r:r + 10000], want)
+
+
 def rows_case(T, top, E, align, K, seed, none=0.1):
     g = generator(seed)
     ex = experts_of(seed, T, top, E, none=none)
