@@ -12,6 +12,11 @@
 // there the first, is the lowest index.  More experts, and groups that are not a
 // power of two of such lanes, take a wave per token.  The bytes (4 an expert) take
 // less time than the instructions: the exponentials and `top` maxima bound it.
+//
+// Measured for 16384 tokens, 8 experts each: 256 experts by sigmoid, bias, 4 of 8
+// groups 17.6 us (its 18 MB would take 3.4; some 460 vector instructions a token, a
+// third of them fp64), by softmax without bias or groups 10.7 us, 64 experts 5.8 us;
+// 32 tokens 3 us.  The gradient: 64 experts with dscores 6.0 us, 256 16.2 us.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"

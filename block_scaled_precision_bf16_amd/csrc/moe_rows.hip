@@ -5,9 +5,11 @@
 // The sort counts.  A workgroup's slots are taken in order, a run of them by each
 // wave; a wave counts 64 slots at a time, the lanes of one expert found by a
 // ballot for each bit of its index, so that ranks are those of the slots' order
-// and nothing depends on the order of atomics.  Few slots take one workgroup and
-// one launch; more, three: counts of each workgroup, sums over the workgroups and
-// experts, ranks.
+// and nothing depends on the order of atomics.  Few slots take one workgroup; more
+// take up to 16 in one launch, each of which counts everything; still more take two
+// launches, counts of each workgroup and then their sums and the ranks.  What bounds
+// it is the chain of its steps, not bytes: 1024 slots of 256 experts 7.3 us, 16384 of 8
+// 11.5 us, 131072 of 256 4.5 + 11.2 us.
 //
 // The rest moves rows and is bound by memory: 16-byte accesses, at any byte, several
 // in flight for each lane.
@@ -457,7 +459,8 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[8])
                       bf16x2_rne(v[6], v[7]));
 }
 
-// One chunk of 8 elements of one token per thread; four rows' loads under way.
+// One chunk of 8 elements of one token per thread; four rows' loads under way.  4096
+// tokens from 4 experts each, rows of 7168: 56 us (294 MB, 5.2 TB/s).
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int64_t parts)
 {
     for (int64_t b = blockIdx.x; b < a.T * parts; b += gridDim.x) {
@@ -506,7 +509,8 @@ static bool rows_stream(const CombineArgs &a) { return 2 * a.rows * a.K > int64_
 
 // First a wave per kZeroRows rows for those without a slot (first, and few to a wave:
 // the rows behind the last expert's lie together, and a wave that has 64 of them
-// ends long after all others), then a wave per slot.
+// ends long after all others), then a wave per slot.  4096 tokens from 4 experts each,
+// rows of 7168: 99 us (0.53 GB, 5.3 TB/s).
 constexpr int kZeroRows = 8;
 
 template <bool NT>

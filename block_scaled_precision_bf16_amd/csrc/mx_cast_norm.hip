@@ -2,7 +2,9 @@
 // output: the cast kernel of mx_cast.h whose elements are (h rstd[row])
 // weight[column], rounded to bf16, recomputed from h (2 bytes read instead of
 // the 4 that writing and reading y would take).  The row-wise cast leaves with
-// the norm itself (norm.hip), which holds whole rows.
+// the norm itself (norm.hip), which holds whole rows.  The last rows, which the norm
+// wrote last, come first: some of them are still in the last cache.  16384 x 7168: 80
+// us (0.36 GB, 4.5 TB/s) right behind the norm, whose stores are still draining.
 #include "launch_norm.h"
 #include "mx_cast.h"
 

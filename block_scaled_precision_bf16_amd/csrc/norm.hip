@@ -6,14 +6,21 @@
 //   dw = sum over rows of dy xhat
 //
 // Both are bound by memory: a handful of fp32 operations per element against 4 to
-// 9 bytes.  A workgroup holds one row in registers (16-byte loads, a lane's chunks
-// 64 lanes apart), so that every input is read once: the sum over the row, one
-// barrier, then the outputs.  The loads of the workgroup's next row are issued
-// before that sum.  The row-wise MXFP8 blocks (32 elements, 4 lanes) leave in the
-// same pass; the column-wise casts need all rows' rstd first and re-read h
-// (mx_cast_norm.hip).  The backward's weight gradients are summed in registers
-// over the workgroup's rows and leave as one row of partial sums per workgroup,
-// which a second kernel adds in a fixed order.
+// 10 bytes.  A workgroup holds one row in registers (16-byte loads, neighbouring
+// chunks in neighbouring lanes), so that every input is read once: the sum over the
+// row, one barrier, then the outputs.  The loads of the workgroup's next row are
+// issued before that sum.  The row-wise MXFP8 blocks (32 elements, 4 lanes) leave in
+// the same pass; the column-wise casts need all rows' rstd first and re-read h
+// (mx_cast_norm.hip).  The backward's weight gradients are summed in registers over
+// the rows that a workgroup's threads take and leave as one row of partial sums per
+// workgroup, which a second kernel adds in a fixed order.
+//
+// Measured (a copy of 1 GiB runs at 5.1 TB/s, one of 118 MB at 5.5 to 7): 16384 x 7168
+// with a residual, the row-wise cast and the 8-bit copy 168 us (0.95 GB, 5.6 TB/s),
+// 2048 x 8192 with a residual and the row-wise cast 23.2 us (118 MB, 5.1 TB/s), one row
+// of 4096 3 us.  Backward of 16384 x 7168 with dres from bf16 151 us (0.94 GB, 6.2
+// TB/s), from 8 bits 135 us (0.83 GB, 6.1 TB/s), the sums of its partial weight
+// gradients 4.5 us more.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_norm.h"
@@ -216,7 +223,8 @@ __device__ __forceinline__ int64_t norm_rows(const NormArgs &a)
 }
 
 // NT: the policy of what is read and written once (kNT or 0); AL: K is a multiple of
-// 8.
+// 8 (other rows start at any byte: 16384 x 7001 with y and the row-wise cast 201 us,
+// 2.9 TB/s).
 template <int FMT, int CH, int NT, bool AL>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 {
@@ -260,7 +268,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 }
 
 // Rows of any length, in two passes: the second finds the row in the caches (and
-// each thread what it wrote itself).
+// each thread what it wrote itself).  4096 x 20480 with a residual and the row-wise
+// cast 158 us (0.59 GB, 3.7 TB/s).
 template <int FMT>
 __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
@@ -557,7 +566,8 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
     }
 }
 
-// Rows of any length.  Chunk c of a row: g = dy w and xhat.
+// Rows of any length, in two passes, and their weight gradients in a third.  Chunk c
+// of a row: g = dy w and xhat.
 __device__ __forceinline__ void long_chunk(const NormBackArgs &a, int64_t row, uint32_t c, float rstd, uint4 dyw,
                                            float (&dy)[8], float (&g)[8], float (&xh)[8])
 {
