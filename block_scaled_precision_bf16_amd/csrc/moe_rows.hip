@@ -8,8 +8,8 @@
 // and nothing depends on the order of atomics.  Few slots take one workgroup; more
 // take up to 16 in one launch, each of which counts everything; still more take two
 // launches, counts of each workgroup and then their sums and the ranks.  What bounds
-// it is the chain of its steps, not bytes: 1024 slots of 256 experts 7.3 us, 16384 of 8
-// 11.5 us, 131072 of 256 4.5 + 11.2 us.
+// it is the chain of its steps, not bytes: in a graph 1024 slots of 256 experts 4.9 us,
+// 16384 of 8 7.3 us, 32768 of 256 11.2 us, 131072 of 256 13.7 us.
 //
 // The rest moves rows and is bound by memory: 16-byte accesses, at any byte, several
 // in flight for each lane.
@@ -63,26 +63,24 @@ __device__ __forceinline__ int expert_of(const SortArgs &a, int64_t slot, int64_
     return e;
 }
 
-// Sum of v over the workgroup's threads before this one (red: a word per wave),
-// and over all of them.
-__device__ __forceinline__ int before_sum(int v, int32_t *red, int waves, int &total)
+// Sum of v over the workgroup's threads before this one (red: a word per wave, used
+// once), and over all of them.
+template <int WAVES>
+__device__ __forceinline__ int before_sum(int v, int32_t *red, int &total)
 {
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    int s = v;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(s, d, 64);
-        s += lane >= d ? o : 0;
-    }
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int s = (int)wave_scan((uint32_t)v);
     if (lane == 63)
         red[wave] = s;
     __syncthreads();
     int base = 0;
     total = 0;
-    for (int w = 0; w < waves; w++) {
-        base += w < wave ? red[w] : 0;
-        total += red[w];
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+        const int n = red[w];
+        base += w < wave ? n : 0;
+        total += n;
     }
-    __syncthreads();
     return base + s - v;
 }
 
@@ -147,7 +145,7 @@ __global__ __launch_bounds__(64 * WAVES) void sort_alone_kernel(SortArgs a)
         mine += (n + a.align - 1) / a.align * a.align;
     }
     int total;
-    int at = before_sum(mine, red, WAVES, total);
+    int at = before_sum<WAVES>(mine, red, total);
     for (int k = e0; k < e0 + per && k < a.E; k++) {
         start[k] = at;
         at += (counts[k] + a.align - 1) / a.align * a.align;
@@ -166,12 +164,20 @@ __global__ __launch_bounds__(64 * WAVES) void sort_alone_kernel(SortArgs a)
     fill_rows(a, start, counts, total, 0, 1);
 }
 
-// Rows of a workgroup's slots, its waves' runs of a.chunk / WAVES one after the
-// other from `first` on: base[e], the row of the first of expert e's among them;
-// runs: 16-bit counts [WAVES][E], any values.  Each run is ranked twice where it is
-// longer than RUN 64 (the first ranks are not kept), once otherwise.
+// The first slots of this wave's run of a workgroup's a.chunk, whose first is `first`.
 template <int WAVES>
-__device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, const int32_t *base,
+__device__ __forceinline__ int first_of_run(const SortArgs &a, int64_t first)
+{
+    const int64_t run = a.chunk / WAVES, from = first + (threadIdx.x >> 6) * run;
+    return expert_of(a, from + (threadIdx.x & 63), from + run < a.N ? from + run : a.N);
+}
+
+// Rows of a workgroup's slots, its waves' runs of a.chunk / WAVES one after the
+// other from `first` on, e0 = first_of_run: base[e], the row of the first of expert
+// e's among them; runs: 16-bit counts [WAVES][E], any values.  Each run is ranked
+// twice where it is longer than 64 (the first ranks are not kept), once otherwise.
+template <int WAVES>
+__device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, int e0, const int32_t *base,
                                             uint16_t *runs)
 {
     constexpr int THREADS = 64 * WAVES;
@@ -182,11 +188,11 @@ __device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, co
     for (int k = lane; k < a.E; k += 64)
         cnt[k] = 0;
     __builtin_amdgcn_wave_barrier();
-    int e = expert_of(a, from + lane, end), rank = -1;
+    int e = e0, rank = -1;
     for (int64_t s = from; s < end; s += 64) {
-        const int next = expert_of(a, s + 64 + lane, end);
+        const int next = run > 64 ? expert_of(a, s + 64 + lane, end) : a.E;
         rank = rank_and_count(cnt, e, a.E, bits, lane);
-        e = run > 64 ? next : e;
+        e = next;
     }
     __syncthreads();
     for (int k = threadIdx.x; k < a.E; k += THREADS) {
@@ -199,8 +205,7 @@ __device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, co
         }
     }
     __syncthreads();
-    if (run > 64)
-        e = expert_of(a, from + lane, end);
+    e = e0;
     for (int64_t s = from; s < end; s += 64) {
         const int next = run > 64 ? expert_of(a, s + 64 + lane, end) : a.E;
         if (run > 64)
@@ -218,14 +223,25 @@ __device__ __forceinline__ void place_slots(const SortArgs &a, int64_t first, co
 }
 
 // Up to 16 workgroups in one launch: each counts all slots (wave w those of
-// workgroup w), so that it knows what comes before its own.
-constexpr int kFewWaves = 16, kFewCopies = 8;
-// Few experts: neighbouring lanes count in arrays of their own, or they would queue
-// for the same words.
-__host__ __device__ inline int few_copies(int E) { return E <= 64 ? kFewCopies : 1; }
-__global__ __launch_bounds__(64 * kFewWaves) void sort_few_kernel(SortArgs a)
+// workgroup w, at most 2048), so that it knows what comes before its own.  All of a
+// lane's loads are under way at once.  Few experts are counted in several copies, by
+// neighbouring lanes, or these would queue for the same words.
+constexpr int kFewWaves = 16, kFewLoads = 8;
+static_assert(kSortFew <= 16 * 64 * 4 * kFewLoads, "a wave's slots in one step");
+static int few_copies(int E)
 {
-    extern __shared__ int32_t lds[];       // base [E], start [E], counts [E], runs [16 copies][E] (16 bits)
+    int n = 1;
+    while (n < 32 && 2 * n * E <= 512)
+        n *= 2;
+    return n;
+}
+// 32-bit words of one copy, two experts of a wave in each; one more, so that the
+// copies' words lie in different banks.
+__host__ __device__ inline int few_words(int E) { return kFewWaves * ((E + 1) / 2) + 1; }
+
+__global__ __launch_bounds__(64 * kFewWaves) void sort_few_kernel(SortArgs a, int copies)
+{
+    extern __shared__ int32_t lds[];       // base [E], start [E], counts [E], copies of [16][E] (16 bits)
     __shared__ int32_t red[kFewWaves];
     constexpr int THREADS = 64 * kFewWaves;
     const int E2 = (a.E + 1) & ~1;
@@ -233,43 +249,51 @@ __global__ __launch_bounds__(64 * kFewWaves) void sort_few_kernel(SortArgs a)
     uint32_t *const words = reinterpret_cast<uint32_t *>(counts + E2);
     uint16_t *const runs = reinterpret_cast<uint16_t *>(words);
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, me = (int)blockIdx.x;
-    const int copies = few_copies(a.E);
-    for (int i = threadIdx.x; i < kFewWaves * copies * E2 / 2; i += THREADS)
+    const int64_t from = (int64_t)wave * a.chunk + 4 * lane;
+    const int64_t end = (int64_t)(wave + 1) * a.chunk < a.N ? (int64_t)(wave + 1) * a.chunk : a.N;
+    int4 v[kFewLoads];
+#pragma unroll
+    for (int i = 0; i < kFewLoads; i++) {
+        const int64_t s = from + 256 * i;
+        if (s + 4 <= end)
+            v[i] = *reinterpret_cast<const int4 *>(a.experts + s);
+        else
+            v[i] = make_int4(s < end ? a.experts[s] : -1, s + 1 < end ? a.experts[s + 1] : -1,
+                             s + 2 < end ? a.experts[s + 2] : -1, -1);
+    }
+    const int e0 = first_of_run<kFewWaves>(a, (int64_t)me * a.chunk);
+    for (int i = threadIdx.x; i < copies * few_words(a.E); i += THREADS)
         words[i] = 0;
     __syncthreads();
-    const int64_t from = (int64_t)wave * a.chunk;
-    const int64_t end = from + a.chunk < a.N ? from + a.chunk : a.N;
-    for (int64_t s = from; s < end; s += 8 * 64) {
-        int e[8];
+    uint32_t *const mine_at = words + (lane & (copies - 1)) * few_words(a.E) + wave * (E2 / 2);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            e[i] = expert_of(a, s + 64 * i + lane, end);
+    for (int i = 0; i < kFewLoads; i++) {
+        if (wave * a.chunk + 256 * i >= a.N || 256 * i >= a.chunk)
+            break;
+        const int e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (e[i] < a.E)            // sums of ones: the same in any order
-                atomicAdd(&words[((wave * copies + (lane & (copies - 1))) * E2 + e[i]) >> 1],
-                          1u << (16 * (e[i] & 1)));
+        for (int j = 0; j < 4; j++)
+            if (e[j] >= 0 && e[j] < a.E)   // sums of ones: the same in any order
+                atomicAdd(mine_at + (e[j] >> 1), 1u << (16 * (e[j] & 1)));
     }
     __syncthreads();
     // the copies into the first one, two counts a word (none passes 16 bits)
     for (int i = threadIdx.x; copies > 1 && i < kFewWaves * E2 / 2; i += THREADS) {
-        const int w = i / (E2 / 2);
-        uint32_t *const at = words + w * copies * (E2 / 2) + (i - w * (E2 / 2));
-        uint32_t v = at[0];
-#pragma unroll
-        for (int c = 1; c < kFewCopies; c++)
-            v += at[c * (E2 / 2)];
-        at[0] = v;
+        uint32_t n = words[i];
+#pragma unroll 4
+        for (int c = 1; c < copies; c++)
+            n += words[c * few_words(a.E) + i];
+        words[i] = n;
     }
     __syncthreads();
     // each thread's experts are neighbours, so that the threads' sums are in order
-    const int per = (a.E + THREADS - 1) / THREADS, e0 = (int)threadIdx.x * per;
+    const int per = (a.E + THREADS - 1) / THREADS, k0 = (int)threadIdx.x * per;
     int mine = 0;
-    for (int k = e0; k < e0 + per && k < a.E; k++) {
+    for (int k = k0; k < k0 + per && k < a.E; k++) {
         int n = 0, before = 0;
 #pragma unroll
         for (int w = 0; w < kFewWaves; w++) {
-            const int c = runs[w * copies * E2 + k];
+            const int c = runs[w * E2 + k];
             before += w < me ? c : 0;
             n += c;
         }
@@ -280,14 +304,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void sort_few_kernel(SortArgs a)
         mine += (n + a.align - 1) / a.align * a.align;
     }
     int total;
-    int at = before_sum(mine, red, kFewWaves, total);
-    for (int k = e0; k < e0 + per && k < a.E; k++) {
+    int at = before_sum<kFewWaves>(mine, red, total);
+    for (int k = k0; k < k0 + per && k < a.E; k++) {
         start[k] = at;
         base[k] += at;
         at += (counts[k] + a.align - 1) / a.align * a.align;
     }
     __syncthreads();
-    place_slots<kFewWaves>(a, (int64_t)me * a.chunk, base, runs);
+    place_slots<kFewWaves>(a, (int64_t)me * a.chunk, e0, base, runs);
     fill_rows(a, start, counts, total, me, (int)gridDim.x);
 }
 
@@ -318,6 +342,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a)
     int32_t *const base = lds, *const start = base + a.E, *const counts = start + a.E;
     const int per = (a.E + kSortThreads - 1) / kSortThreads, e0 = (int)threadIdx.x * per;
     const int me = (int)blockIdx.x;
+    const int e1 = first_of_run<kSortWaves>(a, (int64_t)me * a.chunk);
     // a thread's share: experts k, k + 512, .. when they are many, or a part of the
     // workgroups' counts of one expert when they are few
     for (int k = threadIdx.x; k < a.E; k += kSortThreads)
@@ -342,7 +367,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a)
     for (int k = e0; k < e0 + per && k < a.E; k++)
         mine += (counts[k] + a.align - 1) / a.align * a.align;
     int total;
-    int at = before_sum(mine, red, kSortWaves, total);
+    int at = before_sum<kSortWaves>(mine, red, total);
     for (int k = e0; k < e0 + per && k < a.E; k++) {
         start[k] = at;
         base[k] += at;
@@ -351,7 +376,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a)
             a.counts[k] = counts[k];
     }
     __syncthreads();
-    place_slots<kSortWaves>(a, (int64_t)me * a.chunk, base, reinterpret_cast<uint16_t *>(counts + a.E));
+    place_slots<kSortWaves>(a, (int64_t)me * a.chunk, e1, base, reinterpret_cast<uint16_t *>(counts + a.E));
     fill_rows(a, start, counts, total, me, (int)gridDim.x);
 }
 
@@ -362,8 +387,9 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t s)
     if (a.N <= 1024) {
         hipLaunchKernelGGL((sort_alone_kernel<4, 4>), dim3(1), dim3(256), sums + 4 * run, s, a);
     } else if (!a.ws) {
-        hipLaunchKernelGGL(sort_few_kernel, dim3(a.blocks), dim3(64 * kFewWaves), sums + few_copies(a.E) * kFewWaves * run,
-                           s, a);
+        const int copies = few_copies(a.E);
+        hipLaunchKernelGGL(sort_few_kernel, dim3(a.blocks), dim3(64 * kFewWaves),
+                           sums + (size_t)copies * few_words(a.E) * sizeof(uint32_t), s, a, copies);
     } else {
         hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, s, a);
         hipLaunchKernelGGL(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads), sums + kSortWaves * run,

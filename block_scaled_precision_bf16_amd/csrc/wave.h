@@ -12,6 +12,7 @@ namespace mxk {
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;            // quad_perm [1,0,3,2], [2,3,0,1]
 constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;  // lane i <-> 7 - i, 15 - i
 constexpr int kDppBcast15 = 0x142, kDppBcast31 = 0x143;
+constexpr int kDppShr1 = 0x111, kDppShr2 = 0x112, kDppShr4 = 0x114, kDppShr8 = 0x118;   // lane i <- i - n of its row
 
 // v of the lane that CTRL names; `old` where ROWS (a mask of rows of 16) or CTRL
 // leaves a lane out.
@@ -56,6 +57,17 @@ __device__ __forceinline__ T wave_sum(T v)
     v += dpp<kDppBcast15, 0xA>(T(0), v);
     v += dpp<kDppBcast31, 0xC>(T(0), v);
     return from_lane(v, 63);
+}
+
+// Each lane's sum of the lanes up to it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v)
+{
+    v += dpp<kDppShr1>(0u, v);
+    v += dpp<kDppShr2>(0u, v);
+    v += dpp<kDppShr4>(0u, v);
+    v += dpp<kDppShr8>(0u, v);
+    v += dpp<kDppBcast15, 0xA>(0u, v);
+    return v + dpp<kDppBcast31, 0xC>(0u, v);
 }
 
 __device__ __forceinline__ float max_of(float a, float b) { return __builtin_fmaxf(a, b); }
