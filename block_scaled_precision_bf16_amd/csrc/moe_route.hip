@@ -14,9 +14,9 @@
 // less time than the instructions: the exponentials and `top` maxima bound it.
 //
 // Measured for 16384 tokens, 8 experts each: 256 experts by sigmoid, bias, 4 of 8
-// groups 17.6 us (its 18 MB would take 3.4; some 460 vector instructions a token, a
-// third of them fp64), by softmax without bias or groups 10.7 us, 64 experts 5.8 us;
-// 32 tokens 3 us.  The gradient: 64 experts with dscores 6.0 us, 256 16.2 us.
+// groups 16.1 us (its 18 MB would take 3.4; 430 vector instructions a token, a
+// third of them fp64; 65536 tokens 45 us), by softmax without bias or groups 10.4 us,
+// 64 experts 5.8 us; 32 tokens 3 us.  The gradient: 64 experts with dscores 6.0 us, 256 16.2 us.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"
@@ -77,9 +77,8 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t t, int64_t ro
 // the hardware's reciprocal, measured good to 2^-24, and one Newton step); and double.
 struct Quick {
     typedef double type;
-    static __device__ __forceinline__ double exp_nonpos(double a)
+    static __device__ __forceinline__ double exp_in_range(double c)
     {
-        const double c = __builtin_fmax(a, -1100.0);    // 0 already; NaN: the last select
         const double n = __builtin_rint(c * 1.44269504088896340736);
         double r = __builtin_fma(n, -0.693359375, c);              // 355/512
         r = __builtin_fma(n, 2.1219444005469058277e-4, r);         // ln 2 - 355/512
@@ -93,13 +92,23 @@ struct Quick {
         p = __builtin_fma(p, r, 0.5);
         p = __builtin_fma(p, r, 1.0);
         p = __builtin_fma(p, r, 1.0);
-        p = __builtin_ldexp(p, (int)n);
+        return __builtin_ldexp(p, (int)n);
+    }
+    static __device__ __forceinline__ double exp_nonpos(double a)
+    {
+        const double p = exp_in_range(__builtin_fmax(a, -1100.0));    // 0 already
         return a != a ? a : p;
     }
     static __device__ __forceinline__ double rcp(double d)
     {
         const double r = __builtin_amdgcn_rcp(d);
         return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    }
+    // 1 / (1 + e^-x), of a number (in double no x needs the other form; past 110 it
+    // is 1, and below -110 it rounds to 0 in fp32)
+    static __device__ __forceinline__ double sigmoid(float x)
+    {
+        return rcp(1.0 + exp_in_range((double)__builtin_amdgcn_fmed3f(-x, -110.0f, 110.0f)));
     }
 };
 struct Single {
@@ -169,21 +178,29 @@ struct Fixed {
 template <int NPL, bool ROW>
 __device__ __forceinline__ Fixed fixed_point(const float (&bias)[NPL])
 {
-    float most = 0.0f;
-    bool inf = false;
+    uint32_t all = 0u;
 #pragma unroll
-    for (int i = 0; i < NPL; i++) {
-        const float b = __builtin_fabsf(bias[i]);
-        inf |= bias[i] == __builtin_inff();
-        most = b < __builtin_inff() ? __builtin_fmaxf(most, b) : most;
+    for (int i = 0; i < NPL; i++)
+        all = max_u32(all, bits_f32(bias[i]) & 0x7FFFFFFFu);
+    all = ROW ? row_max(all) : wave_max(all);
+    bool inf = false;
+    if (__builtin_amdgcn_ballot_w64(all >= 0x7F800000u)) {   // without infinite ones and NaN
+        all = 0u;
+#pragma unroll
+        for (int i = 0; i < NPL; i++) {
+            const uint32_t b = bits_f32(bias[i]) & 0x7FFFFFFFu;
+            inf |= bias[i] == __builtin_inff();
+            all = b < 0x7F800000u ? max_u32(all, b) : all;
+        }
+        all = ROW ? row_max(all) : wave_max(all);
     }
-    most = ROW ? row_max(most) : wave_max(most);
+    const float most = f32_bits(all);
     const int e = __builtin_amdgcn_frexp_exp(1.0 + (double)most);   // 1 + most < 2^e
     return Fixed{__builtin_ldexp(1.0, 29 - e), __builtin_amdgcn_ballot_w64(inf) != 0};
 }
-__device__ __forceinline__ uint32_t order_of(double k, const Fixed &f)
+__device__ __forceinline__ uint32_t order_of(double score, float bias, const Fixed &f)
 {
-    return (uint32_t)__builtin_fma(k, f.mul, (double)(kFixedZero - 1)) + 1u;
+    return (uint32_t)__builtin_fma(score, f.mul, __builtin_fma((double)bias, f.mul, (double)kFixedZero));
 }
 
 // What a token's choice leaves: lane j's expert (-1: none) of slot j; sure: that
@@ -476,14 +493,23 @@ __device__ __forceinline__ bool keys_of(const RouteArgs &a, const float (&x)[NPL
         const Fixed f = fixed_point<NPL, ROW>(bias);
         infinite = f.infinite;
         double s[NPL], q[NPL];
-        scores_of<Quick, NPL, ROW>(x, a.sigmoid != 0, s, q);
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < NPL; i++) {
+                s[i] = Quick::sigmoid(x[i]);
+                p[i] = x[i] != x[i] ? x[i] : (float)s[i];
+            }
+        } else {
+            scores_of<Quick, NPL, ROW>(x, false, s, q);
+#pragma unroll
+            for (int i = 0; i < NPL; i++)
+                p[i] = (float)s[i];
+        }
 #pragma unroll
         for (int i = 0; i < NPL; i++) {
-            const double k = s[i] + (double)bias[i];
             const bool masked = x[i] == -__builtin_inff() || bias[i] == -__builtin_inff();
-            p[i] = (float)s[i];
-            key[i] = masked ? 0u : order_of(k, f);
-            nan |= !masked & (k != k);
+            key[i] = masked ? 0u : order_of(s[i], bias[i], f);
+            nan |= !masked & __builtin_isunordered(p[i], bias[i]);
         }
     } else {
         float q[NPL];
@@ -631,36 +657,36 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route16_kernel(RouteArgs a)
         for (int i = 0; i < PER; i++)
             part[i] = key[c * 4 + i];
         list[c] = sort_lane<PER>(part);
+        list[c].at += 0x04040404u * c;
     }
     const int rounds = a.top + (VALUE ? 1 : 0);
     int n = 0;
     for (int j = 0; j < rounds; j++) {
-        uint32_t best = list[0].k0, at = list[0].at;
-        int which = 0;
+        uint32_t best = list[0].k0;
 #pragma unroll
-        for (int c = 1; c < LISTS; c++) {
-            const bool more = list[c].k0 > best;
-            best = more ? list[c].k0 : best;
-            at = more ? list[c].at : at;
-            which = more ? c : which;
-        }
+        for (int c = 1; c < LISTS; c++)
+            best = max_u32(best, list[c].k0);
         const uint32_t m = row_max(best);
         if (__builtin_amdgcn_ballot_w64(m != 0u) == 0)
             break;
         const uint32_t who = (uint32_t)(__builtin_amdgcn_ballot_w64(best == m) >> (lane & 48));
         const bool mine = m != 0u && (int)__builtin_ctz(who | 0x10000u) == l;
-        if (mine)
-            found[wave][row][j] = make_uint2((uint32_t)(l * NPL + which * 4) + (at & 0xFFu), m);
         n += m != 0u ? 1 : 0;
+        uint32_t at = 0u;
+        bool left = mine;              // the first of its lists that has the key
 #pragma unroll
         for (int c = 0; c < LISTS; c++) {
-            const bool up = mine && which == c;
+            const bool up = left && list[c].k0 == m;
+            left = left && !up;
+            at = up ? list[c].at : at;
             list[c].k0 = up ? list[c].k1 : list[c].k0;
             list[c].k1 = up ? list[c].k2 : list[c].k1;
             list[c].k2 = up ? list[c].k3 : list[c].k2;
             list[c].k3 = up ? 0u : list[c].k3;
             list[c].at = up ? list[c].at >> 8 : list[c].at;
         }
+        if (mine)
+            found[wave][row][j] = make_uint2((uint32_t)(l * NPL) + (at & 0xFFu), m);
     }
     __builtin_amdgcn_wave_barrier();
     if constexpr (VALUE) {
