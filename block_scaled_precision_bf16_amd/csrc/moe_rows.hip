@@ -505,8 +505,11 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int64_t par
                 w[j] = a.weights && r[j] >= 0 ? a.weights[s] : 1.0f;
             }
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                y[j] = load_chunk<false>(a.y + (r[j] < 0 ? 0 : r[j]) * a.K, c, r[j] < 0 ? 0 : a.K);
+            for (int j = 0; j < 4; j++) {
+                const int64_t len = r[j] < 0 ? 0 : a.K;
+                const uint16_t *const yr = a.y + (r[j] < 0 ? 0 : r[j]) * a.K;
+                y[j] = 8 * c + 8 <= len ? whole_chunk<false>(yr, c) : load_chunk<false>(yr, c, len);
+            }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 float v[8];
@@ -543,7 +546,7 @@ template <bool NT>
 __global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a, int64_t zeros)
 {
     const int lane = (int)threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), s = w - zeros;
+    const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), s = w - zeros;
     if (s < 0) {
         const int64_t r0 = w * kZeroRows;
         const bool empty = lane < kZeroRows && r0 + lane < a.rows && a.slots[r0 + lane] == -1;

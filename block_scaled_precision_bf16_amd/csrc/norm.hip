@@ -210,9 +210,9 @@ __device__ __forceinline__ void norm_load(const NormArgs &a, int64_t row, NormRo
     const Row<AL, const uint16_t> x = row_at<AL>(a.x, at, len), r = row_at<AL>(a.res, at, a.res ? len : 0);
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        v.x[i] = row_load<AUX>(x, threadIdx.x + i * blockDim.x);
+        v.x[i] = row_raw<AUX>(x, threadIdx.x + i * blockDim.x);
         if (a.res)
-            v.r[i] = row_load<AUX>(r, threadIdx.x + i * blockDim.x);
+            v.r[i] = row_raw<AUX>(r, threadIdx.x + i * blockDim.x);
     }
 }
 
@@ -223,8 +223,8 @@ __device__ __forceinline__ int64_t norm_rows(const NormArgs &a)
 }
 
 // NT: the policy of what is read and written once (kNT or 0); AL: K is a multiple of
-// 8 (other rows start at any byte: 16384 x 7001 with y and the row-wise cast 201 us,
-// 2.9 TB/s).
+// 8 (other rows start at any byte: 16384 x 7001 with a residual, the row-wise cast and
+// the 8-bit copy 232 us, 4.0 TB/s).
 template <int FMT, int CH, int NT, bool AL>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 {
@@ -246,8 +246,11 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
-            const uint32_t x[4] = {next.x[i].x, next.x[i].y, next.x[i].z, next.x[i].w};
-            norm_sum(x, a.res ? &next.r[i] : nullptr, h[i], s0, s1);
+            const uint32_t c = threadIdx.x + i * blockDim.x;
+            const uint4 u = row_fix<AL>(next.x[i], c, (uint32_t)a.K);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+            const uint4 r = row_fix<AL>(next.r[i], c, (uint32_t)a.K);
+            norm_sum(x, a.res ? &r : nullptr, h[i], s0, s1);
         }
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
         norm_load<CH, NT, AL>(a, after, next);
@@ -269,39 +272,53 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 
 // Rows of any length, in two passes: the second finds the row in the caches (and
 // each thread what it wrote itself).  4096 x 20480 with a residual and the row-wise
-// cast 158 us (0.59 GB, 3.7 TB/s).
-template <int FMT>
+// cast 144 us (0.59 GB, 4.1 TB/s; its h read again from the caches), x 20481 200 us.
+template <int FMT, bool AL>
 __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
-    const uint32_t nb = (uint32_t)((a.K + 31) >> 5), chunks = (uint32_t)((a.K + 7) >> 3);
+    const uint32_t nb = (uint32_t)((a.K + 31) >> 5), chunks = (uint32_t)((a.K + 7) >> 3), K = (uint32_t)a.K;
     // whole waves, which cover the tile layout's padding blocks too
     const uint32_t upto = (chunks + 63) & ~63u;
     const int64_t rows = norm_rows(a);
-    const Row<false, const uint16_t> w = row_at<false>(a.w, 0, a.w ? a.K : 0);
+    const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     int step = 0;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, step ^= 1) {
         const int64_t at = row * a.K, len = row < a.M ? a.K : 0;
-        const Row<false, const uint16_t> x = row_at<false>(a.x, at, len), r = row_at<false>(a.res, at, a.res ? len : 0);
-        const NormOut<false> o = norm_out<false>(a, row, nb);
+        const Row<AL, const uint16_t> x = row_at<AL>(a.x, at, len), r = row_at<AL>(a.res, at, a.res ? len : 0);
+        const NormOut<AL> o = norm_out<AL>(a, row, nb);
         float s0 = 0.0f, s1 = 0.0f;
-        for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
-            const uint4 v = row_load<0>(x, c), q = row_load<0>(r, c);
-            const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
-            norm_sum(xw, a.res ? &q : nullptr, h, s0, s1);
-            if (a.h)
-                row_store<0>(o.h, c, make_uint4(h[0], h[1], h[2], h[3]));
+        for (uint32_t c0 = threadIdx.x; c0 < chunks; c0 += 2 * 512) {
+            uint4 xv[2], rv[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                xv[i] = row_raw<0>(x, c0 + 512 * i);
+                if (a.res)
+                    rv[i] = row_raw<0>(r, c0 + 512 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const uint32_t c = c0 + 512 * i;
+                const uint4 v = row_fix<AL>(xv[i], c, K), q = row_fix<AL>(rv[i], c, K);
+                const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
+                uint32_t h[4];
+                norm_sum(xw, a.res ? &q : nullptr, h, s0, s1);
+                if (a.h)
+                    row_store<0>(o.h, c, make_uint4(h[0], h[1], h[2], h[3]));
+            }
         }
         const float rstd = rstd_of(block_sum(s0 + s1, red[step], 8), a.K, a.eps);
         if (row < a.M && threadIdx.x == 0)
             a.rstd[row] = rstd;
-        const Row<false, const uint16_t> hr = a.h ? row_at<false>((const uint16_t *)a.h, at, len) : x;
+        const Row<AL, const uint16_t> hr = a.h ? row_at<AL>((const uint16_t *)a.h, at, len) : x;
         for (uint32_t c = threadIdx.x; c < upto; c += 512) {
-            const uint4 v = row_load<0>(hr, c);
+            uint4 wt = make_uint4(kOnes, kOnes, kOnes, kOnes), v = row_raw<0>(hr, c);
+            if (a.w)
+                wt = row_raw<0>(w, c);
+            v = row_fix<AL>(v, c, K);
+            wt = a.w ? row_fix<AL>(wt, c, K) : wt;
             const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-            norm_write<FMT, 0, false>(a, o, row, c, nb, h, rstd,
-                                      a.w ? row_load<0>(w, c) : make_uint4(kOnes, kOnes, kOnes, kOnes));
+            norm_write<FMT, 0, AL>(a, o, row, c, nb, h, rstd, wt);
         }
     }
 }
@@ -316,7 +333,8 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
     const int64_t most = 256 * (n.chunks == 0 ? 4 : 1024 / n.threads);
     const dim3 grid((unsigned)(rows < most ? rows : most)), block(n.threads);
     if (n.chunks == 0)
-        hipLaunchKernelGGL(norm_long_kernel<FMT>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((a.K % 8 == 0 ? norm_long_kernel<FMT, true> : norm_long_kernel<FMT, false>), grid, block,
+                           0, s, a);
     else if (a.K % 8 != 0)
         hipLaunchKernelGGL((a.stream ? norm_kernel<FMT, 2, kNT, false> : norm_kernel<FMT, 2, 0, false>), grid,
                            block, 0, s, a);
@@ -377,15 +395,15 @@ __device__ __forceinline__ void back_load(const NormBackArgs &a, int64_t row, ui
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const uint32_t c = tid + i * n;
-        v.dy[i] = row_load<AUX>(dy, c);
+        v.dy[i] = row_raw<AUX>(dy, c);
         if constexpr (CK) {
-            v.q[i] = row_load<AUX>(q, c);
+            v.q[i] = row_raw<AUX>(q, c);
             v.s[i] = buf_load1(s, c >> 2);
         } else {
-            v.h[i] = row_load<AUX>(h, c);
+            v.h[i] = row_raw<AUX>(h, c);
         }
         if (a.dres)
-            v.dres[i] = row_load<AUX>(dres, c);
+            v.dres[i] = row_raw<AUX>(dres, c);
     }
 }
 
@@ -446,12 +464,13 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
         float g[CH][8], xh[CH][8], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
-            const uint32_t dy[4] = {v.dy[i].x, v.dy[i].y, v.dy[i].z, v.dy[i].w};
+            const uint4 u = row_fix<AL>(v.dy[i], tid + i * n, (uint32_t)a.K);
+            const uint32_t dy[4] = {u.x, u.y, u.z, u.w};
             float hv[8];
             if constexpr (CK)
-                h_values(v.q[i], v.s[i], hv);
+                h_values(row_fix<AL>(v.q[i], tid + i * n, (uint32_t)a.K), v.s[i], hv);
             else
-                h_values(v.h[i], hv);
+                h_values(row_fix<AL>(v.h[i], tid + i * n, (uint32_t)a.K), hv);
 #pragma unroll
             for (int d = 0; d < 4; d++) {
                 const float y0 = bf16_lo(dy[d]), y1 = bf16_hi(dy[d]);
@@ -469,7 +488,8 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
         const Row<AL, uint16_t> ro = row_at<AL>(a.dh, row * a.K, row < a.M ? a.K : 0);
 #pragma unroll
         for (int i = 0; i < CH; i++) {
-            const uint32_t dr[4] = {v.dres[i].x, v.dres[i].y, v.dres[i].z, v.dres[i].w};
+            const uint4 u = row_fix<AL>(v.dres[i], tid + i * n, (uint32_t)a.K);
+            const uint32_t dr[4] = {u.x, u.y, u.z, u.w};
             uint32_t o[4];
 #pragma unroll
             for (int d = 0; d < 4; d++) {
@@ -567,66 +587,112 @@ __global__ __launch_bounds__(T) void norm_back_kernel(NormBackArgs a, int rows)
 }
 
 // Rows of any length, in two passes, and their weight gradients in a third.  Chunk c
-// of a row: g = dy w and xhat.
-__device__ __forceinline__ void long_chunk(const NormBackArgs &a, int64_t row, uint32_t c, float rstd, uint4 dyw,
+// of a row: dy, g = dy w and xhat.
+template <bool AL>
+struct LongRow {
+    Row<AL, const uint16_t> dy, h, dres;
+    Row<AL, const uint8_t> q;
+    rsrc_t s;
+};
+
+template <bool AL>
+__device__ __forceinline__ LongRow<AL> long_row(const NormBackArgs &a, int64_t row)
+{
+    const int64_t at = row * a.K, nb = (a.K + 31) >> 5;
+    LongRow<AL> v;
+    v.dy = row_at<AL>(a.dy, at, a.K);
+    v.h = row_at<AL>(a.h, at, a.h ? a.K : 0);
+    v.dres = row_at<AL>(a.dres, at, a.dres ? a.K : 0);
+    v.q = row_at<AL>(a.q_h, at, a.h ? 0 : a.K);
+    v.s = make_rsrc(a.s_h + (a.h ? 0 : row * nb), 0, a.h ? 0 : nb);
+    return v;
+}
+
+template <bool AL>
+__device__ __forceinline__ void long_chunk(const NormBackArgs &a, const LongRow<AL> &v,
+                                           const Row<AL, const uint16_t> &wr, uint32_t c, float rstd,
                                            float (&dy)[8], float (&g)[8], float (&xh)[8])
 {
-    const int64_t at = row * a.K;
-    h_values(dyw, dy);
+    const uint32_t K = (uint32_t)a.K;
+    uint4 w = make_uint4(kOnes, kOnes, kOnes, kOnes), h;
+    uint2 q;
+    uint32_t sb;
+    const uint4 d = row_raw<0>(v.dy, c);
+    if (a.h) {
+        h = row_raw<0>(v.h, c);
+    } else {
+        q = row_raw<0>(v.q, c);
+        sb = buf_load1(v.s, c >> 2);
+    }
+    if (a.w)
+        w = row_raw<0>(wr, c);
+    h_values(row_fix<AL>(d, c, K), dy);
     if (a.h)
-        h_values(load_chunk<false>(a.h + at, c, a.K), xh);
+        h_values(row_fix<AL>(h, c, K), xh);
     else
-        h_values(load_codes<false>(a.q_h + at, c, a.K), a.s_h[row * ((a.K + 31) >> 5) + (c >> 2)], xh);
-    float w[8];
-    h_values(a.w ? load_chunk<false>(a.w, c, a.K) : make_uint4(kOnes, kOnes, kOnes, kOnes), w);
+        h_values(row_fix<AL>(q, c, K), sb, xh);
+    float wv[8];
+    h_values(a.w ? row_fix<AL>(w, c, K) : w, wv);
 #pragma unroll
-    for (int d = 0; d < 8; d++) {
-        xh[d] *= rstd;
-        g[d] = dy[d] * w[d];
+    for (int i = 0; i < 8; i++) {
+        xh[i] *= rstd;
+        g[i] = dy[i] * wv[i];
     }
 }
 
+template <bool AL>
 __global__ __launch_bounds__(512) void norm_back_long_kernel(NormBackArgs a)
 {
     __shared__ float red[2][16];
     const uint32_t chunks = (uint32_t)((a.K + 7) >> 3);
+    const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     int step = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, step ^= 1) {
         const float rstd = a.rstd[row];
-        const uint16_t *const dyr = a.dy + row * a.K;
+        const LongRow<AL> v = long_row<AL>(a, row);
+        const Row<AL, uint16_t> dh = row_at<AL>(a.dh, row * a.K, a.K);
         float s = 0.0f, dy[8], g[8], xh[8];
+#pragma unroll 4
         for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
-            long_chunk(a, row, c, rstd, load_chunk<false>(dyr, c, a.K), dy, g, xh);
+            long_chunk<AL>(a, v, w, c, rstd, dy, g, xh);
 #pragma unroll
             for (int d = 0; d < 8; d++)
                 s = __builtin_fmaf(g[d], xh[d], s);
         }
         const float mean = block_sum(s, red[step], 8) / (float)a.K;
         for (uint32_t c = threadIdx.x; c < chunks; c += 512) {
-            long_chunk(a, row, c, rstd, load_chunk<false>(dyr, c, a.K), dy, g, xh);
             float r[8] = {};
+            uint4 dr;
             if (a.dres)
-                h_values(load_chunk<false>(a.dres + row * a.K, c, a.K), r);
+                dr = row_raw<0>(v.dres, c);
+            long_chunk<AL>(a, v, w, c, rstd, dy, g, xh);
+            if (a.dres)
+                h_values(row_fix<AL>(dr, c, (uint32_t)a.K), r);
             uint32_t o[4];
 #pragma unroll
             for (int d = 0; d < 4; d++)
                 o[d] = bf16x2_rne(rstd * __builtin_fmaf(-xh[2 * d], mean, g[2 * d]) + r[2 * d],
                                   rstd * __builtin_fmaf(-xh[2 * d + 1], mean, g[2 * d + 1]) + r[2 * d + 1]);
-            store_chunk<false>(a.dh + row * a.K, c, a.K, make_uint4(o[0], o[1], o[2], o[3]));
+            row_store<0>(dh, c, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
 
-// Their partial weight gradients: slice blockIdx.y of the rows, a chunk per thread.
+// Their partial weight gradients: slice blockIdx.y of the rows, a chunk per thread, four
+// rows' loads under way.  Both and their sums, 4096 x 20480 with dres: from bf16 208 us,
+// from 8 bits 193 us (0.67 GB; 1.2 GB with what is read twice).
+template <bool AL>
 __global__ __launch_bounds__(256) void norm_dweight_long_kernel(NormBackArgs a)
 {
     const uint32_t c = blockIdx.x * 256 + threadIdx.x;
     if (8 * (int64_t)c >= a.K)
         return;
+    const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     float sum[8] = {};
+#pragma unroll 4
     for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
         float dy[8], g[8], xh[8];
-        long_chunk(a, row, c, a.rstd[row], load_chunk<false>(a.dy + row * a.K, c, a.K), dy, g, xh);
+        long_chunk<AL>(a, long_row<AL>(a, row), w, c, a.rstd[row], dy, g, xh);
 #pragma unroll
         for (int d = 0; d < 8; d++)
             sum[d] = __builtin_fmaf(dy[d], xh[d], sum[d]);
@@ -677,10 +743,11 @@ hipError_t launch_norm_back(const NormBackArgs &a, hipStream_t s)
     const int rows = norm_back_rows(n);
     const bool al = a.K % 8 == 0;
     if (n.chunks == 0) {
-        hipLaunchKernelGGL(norm_back_long_kernel, dim3((unsigned)(a.M < 1024 ? a.M : 1024)), dim3(512), 0, s, a);
+        hipLaunchKernelGGL((al ? norm_back_long_kernel<true> : norm_back_long_kernel<false>),
+                           dim3((unsigned)(a.M < 1024 ? a.M : 1024)), dim3(512), 0, s, a);
         if (a.partials)
-            hipLaunchKernelGGL(norm_dweight_long_kernel, dim3((unsigned)((a.K + 2047) / 2048), parts), dim3(256),
-                               0, s, a);
+            hipLaunchKernelGGL((al ? norm_dweight_long_kernel<true> : norm_dweight_long_kernel<false>),
+                               dim3((unsigned)((a.K + 2047) / 2048), parts), dim3(256), 0, s, a);
     } else if (rows > 1) {
         (!al             ? launch_back<2, false, true, 512>
          : n.chunks == 1 ? launch_back<1, true, true, 512>

@@ -484,6 +484,30 @@ def test_combine(T, top, E, align, K):
     assert np.all(np.abs(f64(o) - want) <= 2.0 ** -8 * np.abs(want) + top * HALF * mag * 1.01 + 1e-38)
 
 
+def test_combine_at_every_end_of_a_row():
+    for K in (*range(1, 18), *range(2041, 2058)):
+        g = generator(K)
+        y, w, dout = normal(g, 7, K), torch.randn(5, 2, generator=g), normal(g, 5, K)
+        pos = torch.tensor([[0, 6], [-1, 2], [3, 3], [7, 1], [5, 4]], dtype=I32)
+        slots = torch.tensor([0, 7, 3, 4, 9, 8, 1], dtype=I32)
+        bufs, broken = outs(dict(out=((5, K), BF16), dy=((7, K), BF16), dweights=((5, 2), F32)))
+        o = mx.moe_combine(y.cuda(), w.cuda(), pos.cuda(), out=bufs["out"])
+        b = mx.moe_combine_backward(dout.cuda(), y.cuda(), w.cuda(), pos=pos.cuda(), slots=slots.cuda(),
+                                    out=bufs)
+        torch.cuda.synchronize()
+        assert broken() == []
+        want, mag = combine_ref(f64(y), f64(w), pos.numpy())
+        assert np.all(np.abs(f64(o) - want) <= 2.0 ** -8 * np.abs(want) + 2 * HALF * mag * 1.01 + 1e-38)
+        s = slots.numpy()
+        dy = f64(w).reshape(-1)[s, None] * f64(dout)[s // 2]
+        assert np.all(np.abs(f64(b["dy"]) - dy) <= (2.0 ** -8 + 2 * HALF) * np.abs(dy))
+        p = pos.numpy()
+        live = (p >= 0) & (p < 7)
+        prod = np.where(live[:, :, None], f64(y)[np.where(live, p, 0)], 0.0) * f64(dout)[:, None, :]
+        adds = 8 * -(-K // 512) + 7
+        assert np.all(np.abs(f64(b["dweights"]) - prod.sum(2)) <= adds * HALF * np.abs(prod).sum(2) + 1e-38)
+
+
 def test_combine_of_any_positions():
     """Rows named twice or by no slot, positions outside the rows."""
     g = generator(12)

@@ -99,6 +99,17 @@ def test_norm(M, K):
     check_norm(x, None, res, axis=3 | mx.ELEM_E5M2 | mx.SCALE_ROUND_UP)
 
 
+@pytest.mark.parametrize("first", [1, 4089, 8193, 16385])
+def test_every_end_of_a_row(first):
+    """Row lengths of every remainder mod 8, in each kind of kernel, forward and back."""
+    for K in range(first, first + (24 if first == 1 else 8)):
+        g = generator(K)
+        dy, x, w, res = normal(g, 3, K), normal(g, 3, K), normal(g, K), normal(g, 3, K)
+        check_norm(x, w, res, axis=3, ckpt=True)
+        check_back(dy, x, w, res)
+        check_back(dy, x, w, res, ckpt=True)
+
+
 def test_norm_without_y_gives_the_same_casts():
     g = generator(1)
     for M, K in ((96, 1000), (37, 77)):
