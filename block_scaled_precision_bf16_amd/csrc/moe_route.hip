@@ -7,16 +7,16 @@
 //   dp_j = (scale / s) (dw_j - sum_i dw_i p_i / s) for the chosen ones, plus the
 //   scores' own gradient
 //
-// Up to 256 experts: four tokens a wave, 16 lanes each; lane l of them holds the
-// experts l NPL .. l NPL + NPL - 1, so that the lowest lane among equal keys, and
-// there the first, is the lowest index.  More experts, and groups that are not a
-// power of two of such lanes, take a wave per token.  The bytes (4 an expert) take
-// less time than the instructions: the exponentials and `top` maxima bound it.
+// Many tokens of up to 256 experts: four tokens a wave, 16 lanes each; lane l of them
+// holds the experts l NPL .. l NPL + NPL - 1, so that the lowest lane among equal keys,
+// and there the first, is the lowest index.  Few tokens, more experts, and groups that
+// are not a power of two of such lanes, take a wave per token.  The bytes (4 an expert)
+// take less time than the instructions: the exponentials and `top` maxima bound it.
 //
 // Measured for 16384 tokens, 8 experts each: 256 experts by sigmoid, bias, 4 of 8
 // groups 16.1 us (its 18 MB would take 3.4; 430 vector instructions a token, a
 // third of them fp64; 65536 tokens 45 us), by softmax without bias or groups 10.4 us,
-// 64 experts 5.8 us; 32 tokens 3 us.  The gradient: 64 experts with dscores 6.0 us, 256 16.2 us.
+// 64 experts 5.8 us.  The gradient: 64 experts with dscores 6.0 us.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"
@@ -854,11 +854,19 @@ static void launch_npl16(const RouteArgs &a, bool value, hipStream_t s)
         hipLaunchKernelGGL((route16_kernel<NPL, false>), grid, block, 0, s, a);
 }
 
+// Tokens up to which a wave takes one alone, for its shorter chain of steps; more fill
+// the chip's 1024 SIMDs with four to a wave.  In a graph, one and four to a wave, 256
+// experts by sigmoid, bias and groups: 32 tokens 4.5 and 7.8 us, 2048 5.2 and 8.0, 8192
+// 10.6 and 10.4; 64 by softmax: 32 tokens 2.8 and 3.4, 2048 3.2 and 3.6, 4096 3.7 and
+// 3.6.  The gradient of 64: 32 tokens 3.1 and 3.4, 4096 3.8 and 3.8, 16384 7.5 and 4.8;
+// of 256 with a wave to each always (16384 11.9 and 13.9, 65536 38.3 and 37.6).
+constexpr int64_t kFewTokens = 2048;
+
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 {
     const bool value = a.bias || (a.pair && a.groups > 1);
     const int npl = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 128 ? 8 : 16;
-    if (a.E <= 256 && groups_of_lanes(a.E, a.groups, npl)) {
+    if (a.E <= 256 && a.T > kFewTokens && groups_of_lanes(a.E, a.groups, npl)) {
         switch (npl) {
         case 1: launch_npl16<1>(a, value, s); break;
         case 2: launch_npl16<2>(a, value, s); break;
@@ -890,7 +898,12 @@ static void launch_back(const RouteBackArgs &a, hipStream_t s)
 
 hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t s)
 {
-    if (a.E <= 16)
+    const bool few = a.T <= kFewTokens;
+    if (a.E <= 64 && few)
+        launch_back<1, false>(a, s);
+    else if (a.E <= 128 && few)
+        launch_back<2, false>(a, s);
+    else if (a.E <= 16)
         launch_back<1, true>(a, s);
     else if (a.E <= 32)
         launch_back<2, true>(a, s);
@@ -899,7 +912,7 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t s)
     else if (a.E <= 128)
         launch_back<8, true>(a, s);
     else if (a.E <= 256)
-        launch_back<16, true>(a, s);
+        launch_back<4, false>(a, s);
     else if (a.E <= 512)
         launch_back<8, false>(a, s);
     else
