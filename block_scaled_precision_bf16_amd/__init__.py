@@ -51,7 +51,7 @@ EXPORTS = ("mx_quantize", "mx_quantize_workspace_size", "mx_quantize_noalloc", "
            "mx_matmul", "mx_matmul_grouped", "mx_matmul_wgrad_grouped",
            "mx_matmul_workspace_size", "mx_matmul_grouped_workspace_size",
            "mx_matmul_wgrad_grouped_workspace_size", "nvfp4_matvec", "nvfp4_matvec_experts",
-           "mx_rmsnorm", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size",
+           "mx_rmsnorm", "mx_rmsnorm_workspace_size", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size",
            "moe_route", "moe_route_backward", "moe_sort", "moe_sort_rows", "moe_sort_workspace_size",
            "moe_gather", "moe_combine", "moe_combine_backward",
            "mx_status_str", "mx_abi_version")
@@ -142,7 +142,7 @@ def lib():
                                            _i64, ctypes.c_uint, _vp, _vp]
         u32, f32, sz = ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
         for name, args in (
-                ("mx_rmsnorm", [_vp] * 3 + [_i64, _i64, f32, u32] + [_vp] * 10),
+                ("mx_rmsnorm", [_vp] * 3 + [_i64, _i64, f32, u32] + [_vp] * 10 + [sz, _vp]),
                 ("mx_rmsnorm_backward", [_vp] * 7 + [_i64, _i64] + [_vp] * 3 + [sz, _vp]),
                 ("moe_route", [_vp] * 2 + [_i64] * 5 + [f32, u32] + [_vp] * 4),
                 ("moe_route_backward", [_vp] * 4 + [_i64] * 3 + [f32, u32] + [_vp] * 2),
@@ -152,6 +152,8 @@ def lib():
                 ("moe_combine_backward", [_vp, _vp, _i64, _i64] + [_vp] * 3 + [_i64, _i64] + [_vp] * 3)):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = args
+        L.mx_rmsnorm_workspace_size.restype = sz
+        L.mx_rmsnorm_workspace_size.argtypes = [_i64, u32]
         L.mx_rmsnorm_backward_workspace_size.restype = sz
         L.mx_rmsnorm_backward_workspace_size.argtypes = [_i64, _i64]
         L.moe_sort_rows.restype = _i64
@@ -931,8 +933,12 @@ def _scales_of(rows, cols, axis):
     return (rows, -(-cols // 32))
 
 
+def mx_rmsnorm_workspace_size(M: int, axis: int) -> int:
+    return lib().mx_rmsnorm_workspace_size(M, axis)
+
+
 def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, checkpoint=False,
-               out=None, stream=None):
+               out=None, workspace=None, stream=None):
     """h = x + residual (x itself without), y = h rstd weight with rstd =
     (mean h^2 + eps)^(-1/2) of each row, for bf16 x [M][K], and the MXFP8 casts
     of y that `axis` asks for (0: none; flags as for mx_quantize).  Returns {h, y,
@@ -944,7 +950,8 @@ def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, che
     M, K = shape
     rp = _want(residual, shape, _BF16_BITS, "residual", dev)
     wp = _want(weight, (K,), _BF16_BITS, "weight", dev)
-    h = y = q_row = s_row = q_col = s_col = q_h = s_h = None
+    h = y = q_row = s_row = q_col = s_col = q_h = s_h = ws = wp_ = None
+    wn = 0
     new = _new(x, out, stream)
     if residual is not None:
         h = new("h", shape, BF16)
@@ -955,12 +962,18 @@ def mx_rmsnorm(x, weight=None, residual=None, eps=1e-6, axis=0, want_y=None, che
         q_row, s_row = new("q_row", shape, U8), new("s_row", _scales_of(M, K, axis), U8)
     if axis & COLWISE:
         q_col, s_col = new("q_col", (K, M), U8), new("s_col", _scales_of(K, M, axis), U8)
+        if workspace is None:
+            ws, wn = new("workspace", (2 * M,), F32), 8 * M
+            wp_ = ws.data_ptr()
+        else:
+            ws, wp_, wn = _product_ws(workspace, 8 * M, dev, stream)
     if checkpoint:
         q_h, s_h = new("q_h", shape, U8), new("s_h", (M, -(-K // 32)), U8)
     if dev.index is None:
         _gpu(dev)
     _launch("mx_rmsnorm", dev, stream, lib().mx_rmsnorm, x.data_ptr(), rp, wp, M, K, eps, axis, _at(h),
-            _at(y), _at(q_row), _at(s_row), _at(q_col), _at(s_col), _at(q_h), _at(s_h), rstd.data_ptr())
+            _at(y), _at(q_row), _at(s_row), _at(q_col), _at(s_col), _at(q_h), _at(s_h), rstd.data_ptr(),
+            wp_, wn)
     return {"h": x if h is None else h, "y": y, "rstd": rstd, "q_row": q_row, "s_row": s_row,
             "q_col": q_col, "s_col": s_col, "q_h": q_h, "s_h": s_h}
 

@@ -69,15 +69,17 @@ uint64_t scale_bytes(int64_t rows, int64_t cols, bool tiled)
 
 mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; }
 
-// The column-wise casts of the norm's output, from h and the rows' rstd.
+// The column-wise casts of the norm's output, from h and the rows' scales.
 mx_status norm_columns(const void *h, const void *weight, int64_t M, int64_t K, unsigned axis_mask,
-                       uint8_t *q_col, uint8_t *s_col, const float *rstd, hipStream_t stream)
+                       uint8_t *q_col, uint8_t *s_col, const float *cut, const float *low,
+                       hipStream_t stream)
 {
     const unsigned fmt = axis_mask & (MX_ELEM_E5M2 | MX_SCALE_ROUND_UP);
     mxk::MxArgs a{};
     a.x = static_cast<const uint16_t *>(h);
     a.aux = static_cast<const uint16_t *>(weight);
-    a.row_scale = rstd;
+    a.row_scale = cut;
+    a.row_low = low;
     a.M = M;
     a.K = a.ldx = K;
     a.q_col = q_col;
@@ -117,7 +119,7 @@ extern "C" {
 mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, int64_t M, int64_t K,
                      float eps, unsigned axis_mask, void *h, void *y, uint8_t *q_row,
                      uint8_t *s_row, uint8_t *q_col, uint8_t *s_col, uint8_t *q_h, uint8_t *s_h,
-                     float *rstd, hipStream_t stream)
+                     float *rstd, void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const bool row = axis_mask & MX_ROWWISE, col = axis_mask & MX_COLWISE;
     if ((axis_mask & ~kModeBits) || (axis_mask && !row && !col) || !(eps >= 0.0f && eps <= FLT_MAX))
@@ -130,7 +132,8 @@ mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, in
     const bool tiled = (axis_mask & MX_SCALE_TILED) != 0;
     const uint64_t n = (uint64_t)(M * K);
     const Span in[3] = {{x, 2 * n}, {residual, 2 * n}, {weight, 2 * (uint64_t)K}};
-    const Span out[9] = {{residual ? h : nullptr, 2 * n},
+    const uint64_t need = mx_rmsnorm_workspace_size(M, axis_mask);
+    const Span out[10] = {{residual ? h : nullptr, 2 * n},
                          {y, 2 * n},
                          {row ? q_row : nullptr, n},
                          {row ? s_row : nullptr, scale_bytes(M, K, tiled)},
@@ -138,10 +141,13 @@ mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, in
                          {col ? s_col : nullptr, scale_bytes(K, M, tiled)},
                          {q_h, n},
                          {s_h, scale_bytes(M, K, false)},
-                         {rstd, 4 * (uint64_t)M}};
-    if (!all_aligned(in, 3) || !all_aligned(out, 9))
+                         {rstd, 4 * (uint64_t)M},
+                         {need ? workspace : nullptr, need}};
+    if (!all_aligned(in, 3) || !all_aligned(out, 10))
         return MX_ERR_ALIGN;
-    if (any_alias(in, 3, out, 9))
+    if (need && (!workspace || workspace_bytes < need))
+        return MX_ERR_WORKSPACE;
+    if (any_alias(in, 3, out, 10))
         return MX_ERR_ALIAS;
 
     mxk::NormArgs a{};
@@ -158,13 +164,20 @@ mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, in
     a.q_h = q_h;
     a.s_h = s_h;
     a.rstd = rstd;
+    a.cut = need ? static_cast<float *>(workspace) : nullptr;
+    a.low = need ? a.cut + M : nullptr;
     a.tiled = tiled;
     a.stream = mxk::norm_streams(M, K);
     const hipError_t e =
         mxk::launch_norm(axis_mask & (MX_ELEM_E5M2 | MX_SCALE_ROUND_UP), a, stream);
     if (e != hipSuccess || !col)
         return from_hip(e);
-    return norm_columns(residual ? h : x, weight, M, K, axis_mask, q_col, s_col, rstd, stream);
+    return norm_columns(residual ? h : x, weight, M, K, axis_mask, q_col, s_col, a.cut, a.low, stream);
+}
+
+size_t mx_rmsnorm_workspace_size(int64_t M, unsigned axis_mask)
+{
+    return (axis_mask & MX_COLWISE) && M > 0 && M <= kMaxDim ? (size_t)M * 2 * sizeof(float) : 0;
 }
 
 size_t mx_rmsnorm_backward_workspace_size(int64_t M, int64_t K)

@@ -414,12 +414,16 @@ __device__ __forceinline__ uint32_t dgated_pair(uint32_t g, uint32_t dy, uint32_
                       dgated_value<OP>(bf16_hi(g), bf16_hi(dy), bf16_hi(l), gate_half));
 }
 
-// The norm's output of a packed pair: each element times its column's weight (16
-// significant bits at most, exact in fp32), times its row's rstd, rounded once to
-// fp32 and then to bf16.
-__device__ __forceinline__ uint32_t norm_pair(uint32_t h, float rstd, uint32_t w)
+// The norm's output: an element times its column's weight (hw: 16 significant bits at
+// most, exact in fp32), times its row's reciprocal root mean square in 64 bits (r, cut to
+// fp32, and low, what is left), rounded to fp32 and then to bf16.
+__device__ __forceinline__ float norm_value(float hw, float r, float low)
 {
-    return bf16x2_rne((bf16_lo(h) * bf16_lo(w)) * rstd, (bf16_hi(h) * bf16_hi(w)) * rstd);
+    return __builtin_fmaf(hw, r, hw * low);
+}
+__device__ __forceinline__ uint32_t norm_pair(uint32_t h, float r, float low, uint32_t w)
+{
+    return bf16x2_rne(norm_value(bf16_lo(h) * bf16_lo(w), r, low), norm_value(bf16_hi(h) * bf16_hi(w), r, low));
 }
 
 // ---------------------------------------------------------------------------

@@ -187,7 +187,8 @@ struct MxArgs {
     int group, groups_m;   // sub-tiles per workgroup walk, walks along M
     int tiled;             // scales in the GEMM-ready tile layout (walks of >= 2 sub-tiles)
     int qcol_nt;           // plain cast with both outputs: transposed stores non-temporal
-    const float *row_scale = nullptr;   // OP_NORM: the rows' reciprocal root mean squares
+    // OP_NORM: the rows' reciprocal root mean squares, cut to fp32, and what that left
+    const float *row_scale = nullptr, *row_low = nullptr;
 };
 
 // The plain cast's transposed stores are non-temporal only for a transposed

@@ -17,6 +17,8 @@ struct NormArgs {
     uint8_t *q_row, *s_row;        // null without row-wise outputs
     uint8_t *q_h, *s_h;            // 8-bit copy of h, may be null
     float *rstd;
+    float *cut, *low;              // rstd cut to fp32 and what that left, for the
+                                   // column-wise cast, or null
     int tiled;                     // s_row in the tile layout
     int stream;                    // too large for the caches: norm_streams
 };
@@ -73,7 +75,7 @@ inline int64_t norm_back_parts(int64_t M, int64_t K)
 hipError_t launch_norm(unsigned fmt, const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_back(const NormBackArgs &a, hipStream_t s);
 // The column-wise casts of the norm's output (OP_NORM), from h and rstd: a as
-// for launch_mx_cast with aux the weight (ldg 0) and row_scale; gt null, or for
+// for launch_mx_cast with aux the weight (ldg 0), row_scale and row_low; gt null, or for
 // transposed rows at any byte the tensor as a stack of one group.
 hipError_t launch_mx_cast_norm(unsigned fmt, const MxArgs &a, const GroupTable *gt, hipStream_t s);
 

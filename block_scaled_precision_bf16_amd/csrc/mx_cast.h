@@ -202,17 +202,20 @@ __device__ __forceinline__ void load_tile(const MxArgs &a, const LaneAt &l, int 
             wt = buf_load16(make_rsrc(a.aux, 2 * (int64_t)tk * kTileK, 2 * a.K),
                             live ? (uint32_t)(2 * kColsPerLane * l.cl) : kDead);
         const rsrc_t rr = make_rsrc(a.row_scale, 4 * (int64_t)tm * kTileM, 4 * a.M);
-        float sc[kRowsPerLane];
+        const rsrc_t rl = make_rsrc(a.row_low, 4 * (int64_t)tm * kTileM, 4 * a.M);
+        float sc[kRowsPerLane], low[kRowsPerLane];
 #pragma unroll
-        for (int r = 0; r < kRowsPerLane; r++)
+        for (int r = 0; r < kRowsPerLane; r++) {
             sc[r] = f32_bits(buf_load4(rr, live ? (uint32_t)(4 * (l.row + r)) : kDead));
+            low[r] = f32_bits(buf_load4(rl, live ? (uint32_t)(4 * (l.row + r)) : kDead));
+        }
 #pragma unroll
         for (int r = 0; r < kRowsPerLane; r++) {
             const uint4 v = buf_load16<XA>(rx, off + r * rs);
-            w[r][0] = norm_pair(v.x, sc[r], wt.x);
-            w[r][1] = norm_pair(v.y, sc[r], wt.y);
-            w[r][2] = norm_pair(v.z, sc[r], wt.z);
-            w[r][3] = norm_pair(v.w, sc[r], wt.w);
+            w[r][0] = norm_pair(v.x, sc[r], low[r], wt.x);
+            w[r][1] = norm_pair(v.y, sc[r], low[r], wt.y);
+            w[r][2] = norm_pair(v.z, sc[r], low[r], wt.z);
+            w[r][3] = norm_pair(v.w, sc[r], low[r], wt.w);
         }
         return;
     }

@@ -8,7 +8,8 @@
 // Both are bound by memory: a handful of fp32 operations per element against 4 to
 // 10 bytes.  A workgroup holds one row in registers (16-byte loads, neighbouring
 // chunks in neighbouring lanes), so that every input is read once: the sum over the
-// row, one barrier, then the outputs.  The loads of the workgroup's next row are
+// row (in 64 bits: fp32 sums would move y by a step of bf16 in one element of 10^5, and
+// cost the same), one barrier, then the outputs.  The loads of the workgroup's next row are
 // issued before that sum.  The row-wise MXFP8 blocks (32 elements, 4 lanes) leave in
 // the same pass; the column-wise casts need all rows' rstd first and re-read h
 // (mx_cast_norm.hip).  The backward's weight gradients are summed in registers over
@@ -44,7 +45,8 @@ __device__ __forceinline__ int64_t row_of(int64_t step, int b, int n)
 // Sum over `waves` waves of the workgroup, from wave `first` on, the same in each of
 // their threads; red: a float for each wave of the workgroup, others for the next
 // call.
-__device__ __forceinline__ float block_sum(float v, float *red, int waves, int first = 0)
+template <class T>
+__device__ __forceinline__ T block_sum(T v, T *red, int waves, int first = 0)
 {
     v = wave_sum(v);
     if (waves == 1)
@@ -52,22 +54,36 @@ __device__ __forceinline__ float block_sum(float v, float *red, int waves, int f
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
-    float s = red[first];
+    T s = red[first];
     for (int i = 1; i < waves; i++)
         s += red[first + i];
     return s;
 }
 
-// (sum / K + eps)^(-1/2) in 64 bits, rounded once (in fp32 the mean, the root and
-// the reciprocal would each add their rounding, and every element of the row has
-// this factor): the hardware's estimate, measured good to 2^-24, and one Newton step,
-// which leaves 2^-47.  0 and Inf go through fp32, where the step would make NaN of them.
-__device__ __forceinline__ float rstd_of(float sum, int64_t K, float eps)
+// (sum / K + eps)^(-1/2) in 64 bits, where every element of the row has this factor: the
+// hardware's estimate, measured good to 2^-24, and one Newton step, which leaves 2^-47;
+// near, as the nearest fp32 number, for the caller; r and low, cut to fp32 and what is
+// left (not negative, so that a zero's sign stays), for y.  0 and Inf go through fp32,
+// where the step would make NaN of them.
+struct Rstd {
+    float near, r, low;
+};
+__device__ __forceinline__ Rstd rstd_of(double sum, int64_t K, float eps)
 {
-    const double v = (double)sum / (double)K + (double)eps;
+    const double v = sum / (double)K + (double)eps;
     const double r = __builtin_amdgcn_rsq(v);
     const double s = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
-    return v > 0.0 && v < 1e300 ? (float)s : 1.0f / sqrtf((float)v);
+    Rstd o;
+    o.near = o.r = 1.0f / sqrtf((float)v);
+    o.low = 0.0f;
+    if (v > 0.0 && v < 1e300) {
+        o.near = o.r = (float)s;
+        if (o.r < __builtin_inff()) {
+            o.r = (double)o.r > s ? f32_bits(bits_f32(o.r) - 1u) : o.r;
+            o.low = (float)(s - (double)o.r);
+        }
+    }
+    return o;
 }
 
 __device__ __forceinline__ uint32_t add_pair(uint32_t a, uint32_t b)
@@ -164,15 +180,16 @@ __device__ __forceinline__ NormOut<AL> norm_out(const NormArgs &a, int64_t row, 
 // The outputs of chunk c of a row; every lane of a wave takes part.
 template <int FMT, int NT, bool AL>
 __device__ __forceinline__ void norm_write(const NormArgs &a, const NormOut<AL> &o, int64_t row, uint32_t c,
-                                           uint32_t nb, const uint32_t (&h)[4], float rstd, uint4 wt)
+                                           uint32_t nb, const uint32_t (&h)[4], const Rstd &rstd, uint4 wt)
 {
     const bool quad = (nb & 3) == 0;
     if (a.q_h)
         store_scales(o.ks, cast8<kFmtRoundUp, NT>(o.k, h, c), c, nb, quad);
     if (!a.y && !a.q_row)
         return;
-    const uint32_t y[4] = {norm_pair(h[0], rstd, wt.x), norm_pair(h[1], rstd, wt.y),
-                           norm_pair(h[2], rstd, wt.z), norm_pair(h[3], rstd, wt.w)};
+    const uint32_t y[4] = {
+        norm_pair(h[0], rstd.r, rstd.low, wt.x), norm_pair(h[1], rstd.r, rstd.low, wt.y),
+        norm_pair(h[2], rstd.r, rstd.low, wt.z), norm_pair(h[3], rstd.r, rstd.low, wt.w)};
     if (a.y)
         row_store<0>(o.y, c, make_uint4(y[0], y[1], y[2], y[3]));
     if (!a.q_row)
@@ -185,15 +202,16 @@ __device__ __forceinline__ void norm_write(const NormArgs &a, const NormOut<AL> 
         store_scales(o.s, sb, c, nb, quad);
 }
 
-__device__ __forceinline__ void norm_sum(const uint32_t (&x)[4], const uint4 *r, uint32_t (&h)[4], float &s0,
-                                         float &s1)
+__device__ __forceinline__ void norm_sum(const uint32_t (&x)[4], const uint4 *r, uint32_t (&h)[4], double &s0,
+                                         double &s1)
 {
     const uint32_t rr[4] = {r ? r->x : 0u, r ? r->y : 0u, r ? r->z : 0u, r ? r->w : 0u};
 #pragma unroll
     for (int d = 0; d < 4; d++) {
         h[d] = r ? add_pair(x[d], rr[d]) : x[d];
-        s0 = __builtin_fmaf(bf16_lo(h[d]), bf16_lo(h[d]), s0);
-        s1 = __builtin_fmaf(bf16_hi(h[d]), bf16_hi(h[d]), s1);
+        const double lo = bf16_lo(h[d]), hi = bf16_hi(h[d]);
+        s0 = __builtin_fma(lo, lo, s0);
+        s1 = __builtin_fma(hi, hi, s1);
     }
 }
 
@@ -216,6 +234,16 @@ __device__ __forceinline__ void norm_load(const NormArgs &a, int64_t row, NormRo
     }
 }
 
+// For the caller, and for the column-wise cast.
+__device__ __forceinline__ void put_rstd(const NormArgs &a, int64_t row, const Rstd &rstd)
+{
+    a.rstd[row] = rstd.near;
+    if (a.cut) {
+        a.cut[row] = rstd.r;
+        a.low[row] = rstd.low;
+    }
+}
+
 // Rows that the tile layout pads to have scales of 0.
 __device__ __forceinline__ int64_t norm_rows(const NormArgs &a)
 {
@@ -228,7 +256,7 @@ __device__ __forceinline__ int64_t norm_rows(const NormArgs &a)
 template <int FMT, int CH, int NT, bool AL>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 {
-    __shared__ float red[2][16];
+    __shared__ double red[2][16];
     const int waves = (int)blockDim.x >> 6, n = (int)gridDim.x;
     const uint32_t nb = (uint32_t)((a.K + 31) >> 5);
     const int64_t rows = norm_rows(a);
@@ -243,7 +271,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
     norm_load<CH, NT, AL>(a, row, next);
     for (int64_t step = 0; row < rows; step++) {
         uint32_t h[CH][4];
-        float s0 = 0.0f, s1 = 0.0f;
+        double s0 = 0.0, s1 = 0.0;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t c = threadIdx.x + i * blockDim.x;
@@ -255,9 +283,9 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
         norm_load<CH, NT, AL>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
-        const float rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), a.K, a.eps);
+        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), a.K, a.eps);
         if (row < a.M && threadIdx.x == 0)
-            a.rstd[row] = rstd;
+            put_rstd(a, row, rstd);
         const NormOut<AL> o = norm_out<AL>(a, row, nb);
 #pragma unroll
         for (int i = 0; i < CH; i++) {
@@ -276,7 +304,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 template <int FMT, bool AL>
 __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
-    __shared__ float red[2][16];
+    __shared__ double red[2][16];
     const uint32_t nb = (uint32_t)((a.K + 31) >> 5), chunks = (uint32_t)((a.K + 7) >> 3), K = (uint32_t)a.K;
     // whole waves, which cover the tile layout's padding blocks too
     const uint32_t upto = (chunks + 63) & ~63u;
@@ -287,7 +315,7 @@ __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
         const int64_t at = row * a.K, len = row < a.M ? a.K : 0;
         const Row<AL, const uint16_t> x = row_at<AL>(a.x, at, len), r = row_at<AL>(a.res, at, a.res ? len : 0);
         const NormOut<AL> o = norm_out<AL>(a, row, nb);
-        float s0 = 0.0f, s1 = 0.0f;
+        double s0 = 0.0, s1 = 0.0;
         for (uint32_t c0 = threadIdx.x; c0 < chunks; c0 += 2 * 512) {
             uint4 xv[2], rv[2];
 #pragma unroll
@@ -307,9 +335,9 @@ __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
                     row_store<0>(o.h, c, make_uint4(h[0], h[1], h[2], h[3]));
             }
         }
-        const float rstd = rstd_of(block_sum(s0 + s1, red[step], 8), a.K, a.eps);
+        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step], 8), a.K, a.eps);
         if (row < a.M && threadIdx.x == 0)
-            a.rstd[row] = rstd;
+            put_rstd(a, row, rstd);
         const Row<AL, const uint16_t> hr = a.h ? row_at<AL>((const uint16_t *)a.h, at, len) : x;
         for (uint32_t c = threadIdx.x; c < upto; c += 512) {
             uint4 wt = make_uint4(kOnes, kOnes, kOnes, kOnes), v = row_raw<0>(hr, c);

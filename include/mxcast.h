@@ -560,8 +560,8 @@ mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T,
 /*
  * Root-mean-square norm of a residual stream, with the casts of its output:
  *   h[m][k]  = bf16(fl32(x + residual)); x itself without a residual
- *   rstd[m]  = (mean_k h[m][k]^2 + eps)^(-1/2), the sum in fp32 in a fixed order
- *   y[m][k]  = bf16(fl32((h weight) rstd)), where fp32 holds h weight exactly
+ *   rstd[m]  = (mean_k h[m][k]^2 + eps)^(-1/2), in 64 bits in a fixed order
+ *   y[m][k]  = bf16(fl32(h weight rstd)), with the rstd of 64 bits
  * and the MXFP8 casts of y, exactly as mx_quantize casts that tensor.
  *   x, residual  device, bf16 [M][K]; residual may be NULL
  *   weight     device, bf16 [K]; NULL: ones
@@ -577,14 +577,20 @@ mx_status nvfp4_matvec_experts(const void *x, const int32_t *experts, int64_t T,
  *              scales, [M][K] and [M][ceil(K/32)], whatever axis_mask says.  It
  *              is the activation checkpoint of mx_rmsnorm_backward, at half of
  *              h's memory; one step of its elements is 2^-3 of their binade
- *   rstd       fp32 [M]
- * A row that holds Inf or NaN, or whose squares' sum passes fp32, gets what these
- * formulas give in fp32 (a NaN or 0 rstd).  Errors as for mx_quantize.
+ *   rstd       fp32 [M], rounded once
+ *   workspace, workspace_bytes  device scratch of at least
+ *              mx_rmsnorm_workspace_size() bytes (8 M with MX_COLWISE: rstd in
+ *              more bits; otherwise 0: NULL and 0 then).  Calls that may overlap in time
+ *              need workspaces of their own
+ * A row that holds Inf or NaN gets what these formulas give (rstd 0 or NaN); where rstd
+ * passes fp32 (rows of tiny numbers with eps 0) it is Inf, in y too.  Errors as for
+ * mx_quantize, and MX_ERR_WORKSPACE.
  */
 mx_status mx_rmsnorm(const void *x, const void *residual, const void *weight, int64_t M, int64_t K,
                      float eps, unsigned axis_mask, void *h, void *y, uint8_t *q_row,
                      uint8_t *s_row, uint8_t *q_col, uint8_t *s_col, uint8_t *q_h, uint8_t *s_h,
-                     float *rstd, hipStream_t stream);
+                     float *rstd, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t mx_rmsnorm_workspace_size(int64_t M, unsigned axis_mask);
 
 /*
  * Gradients of mx_rmsnorm.  With xhat = h rstd, g = dy weight and

@@ -77,7 +77,7 @@ static void norm_case(int64_t M, int64_t K, unsigned axis, bool res)
     const int before = g_norm + g_cols + g_any;
     const mx_status st = mx_rmsnorm(at(1), res ? at(2) : nullptr, at(3), M, K, 1e-6f, axis, at(4), nullptr,
                                     as<uint8_t>(5), as<uint8_t>(6), as<uint8_t>(7), as<uint8_t>(8), nullptr,
-                                    nullptr, as<float>(9), nullptr);
+                                    nullptr, as<float>(9), at(10), mx_rmsnorm_workspace_size(M, axis), nullptr);
     if (M > (1 << 23) || K > (1 << 23) || M * K > (int64_t(1) << 40)) {
         CHECK(st == MX_ERR_SHAPE && g_norm + g_cols + g_any == before);
         return;
@@ -96,7 +96,8 @@ static void norm_case(int64_t M, int64_t K, unsigned axis, bool res)
     CHECK(norm_back_parts(M, K) >= 1 && norm_back_parts(M, K) <= 256);
     if (!(axis & 2))
         return;
-    CHECK(g_m.row_scale == at(9) && g_m.x == (res ? at(4) : at(1)) && g_m.aux == at(3) && g_m.ldg == 0);
+    CHECK(mx_rmsnorm_workspace_size(M, axis) == 8 * (size_t)M && g_n.cut == at(10) && g_n.low == g_n.cut + M);
+    CHECK(g_m.row_scale == g_n.cut && g_m.row_low == g_n.low && g_m.x == (res ? at(4) : at(1)) && g_m.aux == at(3) && g_m.ldg == 0);
     const bool any = K % 8 != 0;
     const int64_t tm = any ? kAnyTileM : kTileM, tk = any ? kAnyTileK : kTileK;
     CHECK(g_m.tiles_m == cdiv(M, tm) && g_m.tiles_k == cdiv(K, tk));

@@ -27,18 +27,18 @@ def call(fn, h, names, values):
 
 M, K = 48, 96
 NORM = ("x", "residual", "weight", "M", "K", "eps", "axis", "h", "y", "q_row", "s_row", "q_col",
-        "s_col", "q_h", "s_h", "rstd")
+        "s_col", "q_h", "s_h", "rstd", "ws", "wn")
 
 
 @pytest.fixture
 def nh():
     n = M * K
     return Host(x=2 * n, residual=2 * n, weight=2 * K, h=2 * n, y=2 * n, q_row=n, s_row=2 * 256,
-                q_col=n, s_col=3 * 256, q_h=n, s_h=M * 3, rstd=4 * M)
+                q_col=n, s_col=3 * 256, q_h=n, s_h=M * 3, rstd=4 * M, ws=8 * M)
 
 
 def norm(host, /, **kw):
-    return call("mx_rmsnorm", host, NORM, dict(M=M, K=K, eps=1e-6, axis=3) | kw)
+    return call("mx_rmsnorm", host, NORM, dict(M=M, K=K, eps=1e-6, axis=3, wn=8 * M) | kw)
 
 
 def test_norm_errors(nh):
@@ -55,7 +55,11 @@ def test_norm_errors(nh):
     for name in NORM:
         if name in nh.raw:
             assert norm(nh, **{name: nh.p(name, 8)}) == mx.MX_ERR_ALIGN, name
-    outputs = ("h", "y", "q_row", "s_row", "q_col", "s_col", "q_h", "s_h", "rstd")
+    assert norm(nh, ws=None) == mx.MX_ERR_WORKSPACE and norm(nh, wn=8 * M - 1) == mx.MX_ERR_WORKSPACE
+    assert norm(nh, axis=2, ws=None, wn=0) == mx.MX_ERR_WORKSPACE
+    size = mx.mx_rmsnorm_workspace_size
+    assert size(M, 3) == size(M, 2) == 8 * M and size(M, 1) == size(M, 0) == size(0, 2) == size(-1, 2) == 0
+    outputs = ("h", "y", "q_row", "s_row", "q_col", "s_col", "q_h", "s_h", "rstd", "ws")
     for o in outputs:
         for i in ("x", "residual", "weight") + tuple(p for p in outputs if p != o):
             assert norm(nh, **{o: nh.p(i)}) == mx.MX_ERR_ALIAS, (o, i)
@@ -281,6 +285,8 @@ WRONG = [
     lambda: mx.mx_rmsnorm(x, residual=z(4, 32)),
     lambda: mx.mx_rmsnorm(x, out=dict(y=z(4, 32))),
     lambda: mx.mx_rmsnorm(x, axis=1, out=dict(s_row=z(4, 3, dtype=U8))),
+    lambda: mx.mx_rmsnorm(x, axis=2, workspace=7),
+    lambda: mx.mx_rmsnorm(x, axis=2, workspace=z(64, 4).t()),
     lambda: mx.mx_rmsnorm_backward(x, z(4, dtype=F32)),
     lambda: mx.mx_rmsnorm_backward(x, z(4, dtype=F32), h=x, q_h=z(4, 64, dtype=U8),
                                    s_h=z(4, 2, dtype=U8)),
