@@ -17,8 +17,8 @@
 // workgroup, which a second kernel adds in a fixed order.
 //
 // Measured (a copy of 1 GiB runs at 5.1 TB/s, one of 118 MB at 5.5 to 7): 16384 x 7168
-// with a residual, the row-wise cast and the 8-bit copy 168 us (0.95 GB, 5.6 TB/s),
-// 2048 x 8192 with a residual and the row-wise cast 23.2 us (118 MB, 5.1 TB/s), one row
+// with a residual, the row-wise cast and the 8-bit copy 170 us (0.95 GB, 5.6 TB/s),
+// 2048 x 8192 with a residual and the row-wise cast 23.5 us (118 MB, 5.0 TB/s), one row
 // of 4096 3 us.  Backward of 16384 x 7168 with dres from bf16 151 us (0.94 GB, 6.2
 // TB/s), from 8 bits 135 us (0.83 GB, 6.1 TB/s), the sums of its partial weight
 // gradients 4.5 us more.
@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t row_of(int64_t step, int b, int n)
 }
 
 // Sum over `waves` waves of the workgroup, from wave `first` on, the same in each of
-// their threads; red: a float for each wave of the workgroup, others for the next
+// their threads; red: a number for each wave of the workgroup, others for the next
 // call.
 template <class T>
 __device__ __forceinline__ T block_sum(T v, T *red, int waves, int first = 0)
@@ -54,34 +54,31 @@ __device__ __forceinline__ T block_sum(T v, T *red, int waves, int first = 0)
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
-    T s = red[first];
-    for (int i = 1; i < waves; i++)
-        s += red[first + i];
-    return s;
+    const int i = (int)threadIdx.x & 15;       // all at once, in each row of 16 lanes
+    return row_sum(i < waves ? red[first + i] : T(0));
 }
 
 // (sum / K + eps)^(-1/2) in 64 bits, where every element of the row has this factor: the
-// hardware's estimate, measured good to 2^-24, and one Newton step, which leaves 2^-47;
-// near, as the nearest fp32 number, for the caller; r and low, cut to fp32 and what is
+// hardware's estimate, measured good to 2^-24, and one Newton step, which leaves 2^-47
+// (inv_k = 1 / K: a division would be one more of the steps that all waves wait for).
+// near, the nearest fp32 number, is for the caller; r and low, cut to fp32 and what is
 // left (not negative, so that a zero's sign stays), for y.  0 and Inf go through fp32,
-// where the step would make NaN of them.
+// where the step would make NaN of them, and what passes fp32 is Inf.
 struct Rstd {
     float near, r, low;
 };
-__device__ __forceinline__ Rstd rstd_of(double sum, int64_t K, float eps)
+__device__ __forceinline__ Rstd rstd_of(double sum, double inv_k, float eps)
 {
-    const double v = sum / (double)K + (double)eps;
+    const double v = __builtin_fma(sum, inv_k, (double)eps);
     const double r = __builtin_amdgcn_rsq(v);
     const double s = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
     Rstd o;
-    o.near = o.r = 1.0f / sqrtf((float)v);
-    o.low = 0.0f;
-    if (v > 0.0 && v < 1e300) {
-        o.near = o.r = (float)s;
-        if (o.r < __builtin_inff()) {
-            o.r = (double)o.r > s ? f32_bits(bits_f32(o.r) - 1u) : o.r;
-            o.low = (float)(s - (double)o.r);
-        }
+    o.near = o.r = (float)s;
+    o.r = (double)o.r > s ? f32_bits(bits_f32(o.r) - 1u) : o.r;
+    o.low = (float)(s - (double)o.r);
+    if (!(v > 0.0 && v < 1e300 && s <= 0x1.fffffep127)) {
+        o.near = o.r = 1.0f / sqrtf((float)v);
+        o.low = 0.0f;
     }
     return o;
 }
@@ -260,6 +257,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
     const int waves = (int)blockDim.x >> 6, n = (int)gridDim.x;
     const uint32_t nb = (uint32_t)((a.K + 31) >> 5);
     const int64_t rows = norm_rows(a);
+    const double inv_k = 1.0 / (double)a.K;
     const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     uint4 wt[CH];
 #pragma unroll
@@ -283,7 +281,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
         norm_load<CH, NT, AL>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
-        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), a.K, a.eps);
+        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), inv_k, a.eps);
         if (row < a.M && threadIdx.x == 0)
             put_rstd(a, row, rstd);
         const NormOut<AL> o = norm_out<AL>(a, row, nb);
@@ -300,7 +298,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 
 // Rows of any length, in two passes: the second finds the row in the caches (and
 // each thread what it wrote itself).  4096 x 20480 with a residual and the row-wise
-// cast 144 us (0.59 GB, 4.1 TB/s; its h read again from the caches), x 20481 200 us.
+// cast 141 us (0.59 GB, 4.2 TB/s; its h read again from the caches), x 20481 200 us.
 template <int FMT, bool AL>
 __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
@@ -309,6 +307,7 @@ __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
     // whole waves, which cover the tile layout's padding blocks too
     const uint32_t upto = (chunks + 63) & ~63u;
     const int64_t rows = norm_rows(a);
+    const double inv_k = 1.0 / (double)a.K;
     const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
     int step = 0;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, step ^= 1) {
@@ -335,7 +334,7 @@ __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
                     row_store<0>(o.h, c, make_uint4(h[0], h[1], h[2], h[3]));
             }
         }
-        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step], 8), a.K, a.eps);
+        const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step], 8), inv_k, a.eps);
         if (row < a.M && threadIdx.x == 0)
             put_rstd(a, row, rstd);
         const Row<AL, const uint16_t> hr = a.h ? row_at<AL>((const uint16_t *)a.h, at, len) : x;
