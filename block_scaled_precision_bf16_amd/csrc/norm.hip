@@ -17,7 +17,7 @@
 // workgroup, which a second kernel adds in a fixed order.
 //
 // Measured (a copy of 1 GiB runs at 5.1 TB/s, one of 118 MB at 5.5 to 7): 16384 x 7168
-// with a residual, the row-wise cast and the 8-bit copy 170 us (0.95 GB, 5.6 TB/s),
+// with a residual, the row-wise cast and the 8-bit copy 168 us (0.95 GB, 5.6 TB/s),
 // 2048 x 8192 with a residual and the row-wise cast 23.5 us (118 MB, 5.0 TB/s), one row
 // of 4096 3 us.  Backward of 16384 x 7168 with dres from bf16 151 us (0.94 GB, 6.2
 // TB/s), from 8 bits 135 us (0.83 GB, 6.1 TB/s), the sums of its partial weight
@@ -355,9 +355,16 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
 {
     const NormShape n = norm_shape(a.K);
     const int64_t rows = a.tiled && a.s_row ? (a.M + 31) / 32 * 32 : a.M;
-    // 1024 threads a CU, whose next rows are on their way meanwhile (2048 x 8192: 21.4
-    // us, with twice as many that take two rows each 23.2, with half 26.2)
-    const int64_t most = 256 * (n.chunks == 0 ? 4 : 1024 / n.threads);
+    // 1024 threads a CU, whose next rows are on their way meanwhile (2048 x 8192 row-wise:
+    // 23.7 us, with twice as many that take two rows each 24.7, with half 29.4; 4096 x 8192
+    // 41.5, 42.7, 54.4).  From 16384 rows on that are too large for the caches workgroups
+    // of two rows, handed out as others end, are faster: 16384 x 7168 row-wise 166 -> 157
+    // us, 16384 x 8192 to bf16 199 -> 182, 131072 x 1024 row-wise 187 -> 158, 32768 x 2048
+    // 79 -> 74; but 8192 x 8192 78 -> 79, one workgroup a CU (16400 x 16384) 341 -> 370,
+    // rows at any byte 200 -> 219.
+    const bool many = a.stream && rows >= 16384 && a.K % 8 == 0 && n.chunks != 0 && n.threads <= 512;
+    const int64_t pairs = (rows + 511) / 512 * 256;
+    const int64_t most = n.chunks == 0 ? 1024 : !many ? 256 * (1024 / n.threads) : pairs < 65536 ? pairs : 65536;
     const dim3 grid((unsigned)(rows < most ? rows : most)), block(n.threads);
     if (n.chunks == 0)
         hipLaunchKernelGGL((a.K % 8 == 0 ? norm_long_kernel<FMT, true> : norm_long_kernel<FMT, false>), grid, block,

@@ -110,6 +110,15 @@ def test_every_end_of_a_row(first):
         check_back(dy, x, w, res, ckpt=True)
 
 
+@pytest.mark.parametrize("M,K", [(16411, 1024), (16384, 1032)])
+def test_norm_of_many_rows(M, K):
+    """Two rows a workgroup, a few of them none."""
+    g = generator(M + K)
+    x, w, res = normal(g, M, K), normal(g, K), normal(g, M, K, scale=3.0)
+    check_norm(x, w, res, axis=3 | mx.SCALE_TILED, ckpt=True)
+    check_norm(x, w, None, axis=1)
+
+
 def test_norm_without_y_gives_the_same_casts():
     g = generator(1)
     for M, K in ((96, 1000), (37, 77)):
