@@ -749,7 +749,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackA
     if (t0 >= a.T)
         return;
     const int64_t rows = a.T - t0 < TOKENS ? a.T - t0 : TOKENS, t = t0 + row;
-    const auto sum_of = [](float v) { return ROW ? row_sum(v) : wave_sum(v); };
+    const auto sum_of = [](auto v) { return ROW ? row_sum(v) : wave_sum(v); };
     float x[NPL], p[NPL], q[NPL], dp[NPL];
     load_logits<NPL>(a.logits, t0, rows, row, l * NPL, a.E, a.f32, x);
     if (a.dscores)
@@ -773,25 +773,40 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackA
             all += p[i] * dp[i];
         all = sum_of(all);
     }
-    // slots s0 + l: the chosen p's sum, and that of p times its gradient
-    float sp = 0.0f, sd = 0.0f;
+    // slots s0 + l: the chosen p's sum, and that of p times its gradient d = scale dw.
+    // d sp - sd cancels, to 0 where one choice is live: 64 bits hold each product
+    // exactly, and 1 / sp of any fp32 numbers
+    double sp = 0.0, sd = 0.0;
     for (int s = l; s < a.top; s += LANES) {
         const int e = row < rows ? a.experts[t * a.top + s] : -1;
         const bool is = e >= 0 && e < a.E;
-        const float pj = is ? ps[wave][row][e] : 0.0f;
-        sp += pj;
-        sd += is ? a.scale * a.dweights[t * a.top + s] * pj : 0.0f;
+        const float pj = is ? ps[wave][row][e] : 0.0f, d = is ? a.scale * a.dweights[t * a.top + s] : 0.0f;
+        sp += (double)pj;
+        sd = __builtin_fma((double)d, (double)pj, sd);
     }
-    sp = sum_of(sp);
     sd = sum_of(sd);
-    if (!a.renorm && !a.sigmoid)
-        all += sd;
+    double inv = 0.0;
+    if (a.renorm) {
+        sp = sum_of(sp);
+        inv = sp > 0.0 ? Quick::rcp(sp) : 0.0;
+    } else if (!a.sigmoid) {
+        all += (float)sd;
+    }
+    // with normalised weights all gradients are taken times p from here on: the chosen
+    // ones' part, which the loop adds, is w (d - sum w d) with w = p / sp
+    if (a.renorm) {
+#pragma unroll
+        for (int i = 0; i < NPL; i++)
+            dp[i] = p[i] * (dp[i] - all);
+    }
     for (int s0 = 0; s0 < a.top; s0 += LANES) {
         const int s = s0 + l;
         const int e = row < rows && s < a.top ? a.experts[t * a.top + s] : -1;
-        float d = e >= 0 && e < a.E ? a.scale * a.dweights[t * a.top + s] : 0.0f;
+        const bool is = e >= 0 && e < a.E;
+        float d = is ? a.scale * a.dweights[t * a.top + s] : 0.0f;
         if (a.renorm)
-            d = sp > 0.0f ? (d - sd / sp) / sp : 0.0f;
+            d = (float)((is ? (double)ps[wave][row][e] : 0.0) * inv) *
+                (float)(__builtin_fma((double)d, sp, -sd) * inv);
         const int n = a.top - s0 < LANES ? a.top - s0 : LANES;
         for (int j = 0; j < n; j++) {
             const int ej = __shfl(e, (lane & ~(LANES - 1)) + j, 64);
@@ -805,8 +820,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_back_kernel(RouteBackA
         return;
     float o[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; i++)
-        o[i] = a.sigmoid ? dp[i] * (p[i] * q[i]) : p[i] * (dp[i] - all);
+    for (int i = 0; i < NPL; i++) {
+        if (a.sigmoid)
+            o[i] = dp[i] * (a.renorm ? q[i] : p[i] * q[i]);
+        else
+            o[i] = a.renorm ? dp[i] : p[i] * (dp[i] - all);
+    }
     if (NPL % 4 == 0 && a.E % 4 == 0) {
 #pragma unroll
         for (int i = 0; i + 3 < NPL; i += 4) {
