@@ -217,6 +217,13 @@ __device__ __forceinline__ void load_tile(const MxArgs &a, const LaneAt &l, int 
             w[r][2] = norm_pair(v.z, sc[r], low[r], wt.z);
             w[r][3] = norm_pair(v.w, sc[r], low[r], wt.w);
         }
+        // (a weight of Inf or NaN has made NaN of the zeros past M)
+        if ((int64_t)(tm + 1) * kTileM > a.M) {
+#pragma unroll
+            for (int r = 0; r < kRowsPerLane; r++)
+                if ((int64_t)tm * kTileM + l.row + r >= a.M)
+                    w[r][0] = w[r][1] = w[r][2] = w[r][3] = 0u;
+        }
         return;
     }
     rsrc_t rb = rx;

@@ -124,7 +124,9 @@ __device__ __forceinline__ void any_load(const MxArgs &a, const AnyView &v, int6
             const float hw0 = bf16_lo(e[2 * i]) * bf16_lo(wt), hw1 = bf16_lo(e[2 * i + 1]) * bf16_lo(wt);
             const float l0 = m + 2 * i < v.M ? a.row_low[m + 2 * i] : 0.0f;
             const float l1 = m + 2 * i + 1 < v.M ? a.row_low[m + 2 * i + 1] : 0.0f;
-            w[i] = bf16x2_rne(norm_value(hw0, s0, l0), norm_value(hw1, s1, l1));
+            // (outside the tensor 0 times an Inf or NaN of a row or a weight is not 0)
+            w[i] = bf16x2_rne(col_ok && m + 2 * i < v.M ? norm_value(hw0, s0, l0) : 0.0f,
+                              col_ok && m + 2 * i + 1 < v.M ? norm_value(hw1, s1, l1) : 0.0f);
         }
     } else {
         // second operand: the linear half (gated) or grad (dGELU, dSiLU)

@@ -193,8 +193,9 @@ __device__ __forceinline__ void norm_write(const NormArgs &a, const NormOut<AL> 
         return;
     const uint32_t sb = cast8<FMT, NT>(o.q, y, c);
     const uint32_t RT = (uint32_t)((a.M + 31) >> 5);
-    if (a.tiled)
-        store_scales_tiled(a.s_row + (row >> 5) * 256, row < a.M ? sb : 0u, c, (uint32_t)row, RT, (nb + 7) >> 3);
+    if (a.tiled)   // padding is 0, though the zeros there times an Inf or NaN rstd are NaN
+        store_scales_tiled(a.s_row + (row >> 5) * 256, row < a.M && (c >> 2) < nb ? sb : 0u, c, (uint32_t)row,
+                           RT, (nb + 7) >> 3);
     else
         store_scales(o.s, sb, c, nb, quad);
 }
