@@ -415,8 +415,8 @@ __device__ __forceinline__ uint32_t dgated_pair(uint32_t g, uint32_t dy, uint32_
 }
 
 // The norm's output: an element times its column's weight (hw: 16 significant bits at
-// most, exact in fp32), times its row's reciprocal root mean square in 64 bits (r, cut to
-// fp32, and low, what is left), rounded to fp32 and then to bf16.
+// most) times its row's reciprocal root mean square s in 64 bits, rounded to fp32 and then
+// to bf16.  s comes as two fp32 numbers, r, cut to fp32, and low, what is left.
 __device__ __forceinline__ float norm_value(float hw, float r, float low)
 {
     return __builtin_fmaf(hw, r, hw * low);
@@ -424,6 +424,34 @@ __device__ __forceinline__ float norm_value(float hw, float r, float low)
 __device__ __forceinline__ uint32_t norm_pair(uint32_t h, float r, float low, uint32_t w)
 {
     return bf16x2_rne(norm_value(bf16_lo(h) * bf16_lo(w), r, low), norm_value(bf16_hi(h) * bf16_hi(w), r, low));
+}
+
+// That is right for rows with s from 2^-64 to 2^10 by weights below 2^51: |h| is at most
+// 2^11.5 / s (the root of the longest row), so that no hw passes fp32; and one that falls
+// below fp32's normal numbers is off by 2^-150 at most, the output by 2^-140.  All else
+// takes 64 bits: its rows, Inf and NaN among them, come with r's sign set (and below 2^-64
+// r and low are of s 2^64, where fp32 has all their bits).
+__device__ __forceinline__ bool norm_is_wide(float r) { return bits_f32(r) >> 31; }
+__device__ __forceinline__ bool norm_is_wide(uint4 w)
+{
+    const uint32_t a = pk_max_u16(pk_max_u16(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                  pk_max_u16(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    return a >= 0x59000000u || (a & 0xFFFFu) >= 0x5900u;      // 2^51
+}
+__device__ __forceinline__ double norm_factor(float r, float low)
+{
+    const float m = __builtin_fabsf(r);
+    return ((double)m + (double)low) * (m < 1.0f && norm_is_wide(r) ? 0x1p-64 : 1.0);
+}
+__device__ __forceinline__ float norm_value_wide(float h, double s, float w)
+{
+    return (float)((double)h * (double)w * s);
+}
+__device__ __forceinline__ uint32_t norm_pair_wide(uint32_t h, double s, uint32_t w)
+{
+    // (or the doubles of a row's sum of squares and of the weights would be kept for this)
+    asm("" : "+v"(h), "+v"(w));
+    return bf16x2_rne(norm_value_wide(bf16_lo(h), s, bf16_lo(w)), norm_value_wide(bf16_hi(h), s, bf16_hi(w)));
 }
 
 // ---------------------------------------------------------------------------

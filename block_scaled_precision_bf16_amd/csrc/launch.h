@@ -187,7 +187,7 @@ struct MxArgs {
     int group, groups_m;   // sub-tiles per workgroup walk, walks along M
     int tiled;             // scales in the GEMM-ready tile layout (walks of >= 2 sub-tiles)
     int qcol_nt;           // plain cast with both outputs: transposed stores non-temporal
-    // OP_NORM: the rows' reciprocal root mean squares, cut to fp32, and what that left
+    // OP_NORM: the rows' reciprocal root mean squares as norm_value takes them (device_math.h)
     const float *row_scale = nullptr, *row_low = nullptr;
 };
 

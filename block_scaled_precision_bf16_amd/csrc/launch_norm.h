@@ -17,8 +17,8 @@ struct NormArgs {
     uint8_t *q_row, *s_row;        // null without row-wise outputs
     uint8_t *q_h, *s_h;            // 8-bit copy of h, may be null
     float *rstd;
-    float *cut, *low;              // rstd cut to fp32 and what that left, for the
-                                   // column-wise cast, or null
+    float *cut, *low;              // rstd as two numbers (norm_value, device_math.h), for
+                                   // the column-wise cast, or null
     int tiled;                     // s_row in the tile layout
     int stream;                    // too large for the caches: norm_streams
 };

@@ -203,11 +203,14 @@ __device__ __forceinline__ void load_tile(const MxArgs &a, const LaneAt &l, int 
                             live ? (uint32_t)(2 * kColsPerLane * l.cl) : kDead);
         const rsrc_t rr = make_rsrc(a.row_scale, 4 * (int64_t)tm * kTileM, 4 * a.M);
         const rsrc_t rl = make_rsrc(a.row_low, 4 * (int64_t)tm * kTileM, 4 * a.M);
+        // one row of the half-wave's 16 by each lane, inside K or not: whether any is wide
+        const uint32_t at = live ? (uint32_t)(4 * l.row) : kDead;
+        const uint32_t own = buf_load4(rr, (uint32_t)(4 * (l.row + (l.cl & 15))));
         float sc[kRowsPerLane], low[kRowsPerLane];
 #pragma unroll
         for (int r = 0; r < kRowsPerLane; r++) {
-            sc[r] = f32_bits(buf_load4(rr, live ? (uint32_t)(4 * (l.row + r)) : kDead));
-            low[r] = f32_bits(buf_load4(rl, live ? (uint32_t)(4 * (l.row + r)) : kDead));
+            sc[r] = f32_bits(buf_load4(rr, at + 4 * r));
+            low[r] = f32_bits(buf_load4(rl, at + 4 * r));
         }
 #pragma unroll
         for (int r = 0; r < kRowsPerLane; r++) {
@@ -217,12 +220,22 @@ __device__ __forceinline__ void load_tile(const MxArgs &a, const LaneAt &l, int 
             w[r][2] = norm_pair(v.z, sc[r], low[r], wt.z);
             w[r][3] = norm_pair(v.w, sc[r], low[r], wt.w);
         }
-        // (a weight of Inf or NaN has made NaN of the zeros past M)
-        if ((int64_t)(tm + 1) * kTileM > a.M) {
+        if (__builtin_amdgcn_ballot_w64(norm_is_wide(f32_bits(own)) || norm_is_wide(wt)) == 0)
+            return;
+        // once more, from the loads on (or their 96 registers would be kept for this); a
+        // weight of Inf or NaN makes NaN of the zeros past M
+        uint32_t at2 = at, off2 = off;
+        asm("" : "+v"(at2), "+v"(off2));
 #pragma unroll
-            for (int r = 0; r < kRowsPerLane; r++)
-                if ((int64_t)tm * kTileM + l.row + r >= a.M)
-                    w[r][0] = w[r][1] = w[r][2] = w[r][3] = 0u;
+        for (int r = 0; r < kRowsPerLane; r++) {
+            __builtin_amdgcn_sched_barrier(0);
+            const double f = norm_factor(f32_bits(buf_load4(rr, at2 + 4 * r)), f32_bits(buf_load4(rl, at2 + 4 * r)));
+            const uint4 v = buf_load16(rx, off2 + r * rs);
+            const bool in = (int64_t)tm * kTileM + l.row + r < a.M;
+            w[r][0] = in ? norm_pair_wide(v.x, f, wt.x) : 0u;
+            w[r][1] = in ? norm_pair_wide(v.y, f, wt.y) : 0u;
+            w[r][2] = in ? norm_pair_wide(v.z, f, wt.z) : 0u;
+            w[r][3] = in ? norm_pair_wide(v.w, f, wt.w) : 0u;
         }
         return;
     }

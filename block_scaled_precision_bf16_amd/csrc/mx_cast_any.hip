@@ -117,16 +117,31 @@ __device__ __forceinline__ void any_load(const MxArgs &a, const AnyView &v, int6
         // the column's weight, and the row scales (0 past the last row; one
         // address for all lanes of a wave)
         const uint32_t wt = !a.aux ? 0x3F803F80u : col_ok ? (uint32_t)a.aux[k] * 0x10001u : 0u;
+        // one of the 32 rows by each lane: whether any of them is wide
+        const int64_t own = m + (threadIdx.x & 31);
+        const bool wide = (own < v.M && norm_is_wide(a.row_scale[own])) || norm_is_wide(make_uint4(wt, wt, wt, wt));
+        if (__builtin_amdgcn_ballot_w64(wide) == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const float s0 = m + 2 * i < v.M ? a.row_scale[m + 2 * i] : 0.0f;
+                const float s1 = m + 2 * i + 1 < v.M ? a.row_scale[m + 2 * i + 1] : 0.0f;
+                const float hw0 = bf16_lo(e[2 * i]) * bf16_lo(wt), hw1 = bf16_lo(e[2 * i + 1]) * bf16_lo(wt);
+                const float l0 = m + 2 * i < v.M ? a.row_low[m + 2 * i] : 0.0f;
+                const float l1 = m + 2 * i + 1 < v.M ? a.row_low[m + 2 * i + 1] : 0.0f;
+                w[i] = bf16x2_rne(norm_value(hw0, s0, l0), norm_value(hw1, s1, l1));
+            }
+            return;
+        }
+        // (outside the tensor 0 times an Inf or NaN of a row or a weight is not 0)
+        const auto value = [&](int i) {
+            if (!col_ok || m + i >= v.M)
+                return 0.0f;
+            return norm_value_wide(bf16_lo(e[i]), norm_factor(a.row_scale[m + i], a.row_low[m + i]), bf16_lo(wt));
+        };
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const float s0 = m + 2 * i < v.M ? a.row_scale[m + 2 * i] : 0.0f;
-            const float s1 = m + 2 * i + 1 < v.M ? a.row_scale[m + 2 * i + 1] : 0.0f;
-            const float hw0 = bf16_lo(e[2 * i]) * bf16_lo(wt), hw1 = bf16_lo(e[2 * i + 1]) * bf16_lo(wt);
-            const float l0 = m + 2 * i < v.M ? a.row_low[m + 2 * i] : 0.0f;
-            const float l1 = m + 2 * i + 1 < v.M ? a.row_low[m + 2 * i + 1] : 0.0f;
-            // (outside the tensor 0 times an Inf or NaN of a row or a weight is not 0)
-            w[i] = bf16x2_rne(col_ok && m + 2 * i < v.M ? norm_value(hw0, s0, l0) : 0.0f,
-                              col_ok && m + 2 * i + 1 < v.M ? norm_value(hw1, s1, l1) : 0.0f);
+            w[i] = bf16x2_rne(value(2 * i), value(2 * i + 1));
+            __builtin_amdgcn_sched_barrier(0);
         }
     } else {
         // second operand: the linear half (gated) or grad (dGELU, dSiLU)

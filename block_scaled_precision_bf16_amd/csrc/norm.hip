@@ -61,11 +61,12 @@ __device__ __forceinline__ T block_sum(T v, T *red, int waves, int first = 0)
 // (sum / K + eps)^(-1/2) in 64 bits, where every element of the row has this factor: the
 // hardware's estimate, measured good to 2^-24, and one Newton step, which leaves 2^-47
 // (inv_k = 1 / K: a division would be one more of the steps that all waves wait for).
-// near, the nearest fp32 number, is for the caller; r and low, cut to fp32 and what is
-// left (not negative, so that a zero's sign stays), for y.  0 and Inf go through fp32,
-// where the step would make NaN of them, and what passes fp32 is Inf.
+// near, the nearest fp32 number, is for the caller; r and low, as the output's functions
+// take them, for y (low is not negative, so that a zero's sign stays).  0 and Inf go
+// through fp32, where the step would make NaN of them, and what passes fp32 is Inf.
 struct Rstd {
     float near, r, low;
+    int wide;                      // as norm_is_wide(r), in a scalar register
 };
 __device__ __forceinline__ Rstd rstd_of(double sum, double inv_k, float eps)
 {
@@ -73,12 +74,20 @@ __device__ __forceinline__ Rstd rstd_of(double sum, double inv_k, float eps)
     const double r = __builtin_amdgcn_rsq(v);
     const double s = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
     Rstd o;
+    o.wide = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(!(s >= 0x1p-64 && s <= 0x1p10)) != 0));
     o.near = o.r = (float)s;
     o.r = (double)o.r > s ? f32_bits(bits_f32(o.r) - 1u) : o.r;
     o.low = (float)(s - (double)o.r);
-    if (!(v > 0.0 && v < 1e300 && s <= 0x1.fffffep127)) {
-        o.near = o.r = 1.0f / sqrtf((float)v);
-        o.low = 0.0f;
+    if (__builtin_expect(o.wide != 0, 0)) {
+        const double t = s < 0x1p-64 ? s * 0x1p64 : s;
+        o.r = (float)t;
+        o.r = (double)o.r > t ? f32_bits(bits_f32(o.r) - 1u) : o.r;
+        o.low = (float)(t - (double)o.r);
+        if (!(v > 0.0 && v < 1e300 && s <= 0x1.fffffep127)) {
+            o.near = o.r = 1.0f / sqrtf((float)v);
+            o.low = 0.0f;
+        }
+        o.r = f32_bits(bits_f32(o.r) | 0x80000000u);
     }
     return o;
 }
@@ -174,19 +183,32 @@ __device__ __forceinline__ NormOut<AL> norm_out(const NormArgs &a, int64_t row, 
     return o;
 }
 
-// The outputs of chunk c of a row; every lane of a wave takes part.
+// The outputs of chunk c of a row; every lane of a wave takes part.  wide: by 64 bits,
+// the same for all of them.
 template <int FMT, int NT, bool AL>
 __device__ __forceinline__ void norm_write(const NormArgs &a, const NormOut<AL> &o, int64_t row, uint32_t c,
-                                           uint32_t nb, const uint32_t (&h)[4], const Rstd &rstd, uint4 wt)
+                                           uint32_t nb, const uint32_t (&h)[4], const Rstd &rstd, uint4 wt,
+                                           int wide)
 {
     const bool quad = (nb & 3) == 0;
     if (a.q_h)
         store_scales(o.ks, cast8<kFmtRoundUp, NT>(o.k, h, c), c, nb, quad);
     if (!a.y && !a.q_row)
         return;
-    const uint32_t y[4] = {
-        norm_pair(h[0], rstd.r, rstd.low, wt.x), norm_pair(h[1], rstd.r, rstd.low, wt.y),
-        norm_pair(h[2], rstd.r, rstd.low, wt.z), norm_pair(h[3], rstd.r, rstd.low, wt.w)};
+    uint32_t y[4];
+    const uint32_t w[4] = {wt.x, wt.y, wt.z, wt.w};
+    if (__builtin_expect(wide == 0, 1)) {
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+            y[d] = norm_pair(h[d], rstd.r, rstd.low, w[d]);
+    } else {
+        const double f = norm_factor(rstd.r, rstd.low);
+#pragma unroll
+        for (int d = 0; d < 4; d++) {
+            y[d] = norm_pair_wide(h[d], f, w[d]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
     if (a.y)
         row_store<0>(o.y, c, make_uint4(y[0], y[1], y[2], y[3]));
     if (!a.q_row)
@@ -268,6 +290,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
     NormRow<CH> next;
     int64_t row = row_of(0, (int)blockIdx.x, n);
     norm_load<CH, NT, AL>(a, row, next);
+    int large = 0;                 // a weight of the wave's
     for (int64_t step = 0; row < rows; step++) {
         uint32_t h[CH][4];
         double s0 = 0.0, s1 = 0.0;
@@ -282,16 +305,26 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
         norm_load<CH, NT, AL>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
+        if (step == 0) {           // here, or the first row's loads would wait for the weights
+            bool l = false;
+#pragma unroll
+            for (int i = 0; i < CH; i++) {
+                asm("" : "+v"(wt[i].x), "+v"(wt[i].y), "+v"(wt[i].z), "+v"(wt[i].w));
+                l |= norm_is_wide(wt[i]);
+            }
+            large = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(l) != 0));
+        }
         const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), inv_k, a.eps);
         if (row < a.M && threadIdx.x == 0)
             put_rstd(a, row, rstd);
         const NormOut<AL> o = norm_out<AL>(a, row, nb);
+        const int wide = large | rstd.wide;
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             const uint32_t c = threadIdx.x + i * blockDim.x;
             if (a.h)
                 row_store<0>(o.h, c, make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]));
-            norm_write<FMT, NT, AL>(a, o, row, c, nb, h[i], rstd, wt[i]);
+            norm_write<FMT, NT, AL>(a, o, row, c, nb, h[i], rstd, wt[i], wide);
         }
         row = after;
     }
@@ -346,7 +379,9 @@ __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
             v = row_fix<AL>(v, c, K);
             wt = a.w ? row_fix<AL>(wt, c, K) : wt;
             const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-            norm_write<FMT, 0, AL>(a, o, row, c, nb, h, rstd, wt);
+            const int wide =
+                rstd.wide | __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(norm_is_wide(wt)) != 0));
+            norm_write<FMT, 0, AL>(a, o, row, c, nb, h, rstd, wt, wide);
         }
     }
 }
