@@ -749,28 +749,39 @@ __global__ __launch_bounds__(512) void norm_back_long_kernel(NormBackArgs a)
 }
 
 // Their partial weight gradients: slice blockIdx.y of the rows, a chunk per thread, four
-// rows' loads under way.  Both and their sums, 4096 x 20480 with dres: from bf16 208 us,
-// from 8 bits 193 us (0.67 GB; 1.2 GB with what is read twice).
+// rows' loads under way (at any byte 168 registers, with a few of them spilled: x 20481
+// from bf16 276 us, with the 187 that it would take, two waves a SIMD, 301).  Both and
+// their sums, 4096 x 20480 with dres: from bf16 209 us, from 8 bits 191 us (0.67 GB; 1.2 GB
+// with what is read twice).
 template <bool AL>
-__global__ __launch_bounds__(256) void norm_dweight_long_kernel(NormBackArgs a)
+__global__ __launch_bounds__(256, AL ? 1 : 3) void norm_dweight_long_kernel(NormBackArgs a)
 {
     const uint32_t c = blockIdx.x * 256 + threadIdx.x;
     if (8 * (int64_t)c >= a.K)
         return;
     const Row<AL, const uint16_t> w = row_at<AL>(a.w, 0, a.w ? a.K : 0);
-    float sum[8] = {};
+    // in fp32 over 64 rows at a time, those sums in 64 bits: a slice of 2^17 rows in one
+    // line would be off by 2^-7 of its terms' magnitudes at worst
+    double sum[8] = {};
+    for (int64_t row0 = blockIdx.y; row0 < a.M; row0 += 64 * (int64_t)gridDim.y) {
+        const int64_t end = row0 + 64 * (int64_t)gridDim.y < a.M ? row0 + 64 * (int64_t)gridDim.y : a.M;
+        float run[8] = {};
 #pragma unroll 4
-    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
-        float dy[8], g[8], xh[8];
-        long_chunk<AL>(a, long_row<AL>(a, row), w, c, a.rstd[row], dy, g, xh);
+        for (int64_t row = row0; row < end; row += gridDim.y) {
+            float dy[8], g[8], xh[8];
+            long_chunk<AL>(a, long_row<AL>(a, row), w, c, a.rstd[row], dy, g, xh);
+#pragma unroll
+            for (int d = 0; d < 8; d++)
+                run[d] = __builtin_fmaf(dy[d], xh[d], run[d]);
+        }
 #pragma unroll
         for (int d = 0; d < 8; d++)
-            sum[d] = __builtin_fmaf(dy[d], xh[d], sum[d]);
+            sum[d] += (double)run[d];
     }
 #pragma unroll
     for (int d = 0; d < 8; d++)
         if (8 * (int64_t)c + d < a.K)
-            a.partials[(int64_t)blockIdx.y * a.K + 8 * (int64_t)c + d] = sum[d];
+            a.partials[(int64_t)blockIdx.y * a.K + 8 * (int64_t)c + d] = (float)sum[d];
 }
 
 // dweight[k] = sum of partials[p][k]: 32 columns by 32 slices of p a workgroup,

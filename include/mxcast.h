@@ -598,7 +598,9 @@ size_t mx_rmsnorm_workspace_size(int64_t M, unsigned axis_mask);
  *   dh[m][k]    = bf16(dres + rstd (g - xhat c))     the gradient of x, and the
  *                 same of the residual
  *   dweight[k]  = sum_m dy xhat
- * sums in fp32 in a fixed order (results are run-to-run identical).
+ * g, xhat and the sums in fp32, these in a fixed order (results are run-to-run
+ * identical); a column's weight gradient in lines of at most ceil(M / 256) rows, of 64
+ * where rows are longer than 16384.
  *   dy         device, bf16 [M][K]: the gradient of y
  *   h          bf16 [M][K], or NULL: then
  *   q_h, s_h   the forward's 8-bit copy is read in its place (NULL with h)
