@@ -1157,7 +1157,8 @@ def moe_combine_backward(dout, y, weights=None, pos=None, slots=None, want_dweig
                          stream=None):
     """Gradients of moe_combine from that of its output, dout bf16 [T][K]: {dy (of
     y's shape, zeros in rows without a slot), dweights (float32 [T][top])}.  With
-    pos, slots as moe_sort returned it."""
+    pos, slots as moe_sort returned it: a row whose slot's pos is another row is not
+    written."""
     T, top, rows, K, pp, wp = _rows_and_slots(y, weights, pos)
     dev = y.device
     if (pos is None) != (slots is None):

@@ -552,7 +552,11 @@ __global__ __launch_bounds__(256) void combine_back_kernel(CombineArgs a, int64_
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), s = w - zeros;
     if (s < 0) {
         const int64_t r0 = w * kZeroRows;
-        const bool empty = lane < kZeroRows && r0 + lane < a.rows && a.slots[r0 + lane] == -1;
+        bool empty = false;
+        if (lane < kZeroRows && r0 + lane < a.rows) {
+            const int32_t slot = a.slots[r0 + lane];
+            empty = slot < 0 || slot >= a.T * a.top;
+        }
         for (uint64_t m = __builtin_amdgcn_ballot_w64(empty); m; m &= m - 1) {
             uint16_t *const out = a.out + (r0 + __builtin_ctzll(m)) * a.K;
             int64_t c = lane;

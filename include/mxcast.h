@@ -741,9 +741,9 @@ mx_status moe_combine(const void *y, int64_t rows, int64_t K, const int32_t *pos
  *   dy[r][k]       = bf16(weights[s] dout[t][k]) for the row r of slot s = (t, j)
  *   dweights[t][j] = sum_k dout[t][k] y[r][k], in fp32; 0 for a slot without a row
  *   pos, slots  device, both as moe_sort gives them, or both NULL (slot i is row
- *             i, rows = T * top).  A row whose slot is -1 gets zeros.  Row r is
- *             its slot's where pos[slots[r]] is r again; a row for which that is
- *             not so is left as it was (moe_sort gives none)
+ *             i, rows = T * top).  A row whose slot is outside 0 .. T * top - 1 gets
+ *             zeros.  Row r is its slot's where pos[slots[r]] is r again; a row
+ *             for which that is not so is left as it was (moe_sort gives none)
  *   weights   fp32 [T][top] or NULL (ones)
  *   dy        bf16 [rows][K]
  *   dweights  fp32 [T][top], or NULL: not computed
