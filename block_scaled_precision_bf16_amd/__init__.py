@@ -887,15 +887,8 @@ def _new(like, out, stream):
     out's tensor of that name, of as many elements, or a new one (of the pool of the
     stream that works on it)."""
     if out is None and stream is None:
-        empty, bf16 = like.new_empty, like.dtype == BF16
-        same = like.shape
-
-        def give(name, shape, dtype):
-            if shape is same and bf16 and dtype is BF16:      # the fastest of torch's ways
-                return torch.empty_like(like)
-            return empty(shape, dtype=dtype)
-
-        return give
+        empty = like.new_empty
+        return lambda name, shape, dtype: empty(shape, dtype=dtype)
     dev = like.device
 
     def take(name, shape, dtype):
