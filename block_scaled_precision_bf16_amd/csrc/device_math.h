@@ -430,7 +430,8 @@ __device__ __forceinline__ uint32_t norm_pair(uint32_t h, float r, float low, ui
 // 2^11.5 / s (the root of the longest row), so that no hw passes fp32; and one that falls
 // below fp32's normal numbers is off by 2^-150 at most, the output by 2^-140.  All else
 // takes 64 bits: its rows, Inf and NaN among them, come with r's sign set (and below 2^-64
-// r and low are of s 2^64, where fp32 has all their bits).
+// r and low are of s 2^64, where fp32 has all their bits).  16384 x 7168 with both casts,
+// all rows so: 268 us instead of 233.
 __device__ __forceinline__ bool norm_is_wide(float r) { return bits_f32(r) >> 31; }
 __device__ __forceinline__ bool norm_is_wide(uint4 w)
 {

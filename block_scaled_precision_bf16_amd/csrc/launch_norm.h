@@ -61,8 +61,8 @@ inline NormShape norm_shape(int64_t K)
 
 // The backward kernel's workgroups: as many rows at a time as 512 threads hold (a
 // row's elements stay with the same threads, whose weight gradients they are), one
-// workgroup a CU or two where a row takes at most 256 threads, each of which leaves
-// one row of partial sums.  The two-pass kernels: row slices.
+// workgroup a CU, each of which leaves one row of partial sums.  The two-pass kernels: 64
+// slices of the rows.
 inline int norm_back_rows(const NormShape &s) { return s.threads >= 512 ? 1 : 512 / s.threads; }
 inline int64_t norm_back_parts(int64_t M, int64_t K)
 {

@@ -16,7 +16,7 @@
 // Measured for 16384 tokens, 8 experts each: 256 experts by sigmoid, bias, 4 of 8
 // groups 16.1 us (its 18 MB would take 3.4; 430 vector instructions a token, a
 // third of them fp64; 65536 tokens 45 us), by softmax without bias or groups 10.4 us,
-// 64 experts 5.8 us.  The gradient: 64 experts with dscores 6.0 us.
+// 64 experts 5.8 us.  The gradient: 64 experts with dscores 6.4 us.
 #include "bufio.h"
 #include "device_math.h"
 #include "launch_moe.h"
@@ -874,11 +874,16 @@ static void launch_npl16(const RouteArgs &a, bool value, hipStream_t s)
 }
 
 // Tokens up to which a wave takes one alone, for its shorter chain of steps; more fill
-// the chip's 1024 SIMDs with four to a wave.  In a graph, one and four to a wave, 256
-// experts by sigmoid, bias and groups: 32 tokens 4.5 and 7.8 us, 2048 5.2 and 8.0, 8192
-// 10.6 and 10.4; 64 by softmax: 32 tokens 2.8 and 3.4, 2048 3.2 and 3.6, 4096 3.7 and
-// 3.6.  The gradient of 64: 32 tokens 3.1 and 3.4, 4096 3.8 and 3.8, 16384 7.5 and 4.8;
-// of 256 with a wave to each always (16384 11.9 and 13.9, 65536 38.3 and 37.6).
+// the chip's 1024 SIMDs with four to a wave.  In a graph, one and four to a wave, us:
+//                             32 tokens   2048        3000        4096        6000        16384
+//   256, sigmoid, bias, groups 4.5  7.8    5.3  8.0    6.1  8.1    7.0  8.2    8.9 10.1   18.2 15.2
+//   256, softmax               3.8  5.7    4.3  5.8    4.9  5.9    5.6  6.0    6.8  6.8   13.2  9.9
+//   64, softmax                2.8  3.2    3.1  3.5    3.3  3.5    3.6  3.6    4.3  3.7    7.5  4.7
+//   8, softmax                 2.5  2.7    2.8  2.9    3.0  3.0    3.2  3.0    3.7  3.1    6.2  3.5
+// They cross near 3000 tokens of 8 experts and 8000 of 256 by sigmoid; the one number lies
+// below all of that, which costs 256 experts up to 2 us between 2049 and 8000 tokens.  The
+// gradient of 64: 32 tokens 3.4 and 3.9, 4096 4.2 and 4.1, 16384 9.4 and 5.6; of 256 with a
+// wave to each always (4096 5.5 and 6.9, 16384 13.7 and 13.6, 65536 42.5 and 37.3).
 constexpr int64_t kFewTokens = 2048;
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)

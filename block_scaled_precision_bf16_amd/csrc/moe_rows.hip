@@ -452,7 +452,10 @@ hipError_t launch_gather(const GatherArgs &a, hipStream_t s)
     // are read faster; with few reads of each that is more than the L2 saves (of 8
     // experts, in order and in stretches: 64 MiB of tokens to 2 experts 38.5 and 31 us,
     // 112 MiB 67 and 73 us, 128 MiB 78 and 88 us; to 4, 64 MiB 75 and 54 us, 112 MiB 133
-    // and 125 us, 224 MiB 273 and 250 us).
+    // and 125 us, 224 MiB 273 and 250 us).  With many experts it matters little: 56 MiB of
+    // tokens to 8 of 64 133.7 and 134.8 us, of 256 137.9 and 136.4, to 2 of 64 36.7 and 36.1;
+    // 128 MiB to 4 of 64 152.6 and 147.8, to 8 of 256 304.9 and 304.8, to 4 of 256 in rows of
+    // 2048 bytes 153.4 and 155.2.
     const bool near = a.T * a.row_bytes <= int64_t(1) << 26 || a.top >= 4;
     const int64_t stretch = near ? (units + 8 * kSlices - 1) / (8 * kSlices) : 0;
     const int64_t blocks = near ? 8 * kSlices * stretch : units;

@@ -17,10 +17,10 @@
 // workgroup, which a second kernel adds in a fixed order.
 //
 // Measured (a copy of 1 GiB runs at 5.1 TB/s, one of 118 MB at 5.5 to 7): 16384 x 7168
-// with a residual, the row-wise cast and the 8-bit copy 168 us (0.95 GB, 5.6 TB/s),
-// 2048 x 8192 with a residual and the row-wise cast 23.5 us (118 MB, 5.0 TB/s), one row
-// of 4096 3 us.  Backward of 16384 x 7168 with dres from bf16 151 us (0.94 GB, 6.2
-// TB/s), from 8 bits 135 us (0.83 GB, 6.1 TB/s), the sums of its partial weight
+// with a residual, the row-wise cast and the 8-bit copy 169 us (0.95 GB, 5.6 TB/s),
+// 2048 x 8192 with a residual and the row-wise cast 24.2 us (118 MB, 4.9 TB/s), one row
+// of 4096 3.8 us.  Backward of 16384 x 7168 with dres from bf16 153 us (0.94 GB, 6.1
+// TB/s), from 8 bits 143 us (0.83 GB, 5.8 TB/s), the sums of its partial weight
 // gradients 4.5 us more.
 #include "bufio.h"
 #include "device_math.h"
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
 
 // Rows of any length, in two passes: the second finds the row in the caches (and
 // each thread what it wrote itself).  4096 x 20480 with a residual and the row-wise
-// cast 141 us (0.59 GB, 4.2 TB/s; its h read again from the caches), x 20481 200 us.
+// cast 144 us (0.59 GB, 4.1 TB/s; its h read again from the caches), x 20481 164 us.
 template <int FMT, bool AL>
 __global__ __launch_bounds__(512) void norm_long_kernel(NormArgs a)
 {
@@ -394,10 +394,13 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
     // 1024 threads a CU, whose next rows are on their way meanwhile (2048 x 8192 row-wise:
     // 23.7 us, with twice as many that take two rows each 24.7, with half 29.4; 4096 x 8192
     // 41.5, 42.7, 54.4).  From 16384 rows on that are too large for the caches workgroups
-    // of two rows, handed out as others end, are faster: 16384 x 7168 row-wise 166 -> 157
-    // us, 16384 x 8192 to bf16 199 -> 182, 131072 x 1024 row-wise 187 -> 158, 32768 x 2048
-    // 79 -> 74; but 8192 x 8192 78 -> 79, one workgroup a CU (16400 x 16384) 341 -> 370,
-    // rows at any byte 200 -> 219.
+    // of two rows, handed out as others end, are faster (whole calls; a trace charges a
+    // kernel for the stores of the one before it as well): 16384 x 7168 row-wise 168 -> 155
+    // us, with the 8-bit copy 188 -> 169, with both casts too 256 -> 241, 16384 x 8192 to
+    // bf16 202 -> 183, 131072 x 1024 row-wise 190 -> 160, 32768 x 2048 79 -> 74, 16384 x 4096
+    // 78 -> 74.  Below, it depends on the row: 8192 x 7168 73.6 -> 74.7, 8192 x 8192 78.6 ->
+    // 80.7, 10240 x 8192 to bf16 123 -> 135, but 10240 x 7168 97 -> 94, 12288 x 7168 124 ->
+    // 113; and one workgroup a CU (16400 x 16384) 341 -> 370, rows at any byte 200 -> 219.
     const bool many = a.stream && rows >= 16384 && a.K % 8 == 0 && n.chunks != 0 && n.threads <= 512;
     const int64_t pairs = (rows + 511) / 512 * 256;
     const int64_t most = n.chunks == 0 ? 1024 : !many ? 256 * (1024 / n.threads) : pairs < 65536 ? pairs : 65536;

@@ -636,8 +636,9 @@ size_t mx_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
  *             groups, the lowest index first.  Keys are compared in 64 bits;
  *             without a bias, and where no two are added, by the logits
  *             themselves, exactly
- *   weights   p of the chosen ones (without the bias), with MX_ROUTE_RENORM
- *             divided by their sum (0 where that is 0), times scale
+ *   weights   p of the chosen ones (without the bias), in fp32 (0 below 2^-150,
+ *             and in steps of 2^-149 below 2^-126), with MX_ROUTE_RENORM divided
+ *             by their sum (0 where that is 0), times scale
  * A slot that no expert is left for (fewer unmasked ones than `top`) gets expert
  * -1 and weight 0, which nvfp4_matvec_experts and moe_sort take as no expert.  A
  * token with a NaN among the keys of its unmasked experts gets experts -1 and
@@ -672,7 +673,8 @@ mx_status moe_route(const void *logits, const float *bias, int64_t T, int64_t E,
  *   dweights  fp32 [T][top];  dscores  fp32 [T][E] or NULL
  *   dlogits   [T][E], of the logits' type
  * Where p is NaN so is the gradient; a masked logit (-Inf) has gradient 0, whatever
- * stands in its dscores.
+ * stands in its dscores.  With MX_ROUTE_RENORM the weights' part is exactly 0 where
+ * one choice is live.
  */
 mx_status moe_route_backward(const void *logits, const int32_t *experts, const float *dweights,
                              const float *dscores, int64_t T, int64_t E, int64_t top, float scale,
