@@ -113,3 +113,25 @@ def test_rows_of_each_magnitude(K):
     x = normal(g, 250, K).float().clamp(-3.9, 3.9) * torch.exp2(torch.arange(250.0) - 124).view(-1, 1)
     for w in (torch.ones(K), 1.5 * torch.ones(K), 2.0 ** 60 * torch.ones(K), 2.0 ** -60 * torch.ones(K)):
         check(x.clamp(-3.3e38, 3.3e38).to(BF16), w.to(BF16))
+
+
+@pytest.mark.parametrize("K", [264, 77, 1111, 16392])
+def test_one_row_of_the_largest_numbers_anywhere(K):
+    """One row among ordinary ones, in each place of a tile and a half of 128 rows: as it
+    is alone, the others as without it, columns as mx_quantize casts that y."""
+    g = generator(K)
+    M = 200
+    x, w = normal(g, M, K).cuda(), (1.25 + torch.rand(K, generator=g)).to(BF16).cuda()
+    clean = mx.mx_rmsnorm(x, w, axis=3, want_y=True)
+    rows = [r for r in range(M) if r % 3 == 0 or r % 32 in (15, 16, 31)] if K > 2000 else range(M)
+    for r in rows:
+        z = x.clone()
+        z[r] *= 2.0 ** 125
+        a = mx.mx_rmsnorm(z, w, axis=3, want_y=True)
+        b = mx.mx_rmsnorm(z[r:r + 1].clone(), w, axis=1, want_y=True)
+        assert torch.equal(a["y"][r], b["y"][0]) and bool(a["y"][r].isfinite().all()), r
+        rest = torch.arange(M, device="cuda") != r
+        assert torch.equal(a["y"][rest], clean["y"][rest]), r
+        assert torch.equal(a["q_row"][rest], clean["q_row"][rest]), r
+        c = mx.mx_quantize(a["y"], axis=2)
+        assert torch.equal(a["q_col"], c["q_col"]) and torch.equal(a["s_col"], c["s_col"]), r
