@@ -17,9 +17,9 @@
 // workgroup, which a second kernel adds in a fixed order.
 //
 // Measured (a copy of 1 GiB runs at 5.1 TB/s, one of 118 MB at 5.5 to 7): 16384 x 7168
-// with a residual, the row-wise cast and the 8-bit copy 169 us (0.95 GB, 5.6 TB/s),
-// 2048 x 8192 with a residual and the row-wise cast 24.2 us (118 MB, 4.9 TB/s), one row
-// of 4096 3.8 us.  Backward of 16384 x 7168 with dres from bf16 153 us (0.94 GB, 6.1
+// with a residual, the row-wise cast and the 8-bit copy 171 us (0.95 GB, 5.6 TB/s),
+// 2048 x 8192 with a residual and the row-wise cast 23.5 us (118 MB, 5.0 TB/s), one row
+// of 4096 3.5 us.  Backward of 16384 x 7168 with dres from bf16 153 us (0.94 GB, 6.1
 // TB/s), from 8 bits 143 us (0.83 GB, 5.8 TB/s), the sums of its partial weight
 // gradients 4.5 us more.
 #include "bufio.h"
@@ -74,7 +74,9 @@ __device__ __forceinline__ Rstd rstd_of(double sum, double inv_k, float eps)
     const double r = __builtin_amdgcn_rsq(v);
     const double s = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
     Rstd o;
-    o.wide = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(!(s >= 0x1p-64 && s <= 0x1p10)) != 0));
+    // (by s's first 32 bits: 2^-64 to 2^10; NaN's and Inf's are larger)
+    const uint32_t first = (uint32_t)((uint64_t)__double_as_longlong(s) >> 32);
+    o.wide = (uint32_t)__builtin_amdgcn_readfirstlane((int)first) - 0x3BF00000u >= 0x40900000u - 0x3BF00000u;
     o.near = o.r = (float)s;
     o.r = (double)o.r > s ? f32_bits(bits_f32(o.r) - 1u) : o.r;
     o.low = (float)(s - (double)o.r);
@@ -290,7 +292,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
     NormRow<CH> next;
     int64_t row = row_of(0, (int)blockIdx.x, n);
     norm_load<CH, NT, AL>(a, row, next);
-    int large = 0;                 // a weight of the wave's
+    // (behind the first row's loads, which are on their way meanwhile)
+    bool l = false;
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+        l |= norm_is_wide(wt[i]);
+    const int large = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(l) != 0));
     for (int64_t step = 0; row < rows; step++) {
         uint32_t h[CH][4];
         double s0 = 0.0, s1 = 0.0;
@@ -305,15 +312,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a)
         const int64_t after = row_of(step + 1, (int)blockIdx.x, n);
         norm_load<CH, NT, AL>(a, after, next);
         __builtin_amdgcn_sched_barrier(0);
-        if (step == 0) {           // here, or the first row's loads would wait for the weights
-            bool l = false;
+        // the weights stay packed: as fp32 they would take 16 registers more, and a wave a
+        // SIMD less (16384 x 7168 row-wise 162 us instead of 156)
+        if constexpr (CH > 1)
 #pragma unroll
-            for (int i = 0; i < CH; i++) {
+            for (int i = 0; i < CH; i++)
                 asm("" : "+v"(wt[i].x), "+v"(wt[i].y), "+v"(wt[i].z), "+v"(wt[i].w));
-                l |= norm_is_wide(wt[i]);
-            }
-            large = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(l) != 0));
-        }
         const Rstd rstd = rstd_of(block_sum(s0 + s1, red[step & 1], waves), inv_k, a.eps);
         if (row < a.M && threadIdx.x == 0)
             put_rstd(a, row, rstd);
@@ -395,12 +399,12 @@ static hipError_t launch_norm_fmt(const NormArgs &a, hipStream_t s)
     // 23.7 us, with twice as many that take two rows each 24.7, with half 29.4; 4096 x 8192
     // 41.5, 42.7, 54.4).  From 16384 rows on that are too large for the caches workgroups
     // of two rows, handed out as others end, are faster (whole calls; a trace charges a
-    // kernel for the stores of the one before it as well): 16384 x 7168 row-wise 168 -> 155
-    // us, with the 8-bit copy 188 -> 169, with both casts too 256 -> 241, 16384 x 8192 to
-    // bf16 202 -> 183, 131072 x 1024 row-wise 190 -> 160, 32768 x 2048 79 -> 74, 16384 x 4096
-    // 78 -> 74.  Below, it depends on the row: 8192 x 7168 73.6 -> 74.7, 8192 x 8192 78.6 ->
-    // 80.7, 10240 x 8192 to bf16 123 -> 135, but 10240 x 7168 97 -> 94, 12288 x 7168 124 ->
-    // 113; and one workgroup a CU (16400 x 16384) 341 -> 370, rows at any byte 200 -> 219.
+    // kernel for the stores of the one before it as well): 16384 x 7168 row-wise 166 -> 158
+    // us, with the 8-bit copy 187 -> 171, with both casts too 255 -> 241, 16384 x 8192 to
+    // bf16 202 -> 180, 131072 x 1024 row-wise 189 -> 161, 32768 x 2048 78 -> 72, 16384 x 4096
+    // 77 -> 74.  Below, it depends on the row: 8192 x 7168 73 -> 78, 8192 x 8192 77 -> 81,
+    // 10240 x 8192 to bf16 122 -> 127, but 12288 x 7168 123 -> 117, to bf16 136 -> 123; and
+    // one workgroup a CU (16400 x 16384) 341 -> 370, rows at any byte 200 -> 219.
     const bool many = a.stream && rows >= 16384 && a.K % 8 == 0 && n.chunks != 0 && n.threads <= 512;
     const int64_t pairs = (rows + 511) / 512 * 256;
     const int64_t most = n.chunks == 0 ? 1024 : !many ? 256 * (1024 / n.threads) : pairs < 65536 ? pairs : 65536;
